@@ -420,6 +420,51 @@ int hq_delta_commit(float *state, const float *k, const float *v, const float *a
                     const int32_t *path, const int32_t *n_accept, int32_t M, int32_t H, int32_t D, uint32_t flags,
                     void *stream);
 
+/* ------------------------------------------------------------------------
+ * A batch of requests.  The calls below run the verify pass for several
+ * sequences at once: sequences that share a long prefix, hold their keys and
+ * values in pages of one cache, and use low-rank adapters of their own beside
+ * the shared quantized projections.  The pages this library follows describe
+ * one sequence; these calls have no counterpart there.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of activations, residuals, adapters and caches. */
+typedef enum { HQ_F32 = 0, HQ_F16 = 1, HQ_BF16 = 2 } hq_type;
+
+/* Residual addition, RMS norm and the quantization of the result for the
+ * layers like `desc`, in one pass over the rows:
+ *     s  = x + residual                        (fp32)
+ *     y  = s / sqrt(mean(s^2) + eps) * weight
+ *     residual_out = round(s), h = round(y)
+ *     x' = the rotated y (hq_rotate_quant_act), sx = max|x'| / 127,
+ *     qx = clamp(rint(x' / sx), -127, 127)
+ * The norm is taken of s before it is rounded into residual_out.  The codes
+ * are formed from weight * s, without the factor 1 / sqrt(mean + eps): it is
+ * the same for the whole row, so it cancels in x' / sx and enters sx alone,
+ * and one reduction per row gives both the norm and the largest value.
+ *   x         x_type [M][K], rows ldx elements apart
+ *   residual  r_type [M][K], rows ldr elements apart, or NULL: s = x
+ *   residual_out  r_type [M][K], rows ldr elements apart, or NULL; may be
+ *             `residual` itself (or x, where types and strides agree)
+ *   weight    fp32 [K];  eps >= 0, finite
+ *   h         h_type [M][K], rows ldh elements apart, or NULL: the normed row
+ *             without rotation (for adapters, routers, ...); must not overlap
+ *             the inputs, except that it may be x with the same type and stride
+ *   signs, qx, gsum, qop, sx  as in hq_rotate_quant_act (qx 8-byte aligned);
+ *             all of qx, gsum and qop may be NULL when h or residual_out is
+ *             given (then signs and sx may be NULL too: the norm alone)
+ *   M         0..HQ_MAX_M with qop, else 0..2^20 (the codes of a longer batch
+ *             feed hq_verify_gemm_q8 in slices)
+ * x, residual, residual_out, weight and h are 16-byte aligned and their rows
+ * too (ldx, ldr, ldh at least K and a multiple of 16 bytes).  An all-zero row
+ * has sx = 0 and codes 0; NaN and infinities of a row reach its sx.  flags:
+ * HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (weight and signs are then read before
+ * the wait for the previous kernel). */
+int hq_add_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, int64_t ldx, const void *residual,
+                      void *residual_out, int32_t r_type, int64_t ldr, const float *weight, float eps, int32_t M,
+                      const uint32_t *signs, void *h, int32_t h_type, int64_t ldh, int8_t *qx, int32_t *gsum,
+                      void *qop, float *sx, uint32_t flags, void *stream);
+
 /* Self-test of the bounded-wait path: launches one block that waits on a
  * shared-memory barrier nothing will ever complete, giving up after
  * `limit_ns` nanoseconds (1000..100000000) and setting the error word of

@@ -194,7 +194,9 @@ const char *hq_status_string(int status) {
     }
 }
 
-int32_t hq_version(void) { return (2 << 16) | 0; }  // 2.0: tensor-memory GEMM, one launch up to 128 rows; opaque activation operand with group sums
+// 2.0: tensor-memory GEMM, one launch up to 128 rows; opaque activation operand with group sums
+// 2.1: the calls for a batch of requests
+int32_t hq_version(void) { return (2 << 16) | 1; }
 
 size_t hq_packed_bytes(const hq_layer_desc *desc) {
     if (!desc_ok(desc)) return 0;

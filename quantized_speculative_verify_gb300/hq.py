@@ -38,7 +38,10 @@ EXPORTS = ("hq_tree_accept_workspace_bytes", "hq_tree_accept", "hq_status_string
            "hq_verify_gemm_q8", "hq_unpack_codes", "hq_workspace_status",
            "hq_selftest_wait_timeout", "hq_selftest_gemm_wait_timeout", "hq_verify_gemm_noalloc", "hq_noalloc_status",
            "hq_tree_attention_workspace_bytes",
-           "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit")
+           "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant")
+
+HQ_F32, HQ_F16, HQ_BF16 = 0, 1, 2
+TYPES = {torch.float32: HQ_F32, torch.float16: HQ_F16, torch.bfloat16: HQ_BF16}
 
 HQ_ATTN_HEAD_DIM = 128
 HQ_DELTA_HEAD_DIM = 128
@@ -72,6 +75,7 @@ def load() -> ctypes.CDLL:
         raise HQError(HQ_ERR_CUDA, f"libhq.so not found at {_build.LIB}")
     lib = ctypes.CDLL(_build.LIB)
     P, I32, U32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
+    I64, F32 = ctypes.c_int64, ctypes.c_float
     D = ctypes.POINTER(hq_layer_desc)
     sig = {
         "hq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -99,6 +103,8 @@ def load() -> ctypes.CDLL:
         "hq_tree_commit_kv": (ctypes.c_int, [P, P, I32, I32, I32, I32, I32, P, P, U32, P]),
         "hq_delta_tree": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, P, U32, P]),
         "hq_delta_commit": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, U32, P]),
+        "hq_add_norm_quant": (ctypes.c_int, [D, P, I32, I64, P, P, I32, I64, P, F32, I32, P, P, I32, I64, P, P, P, P,
+                                             U32, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -444,3 +450,73 @@ def delta_commit(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
     """Advances the state (in place) along the root and the accepted path."""
     M, H, D = k.shape
     hq_delta_commit(state, k, v, alpha, beta, path, n_accept, M, H, D, flags, stream)
+
+
+# ---------------------------------------------------- a batch of requests ---
+def _type(t) -> int:
+    """The library's element type of a tensor (fp32 where there is none)."""
+    if t is None:
+        return HQ_F32
+    ty = TYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"fp32, fp16 or bf16 expected, got {t.dtype}")
+    return ty
+
+
+def _rows(t, cols: int, what: str) -> int:
+    """The distance in elements between the rows of a tensor whose last dimensions are `cols` contiguous elements."""
+    if t is None:
+        return cols
+    n = 1
+    for d in range(t.dim() - 1, 0, -1):  # the dimensions that make up one row
+        if t.shape[d] != 1 and t.stride(d) != n:
+            raise ValueError(f"{what}: the elements of a row must be contiguous")
+        n *= t.shape[d]
+    if n != cols:
+        raise ValueError(f"{what}: rows of {cols} elements expected, got shape {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, dtype, shape, what: str) -> None:
+    """A contiguous tensor of the given type and shape, or None."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def hq_add_norm_quant(desc, x, x_type: int, ldx: int, residual, residual_out, r_type: int, ldr: int, weight, eps: float,
+                      M: int, signs, h, h_type: int, ldh: int, qx, gsum, qop, sx, flags: int = 0, stream=None) -> None:
+    _check(load().hq_add_norm_quant(ctypes.byref(desc), _ptr(x), x_type, ldx, _ptr(residual), _ptr(residual_out),
+                                    r_type, ldr, _ptr(weight), eps, M, _ptr(signs), _ptr(h), h_type, ldh, _ptr(qx),
+                                    _ptr(gsum), _ptr(qop), _ptr(sx), flags, _stream(stream)), "hq_add_norm_quant")
+
+
+def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch.Tensor, signs, eps: float = 1e-6,
+                   residual_out=None, h=None, qx=None, gsum=None, qop=None, sx=None, flags: int = 0,
+                   stream=None) -> None:
+    """Residual addition, RMS norm and the quantization of the result for the
+    layers like `desc` (hq_add_norm_quant), in one pass: residual_out =
+    x + residual, h = the normed row, qx / gsum / qop / sx = its codes (buffers
+    of act_buffers).  x, residual, residual_out and h: [M][K], fp32, fp16 or
+    bf16, rows any 16-byte-aligned distance apart; residual may be None (the
+    norm of x alone) and any output may be None; residual_out may be residual
+    itself.  weight fp32 [K]."""
+    M, K = x.shape
+    _need(K == desc.K, f"add_norm_quant: x has {K} features, the layer {desc.K}")
+    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (h, "h")):
+        _need(t is None or tuple(t.shape) == (M, K), f"add_norm_quant: {what} must be [{M}][{K}]")
+    _dense(weight, torch.float32, (K,), "add_norm_quant: weight")
+    _dense(qx, torch.int8, (M, K), "add_norm_quant: qx")
+    _dense(gsum, torch.int32, (M, K // desc.group), "add_norm_quant: gsum")
+    _dense(sx, torch.float32, (M,), "add_norm_quant: sx")
+    _need(qop is None or qop.numel() * qop.element_size() >= hq_act_operand_bytes(desc, M), "add_norm_quant: qop is too small")
+    r = residual if residual is not None else residual_out
+    if residual is not None and residual_out is not None:
+        _need(residual.dtype == residual_out.dtype and (M < 2 or residual.stride(0) == residual_out.stride(0)),
+              "add_norm_quant: residual and residual_out need the same type and stride")
+    hq_add_norm_quant(desc, x, _type(x), _rows(x, K, "x"), residual, residual_out, _type(r), _rows(r, K, "residual"),
+                      weight, eps, M, signs, h, _type(h), _rows(h, K, "h"), qx, gsum, qop, sx, flags, stream)

@@ -1,0 +1,184 @@
+"""Residual addition, RMS norm and int8 output in one pass, against a plain
+computation in 64 bits.
+
+Tolerances.  s = x + residual is one fp32 rounding, so residual_out is compared
+bit for bit with the fp32 sum rounded to its type.  The sum of squares adds at
+most 64 + 10 terms in a chain (the rest is a tree), so it is off by at most
+2^-17 relative and rstd by half of that plus two roundings: h is within
+2^-17 + eps / 2 of the value.  The rotation of a 32-block is 5 additions, 2
+products and the product with the weight: |dz| <= 8 * 2^-24 * sum|w s| /
+sqrt(32) over the block; a code is the rounding of c = 127 z / max|z|, so
+|q - c| <= 1/2 + 127 * 2 |dz| / max|z| + 127 * 2^-22.
+"""
+import numpy as np
+import pytest
+import torch
+
+from guard import Guarded
+from quantized_speculative_verify_gb300 import hq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def rotate64(y, signs):
+    """The block rotation in 64 bits, as a matrix product."""
+    i = np.arange(32)
+    H = np.where(np.array([[bin(a & b).count("1") & 1 for b in i] for a in i]), -1.0, 1.0)
+    bits = (signs[:, None] >> np.arange(32, dtype=np.uint32)) & 1
+    z = (y * np.where(bits.reshape(-1), -1.0, 1.0)).reshape(y.shape[0], -1, 32)
+    return (z @ H).reshape(y.shape) / np.sqrt(32.0)
+
+
+def make(M, K, xt, rt, seed, pad=0, spread=30.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    big = torch.ones(K, device=DEV)
+    big[torch.randint(0, K, (2,), generator=g, device=DEV)] = spread
+    x = (torch.randn((M, K + pad), generator=g, device=DEV)[:, :K] * big).to(xt)
+    if pad:
+        x = torch.nn.functional.pad(x, (0, pad))[:, :K]
+    r = torch.randn((M, K + pad), generator=g, device=DEV).to(rt)[:, :K]
+    w = 1.0 + 0.3 * torch.randn(K, generator=g, device=DEV)
+    return x, r, w, hq.hq_make_signs(seed, K)
+
+
+def signs_dev(signs):
+    return torch.from_numpy(signs.view(np.int32)).to(DEV)
+
+
+def check(x, r, w, signs, eps, res_out, h, qx, sx):
+    K = x.shape[1]
+    s32 = x.float() + r.float() if r is not None else x.float()
+    if res_out is not None:
+        assert torch.equal(res_out, s32.to(res_out.dtype))
+    s = s32.double().cpu().numpy()
+    w64 = w.double().cpu().numpy()
+    rstd = 1.0 / np.sqrt((s * s).mean(1, keepdims=True) + eps)
+    if h is not None:
+        y = s * rstd * w64
+        rel = 2.0 ** -17 + torch.finfo(h.dtype).eps / 2
+        tiny = torch.finfo(h.dtype).smallest_normal
+        assert np.all(np.abs(h.double().cpu().numpy() - y) <= rel * np.abs(y) + tiny)
+    if qx is not None:
+        z = rotate64(s * w64, signs)
+        dz = 8 * 2.0 ** -24 * np.abs(s * w64).reshape(s.shape[0], -1, 32).sum(2).max(1, keepdims=True) / np.sqrt(32.0)
+        amax = np.abs(z).max(1, keepdims=True)
+        q = qx.cpu().numpy().astype(np.float64)
+        c = 127.0 * z / amax
+        off = np.abs(q - c) - 0.5
+        lim = 254.0 * dz / amax + 127 * 2.0 ** -22
+        assert np.all(off <= lim), f"worst {np.max(off - lim)}"
+        assert np.abs(q).max(1).min() == 127  # the largest value of every row takes the largest code
+        ref = (rstd * amax / 127.0)[:, 0]
+        assert np.all(np.abs(sx.double().cpu().numpy() - ref) <= ref * (2.0 ** -17 + (dz / amax)[:, 0]))
+
+
+CASES = [  # M, K, group, format, x, residual, h
+    (1, 32, 32, "w4", F32, F32, F32), (1, 4096, 64, "w4", F32, BF16, BF16), (3, 256, 16, "w8", F16, F16, F16),
+    (16, 4096, 64, "w4", F32, F32, F16), (17, 1056, 32, "w4", BF16, BF16, F32), (32, 2080, 16, "w4", F32, BF16, BF16),
+    (33, 1024, 64, "w4", F16, F32, F16), (64, 512, 16, "w4", BF16, F32, BF16), (65, 2048, 128, "w8", BF16, BF16, BF16),
+    (128, 8192, 256, "w4", F32, F32, F32), (5, 12288, 128, "w4", F32, BF16, BF16), (2, 16384, 64, "w8", F32, F16, F16),
+    (2, 32768, 256, "w4", BF16, BF16, BF16), (1, 65536, 64, "w4", F32, F32, F16), (3, 9984, 32, "w4", F16, F16, F16),
+]
+
+
+@pytest.mark.parametrize("M,K,G,fmt,xt,rt,ht", CASES)
+def test_norm_matches_64_bits(M, K, G, fmt, xt, rt, ht):
+    x, r, w, signs = make(M, K, xt, rt, seed=M + K)
+    d = hq.make_desc(K, 128, G, fmt)
+    res_out, h = Guarded((M, K), rt, DEV), Guarded((M, K), ht, DEV)
+    qx, sx, gs = Guarded((M, K), torch.int8, DEV), Guarded((M,), F32, DEV), Guarded((M, K // G), torch.int32, DEV)
+    qop = Guarded((hq.hq_act_operand_bytes(d, M),), torch.uint8, DEV)
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), 1e-5, residual_out=res_out.t, h=h.t, qx=qx.t, gsum=gs.t, qop=qop.t,
+                      sx=sx.t)
+    torch.cuda.synchronize()
+    for t in (res_out, h, qx, sx, gs, qop):
+        t.check()
+    check(x, r, w, signs, 1e-5, res_out.t, h.t, qx.t, sx.t)
+    assert torch.equal(gs.t, qx.t.view(M, K // G, G).to(torch.int32).sum(2, dtype=torch.int32))
+    # the operand holds these codes: the GEMM on it equals the GEMM on the codes, bit for bit
+    layer = hq.pack_layer(0.02 * torch.randn((128, K), device=DEV), G, fmt, signs)
+    ws = torch.zeros(hq.hq_workspace_q8_bytes(layer.desc, M), dtype=torch.uint8, device=DEV)
+    Y, Y8 = (torch.empty((M, 128), device=DEV) for _ in range(2))
+    hq.hq_verify_gemm(layer.desc, layer.blob, qop.t, sx.t, M, Y, None, ws, hq.HQ_LAUNCH_EXACT_ORDER)
+    hq.hq_verify_gemm_q8(layer.desc, layer.blob, qx.t, sx.t, None, M, Y8, None, ws, hq.HQ_LAUNCH_EXACT_ORDER)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Y8)
+
+
+@pytest.mark.parametrize("M,K", [(300, 1024), (1000, 4096), (257, 8192)])
+def test_norm_of_many_rows_without_an_operand(M, K):
+    x, r, w, signs = make(M, K, BF16, BF16, seed=M)
+    d = hq.make_desc(K, 128, 32, "w4")
+    h, qx, sx = torch.empty_like(x), torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    out = torch.empty_like(r)
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), 1e-6, residual_out=out, h=h, qx=qx, sx=sx)
+    check(x, r, w, signs, 1e-6, out, h, qx, sx)
+
+
+def test_norm_strided_rows_and_in_place_residual():
+    M, K = 9, 736
+    x, r, w, signs = make(M, K, F32, BF16, seed=5, pad=24)
+    d = hq.make_desc(K, 128, 32, "w8")
+    assert x.stride(0) == K + 24
+    r0 = r.clone()
+    hbuf = torch.full((M, K + 8), 7.0, dtype=F16, device=DEV)
+    qx, sx = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), 1e-5, residual_out=r, h=hbuf[:, :K], qx=qx, sx=sx,
+                      flags=hq.HQ_LAUNCH_PDL)
+    check(x, r0, w, signs, 1e-5, r, hbuf[:, :K], qx, sx)
+    assert bool((hbuf[:, K:] == 7.0).all())
+
+
+def test_norm_alone_and_without_residual():
+    M, K = 4, 512
+    x, _, w, signs = make(M, K, BF16, BF16, seed=6)
+    d = hq.make_desc(K, 128, 64, "w4")
+    h = torch.empty((M, K), device=DEV)
+    hq.add_norm_quant(d, x, None, w, None, 1e-5, h=h)
+    check(x, None, w, signs, 1e-5, None, h, None, None)
+    first = torch.empty_like(x)  # the first layer's residual is x itself
+    hq.add_norm_quant(d, x, None, w, None, 1e-5, residual_out=first, h=x)  # h over x
+    assert torch.equal(first.float().cpu(), make(M, K, BF16, BF16, seed=6)[0].float().cpu())
+    assert np.allclose(x.float().cpu(), h.to(BF16).float().cpu(), rtol=2.0 ** -7, atol=0)
+
+
+def test_norm_degenerate_rows():
+    """Zero rows give zeros; NaN and infinities stay in their row and reach its scale."""
+    M, K = 6, 256
+    x, r, w, signs = make(M, K, F32, F32, seed=7, spread=1.0)
+    x[1], r[1] = 0, 0
+    x[2, 17] = float("nan")
+    x[3, 200] = float("inf")
+    x[4], r[4] = 1e-30, 0
+    d = hq.make_desc(K, 128, 32, "w4")
+    for eps in (0.0, 1e-6):
+        h, qx, sx = torch.empty((M, K), device=DEV), torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+        hq.add_norm_quant(d, x, r, w, signs_dev(signs), eps, h=h, qx=qx, sx=sx)
+        assert not h[1].any() and not qx[1].any() and float(sx[1]) == 0.0
+        assert not torch.isfinite(sx[2]) and not torch.isfinite(sx[3])
+        good = [0, 5]
+        check(x[good], r[good], w, signs, eps, None, h[good], qx[good], sx[good])
+
+
+def test_norm_on_a_side_stream_and_in_a_graph():
+    M, K = 8, 1024
+    x, r, w, signs = make(M, K, F32, BF16, seed=8)
+    sg = signs_dev(signs)
+    d = hq.make_desc(K, 128, 32, "w4")
+    out, h = torch.empty_like(r), torch.empty_like(r)
+    qx, sx = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        hq.add_norm_quant(d, x, r, w, sg, 1e-5, residual_out=out, h=h, qx=qx, sx=sx)
+    st.synchronize()
+    check(x, r, w, signs, 1e-5, out, h, qx, sx)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hq.add_norm_quant(d, x, r, w, sg, 1e-5, residual_out=out, h=h, qx=qx, sx=sx)
+    x.copy_(make(M, K, F32, BF16, seed=9)[0])
+    g.replay()
+    torch.cuda.synchronize()
+    check(x, r, w, signs, 1e-5, out, h, qx, sx)
