@@ -465,6 +465,39 @@ int hq_add_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, 
                       const uint32_t *signs, void *h, int32_t h_type, int64_t ldh, int8_t *qx, int32_t *gsum,
                       void *qop, float *sx, uint32_t flags, void *stream);
 
+/* Low-rank adapters of many requests beside a shared projection: for each row
+ * m with adapter a = ids[m],
+ *     Y[m] = base[m] + scale[a] * B[a] (A[a] x[m])
+ * over the first ranks[a] rows of A[a] and columns of B[a]; a row whose id is
+ * outside [0, n_adapters) has no adapter: Y[m] = base[m].
+ *   x      x_type [M][K], rows ldx elements apart, 16-byte aligned rows
+ *   A      w_type (HQ_F16 or HQ_BF16) [n_adapters][r_max][K], 16-byte aligned
+ *   B      w_type [n_adapters][N][r_max], 16-byte aligned
+ *   ids    int32 [M] (device), in any order; rows of equal id share the reads
+ *          of their adapter, 16 rows at a time
+ *   ranks  int32 [n_adapters] (device) or NULL (r_max each); clamped to
+ *          [0, r_max]; rank 0: no change
+ *   scale  fp32 [n_adapters] (device) or NULL (1 each)
+ *   base   fp32 [M][N], rows ldb elements apart, or NULL (zeros); base may be
+ *          Y itself with ldb = ldy (in place, beside hq_verify_gemm's output)
+ *   Y      fp32 [M][N], rows ldy elements apart (any 4-byte alignment: a part
+ *          of a fused layer's columns); otherwise no overlap with the inputs
+ *   K      a multiple of 8 up to 65536; r_max a multiple of 8 up to 256;
+ *          N >= 1; 0 <= M <= HQ_MAX_M (M = 0: no-op)
+ *   workspace hq_lora_workspace_bytes(M, r_max) bytes, 16-byte aligned
+ * Products of 16-bit values are exact and sums are fp32; fp32 activations (and
+ * the products A x, which stay fp32) enter the tensor cores as three bf16
+ * terms that together hold them.  Sums are taken in a fixed order: results
+ * repeat bit for bit.  Elements of A and B past a rank are not used in any
+ * sum.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (ids, ranks, A and B are
+ * then read before the wait for the previous kernel, which must not write
+ * them).  Launches two kernels. */
+size_t hq_lora_workspace_bytes(int32_t M, int32_t r_max);
+int hq_lora_apply(const void *x, int32_t x_type, int64_t ldx, int32_t M, int32_t K, int32_t N, const void *A,
+                  const void *B, int32_t w_type, int32_t n_adapters, int32_t r_max, const int32_t *ids,
+                  const int32_t *ranks, const float *scale, const float *base, int64_t ldb, float *Y, int64_t ldy,
+                  void *workspace, uint32_t flags, void *stream);
+
 /* Self-test of the bounded-wait path: launches one block that waits on a
  * shared-memory barrier nothing will ever complete, giving up after
  * `limit_ns` nanoseconds (1000..100000000) and setting the error word of

@@ -46,4 +46,14 @@ struct NormArgs {
 };
 cudaError_t launch_norm(const NormArgs &a, bool pdl, cudaStream_t s);
 
+struct LoraArgs {
+    const void *x, *A, *B;
+    const int32_t *ids, *ranks;
+    const float *scale, *base;
+    float *Y, *t;  // t: [M][r_max], the products A x
+    int64_t ldx, ldb, ldy;
+    int x_type, M, K, N, n_adapters, r_max;
+};
+cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s);
+
 }  // namespace hq

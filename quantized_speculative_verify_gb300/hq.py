@@ -38,7 +38,8 @@ EXPORTS = ("hq_tree_accept_workspace_bytes", "hq_tree_accept", "hq_status_string
            "hq_verify_gemm_q8", "hq_unpack_codes", "hq_workspace_status",
            "hq_selftest_wait_timeout", "hq_selftest_gemm_wait_timeout", "hq_verify_gemm_noalloc", "hq_noalloc_status",
            "hq_tree_attention_workspace_bytes",
-           "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant")
+           "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant",
+           "hq_lora_workspace_bytes", "hq_lora_apply")
 
 HQ_F32, HQ_F16, HQ_BF16 = 0, 1, 2
 TYPES = {torch.float32: HQ_F32, torch.float16: HQ_F16, torch.bfloat16: HQ_BF16}
@@ -105,6 +106,9 @@ def load() -> ctypes.CDLL:
         "hq_delta_commit": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, U32, P]),
         "hq_add_norm_quant": (ctypes.c_int, [D, P, I32, I64, P, P, I32, I64, P, F32, I32, P, P, I32, I64, P, P, P, P,
                                              U32, P]),
+        "hq_lora_workspace_bytes": (SZ, [I32, I32]),
+        "hq_lora_apply": (ctypes.c_int, [P, I32, I64, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, I64, P, I64, P,
+                                         U32, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -520,3 +524,41 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
               "add_norm_quant: residual and residual_out need the same type and stride")
     hq_add_norm_quant(desc, x, _type(x), _rows(x, K, "x"), residual, residual_out, _type(r), _rows(r, K, "residual"),
                       weight, eps, M, signs, h, _type(h), _rows(h, K, "h"), qx, gsum, qop, sx, flags, stream)
+
+
+def hq_lora_workspace_bytes(M: int, r_max: int) -> int:
+    return int(load().hq_lora_workspace_bytes(int(M), int(r_max)))
+
+
+def hq_lora_apply(x, x_type: int, ldx: int, M: int, K: int, N: int, A, B, w_type: int, n_adapters: int, r_max: int, ids,
+                  ranks, scale, base, ldb: int, Y, ldy: int, workspace, flags: int = 0, stream=None) -> None:
+    _check(load().hq_lora_apply(_ptr(x), x_type, ldx, M, K, N, _ptr(A), _ptr(B), w_type, n_adapters, r_max, _ptr(ids),
+                                _ptr(ranks), _ptr(scale), _ptr(base), ldb, _ptr(Y), ldy, _ptr(workspace), flags,
+                                _stream(stream)), "hq_lora_apply")
+
+
+def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, ranks=None, scale=None,
+               base=None, Y=None, workspace=None, flags: int = 0, stream=None) -> torch.Tensor:
+    """Y[m] = base[m] + scale[a] * B[a] (A[a] x[m]) with a = ids[m], Y = base
+    where there is no such adapter (hq_lora_apply).  x [M][K]; A [n][r][K] and
+    B [n][N][r], fp16 or bf16; ids int32 [M], ranks int32 [n], scale fp32 [n]
+    on the device; base fp32 [M][N] may be Y itself, or None (zeros)."""
+    M, K = x.shape
+    n, r, _ = A.shape
+    N = B.shape[1]
+    _dense(A, A.dtype, (n, r, K), "lora_apply: A")
+    _dense(B, A.dtype, (n, N, r), "lora_apply: B")
+    _dense(ids, torch.int32, (M,), "lora_apply: ids")
+    _dense(ranks, torch.int32, (n,), "lora_apply: ranks")
+    _dense(scale, torch.float32, (n,), "lora_apply: scale")
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    for t, what in ((base, "base"), (Y, "Y")):
+        _need(t is None or (tuple(t.shape) == (M, N) and t.dtype == torch.float32), f"lora_apply: {what} must be fp32 [{M}][{N}]")
+    need = hq_lora_workspace_bytes(M, r)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _need(workspace.numel() * workspace.element_size() >= need, "lora_apply: the workspace is too small")
+    hq_lora_apply(x, _type(x), _rows(x, K, "x"), M, K, N, A, B, _type(A), n, r, ids, ranks, scale, base,
+                  _rows(base, N, "base"), Y, _rows(Y, N, "Y"), workspace, flags, stream)
+    return Y

@@ -55,3 +55,45 @@ def test_norm_binding_checks_shapes_before_the_library():
         hq.add_norm_quant(d, x, x, w, None, residual_out=torch.zeros((3, 256), dtype=torch.float16))
     with pytest.raises(TypeError, match="CPU tensor"):
         hq.add_norm_quant(d, x, None, w, None, h=x)
+
+
+def lora_call(**kw):
+    a = dict(x=FAKE, xt=hq.HQ_F32, ldx=256, M=4, K=256, N=100, A=FAKE, B=FAKE, wt=hq.HQ_F16, n=3, r=16, ids=FAKE,
+             ranks=FAKE, scale=FAKE, base=FAKE, ldb=100, Y=FAKE + 4096, ldy=100, ws=FAKE, flags=0)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return hq.load().hq_lora_apply(a["x"], a["xt"], a["ldx"], a["M"], a["K"], a["N"], a["A"], a["B"], a["wt"], a["n"],
+                                   a["r"], a["ids"], a["ranks"], a["scale"], a["base"], a["ldb"], a["Y"], a["ldy"],
+                                   a["ws"], a["flags"], None)
+
+
+def test_lora_refuses_bad_arguments():
+    assert lora_call(M=0) == hq.HQ_OK and lora_call(M=0, x=None, ids=None) == hq.HQ_OK
+    bad = [dict(M=-1), dict(M=129), dict(K=0), dict(K=260), dict(K=65544), dict(N=0), dict(r=0), dict(r=12), dict(r=264),
+           dict(n=0), dict(flags=2), dict(xt=5), dict(wt=hq.HQ_F32), dict(wt=9), dict(x=None), dict(A=None),
+           dict(B=None), dict(ids=None), dict(Y=None), dict(ws=None), dict(x=FAKE + 8), dict(A=FAKE + 8),
+           dict(B=FAKE + 2), dict(ws=FAKE + 4), dict(ids=FAKE + 1), dict(ranks=FAKE + 2), dict(scale=FAKE + 2),
+           dict(base=FAKE + 2), dict(Y=FAKE + 3), dict(ldx=248), dict(ldx=258), dict(ldb=99), dict(ldy=99),
+           dict(Y=FAKE, ldb=104)]
+    for b in bad:
+        assert lora_call(**b) == E, b
+    size = hq.hq_lora_workspace_bytes
+    assert size(4, 16) == 256 and size(128, 256) == 131072
+    assert size(0, 16) == size(129, 16) == size(4, 0) == size(4, 12) == size(4, 264) == 0
+
+
+def test_lora_binding_checks_shapes_before_the_library():
+    x, A, B = torch.zeros((2, 64)), torch.zeros((3, 8, 64), dtype=torch.float16), torch.zeros((3, 40, 8), dtype=torch.float16)
+    ids = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="B"):
+        hq.lora_apply(x, A, B.to(torch.bfloat16), ids)
+    with pytest.raises(ValueError, match="ids"):
+        hq.lora_apply(x, A, B, ids.long())
+    with pytest.raises(ValueError, match="A"):
+        hq.lora_apply(torch.zeros((2, 72)), A, B, ids)
+    with pytest.raises(ValueError, match="base"):
+        hq.lora_apply(x, A, B, ids, base=torch.zeros((2, 39)))
+    with pytest.raises(ValueError, match="workspace"):
+        hq.lora_apply(x, A, B, ids, workspace=torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="CPU tensor"):
+        hq.lora_apply(x, A, B, ids)

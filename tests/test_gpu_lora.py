@@ -1,0 +1,150 @@
+"""Low-rank adapters of many requests, against a plain computation in 64 bits.
+
+Tolerance.  The products are exact and each sum is formed in fp32: t = A x adds
+K products (per warp in steps of the tensor cores, then 64 partial sums), B t
+adds 3 r.  A tensor-core step may truncate: one unit of 2^-23 of the largest
+magnitude per step of 16.  With n = K / 16 / 64 + 6 + 64 additions in the
+longest chain of t and 3 r / 16 + 8 in that of B t, the result is within
+2^-22 * (n + 3 r / 16 + 8) of sum_j |B| sum_k |A| |x| times the scale, and the
+last addition rounds once more.
+"""
+import pytest
+import torch
+
+from guard import Guarded
+from quantized_speculative_verify_gb300 import hq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def make(M, K, N, n, r, xt, wt, seed, pad=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.nn.functional.pad(torch.randn((M, K), generator=g, device=DEV).to(xt), (0, pad))[:, :K]
+    A = (torch.randn((n, r, K), generator=g, device=DEV) / K ** 0.5).to(wt)
+    B = (torch.randn((n, N, r), generator=g, device=DEV) / r ** 0.5).to(wt)
+    base = torch.randn((M, N), generator=g, device=DEV)
+    scale = 0.5 + torch.rand(n, generator=g, device=DEV)
+    return x, A, B, base, scale, g
+
+
+def check(Y, x, A, B, ids, ranks, scale, base):
+    n, r, K = A.shape
+    for m, a in enumerate(ids.tolist()):
+        b = base[m].double() if base is not None else torch.zeros(B.shape[1], dtype=torch.float64, device=DEV)
+        if not 0 <= a < n:
+            assert torch.equal(Y[m].double(), b)
+            continue
+        k = min(max(int(ranks[a]), 0), r) if ranks is not None else r
+        s = float(scale[a].double()) if scale is not None else 1.0
+        t = A[a, :k].double() @ x[m].double()
+        d = s * (B[a, :, :k].double() @ t)
+        mag = s * (B[a, :, :k].double().abs() @ (A[a, :k].double().abs() @ x[m].double().abs()))
+        steps = K / 1024 + 70 + 3 * r / 16 + 8
+        lim = 2.0 ** -22 * steps * mag + 2.0 ** -24 * (b + d).abs()
+        err = (Y[m].double() - (b + d)).abs()
+        assert bool((err <= lim).all()), f"row {m}: {float((err - lim).max())}"
+
+
+CASES = [  # M, K, N, adapters, r, x, w
+    (1, 8, 1, 1, 8, F32, F16), (1, 4096, 4096, 3, 16, F16, F16), (2, 40, 33, 2, 8, BF16, BF16),
+    (7, 264, 1000, 4, 24, F32, BF16), (16, 4096, 513, 5, 64, BF16, BF16), (33, 1032, 257, 3, 40, F32, F16),
+    (128, 512, 300, 2, 72, F16, F16), (128, 4096, 777, 1, 128, BF16, BF16), (100, 2048, 4096, 120, 32, F16, BF16),
+    (19, 8192, 129, 6, 256, BF16, F16), (64, 12288, 64, 64, 8, F32, BF16), (5, 65536, 31, 2, 16, F16, F16),
+]
+
+
+@pytest.mark.parametrize("M,K,N,n,r,xt,wt", CASES)
+def test_lora_matches_64_bits(M, K, N, n, r, xt, wt):
+    x, A, B, base, scale, g = make(M, K, N, n, r, xt, wt, seed=M + K + N)
+    ids = torch.randint(-1, n + 1, (M,), generator=g, device=DEV).to(torch.int32)  # -1 and n: none
+    ranks = torch.randint(-2, r + 3, (n,), generator=g, device=DEV).to(torch.int32)
+    Y = Guarded((M, N), F32, DEV, fill=float("nan"))
+    hq.lora_apply(x, A, B, ids, ranks, scale, base=base, Y=Y.t)
+    torch.cuda.synchronize()
+    Y.check()
+    check(Y.t, x, A, B, ids, ranks, scale, base)
+    again = hq.lora_apply(x, A, B, ids, ranks, scale, base=base)
+    assert torch.equal(again, Y.t)  # bit for bit
+    # full ranks, no scale, no base
+    Y = hq.lora_apply(x, A, B, ids)
+    check(Y, x, A, B, ids, None, None, None)
+
+
+@pytest.mark.parametrize("rows", [1, 15, 16, 17, 31, 32, 33, 128])
+def test_lora_rows_of_one_adapter_in_any_order(rows):
+    M, K, N, r = 128, 256, 200, 16
+    x, A, B, base, scale, g = make(M, K, N, 4, r, BF16, BF16, seed=rows)
+    ids = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    ids[torch.randperm(M, generator=g, device=DEV)[:rows]] = 2
+    Y = hq.lora_apply(x, A, B, ids, None, scale, base=base)
+    check(Y, x, A, B, ids, None, scale, base)
+
+
+def test_lora_in_place_on_columns_of_a_fused_output():
+    """Beside one part of a fused projection: Y's rows are wider than N, not 16-byte aligned."""
+    M, K, N, total = 21, 512, 333, 1001
+    x, A, B, _, scale, g = make(M, K, N, 5, 8, F16, F16, seed=3, pad=40)
+    assert x.stride(0) == K + 40
+    full = torch.randn((M, total), generator=g, device=DEV)
+    was = full.clone()
+    ids = (torch.arange(M, device=DEV) % 6 - 1).to(torch.int32)
+    part = full[:, 101:101 + N]
+    ws = torch.empty(hq.hq_lora_workspace_bytes(M, 8), dtype=torch.uint8, device=DEV)
+    hq.lora_apply(x, A, B, ids, None, scale, base=part, Y=part, workspace=ws, flags=hq.HQ_LAUNCH_PDL)
+    check(part, x, A, B, ids, None, scale, was[:, 101:101 + N])
+    assert torch.equal(full[:, :101], was[:, :101]) and torch.equal(full[:, 101 + N:], was[:, 101 + N:])
+
+
+@pytest.mark.parametrize("wt", [F16, BF16])
+def test_lora_does_not_touch_what_is_past_a_rank(wt):
+    """NaN past the rank, in unused adapters and in other rows stays where it is."""
+    M, K, N, r = 6, 128, 70, 24
+    x, A, B, base, scale, g = make(M, K, N, 3, r, F32, wt, seed=4)
+    ranks = torch.tensor([5, 0, 13], dtype=torch.int32, device=DEV)
+    for a, k in enumerate(ranks.tolist()):
+        A[a, k:] = float("nan")
+        B[a, :, k:] = float("nan")
+    ids = torch.tensor([0, 1, 2, -1, 2, 0], dtype=torch.int32, device=DEV)
+    x[3] = float("nan")   # no adapter
+    x[5] = float("inf")   # its own row only
+    Y = hq.lora_apply(x, A, B, ids, ranks, scale, base=base)
+    good = [0, 1, 2, 3, 4]
+    check(Y[good], x[good], A, B, ids[good], ranks, scale, base[good])
+    assert not torch.isfinite(Y[5]).any()
+
+
+def test_lora_extremes_of_the_types():
+    """Largest and subnormal values: the split terms hold them."""
+    K, N, r = 32, 16, 8
+    x = torch.zeros((2, K), device=DEV)
+    x[0, 0], x[0, 1], x[1, 2] = 1.0 + 2.0 ** -23, -1.0, 3.0e-38
+    A = torch.zeros((1, r, K), dtype=F16, device=DEV)
+    A[0, 0, :3] = torch.tensor([2.0 ** -24, 2.0 ** -24, 1.0], device=DEV).to(F16)
+    B = torch.zeros((1, N, r), dtype=F16, device=DEV)
+    B[0, :, 0] = 65504.0
+    Y = hq.lora_apply(x, A, B, torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert float(Y[0, 0]) == 65504.0 * 2.0 ** -47
+    assert abs(float(Y[1, 0]) / (65504.0 * 3.0e-38) - 1) < 2.0 ** -7  # the last terms of 3e-38 are below bf16's range
+
+
+def test_lora_on_a_side_stream_and_in_a_graph():
+    M, K, N, r = 16, 1024, 700, 16
+    x, A, B, base, scale, g = make(M, K, N, 4, r, F16, F16, seed=8)
+    ids = (torch.arange(M, device=DEV) // 4).to(torch.int32)
+    ws = torch.empty(hq.hq_lora_workspace_bytes(M, r), dtype=torch.uint8, device=DEV)
+    Y = torch.empty((M, N), device=DEV)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        hq.lora_apply(x, A, B, ids, None, scale, base=base, Y=Y, workspace=ws)
+    st.synchronize()
+    check(Y, x, A, B, ids, None, scale, base)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hq.lora_apply(x, A, B, ids, None, scale, base=base, Y=Y, workspace=ws)
+    ids.copy_((torch.arange(M, device=DEV) % 3).to(torch.int32))  # the graph follows the ids
+    graph.replay()
+    torch.cuda.synchronize()
+    check(Y, x, A, B, ids, None, scale, base)
