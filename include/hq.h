@@ -56,7 +56,8 @@ typedef enum {
     HQ_ERR_INVALID_ARG = 1, /* NULL pointer, bad size, misaligned pointer   */
     HQ_ERR_UNSUPPORTED = 2, /* valid request the library does not implement */
     HQ_ERR_CUDA = 3,        /* a CUDA runtime call or launch failed          */
-    HQ_ERR_TIMEOUT = 4      /* a bounded device-side wait gave up            */
+    HQ_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up            */
+    HQ_ERR_NO_PAGES = 5     /* a page operation found too few free pages     */
 } hq_status;
 
 typedef enum {
@@ -497,6 +498,108 @@ int hq_lora_apply(const void *x, int32_t x_type, int64_t ldx, int32_t M, int32_t
                   const void *B, int32_t w_type, int32_t n_adapters, int32_t r_max, const int32_t *ids,
                   const int32_t *ranks, const float *scale, const float *base, int64_t ldb, float *Y, int64_t ldy,
                   void *workspace, uint32_t flags, void *stream);
+
+/* A paged key/value cache.  All arrays are the caller's device memory; this
+ * struct is host memory, read during the call only.
+ *   pool    [n_planes][n_pages][heads][page_size] rows of row_bytes bytes
+ *           (a plane: the keys or the values of one layer), planes plane_bytes
+ *           apart, 16-byte aligned
+ *   ref     int32 [n_pages]: how many sequences hold the page; 0 = free
+ *   table   int32 [n_seqs][max_pages]: position p of sequence s lies in row
+ *           p % page_size of page table[s][p / page_size]; unused entries -1
+ *   len     int32 [n_seqs]: positions held (0 = an empty slot)
+ *   status  int32, zeroed once: the first error of a page operation since it
+ *           was last read (hq_pages_status)
+ *   scratch hq_pages_scratch_bytes(&cache) bytes, 16-byte aligned: one call at
+ *           a time
+ * page_size is 16, 32, 64, 128 or 256; row_bytes a multiple of 16 up to 4096;
+ * at most 2^24 pages, 8192 sequences, 2^20 pages a sequence, 65535 heads and
+ * planes; n_pages * page_size and max_pages * page_size below 2^31. */
+typedef struct {
+    void *pool;
+    int32_t *ref;
+    int32_t *table;
+    int32_t *len;
+    int32_t *status;
+    void *scratch;
+    int64_t plane_bytes;
+    int32_t n_planes;
+    int32_t n_pages;
+    int32_t n_seqs;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t row_bytes;
+} hq_pages;
+
+/* Page operations.  Each takes lists in device memory of n entries, n between
+ * 0 and the smaller of 1024 and n_seqs (0: no-op); a sequence may stand in a
+ * list once.  Pages are handed out deterministically: the free pages of lowest
+ * index, to the listed sequences in order, each sequence's positions
+ * ascending.  A call changes everything it was asked to, or nothing: a bad
+ * entry (a sequence outside [0, n_seqs), listed twice, a length that does not
+ * fit, a list that is not ascending) sets the status word to
+ * HQ_ERR_INVALID_ARG, too few free pages to HQ_ERR_NO_PAGES, and nothing is
+ * changed.  A page given up by a call is free for the next call, not for the
+ * same one.  Table entries outside [0, n_pages) inside a sequence's length are
+ * skipped.
+ *
+ * Sequences that share a page never see one another's later writes: a page
+ * held more than once at the time of the call is copied before it is written
+ * (the rows in use, every plane).  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL.
+ *
+ * hq_pages_fork: dst[i], an empty slot, takes the pages and length of src[i]
+ *   (src may repeat, and is not changed); no data moves.
+ * hq_pages_extend: seqs[i] grows by add[i] >= 0 positions; where its last
+ *   page has free rows and is shared, the page is replaced by a copy.
+ * hq_pages_free: gives up every page of seqs[i]; its slot becomes empty (an
+ *   empty slot stays as it is).
+ * hq_pages_compact: drops positions of seqs[i].  base[i] (>= -1, below the
+ *   length) is the last position that stays where it is; the kept ones after
+ *   it are base[i] + keep[i][d], d < n_keep[i], keep strictly ascending from
+ *   at least 1 (rows of `keep` hold max_keep entries, ldkeep apart, 0 <=
+ *   max_keep <= ldkeep <= 2^20, and n_keep[i] is at most max_keep);
+ *   they move to base[i] + 1 + d, the length becomes base[i] + 1 + n_keep[i]
+ *   and the pages past it are given up.  Pages from the first position that
+ *   moves on are replaced where they are shared.  A sequence with n_keep[i] <
+ *   0 is left as it is.  After a tree of m nodes at positions len - m .. len -
+ *   1, base = len - m, keep = hq_tree_accept's path and n_keep = its n_accept
+ *   commit the accepted path.
+ * hq_pages_copy: page dst[i] of every plane becomes a copy of page src[i]
+ *   (counts and tables are not changed).  No page may stand in both lists or
+ *   twice in dst; a pair with an index outside [0, n_pages) is skipped and
+ *   sets the status word to HQ_ERR_INVALID_ARG.  n up to 65535. */
+size_t hq_pages_scratch_bytes(const hq_pages *cache);
+int hq_pages_fork(const hq_pages *cache, const int32_t *src, const int32_t *dst, int32_t n, uint32_t flags,
+                  void *stream);
+int hq_pages_extend(const hq_pages *cache, const int32_t *seqs, const int32_t *add, int32_t n, uint32_t flags,
+                    void *stream);
+int hq_pages_free(const hq_pages *cache, const int32_t *seqs, int32_t n, uint32_t flags, void *stream);
+int hq_pages_compact(const hq_pages *cache, const int32_t *seqs, const int32_t *base, const int32_t *keep,
+                     int32_t ldkeep, int32_t max_keep, const int32_t *n_keep, int32_t n, uint32_t flags,
+                     void *stream);
+int hq_pages_copy(const hq_pages *cache, const int32_t *src, const int32_t *dst, int32_t n, uint32_t flags,
+                  void *stream);
+
+/* Writes the newest rows of B sequences into two planes of the cache: row i
+ * of sequence seqs[b] (seqs NULL: b), i < m_b = starts[b + 1] - starts[b]
+ * (starts NULL: max_rows rows each), goes to position len - m_b + i.
+ *   k, v      in_type [rows][heads][D], rows ldk and ldv elements apart,
+ *             16-byte aligned rows; D = row_bytes / 2
+ *   type      the cache's element type, HQ_F16 or HQ_BF16 (in_type F32 or
+ *             `type`; fp32 is rounded to nearest)
+ *   starts    int32 [B + 1] (device), ascending, within [0, rows]; B <= 65535
+ *   max_rows  the most rows of a sequence, at least 1
+ * Rows whose position or page does not exist are skipped and set the status
+ * word to HQ_ERR_INVALID_ARG.  Pages are written as they are: after a fork,
+ * hq_pages_extend first gives the sequence pages of its own. */
+int hq_pages_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, const void *k, const void *v,
+                   int32_t in_type, int64_t ldk, int64_t ldv, int32_t type, const int32_t *seqs,
+                   const int32_t *starts, int32_t B, int32_t rows, int32_t max_rows, uint32_t flags, void *stream);
+
+/* Synchronizes `stream`, then reads and clears the cache's status word:
+ * HQ_OK, HQ_ERR_INVALID_ARG or HQ_ERR_NO_PAGES. */
+int hq_pages_status(const hq_pages *cache, void *stream);
 
 /* Self-test of the bounded-wait path: launches one block that waits on a
  * shared-memory barrier nothing will ever complete, giving up after

@@ -56,4 +56,45 @@ struct LoraArgs {
 };
 cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s);
 
+// Page operations (k_pages.cu).
+size_t pages_scratch_bytes(const hq_pages &c);
+cudaError_t launch_pages_fork(const hq_pages &c, const int32_t *src, const int32_t *dst, int n, bool pdl, cudaStream_t s);
+cudaError_t launch_pages_extend(const hq_pages &c, const int32_t *seqs, const int32_t *add, int n, bool pdl, cudaStream_t s);
+cudaError_t launch_pages_free(const hq_pages &c, const int32_t *seqs, int n, bool pdl, cudaStream_t s);
+cudaError_t launch_pages_compact(const hq_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
+                                 int ldkeep, int max_keep, const int32_t *n_keep, int n, bool pdl,
+                                 cudaStream_t s);
+cudaError_t launch_pages_copy(const hq_pages &c, const int32_t *src, const int32_t *dst, int n, bool pdl, cudaStream_t s);
+
+struct WriteArgs {
+    const void *k, *v;
+    int64_t ldk, ldv;
+    const int32_t *seqs, *starts;
+    int k_plane, v_plane, in_type, type, B, rows, max_rows;
+};
+cudaError_t launch_pages_write(const hq_pages &c, const WriteArgs &w, bool pdl, cudaStream_t s);
+
+#ifdef __CUDACC__
+// Rows of sequence b of a batch: the first row and their number, always
+// within [0, rows) and at most max_rows, whatever `starts` holds.
+__device__ __forceinline__ void batch_rows(const int32_t *starts, int b, int rows, int max_rows, int &first, int &m) {
+    int lo, hi;
+    if (starts) {
+        lo = starts[b];
+        hi = starts[b + 1];
+    } else {  // B * max_rows is at most rows (checked by the host)
+        lo = b * max_rows;
+        hi = lo + max_rows;
+    }
+    if (lo < 0 || lo > rows || hi < lo) {
+        first = 0;
+        m = 0;
+        return;
+    }
+    if (hi > rows) hi = rows;
+    first = lo;
+    m = hi - lo < max_rows ? hi - lo : max_rows;
+}
+#endif
+
 }  // namespace hq

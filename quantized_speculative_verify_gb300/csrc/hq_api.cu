@@ -190,6 +190,7 @@ const char *hq_status_string(int status) {
         case HQ_ERR_UNSUPPORTED: return "HQ_ERR_UNSUPPORTED";
         case HQ_ERR_CUDA: return "HQ_ERR_CUDA";
         case HQ_ERR_TIMEOUT: return "HQ_ERR_TIMEOUT";
+        case HQ_ERR_NO_PAGES: return "HQ_ERR_NO_PAGES";
         default: return "HQ_ERR_UNKNOWN";
     }
 }

@@ -18,6 +18,27 @@ bool rows_ok(const void *p, int type, int64_t ld, int64_t cols) {
     return aligned(p, 16) && ld >= cols && ld <= (1ll << 40) && (ld * hq::type_bytes(type)) % 16 == 0;
 }
 
+bool cache_ok(const hq_pages *c) {
+    if (!c || !c->pool || !c->ref || !c->table || !c->len || !c->status || !c->scratch) return false;
+    if (!aligned(c->pool, 16) || !aligned(c->scratch, 16) || !aligned(c->ref, 4) || !aligned(c->table, 4) ||
+        !aligned(c->len, 4) || !aligned(c->status, 4))
+        return false;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256)
+        return false;
+    if (c->row_bytes <= 0 || c->row_bytes > 4096 || c->row_bytes % 16 != 0) return false;
+    if (c->n_planes <= 0 || c->n_planes > 65535 || c->heads <= 0 || c->heads > 65535) return false;
+    if (c->n_pages <= 0 || c->n_pages > (1 << 24) || c->n_seqs <= 0 || c->n_seqs > 8192) return false;
+    if (c->max_pages <= 0 || c->max_pages > (1 << 20)) return false;
+    if ((long long)c->n_pages * c->page_size > INT_MAX || (long long)c->max_pages * c->page_size > INT_MAX) return false;
+    const long long page = (long long)c->heads * c->page_size * c->row_bytes;  // below 2^36
+    if (c->plane_bytes % 16 != 0 || c->plane_bytes / page < c->n_pages) return false;
+    // a thread's column number stays an int
+    return (long long)c->n_planes * c->heads * (c->row_bytes / 16) <= INT_MAX - 256;
+}
+
+// A list of a page operation: n entries; a sequence stands in it once.
+bool list_ok(const hq_pages *c, int32_t n) { return n >= 0 && n <= 1024 && n <= c->n_seqs; }
+
 }  // namespace
 
 extern "C" {
@@ -106,6 +127,99 @@ int hq_lora_apply(const void *x, int32_t x_type, int64_t ldx, int32_t M, int32_t
     a.n_adapters = n_adapters;
     a.r_max = r_max;
     return cuda_status(hq::launch_lora(a, w_type, pdl_of(flags), stream_of(stream)));
+}
+
+size_t hq_pages_scratch_bytes(const hq_pages *cache) {
+    if (!cache) return 0;
+    hq_pages c = *cache;  // sized before it is allocated: the pointers do not count
+    alignas(16) static int32_t any[4];
+    c.pool = c.scratch = any;
+    c.ref = c.table = c.len = c.status = any;
+    return cache_ok(&c) ? hq::pages_scratch_bytes(c) : 0;
+}
+
+int hq_pages_fork(const hq_pages *cache, const int32_t *src, const int32_t *dst, int32_t n, uint32_t flags,
+                  void *stream) {
+    if (!cache_ok(cache) || !list_ok(cache, n) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (n == 0) return HQ_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return HQ_ERR_INVALID_ARG;
+    return cuda_status(hq::launch_pages_fork(*cache, src, dst, n, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_extend(const hq_pages *cache, const int32_t *seqs, const int32_t *add, int32_t n, uint32_t flags,
+                    void *stream) {
+    if (!cache_ok(cache) || !list_ok(cache, n) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (n == 0) return HQ_OK;
+    if (!seqs || !add || !aligned(seqs, 4) || !aligned(add, 4)) return HQ_ERR_INVALID_ARG;
+    return cuda_status(hq::launch_pages_extend(*cache, seqs, add, n, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_free(const hq_pages *cache, const int32_t *seqs, int32_t n, uint32_t flags, void *stream) {
+    if (!cache_ok(cache) || !list_ok(cache, n) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (n == 0) return HQ_OK;
+    if (!seqs || !aligned(seqs, 4)) return HQ_ERR_INVALID_ARG;
+    return cuda_status(hq::launch_pages_free(*cache, seqs, n, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_compact(const hq_pages *cache, const int32_t *seqs, const int32_t *base, const int32_t *keep,
+                     int32_t ldkeep, int32_t max_keep, const int32_t *n_keep, int32_t n, uint32_t flags,
+                     void *stream) {
+    if (!cache_ok(cache) || !list_ok(cache, n) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (max_keep < 0 || ldkeep < max_keep || ldkeep > 1 << 20) return HQ_ERR_INVALID_ARG;
+    if (n == 0) return HQ_OK;
+    if (!seqs || !base || !keep || !n_keep || !aligned(seqs, 4) || !aligned(base, 4) || !aligned(keep, 4) ||
+        !aligned(n_keep, 4))
+        return HQ_ERR_INVALID_ARG;
+    return cuda_status(
+        hq::launch_pages_compact(*cache, seqs, base, keep, ldkeep, max_keep, n_keep, n, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_copy(const hq_pages *cache, const int32_t *src, const int32_t *dst, int32_t n, uint32_t flags,
+                  void *stream) {
+    if (!cache_ok(cache) || n < 0 || n > 65535 || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (n == 0) return HQ_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return HQ_ERR_INVALID_ARG;
+    return cuda_status(hq::launch_pages_copy(*cache, src, dst, n, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, const void *k, const void *v,
+                   int32_t in_type, int64_t ldk, int64_t ldv, int32_t type, const int32_t *seqs,
+                   const int32_t *starts, int32_t B, int32_t rows, int32_t max_rows, uint32_t flags, void *stream) {
+    if (!cache_ok(cache) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (k_plane < 0 || k_plane >= cache->n_planes || v_plane < 0 || v_plane >= cache->n_planes) return HQ_ERR_INVALID_ARG;
+    if (!type16(type) || (in_type != HQ_F32 && in_type != type)) return HQ_ERR_INVALID_ARG;
+    if (B < 0 || B > 65535 || rows < 0 || max_rows < 1) return HQ_ERR_INVALID_ARG;
+    if (!starts && (long long)B * max_rows > rows) return HQ_ERR_INVALID_ARG;
+    if (B == 0 || rows == 0) return HQ_OK;
+    const int64_t cols = (int64_t)cache->heads * (cache->row_bytes / 2);
+    if (!k || !v || !rows_ok(k, in_type, ldk, cols) || !rows_ok(v, in_type, ldv, cols)) return HQ_ERR_INVALID_ARG;
+    if (!aligned(seqs, 4) || !aligned(starts, 4)) return HQ_ERR_INVALID_ARG;
+    hq::WriteArgs w;
+    w.k = k;
+    w.v = v;
+    w.ldk = ldk;
+    w.ldv = ldv;
+    w.seqs = seqs;
+    w.starts = starts;
+    w.k_plane = k_plane;
+    w.v_plane = v_plane;
+    w.in_type = in_type;
+    w.type = type;
+    w.B = B;
+    w.rows = rows;
+    w.max_rows = max_rows < rows ? max_rows : rows;
+    return cuda_status(hq::launch_pages_write(*cache, w, pdl_of(flags), stream_of(stream)));
+}
+
+int hq_pages_status(const hq_pages *cache, void *stream) {
+    if (!cache_ok(cache)) return HQ_ERR_INVALID_ARG;
+    if (cudaStreamSynchronize(stream_of(stream)) != cudaSuccess) return HQ_ERR_CUDA;
+    int v = 0;
+    if (cudaMemcpy(&v, cache->status, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return HQ_ERR_CUDA;
+    if (v == 0) return HQ_OK;
+    const int zero = 0;
+    if (cudaMemcpy(cache->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return HQ_ERR_CUDA;
+    return v;
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@ HQ_ERR_INVALID_ARG = 1
 HQ_ERR_UNSUPPORTED = 2
 HQ_ERR_CUDA = 3
 HQ_ERR_TIMEOUT = 4
+HQ_ERR_NO_PAGES = 5
 HQ_W4_ASYM = 0
 HQ_W8_SYM = 1
 HQ_LAUNCH_DEFAULT = 0
@@ -39,7 +40,8 @@ EXPORTS = ("hq_tree_accept_workspace_bytes", "hq_tree_accept", "hq_status_string
            "hq_selftest_wait_timeout", "hq_selftest_gemm_wait_timeout", "hq_verify_gemm_noalloc", "hq_noalloc_status",
            "hq_tree_attention_workspace_bytes",
            "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant",
-           "hq_lora_workspace_bytes", "hq_lora_apply")
+           "hq_lora_workspace_bytes", "hq_lora_apply", "hq_pages_scratch_bytes", "hq_pages_fork", "hq_pages_extend",
+           "hq_pages_free", "hq_pages_compact", "hq_pages_copy", "hq_pages_write", "hq_pages_status")
 
 HQ_F32, HQ_F16, HQ_BF16 = 0, 1, 2
 TYPES = {torch.float32: HQ_F32, torch.float16: HQ_F16, torch.bfloat16: HQ_BF16}
@@ -56,6 +58,14 @@ class HQError(RuntimeError):
 
 class hq_layer_desc(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("group", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class hq_pages(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("ref", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("scratch", ctypes.c_void_p), ("plane_bytes", ctypes.c_int64),
+                ("n_planes", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32)]
 
 
 _lib = None
@@ -77,7 +87,7 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(_build.LIB)
     P, I32, U32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
     I64, F32 = ctypes.c_int64, ctypes.c_float
-    D = ctypes.POINTER(hq_layer_desc)
+    D, C = ctypes.POINTER(hq_layer_desc), ctypes.POINTER(hq_pages)
     sig = {
         "hq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hq_version": (I32, []),
@@ -106,6 +116,14 @@ def load() -> ctypes.CDLL:
         "hq_delta_commit": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, U32, P]),
         "hq_add_norm_quant": (ctypes.c_int, [D, P, I32, I64, P, P, I32, I64, P, F32, I32, P, P, I32, I64, P, P, P, P,
                                              U32, P]),
+        "hq_pages_scratch_bytes": (SZ, [C]),
+        "hq_pages_fork": (ctypes.c_int, [C, P, P, I32, U32, P]),
+        "hq_pages_extend": (ctypes.c_int, [C, P, P, I32, U32, P]),
+        "hq_pages_free": (ctypes.c_int, [C, P, I32, U32, P]),
+        "hq_pages_compact": (ctypes.c_int, [C, P, P, P, I32, I32, P, I32, U32, P]),
+        "hq_pages_copy": (ctypes.c_int, [C, P, P, I32, U32, P]),
+        "hq_pages_write": (ctypes.c_int, [C, I32, I32, P, P, I32, I64, I64, I32, P, P, I32, I32, I32, U32, P]),
+        "hq_pages_status": (ctypes.c_int, [C, P]),
         "hq_lora_workspace_bytes": (SZ, [I32, I32]),
         "hq_lora_apply": (ctypes.c_int, [P, I32, I64, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, I64, P, I64, P,
                                          U32, P]),
@@ -562,3 +580,123 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     hq_lora_apply(x, _type(x), _rows(x, K, "x"), M, K, N, A, B, _type(A), n, r, ids, ranks, scale, base,
                   _rows(base, N, "base"), Y, _rows(Y, N, "Y"), workspace, flags, stream)
     return Y
+
+
+class PagedCache:
+    """A paged key/value cache (hq_pages) over the caller's tensors: pool
+    [planes][pages][heads][page_size][dim] (fp16 or bf16), ref int32 [pages],
+    table int32 [sequences][max_pages], lens int32 [sequences].  `empty` makes
+    one without sequences."""
+
+    def __init__(self, pool: torch.Tensor, ref: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
+        planes, pages, heads, page_size, dim = pool.shape
+        _need(pool.dtype in (torch.float16, torch.bfloat16), f"PagedCache: fp16 or bf16 expected, got {pool.dtype}")
+        _need(pool[0].is_contiguous(), "PagedCache: the pages of a plane must be contiguous")
+        _dense(ref, torch.int32, (pages,), "PagedCache: ref")
+        _dense(table, torch.int32, tuple(table.shape), "PagedCache: table")
+        _need(table.dim() == 2, "PagedCache: table must be [sequences][max_pages]")
+        _dense(lens, torch.int32, (table.shape[0],), "PagedCache: lens")
+        self.pool, self.ref, self.table, self.lens = pool, ref, table, lens
+        self.status = torch.zeros(4, dtype=torch.int32, device=pool.device)
+        plane_bytes = (pool.stride(0) if planes > 1 else pool[0].numel()) * 2
+        self.c = hq_pages(0, 0, 0, 0, 0, 0, plane_bytes, planes, pages, table.shape[0], table.shape[1], page_size, heads,
+                          dim * 2)
+        need = int(load().hq_pages_scratch_bytes(ctypes.byref(self.c)))
+        if need == 0:
+            raise HQError(HQ_ERR_INVALID_ARG, "hq_pages_scratch_bytes")
+        self.scratch = torch.empty(need, dtype=torch.uint8, device=pool.device)
+        for f, t in (("pool", pool), ("ref", ref), ("table", table), ("len", lens), ("status", self.status),
+                     ("scratch", self.scratch)):
+            setattr(self.c, f, _ptr(t))
+
+    @classmethod
+    def empty(cls, planes: int, pages: int, heads: int, page_size: int, dim: int, sequences: int, max_pages: int,
+              dtype=torch.float16, device="cuda") -> "PagedCache":
+        return cls(torch.zeros((planes, pages, heads, page_size, dim), dtype=dtype, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device),
+                   torch.full((sequences, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(sequences, dtype=torch.int32, device=device))
+
+
+def _list(t, n, what: str) -> int:
+    """The length of an int32 list; n: the length it must have, if any."""
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n),
+          f"{what}: contiguous int32 [{'n' if n is None else n}] expected, got {t.dtype} {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def pages_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """Sequences dst (empty slots) take the pages of src; no data moves (hq_pages_fork)."""
+    n = _list(src, None, "pages_fork: src")
+    _list(dst, n, "pages_fork: dst")
+    _check(load().hq_pages_fork(cache.c, _ptr(src), _ptr(dst), n, flags, _stream(stream)), "hq_pages_fork")
+
+
+def pages_extend(cache: PagedCache, seqs: torch.Tensor, add: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """Sequences grow by add positions; a shared last page is copied first (hq_pages_extend)."""
+    n = _list(seqs, None, "pages_extend: seqs")
+    _list(add, n, "pages_extend: add")
+    _check(load().hq_pages_extend(cache.c, _ptr(seqs), _ptr(add), n, flags, _stream(stream)), "hq_pages_extend")
+
+
+def pages_free(cache: PagedCache, seqs: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """Sequences give up their pages and become empty slots (hq_pages_free)."""
+    n = _list(seqs, None, "pages_free: seqs")
+    _check(load().hq_pages_free(cache.c, _ptr(seqs), n, flags, _stream(stream)), "hq_pages_free")
+
+
+def pages_compact(cache: PagedCache, seqs: torch.Tensor, base: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor,
+                  flags: int = 0, stream=None) -> None:
+    """Keeps the positions base + keep[i][:n_keep[i]] after base[i], moved down,
+    and gives up the rest (hq_pages_compact).  keep int32 [n][any], rows any
+    distance apart."""
+    n = _list(seqs, None, "pages_compact: seqs")
+    _list(base, n, "pages_compact: base")
+    _list(n_keep, n, "pages_compact: n_keep")
+    _need(keep.dtype == torch.int32 and keep.dim() == 2 and keep.shape[0] == n and keep.shape[1] >= 1 and
+          (keep.shape[1] == 1 or keep.stride(1) == 1), f"pages_compact: keep must be int32 [{n}][1 or more]")
+    ld = keep.stride(0) if n > 1 else keep.shape[1]
+    _check(load().hq_pages_compact(cache.c, _ptr(seqs), _ptr(base), _ptr(keep), ld, keep.shape[1], _ptr(n_keep), n,
+                                   flags, _stream(stream)), "hq_pages_compact")
+
+
+def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: int = 0, stream=None) -> None:
+    """Pages dst of every plane become copies of pages src (hq_pages_copy)."""
+    n = _list(src, None, "pages_copy: src")
+    _list(dst, n, "pages_copy: dst")
+    _check(load().hq_pages_copy(cache.c, _ptr(src), _ptr(dst), n, flags, _stream(stream)), "hq_pages_copy")
+
+
+def _batch(cache: PagedCache, rows: int, starts, max_rows: int, seqs, what: str) -> int:
+    """The number of sequences of a batch of rows."""
+    if starts is not None:
+        B = _list(starts, None, f"{what}: starts") - 1
+        _need(B >= 0, f"{what}: starts is empty")
+    elif seqs is not None:
+        B = seqs.shape[0]
+    else:
+        B = rows // max_rows
+    if seqs is not None:
+        _list(seqs, B, f"{what}: seqs")
+    else:
+        _need(0 <= B <= cache.c.n_seqs, f"{what}: {B} sequences, the cache has {cache.c.n_seqs}")
+    return B
+
+
+def pages_write(cache: PagedCache, k_plane: int, v_plane: int, k: torch.Tensor, v: torch.Tensor, starts, max_rows: int,
+                seqs=None, flags: int = 0, stream=None) -> None:
+    """Writes the newest rows of sequences (rows starts[b] .. starts[b + 1] of k
+    and v [rows][heads][dim], fp32 or the cache's type) at the end of their
+    positions (hq_pages_write); starts None: max_rows rows each."""
+    rows, c = k.shape[0], cache.c
+    _need(v.shape[0] == rows and v.dtype == k.dtype, "pages_write: k and v need the same rows and type")
+    B = _batch(cache, rows, starts, max_rows, seqs, "pages_write")
+    cols = c.heads * (c.row_bytes // 2)
+    _check(load().hq_pages_write(c, k_plane, v_plane, _ptr(k), _ptr(v), _type(k), _rows(k, cols, "k"),
+                                 _rows(v, cols, "v"), _type(cache.pool), _ptr(seqs), _ptr(starts), B, rows, max_rows,
+                                 flags, _stream(stream)), "hq_pages_write")
+
+
+def pages_status(cache: PagedCache, stream=None) -> int:
+    """Synchronizes; the first error of a page operation since the last call (HQ_OK if none), cleared."""
+    return int(load().hq_pages_status(cache.c, _stream(stream)))

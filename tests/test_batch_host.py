@@ -97,3 +97,86 @@ def test_lora_binding_checks_shapes_before_the_library():
         hq.lora_apply(x, A, B, ids, workspace=torch.zeros(8, dtype=torch.uint8))
     with pytest.raises(TypeError, match="CPU tensor"):
         hq.lora_apply(x, A, B, ids)
+
+
+def pages(**kw):
+    a = dict(pool=FAKE, ref=FAKE, table=FAKE, len=FAKE, status=FAKE, scratch=FAKE, plane_bytes=100 * 2 * 16 * 256,
+             n_planes=2, n_pages=100, n_seqs=8, max_pages=10, page_size=16, heads=2, row_bytes=256)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return hq.hq_pages(**a)
+
+
+BAD_CACHES = [dict(pool=0), dict(ref=0), dict(table=0), dict(len=0), dict(status=0), dict(scratch=0), dict(pool=FAKE + 8),
+              dict(scratch=FAKE + 4), dict(ref=FAKE + 2), dict(table=FAKE + 1), dict(len=FAKE + 2), dict(status=FAKE + 3),
+              dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(page_size=0), dict(row_bytes=0),
+              dict(row_bytes=24), dict(row_bytes=8192), dict(n_planes=0), dict(heads=0), dict(n_pages=0),
+              dict(n_pages=101), dict(n_pages=(1 << 24) + 1), dict(n_seqs=0), dict(n_seqs=8193), dict(max_pages=0),
+              dict(max_pages=(1 << 20) + 1), dict(plane_bytes=100 * 2 * 16 * 256 - 16), dict(plane_bytes=100 * 2 * 16 * 256 + 8),
+              dict(plane_bytes=-16), dict(n_pages=1 << 24, page_size=256, plane_bytes=1 << 60)]
+
+
+def test_page_operations_refuse_bad_arguments():
+    lib = hq.load()
+    ok = pages()
+    calls = {
+        "fork": lambda c, n=2, a=FAKE, b=FAKE, f=0: lib.hq_pages_fork(c, a, b, n, f, None),
+        "extend": lambda c, n=2, a=FAKE, b=FAKE, f=0: lib.hq_pages_extend(c, a, b, n, f, None),
+        "free": lambda c, n=2, a=FAKE, b=FAKE, f=0: lib.hq_pages_free(c, a if b else None, n, f, None),
+        "compact": lambda c, n=2, a=FAKE, b=FAKE, f=0: lib.hq_pages_compact(c, a, b, FAKE, 4, 4, FAKE, n, f, None),
+        "copy": lambda c, n=2, a=FAKE, b=FAKE, f=0: lib.hq_pages_copy(c, a, b, n, f, None),
+    }
+    for name, call in calls.items():
+        assert call(ok, n=0) == hq.HQ_OK, name
+        for kw in BAD_CACHES:
+            assert call(pages(**kw), n=0) == E, (name, kw)
+        assert call(None) == E and call(ok, n=-1) == E and call(ok, a=None) == E and call(ok, b=None) == E, name
+        assert call(ok, f=2) == E and call(ok, a=FAKE + 2) == E, name
+        assert call(ok, n=65536) == E and (name == "copy" or call(ok, n=9) == E), name
+    assert lib.hq_pages_compact(ok, FAKE, FAKE, FAKE, 3, 4, FAKE, 2, 0, None) == E
+    assert lib.hq_pages_compact(ok, FAKE, FAKE, FAKE, 4, -1, FAKE, 2, 0, None) == E
+    assert lib.hq_pages_compact(ok, FAKE, FAKE, None, 4, 4, FAKE, 2, 0, None) == E
+    assert lib.hq_pages_compact(ok, FAKE, FAKE, FAKE, 4, 4, None, 2, 0, None) == E
+    assert lib.hq_pages_status(None, None) == E
+    for kw in BAD_CACHES:
+        assert lib.hq_pages_status(pages(**kw), None) == E, kw
+        if not set(kw) & {"pool", "ref", "table", "len", "status", "scratch"}:
+            assert lib.hq_pages_scratch_bytes(pages(**kw)) == 0, kw
+    assert lib.hq_pages_scratch_bytes(pages(pool=0, ref=0, table=0, len=0, status=0, scratch=0)) \
+        == lib.hq_pages_scratch_bytes(ok) > 0
+    assert hq.status_string(hq.HQ_ERR_NO_PAGES) == "HQ_ERR_NO_PAGES"
+
+
+def test_page_writes_refuse_bad_arguments():
+    lib = hq.load()
+
+    def call(c=None, **kw):
+        a = dict(kp=0, vp=1, k=FAKE, v=FAKE, it=hq.HQ_F32, ldk=256, ldv=256, t=hq.HQ_F16, seqs=FAKE, starts=FAKE, B=2,
+                 rows=6, max_rows=3, flags=0)
+        assert set(kw) <= set(a)
+        a.update(kw)
+        return lib.hq_pages_write(c or pages(), a["kp"], a["vp"], a["k"], a["v"], a["it"], a["ldk"], a["ldv"], a["t"],
+                                  a["seqs"], a["starts"], a["B"], a["rows"], a["max_rows"], a["flags"], None)
+    assert call(B=0) == hq.HQ_OK and call(rows=0) == hq.HQ_OK
+    bad = [dict(kp=-1), dict(kp=2), dict(vp=2), dict(k=None), dict(v=None), dict(k=FAKE + 4), dict(v=FAKE + 8), dict(it=3),
+           dict(it=hq.HQ_BF16), dict(t=hq.HQ_F32), dict(ldk=255), dict(ldv=252), dict(ldk=257), dict(B=-1), dict(B=65536),
+           dict(rows=-1), dict(max_rows=0), dict(starts=None, rows=5), dict(starts=FAKE + 2), dict(seqs=FAKE + 1),
+           dict(flags=2)]
+    for b in bad:
+        assert call(**b) == E, b
+    assert call(pages(n_pages=0)) == E
+
+
+def test_paged_cache_binding_checks():
+    z = torch.zeros
+    i = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match="fp16 or bf16"):
+        hq.PagedCache(z((2, 4, 1, 16, 64)), z(4, **i), z((2, 2), **i), z(2, **i))
+    with pytest.raises(ValueError, match="ref"):
+        hq.PagedCache(z((2, 4, 1, 16, 64), dtype=torch.float16), z(5, **i), z((2, 2), **i), z(2, **i))
+    with pytest.raises(ValueError, match="lens"):
+        hq.PagedCache(z((2, 4, 1, 16, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(3, **i))
+    with pytest.raises(hq.HQError):
+        hq.PagedCache(z((2, 4, 1, 24, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(2, **i))
+    with pytest.raises(TypeError, match="CPU tensor"):
+        hq.PagedCache(z((2, 4, 1, 16, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(2, **i))
