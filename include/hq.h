@@ -268,10 +268,11 @@ int hq_unpack_codes(const hq_layer_desc *desc, const void *blob, uint8_t *codes,
                     void *stream);
 
 /* Synchronizes `stream`, then reads and clears the error word of a
- * workspace (of hq_verify_gemm or hq_tree_attention).  Returns
- * HQ_ERR_TIMEOUT if a bounded wait inside a call that used the workspace
- * gave up since the word was last cleared (the outputs of that call are then
- * incomplete), HQ_OK otherwise. */
+ * workspace (of hq_verify_gemm, hq_tree_attention or hq_prefix_attention).
+ * Returns HQ_ERR_TIMEOUT if a bounded wait inside a call that used the
+ * workspace gave up since the word was last cleared (the outputs of that call
+ * are then incomplete), HQ_ERR_INVALID_ARG if an hq_prefix_attention call met
+ * a bad page table entry or length (see there), HQ_OK otherwise. */
 int hq_workspace_status(void *workspace, void *stream);
 
 /* hq_verify_gemm without a caller-supplied workspace, for callers that
@@ -600,6 +601,47 @@ int hq_pages_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, cons
 /* Synchronizes `stream`, then reads and clears the cache's status word:
  * HQ_OK, HQ_ERR_INVALID_ARG or HQ_ERR_NO_PAGES. */
 int hq_pages_status(const hq_pages *cache, void *stream);
+
+/* Attention of a batch over a paged cache whose sequences share their first
+ * `shared` positions: the shared keys and values are read once for all rows,
+ * each sequence's own positions by its own rows.  Row i of sequence b (its
+ * m_b newest positions, as in hq_pages_write; draft-tree node i) attends to
+ * the positions [0, len_b - m_b), to its ancestors in the tree and to itself;
+ * parent as in hq_tree_attention (numbered within the sequence), or NULL: a
+ * chain (node i - 1 is the parent of node i: the newest tokens of a prompt or
+ * a single token).  Query head h reads key/value head h / (Hq / heads).
+ *   cache     row_bytes = 2 D, D = 64 or 128; type HQ_F16 or HQ_BF16;
+ *             plane_bytes below 2^40
+ *   q         type [rows][Hq][D], rows ldq elements apart, 16-byte aligned rows
+ *   seqs, starts, B, rows, max_rows  as in hq_pages_write; max_rows <= HQ_MAX_M
+ *   parent    int32 [rows] (device) or NULL
+ *   shared    positions that all active sequences hold alike (0: none), at
+ *             most len_b - m_b of each; they are read through the table of the
+ *             first active sequence
+ *   max_len   at least every sequence's length (it sizes the launch), above
+ *             `shared`, at most max_pages * page_size and 2^30
+ *   scale     softmax scale, finite
+ *   out       out_type [rows][Hq][D], rows ldo elements apart, 16-byte aligned
+ *             rows; out_type is `type` or HQ_F32
+ *   workspace hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq,
+ *             heads, D) bytes, 16-byte aligned, its first 16 bytes zeroed once
+ * A row of an empty sequence (len 0), and a row that no sequence claims, is
+ * zero.  A length that contradicts shared, m_b or max_len makes the
+ * sequence's rows zero, a table entry outside [0, n_pages) makes its
+ * positions read as zeros; both set the error word (hq_workspace_status:
+ * HQ_ERR_INVALID_ARG).  Rows past a sequence's length, other branches of the
+ * tree and other sequences' pages do not influence a row, whatever they hold
+ * (infinities and NaN included).  Scores, softmax statistics and outputs are
+ * accumulated in fp32; the probabilities are rounded to `type` for the
+ * product with V (at most eps / 2 of `type` relative each).  Sums are taken
+ * in a fixed order: results repeat bit for bit. */
+size_t hq_prefix_attention_workspace_bytes(int32_t B, int32_t rows, int32_t max_rows, int32_t Hq, int32_t Hkv,
+                                           int32_t D);
+int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32_t type, const void *q,
+                        int64_t ldq, const int32_t *seqs, const int32_t *starts, int32_t B, int32_t rows,
+                        int32_t max_rows, const int32_t *parent, int32_t Hq, int32_t shared, int32_t max_len,
+                        float scale, void *out, int32_t out_type, int64_t ldo, void *workspace, uint32_t flags,
+                        void *stream);
 
 /* Self-test of the bounded-wait path: launches one block that waits on a
  * shared-memory barrier nothing will ever complete, giving up after

@@ -74,6 +74,21 @@ struct WriteArgs {
 };
 cudaError_t launch_pages_write(const hq_pages &c, const WriteArgs &w, bool pdl, cudaStream_t s);
 
+// Attention of a batch over a paged cache (k_prefix.cu).
+struct PrefixArgs {
+    const void *q;
+    void *out;
+    const int32_t *seqs, *starts, *parent, *table, *len;
+    int *err;
+    float *ws_o, *ws_ml;  // [part][row][Hq][D], [part][row][Hq][2]: running maximum (base-2 units), sum
+    int64_t ldq, ldo;
+    int B, rows, max_rows, Hq, Hkv, G, n_seqs, max_pages, page_shift, n_pages, k_plane, v_plane;
+    int shared, max_len, type, out_type;
+    float c_log2;  // scale * log2(e)
+};
+size_t prefix_workspace_bytes(int rows, int Hq, int D);
+cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s);
+
 #ifdef __CUDACC__
 // Rows of sequence b of a batch: the first row and their number, always
 // within [0, rows) and at most max_rows, whatever `starts` holds.

@@ -325,7 +325,7 @@ int hq_workspace_status(void *workspace, void *stream) {
     if (v == 0) return HQ_OK;
     const int zero = 0;
     if (cudaMemcpy(workspace, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return HQ_ERR_CUDA;
-    return HQ_ERR_TIMEOUT;
+    return v == hq::DEV_ERR_TIMEOUT ? HQ_ERR_TIMEOUT : HQ_ERR_INVALID_ARG;
 }
 
 int hq_selftest_gemm_wait_timeout(const hq_layer_desc *desc, const void *blob, const void *qop, const float *sx,

@@ -222,4 +222,66 @@ int hq_pages_status(const hq_pages *cache, void *stream) {
     return v;
 }
 
+size_t hq_prefix_attention_workspace_bytes(int32_t B, int32_t rows, int32_t max_rows, int32_t Hq, int32_t Hkv,
+                                           int32_t D) {
+    if (B <= 0 || B > 65535 || rows <= 0 || max_rows <= 0 || max_rows > HQ_MAX_M || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0)
+        return 0;
+    if ((D != 64 && D != 128) || (long long)rows * Hq > (1 << 28)) return 0;
+    return hq::prefix_workspace_bytes(rows, Hq, D);
+}
+
+int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32_t type, const void *q,
+                        int64_t ldq, const int32_t *seqs, const int32_t *starts, int32_t B, int32_t rows,
+                        int32_t max_rows, const int32_t *parent, int32_t Hq, int32_t shared, int32_t max_len,
+                        float scale, void *out, int32_t out_type, int64_t ldo, void *workspace, uint32_t flags,
+                        void *stream) {
+    if (!cache_ok(cache) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
+    if (k_plane < 0 || k_plane >= cache->n_planes || v_plane < 0 || v_plane >= cache->n_planes) return HQ_ERR_INVALID_ARG;
+    if (!type16(type) || (out_type != HQ_F32 && out_type != type)) return HQ_ERR_INVALID_ARG;
+    if (B < 0 || B > 65535 || rows < 0 || max_rows < 1 || max_rows > HQ_MAX_M) return HQ_ERR_INVALID_ARG;
+    if (!starts && (long long)B * max_rows > rows) return HQ_ERR_INVALID_ARG;
+    if (Hq <= 0 || Hq % cache->heads != 0 || (long long)rows * Hq > (1 << 28)) return HQ_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return HQ_ERR_INVALID_ARG;
+    if (shared < 0 || max_len < 1 || max_len > 1 << 30 || shared >= max_len ||
+        max_len > (long long)cache->max_pages * cache->page_size)
+        return HQ_ERR_INVALID_ARG;
+    if (B == 0 || rows == 0) return HQ_OK;
+    const int D = cache->row_bytes / 2;
+    if (!q || !out || !workspace || !rows_ok(q, type, ldq, (int64_t)Hq * D) ||
+        !rows_ok(out, out_type, ldo, (int64_t)Hq * D))
+        return HQ_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16) || !aligned(seqs, 4) || !aligned(starts, 4) || !aligned(parent, 4))
+        return HQ_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return HQ_ERR_UNSUPPORTED;
+    if (cache->plane_bytes >= (1ll << 40)) return HQ_ERR_UNSUPPORTED;  // the tensor map's largest stride
+    hq::PrefixArgs a = {};
+    a.q = q;
+    a.out = out;
+    a.seqs = seqs;
+    a.starts = starts;
+    a.parent = parent;
+    a.table = cache->table;
+    a.len = cache->len;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.B = B;
+    a.rows = rows;
+    a.max_rows = max_rows;
+    a.Hq = Hq;
+    a.Hkv = cache->heads;
+    a.G = Hq / cache->heads;
+    a.n_seqs = cache->n_seqs;
+    a.max_pages = cache->max_pages;
+    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
+    a.n_pages = cache->n_pages;
+    a.k_plane = k_plane;
+    a.v_plane = v_plane;
+    a.shared = shared;
+    a.max_len = max_len;
+    a.type = type;
+    a.out_type = out_type;
+    a.c_log2 = scale * 1.4426950408889634f;
+    return cuda_status(hq::launch_prefix_attention(*cache, a, D, workspace, pdl_of(flags), stream_of(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,617 @@
+// k_prefix.cu -- attention of a batch over a paged cache whose sequences share
+// a long prefix, the shared keys and values read once for all rows.
+//
+//   out[i][h] = sum_p w_p V[p] / sum_p w_p,   w_p = exp(scale q[i][h] . K[p])
+//
+// over the positions row i sees.  A softmax over a union of positions is the
+// merge of the softmaxes over its parts, each known by its running maximum m,
+// its sum l = sum exp(x - m) and its unnormalized output: so the positions are
+// cut into parts that different thread blocks take, and a second kernel merges
+// them.  The parts of a row:
+//   - the shared positions, in whole tiles of 64: all rows of the batch that
+//     read one key/value head (rows * G of them) are one matrix, cut into
+//     tiles of 64 rows; long prefixes are split further;
+//   - the sequence's own positions (with what the shared ones leave over of a
+//     tile), for the sequence's own rows only.
+// Shared tiles have no mask at all; the own positions end with the tree.
+//
+// Per block: one producer warp brings each 64-position tile of K and V with
+// TMA tiled copies (a page, or 64 positions of it, per box, in 128-byte
+// swizzle) into a ring of stages; the lanes look the pages up in parallel.
+// Four consumer warps own 16 rows each: S = Q K^T and O += P V on the tensor
+// cores with fp32 accumulation, an online softmax in base-2 units.
+#include <cuda.h>
+
+#include "batch.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int XROWS = 64;     // query rows per thread block
+constexpr int XKEYS = 64;     // positions per stage
+constexpr int XSTAGES = 3;
+constexpr int XCW = 4;        // consumer warps, 16 rows each
+constexpr int XTHREADS = (XCW + 1) * 32;
+constexpr int DEV_ERR_ARG = 2;  // error word: a bad table entry or length
+
+template <int D>
+struct Tile {
+    static constexpr int BOX = XKEYS * 128;           // 64 positions x 64 dimensions
+    static constexpr int BYTES = (D / 64) * BOX;      // K or V of a stage
+    static constexpr int STAGE = 2 * BYTES;
+    static constexpr size_t SMEM = 1024 + (size_t)XSTAGES * STAGE + 2 * XSTAGES * 8 + XROWS * 16 + HQ_MAX_M * 4;
+};
+
+struct PrefixPlan {
+    int s0;             // shared positions taken by the shared parts (a multiple of the tile)
+    int np, pchunk;     // shared parts of a row, positions each
+    int ns, schunk;     // own parts of a row, positions each
+    int ptiles, stiles; // row tiles: all rows, one sequence's rows
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma_x(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (BF)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Whether a pair holds an infinity or NaN (all exponent bits set).
+template <bool BF>
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+    constexpr uint32_t e = BF ? 0x7f80u : 0x7c00u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// Tiled copy (dimension, row in page, head, page, plane) into shared memory.
+// x is 0 or 64 elements of 2 bytes: a multiple of 16 bytes.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int x, int y, int head, int page,
+                                         int plane, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(head), "r"(page), "r"(plane), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t swz128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// A sequence of the batch: its slot, rows, length; `live` false where it is
+// empty or its length contradicts the call.
+struct Seq {
+    int slot, first, m, len;
+    bool live;
+};
+__device__ __forceinline__ Seq seq_of(const PrefixArgs &a, int b) {
+    Seq s;
+    batch_rows(a.starts, b, a.rows, a.max_rows, s.first, s.m);
+    s.slot = a.seqs ? a.seqs[b] : b;
+    s.len = s.slot >= 0 && s.slot < a.n_seqs ? a.len[s.slot] : -1;
+    s.live = s.m > 0 && s.len <= a.max_len && s.len - s.m >= a.shared;
+    if (!s.live && s.m > 0 && s.len != 0) atomicExch(a.err, DEV_ERR_ARG);
+    return s;
+}
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(XTHREADS, 2)
+    k_prefix_attn(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
+    using T = Tile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + (size_t)XSTAGES * T::STAGE);  // full[S], empty[S]
+    uint32_t *s_anc = reinterpret_cast<uint32_t *>(bars + 2 * XSTAGES);                // [XROWS][4]
+    int32_t *s_par = reinterpret_cast<int32_t *>(s_anc + XROWS * 4);                   // [HQ_MAX_M]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < XSTAGES; ++i) {
+            mbar_init(smem_addr(&bars[i]), 1);
+            mbar_init(smem_addr(&bars[XSTAGES + i]), XCW);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // which part this block is
+    int unit = blockIdx.x;
+    const int hk = unit % a.Hkv;
+    unit /= a.Hkv;
+    const int nshared = pl.np * pl.ptiles;
+    int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0;
+    if (unit < nshared) {
+        split = unit / pl.ptiles;
+        rt = unit % pl.ptiles;
+        first = 0;
+        nrows = a.rows * a.G;
+        k0 = split * pl.pchunk;
+        k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
+        // the shared positions are read through the first live sequence
+        int b = 0;
+        Seq s = seq_of(a, 0);
+        while (!s.live && ++b < a.B) s = seq_of(a, b);
+        if (!s.live) return;  // no row of the batch uses this part
+        slot = s.slot;
+    } else {
+        unit -= nshared;
+        const int b = unit / (pl.ns * pl.stiles);
+        unit %= pl.ns * pl.stiles;
+        split = unit / pl.stiles;
+        rt = unit % pl.stiles;
+        const Seq s = seq_of(a, b);
+        if (!s.live || rt * XROWS >= s.m * a.G) return;
+        first = s.first;
+        nodes = s.m;
+        nrows = s.m * a.G;
+        k0 = pl.s0 + split * pl.schunk;
+        k1 = s.len - k0 > pl.schunk ? k0 + pl.schunk : s.len;
+        slot = s.slot;
+        tree0 = s.len - s.m;
+        split += pl.np;
+        if (k0 >= k1) return;  // past the sequence's end: the merge does not look here
+    }
+    const int ntiles = (k1 - k0 + XKEYS - 1) / XKEYS;
+
+    if (warp == XCW) {
+        // ------------------------------------------------------ producer ---
+        // Lane j < boxes loads box j of the tile: `boxr` positions of one page.
+        const int boxr = 1 << (a.page_shift < 6 ? a.page_shift : 6), boxes = XKEYS / boxr;
+        const int32_t *row = a.table + (size_t)slot * a.max_pages;
+        int i = 0;
+        for (; i < ntiles; ++i) {
+            const int st = i % XSTAGES, p = k0 + i * XKEYS + lane * boxr;
+            int page = a.n_pages;  // outside the map: zeros
+            if (lane < boxes && p < k1) {
+                page = row[p >> a.page_shift];
+                if (page < 0 || page >= a.n_pages) {
+                    atomicExch(a.err, DEV_ERR_ARG);
+                    page = a.n_pages;
+                }
+            }
+            if (i >= XSTAGES &&
+                !mbar_wait_bounded(smem_addr(&bars[XSTAGES + st]), (uint32_t)((i / XSTAGES) & 1) ^ 1u, a.err))
+                break;
+            __syncwarp();
+            const uint32_t bar = smem_addr(&bars[st]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::STAGE);
+            __syncwarp();
+            if (lane < boxes) {
+                const uint32_t kt = smem_addr(ring + (size_t)st * T::STAGE) + (uint32_t)(lane * boxr * 128);
+                const int y = p & ((1 << a.page_shift) - 1);
+#pragma unroll
+                for (int bx = 0; bx < D / 64; ++bx) {
+                    tma_page(kt + bx * T::BOX, &map, bx * 64, y, hk, page, a.k_plane, bar);
+                    tma_page(kt + T::BYTES + bx * T::BOX, &map, bx * 64, y, hk, page, a.v_plane, bar);
+                }
+            }
+            __syncwarp();
+        }
+        // no copy may still be landing in shared memory when the block exits
+        for (int j = i > XSTAGES ? i - XSTAGES : 0; j < i; ++j)
+            mbar_wait_bounded(smem_addr(&bars[j % XSTAGES]), (uint32_t)((j / XSTAGES) & 1), a.err);
+        return;
+    }
+
+    // ---------------------------------------------------------- consumers ---
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const int rA = rt * XROWS + warp * 16 + g8, rB = rA + 8;  // this lane's two rows of the part
+    uint32_t qa[D / 16][4];
+    {
+        const bool vA = rA < nrows, vB = rB < nrows;
+        const int nA = vA ? rA : 0, nB = vB ? rB : 0;
+        const uint32_t *qA = reinterpret_cast<const uint32_t *>(
+            static_cast<const uint16_t *>(a.q) + (size_t)(first + nA / a.G) * a.ldq + (size_t)(hk * a.G + nA % a.G) * D);
+        const uint32_t *qB = reinterpret_cast<const uint32_t *>(
+            static_cast<const uint16_t *>(a.q) + (size_t)(first + nB / a.G) * a.ldq + (size_t)(hk * a.G + nB % a.G) * D);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const int c = ks * 8 + t4;  // 32-bit column: dims 2c, 2c + 1
+            qa[ks][0] = vA ? qA[c] : 0u;
+            qa[ks][1] = vB ? qB[c] : 0u;
+            qa[ks][2] = vA ? qA[c + 4] : 0u;
+            qa[ks][3] = vB ? qB[c + 4] : 0u;
+        }
+    }
+    // Ancestor sets of this block's nodes where the part reaches the tree
+    // (without `parent`: a chain, every earlier node).
+    const int node0 = rt * XROWS / a.G;
+    if (k1 > tree0) {
+        if (a.parent)
+            for (int i = threadIdx.x; i < nodes; i += XCW * 32) s_par[i] = a.parent[first + i];
+        named_barrier(1, XCW * 32);
+        if (threadIdx.x < XROWS) {
+            const int node = node0 + threadIdx.x;
+            uint32_t m4[4] = {0u, 0u, 0u, 0u};
+            if (node < nodes) {
+                m4[node >> 5] |= 1u << (node & 31);
+                int cur = node;
+                for (int step = 0; step < HQ_MAX_M && cur > 0; ++step) {
+                    const int p = a.parent ? s_par[cur] : cur - 1;
+                    if (p < 0 || p >= cur) break;
+                    m4[p >> 5] |= 1u << (p & 31);
+                    cur = p;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) s_anc[threadIdx.x * 4 + w] = m4[w];
+        }
+        named_barrier(1, XCW * 32);
+    }
+    const uint32_t *ancA = s_anc + (rA / a.G - node0) * 4, *ancB = s_anc + (rB / a.G - node0) * 4;
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+    float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.0f, 0.0f};
+    bool ok = true;
+    const int k_row = (lane >> 4) * 8 + (lane & 7), k_half = (lane >> 3) & 1;
+    const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_half = lane >> 4;
+
+    for (int i = 0; i < ntiles; ++i) {
+        const int st = i % XSTAGES;
+        if (ok) ok = mbar_wait_bounded(smem_addr(&bars[st]), (uint32_t)((i / XSTAGES) & 1), a.err);
+        __syncwarp();
+        const uint32_t kt = smem_addr(ring + (size_t)st * T::STAGE), vt = kt + T::BYTES;
+        const int p0 = k0 + i * XKEYS;
+
+        float s[XKEYS / 8][4];
+#pragma unroll
+        for (int j = 0; j < XKEYS / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int np = 0; np < XKEYS / 16; ++np) {
+                uint32_t b0, b1, b2, b3;
+                ldsm4(kt + (uint32_t)((ks >> 2) * T::BOX) + swz128(np * 16 + k_row, 2 * (ks & 3) + k_half), b0, b1, b2, b3);
+                mma_x<BF>(s[2 * np], qa[ks], b0, b1);
+                mma_x<BF>(s[2 * np + 1], qa[ks], b2, b3);
+            }
+
+        // mask, scale to base-2 units, running maximum
+        const bool full = p0 + XKEYS <= tree0 && p0 + XKEYS <= k1;
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < XKEYS / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = s[j][e] * a.c_log2;
+                if (!full) {
+                    const int pos = p0 + j * 8 + 2 * t4 + (e & 1);
+                    bool vis = pos < k1;
+                    if (vis && pos >= tree0) {
+                        const int tn = pos - tree0;
+                        const uint32_t *anc = (e >> 1) ? ancB : ancA;
+                        vis = (anc[tn >> 5] >> (tn & 31)) & 1u;
+                    }
+                    if (!vis) x = -INFINITY;
+                }
+                s[j][e] = x;
+                mx[e >> 1] = fmaxf(mx[e >> 1], x);
+            }
+        float alpha[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            const float mnew = fmaxf(mrun[h], mx[h]);
+            alpha[h] = mnew == -INFINITY ? 1.0f : exp2f(mrun[h] - mnew);
+            mx[h] = mnew == -INFINITY ? 0.0f : mnew;  // no visible position yet: probabilities 0
+            mrun[h] = mnew;
+        }
+        float rs[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < XKEYS / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = exp2f(s[j][e] - mx[e >> 1]);
+                s[j][e] = p;
+                rs[e >> 1] += p;
+            }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lrun[h] = lrun[h] * alpha[h] + rs[h];
+        if (!__all_sync(0xffffffffu, alpha[0] == 1.0f && alpha[1] == 1.0f)) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][0] *= alpha[0];
+                o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1];
+                o[j][3] *= alpha[1];
+            }
+        }
+
+        // A masked position weighs 0, and 0 times an infinity or NaN is NaN:
+        // where a tile is masked and its values are not all finite, each row
+        // adds the positions it sees one by one.
+        bool plain = true;
+        if (!full) {
+            bool odd = false;
+            for (int x = lane; x < T::BYTES / 16; x += 32) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(vt + (uint32_t)x * 16));
+                odd |= nonfinite2<BF>(w[0]) || nonfinite2<BF>(w[1]) || nonfinite2<BF>(w[2]) || nonfinite2<BF>(w[3]);
+            }
+            plain = !__any_sync(0xffffffffu, odd);
+        }
+        if (plain) {
+            // O += P V: P rounded to the cache's type
+#pragma unroll
+            for (int kk = 0; kk < XKEYS / 16; ++kk) {
+                uint32_t pa[4];
+                pa[0] = pack2<BF>(s[2 * kk][0], s[2 * kk][1]);
+                pa[1] = pack2<BF>(s[2 * kk][2], s[2 * kk][3]);
+                pa[2] = pack2<BF>(s[2 * kk + 1][0], s[2 * kk + 1][1]);
+                pa[3] = pack2<BF>(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+#pragma unroll
+                for (int dp = 0; dp < D / 16; ++dp) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm4t(vt + (uint32_t)((dp >> 2) * T::BOX) + swz128(kk * 16 + v_row, 2 * (dp & 3) + v_half), b0, b1,
+                           b2, b3);
+                    mma_x<BF>(o[2 * dp], pa, b0, b1);
+                    mma_x<BF>(o[2 * dp + 1], pa, b2, b3);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < XKEYS / 8; ++j)
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const int from = (lane & ~3) | (c >> 1);
+                    const float pA = __shfl_sync(0xffffffffu, (c & 1) ? s[j][1] : s[j][0], from);
+                    const float pB = __shfl_sync(0xffffffffu, (c & 1) ? s[j][3] : s[j][2], from);
+                    const int r = j * 8 + c;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];"
+                                     : "=r"(w)
+                                     : "r"(vt + (uint32_t)((n >> 3) * T::BOX) + swz128(r, n & 7) + (uint32_t)t4 * 4));
+                        const float2 f = unpack2<BF>(w);
+                        if (pA != 0.0f) {
+                            o[n][0] = fmaf(pA, f.x, o[n][0]);
+                            o[n][1] = fmaf(pA, f.y, o[n][1]);
+                        }
+                        if (pB != 0.0f) {
+                            o[n][2] = fmaf(pB, f.x, o[n][2]);
+                            o[n][3] = fmaf(pB, f.y, o[n][3]);
+                        }
+                    }
+                }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars[XSTAGES + st]));
+    }
+
+    // this part's unnormalized outputs, maxima and sums
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 1);
+        lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 2);
+        const int r = h ? rB : rA;
+        if (r >= nrows) continue;
+        const size_t row = ((size_t)split * a.rows + first + r / a.G) * a.Hq + hk * a.G + r % a.G;
+        float *dst = a.ws_o + row * D;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2 *>(dst + j * 8 + 2 * t4) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+        if (t4 == 0) *reinterpret_cast<float2 *>(a.ws_ml + row * 2) = make_float2(mrun[h], lrun[h]);
+    }
+}
+
+// One warp per (row, query head): the parts' maxima and sums, then the
+// weighted sum of their outputs, in ascending order of position.
+template <int D>
+__global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const PrefixPlan pl) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= (long long)a.rows * a.Hq) return;
+    const int row = (int)(w / a.Hq), h = (int)(w % a.Hq);
+    // the sequence the row belongs to: the last one that starts at or before it
+    int b = 0;
+    if (a.starts) {
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.starts[mid] <= row) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    } else {
+        b = row / a.max_rows;
+    }
+    bool live = b < a.B;  // rows past the last sequence's belong to none
+    Seq s = {};
+    if (live) {
+        s = seq_of(a, b);
+        live = s.live && row >= s.first && row < s.first + s.m;
+    }
+    // own parts that reach into the sequence
+    const int parts = !live ? 0 : pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
+    const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h;
+    float top = -INFINITY;
+    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.ws_ml[(r0 + p * step) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    constexpr int E = D / 32;
+    float acc[E], den = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int p = 0; p < parts; ++p) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + (r0 + p * step) * 2);
+        if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // the row saw nothing in this part
+        const float wt = exp2f(ml.x - top);
+        den += wt * ml.y;
+        const float *src = a.ws_o + (r0 + p * step) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wt * src[e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = parts == 0 ? 0.0f : acc[e] / den;
+    const size_t at = (size_t)row * a.ldo + (size_t)h * D + lane * E;
+    if (a.out_type == HQ_F32) {
+        float *o = static_cast<float *>(a.out) + at;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = acc[e];
+    } else {
+        uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            o[e / 2] = a.out_type == HQ_F16 ? pack2<false>(acc[e], acc[e + 1]) : pack2<true>(acc[e], acc[e + 1]);
+    }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static std::atomic<EncodeFn> fn{nullptr};
+    EncodeFn f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess) {
+            f = reinterpret_cast<EncodeFn>(p);
+            fn.store(f, std::memory_order_release);
+        }
+    }
+    return f;
+}
+
+// Map of the pool (dimension, row in page, head, page, plane); boxes of 64
+// dimensions x min(page_size, box_rows) rows, 128-byte swizzle.
+cudaError_t pool_map(CUtensorMap *m, const hq_pages &c, int D, int type, int box_rows) {
+    EncodeFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t row = (cuuint64_t)c.row_bytes, page = row * c.page_size;
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.n_pages,
+                                (cuuint64_t)c.n_planes};
+    const cuuint64_t strides[4] = {row, page, page * c.heads, (cuuint64_t)c.plane_bytes};
+    const cuuint32_t box[5] = {64, (cuuint32_t)(c.page_size < box_rows ? c.page_size : box_rows), 1, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(m, type == HQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                           c.pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Parts a row may be cut into, for a workspace that does not depend on the
+// lengths: many for few rows (every SM needs a block), few for many.
+int max_parts(int rows, int Hq) {
+    const long long p = (1LL << 16) / ((long long)rows * Hq);
+    return p > 64 ? 64 : p < 8 ? 8 : (int)p;
+}
+
+template <int D, bool BF>
+cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, unsigned grid, bool pdl,
+                     cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> configured[CACHE_DEVICES];
+    int done = 0;
+    e = cached_per_device(configured, dev, &done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(k_prefix_attn<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<D>::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(k_prefix_attn<D, BF>, dim3(grid), dim3(XTHREADS), Tile<D>::SMEM, pdl, s, a, pl, map);
+    if (e != cudaSuccess) return e;
+    const long long warps = (long long)a.rows * a.Hq;
+    return launch_kernel(k_prefix_merge<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, true, s, a, pl);
+}
+
+}  // namespace
+
+size_t prefix_workspace_bytes(int rows, int Hq, int D) {
+    return 16 + (size_t)max_parts(rows, Hq) * rows * Hq * (size_t)(D + 2) * 4;
+}
+
+cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorNoDevice;
+    const int cap = max_parts(a.rows, a.Hq);
+    PrefixPlan pl;
+    pl.s0 = a.shared / XKEYS * XKEYS;
+    pl.ptiles = (int)(((long long)a.rows * a.G + XROWS - 1) / XROWS);
+    pl.stiles = (int)(((long long)a.max_rows * a.G + XROWS - 1) / XROWS);
+    // about two blocks per SM for each kind of part, whole tiles, and at most
+    // `cap` parts in all (half of them for each kind)
+    auto cut = [&](long long positions, long long blocks, int most, int &n, int &chunk) {
+        long long want = (2LL * sms + blocks - 1) / blocks;
+        if (want > most) want = most;
+        if (want < 1) want = 1;
+        long long len = (positions + want - 1) / want;
+        len = (len + XKEYS - 1) / XKEYS * XKEYS;
+        if (len < XKEYS) len = XKEYS;
+        chunk = (int)len;
+        n = (int)((positions + len - 1) / len);
+    };
+    cut(pl.s0, (long long)a.Hkv * pl.ptiles, cap / 2, pl.np, pl.pchunk);
+    cut((long long)a.max_len - pl.s0, (long long)a.Hkv * a.B * pl.stiles, cap / 2, pl.ns, pl.schunk);
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.err = reinterpret_cast<int *>(ws);
+    a.ws_o = reinterpret_cast<float *>(ws + 16);
+    a.ws_ml = a.ws_o + (size_t)cap * a.rows * a.Hq * D;
+    CUtensorMap map;
+    cudaError_t e = pool_map(&map, c, D, a.type, XKEYS);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)a.Hkv * ((long long)pl.np * pl.ptiles + (long long)a.B * pl.ns * pl.stiles);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const bool bf = a.type == HQ_BF16;
+    if (D == 128)
+        return bf ? launch_t<128, true>(a, pl, map, (unsigned)grid, pdl, s)
+                  : launch_t<128, false>(a, pl, map, (unsigned)grid, pdl, s);
+    return bf ? launch_t<64, true>(a, pl, map, (unsigned)grid, pdl, s)
+              : launch_t<64, false>(a, pl, map, (unsigned)grid, pdl, s);
+}
+
+}  // namespace hq

@@ -41,7 +41,8 @@ EXPORTS = ("hq_tree_accept_workspace_bytes", "hq_tree_accept", "hq_status_string
            "hq_tree_attention_workspace_bytes",
            "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant",
            "hq_lora_workspace_bytes", "hq_lora_apply", "hq_pages_scratch_bytes", "hq_pages_fork", "hq_pages_extend",
-           "hq_pages_free", "hq_pages_compact", "hq_pages_copy", "hq_pages_write", "hq_pages_status")
+           "hq_pages_free", "hq_pages_compact", "hq_pages_copy", "hq_pages_write", "hq_pages_status",
+           "hq_prefix_attention_workspace_bytes", "hq_prefix_attention")
 
 HQ_F32, HQ_F16, HQ_BF16 = 0, 1, 2
 TYPES = {torch.float32: HQ_F32, torch.float16: HQ_F16, torch.bfloat16: HQ_BF16}
@@ -124,6 +125,9 @@ def load() -> ctypes.CDLL:
         "hq_pages_copy": (ctypes.c_int, [C, P, P, I32, U32, P]),
         "hq_pages_write": (ctypes.c_int, [C, I32, I32, P, P, I32, I64, I64, I32, P, P, I32, I32, I32, U32, P]),
         "hq_pages_status": (ctypes.c_int, [C, P]),
+        "hq_prefix_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
+        "hq_prefix_attention": (ctypes.c_int, [C, I32, I32, I32, P, I64, P, P, I32, I32, I32, P, I32, I32, I32, F32, P, I32,
+                                               I64, P, U32, P]),
         "hq_lora_workspace_bytes": (SZ, [I32, I32]),
         "hq_lora_apply": (ctypes.c_int, [P, I32, I64, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, I64, P, I64, P,
                                          U32, P]),
@@ -700,3 +704,37 @@ def pages_write(cache: PagedCache, k_plane: int, v_plane: int, k: torch.Tensor, 
 def pages_status(cache: PagedCache, stream=None) -> int:
     """Synchronizes; the first error of a page operation since the last call (HQ_OK if none), cleared."""
     return int(load().hq_pages_status(cache.c, _stream(stream)))
+
+
+def hq_prefix_attention_workspace_bytes(B: int, rows: int, max_rows: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, Hkv, D))
+
+
+def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, starts, max_rows: int, shared: int,
+                     max_len: int, scale: float, parent=None, seqs=None, out=None, workspace=None, flags: int = 0,
+                     stream=None) -> torch.Tensor:
+    """Attention of a batch over the paged cache, its first `shared` positions
+    read once for all rows (hq_prefix_attention).  q [rows][Hq][D] of the
+    cache's type: sequence b's rows starts[b] .. starts[b + 1] (None: max_rows
+    rows each) are its newest positions, a draft tree with `parent` (int32
+    [rows]; None: a chain).  max_len: at least every sequence's length.  out
+    [rows][Hq][D] of the cache's type or fp32; workspace: zeroed once."""
+    rows, Hq, D = q.shape
+    c = cache.c
+    _need(D * 2 == c.row_bytes and q.dtype == cache.pool.dtype,
+          f"prefix_attention: q must be {cache.pool.dtype} [rows][heads][{c.row_bytes // 2}]")
+    B = _batch(cache, rows, starts, max_rows, seqs, "prefix_attention")
+    if parent is not None:
+        _list(parent, rows, "prefix_attention: parent")
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
+    _need(tuple(out.shape) == (rows, Hq, D), f"prefix_attention: out must be [{rows}][{Hq}][{D}]")
+    need = hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, c.heads, D)
+    if workspace is None:
+        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+    _need(workspace.numel() * workspace.element_size() >= need, "prefix_attention: the workspace is too small")
+    _check(load().hq_prefix_attention(c, k_plane, v_plane, _type(q), _ptr(q), _rows(q, Hq * D, "q"), _ptr(seqs),
+                                      _ptr(starts), B, rows, max_rows, _ptr(parent), Hq, shared, max_len, scale,
+                                      _ptr(out), _type(out), _rows(out, Hq * D, "out"), _ptr(workspace), flags,
+                                      _stream(stream)), "hq_prefix_attention")
+    return out

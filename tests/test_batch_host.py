@@ -180,3 +180,33 @@ def test_paged_cache_binding_checks():
         hq.PagedCache(z((2, 4, 1, 24, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(2, **i))
     with pytest.raises(TypeError, match="CPU tensor"):
         hq.PagedCache(z((2, 4, 1, 16, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(2, **i))
+
+
+def test_prefix_attention_refuses_bad_arguments():
+    lib = hq.load()
+
+    def call(c=None, **kw):
+        a = dict(kp=0, vp=1, t=hq.HQ_F16, q=FAKE, ldq=512, seqs=FAKE, starts=FAKE, B=2, rows=6, max_rows=4, parent=FAKE,
+                 Hq=4, shared=20, max_len=150, scale=0.1, out=FAKE, ot=hq.HQ_F16, ldo=512, ws=FAKE, flags=0)
+        assert set(kw) <= set(a)
+        a.update(kw)
+        return lib.hq_prefix_attention(c or pages(), a["kp"], a["vp"], a["t"], a["q"], a["ldq"], a["seqs"], a["starts"],
+                                       a["B"], a["rows"], a["max_rows"], a["parent"], a["Hq"], a["shared"], a["max_len"],
+                                       a["scale"], a["out"], a["ot"], a["ldo"], a["ws"], a["flags"], None)
+    assert call(B=0) == hq.HQ_OK and call(rows=0) == hq.HQ_OK
+    bad = [dict(kp=-1), dict(vp=2), dict(t=hq.HQ_F32), dict(ot=hq.HQ_BF16), dict(ot=5), dict(q=None), dict(out=None),
+           dict(ws=None), dict(q=FAKE + 8), dict(out=FAKE + 4), dict(ws=FAKE + 8), dict(ldq=511), dict(ldq=516),
+           dict(ldo=504), dict(seqs=FAKE + 2), dict(starts=FAKE + 1), dict(parent=FAKE + 2), dict(B=-1), dict(B=65536),
+           dict(rows=-1), dict(max_rows=0), dict(max_rows=129), dict(starts=None, rows=7), dict(Hq=3), dict(Hq=0),
+           dict(shared=-1), dict(shared=150), dict(max_len=0), dict(max_len=161), dict(scale=float("nan")),
+           dict(scale=float("inf")), dict(flags=2), dict(rows=1 << 27, ldq=512)]
+    for b in bad:
+        assert call(**b) == E, b
+    U = hq.HQ_ERR_UNSUPPORTED
+    assert call(pages(row_bytes=192)) == U
+    assert call(pages(n_pages=0)) == E
+    assert call(pages(plane_bytes=1 << 40)) == U
+    size = hq.hq_prefix_attention_workspace_bytes
+    assert size(2, 6, 4, 4, 2, 128) > 16
+    for z in ((0, 6, 4, 4, 2, 128), (2, 0, 4, 4, 2, 128), (2, 6, 129, 4, 2, 128), (2, 6, 4, 5, 2, 128), (2, 6, 4, 4, 2, 96)):
+        assert size(*z) == 0, z
