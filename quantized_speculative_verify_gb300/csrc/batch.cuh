@@ -84,6 +84,7 @@ struct PrefixArgs {
     int64_t ldq, ldo;
     int B, rows, max_rows, Hq, Hkv, G, n_seqs, max_pages, page_shift, n_pages, k_plane, v_plane;
     int shared, max_len, type, out_type;
+    int own_only;    // the shared parts are another kernel's
     float c_log2;  // scale * log2(e)
 };
 size_t prefix_workspace_bytes(int rows, int Hq, int D);

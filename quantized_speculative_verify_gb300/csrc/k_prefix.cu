@@ -20,9 +20,7 @@
 // swizzle) into a ring of stages; the lanes look the pages up in parallel.
 // Four consumer warps own 16 rows each: S = Q K^T and O += P V on the tensor
 // cores with fp32 accumulation, an online softmax in base-2 units.
-#include <cuda.h>
-
-#include "batch.cuh"
+#include "prefix_common.cuh"
 
 namespace hq {
 namespace {
@@ -32,7 +30,9 @@ constexpr int XKEYS = 64;     // positions per stage
 constexpr int XSTAGES = 3;
 constexpr int XCW = 4;        // consumer warps, 16 rows each
 constexpr int XTHREADS = (XCW + 1) * 32;
-constexpr int DEV_ERR_ARG = 2;  // error word: a bad table entry or length
+constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the tensor-memory kernel
+constexpr int TC_ROWS = 65;
+constexpr int TC_SHARED = 512;
 
 template <int D>
 struct Tile {
@@ -40,13 +40,6 @@ struct Tile {
     static constexpr int BYTES = (D / 64) * BOX;      // K or V of a stage
     static constexpr int STAGE = 2 * BYTES;
     static constexpr size_t SMEM = 1024 + (size_t)XSTAGES * STAGE + 2 * XSTAGES * 8 + XROWS * 16 + HQ_MAX_M * 4;
-};
-
-struct PrefixPlan {
-    int s0;             // shared positions taken by the shared parts (a multiple of the tile)
-    int np, pchunk;     // shared parts of a row, positions each
-    int ns, schunk;     // own parts of a row, positions each
-    int ptiles, stiles; // row tiles: all rows, one sequence's rows
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
@@ -100,35 +93,6 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
     return (w & e) == e || ((w >> 16) & e) == e;
 }
 
-// Tiled copy (dimension, row in page, head, page, plane) into shared memory.
-// x is 0 or 64 elements of 2 bytes: a multiple of 16 bytes.
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int x, int y, int head, int page,
-                                         int plane, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-        "%6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(head), "r"(page), "r"(plane), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t swz128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-// A sequence of the batch: its slot, rows, length; `live` false where it is
-// empty or its length contradicts the call.
-struct Seq {
-    int slot, first, m, len;
-    bool live;
-};
-__device__ __forceinline__ Seq seq_of(const PrefixArgs &a, int b) {
-    Seq s;
-    batch_rows(a.starts, b, a.rows, a.max_rows, s.first, s.m);
-    s.slot = a.seqs ? a.seqs[b] : b;
-    s.len = s.slot >= 0 && s.slot < a.n_seqs ? a.len[s.slot] : -1;
-    s.live = s.m > 0 && s.len <= a.max_len && s.len - s.m >= a.shared;
-    if (!s.live && s.m > 0 && s.len != 0) atomicExch(a.err, DEV_ERR_ARG);
-    return s;
-}
-
 template <int D, bool BF>
 __global__ void __launch_bounds__(XTHREADS, 2)
     k_prefix_attn(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
@@ -155,7 +119,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
     int unit = blockIdx.x;
     const int hk = unit % a.Hkv;
     unit /= a.Hkv;
-    const int nshared = pl.np * pl.ptiles;
+    const int nshared = a.own_only ? 0 : pl.np * pl.ptiles;
     int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0;
     if (unit < nshared) {
         split = unit / pl.ptiles;
@@ -164,10 +128,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         nrows = a.rows * a.G;
         k0 = split * pl.pchunk;
         k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
-        // the shared positions are read through the first live sequence
-        int b = 0;
-        Seq s = seq_of(a, 0);
-        while (!s.live && ++b < a.B) s = seq_of(a, b);
+        const Seq s = first_live(a);
         if (!s.live) return;  // no row of the batch uses this part
         slot = s.slot;
     } else {
@@ -192,36 +153,20 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 
     if (warp == XCW) {
         // ------------------------------------------------------ producer ---
-        // Lane j < boxes loads box j of the tile: `boxr` positions of one page.
-        const int boxr = 1 << (a.page_shift < 6 ? a.page_shift : 6), boxes = XKEYS / boxr;
         const int32_t *row = a.table + (size_t)slot * a.max_pages;
         int i = 0;
         for (; i < ntiles; ++i) {
-            const int st = i % XSTAGES, p = k0 + i * XKEYS + lane * boxr;
-            int page = a.n_pages;  // outside the map: zeros
-            if (lane < boxes && p < k1) {
-                page = row[p >> a.page_shift];
-                if (page < 0 || page >= a.n_pages) {
-                    atomicExch(a.err, DEV_ERR_ARG);
-                    page = a.n_pages;
-                }
-            }
+            const int st = i % XSTAGES, p = k0 + i * XKEYS;
+            const int page = lookup_page<XKEYS>(a, row, p, k1);
             if (i >= XSTAGES &&
                 !mbar_wait_bounded(smem_addr(&bars[XSTAGES + st]), (uint32_t)((i / XSTAGES) & 1) ^ 1u, a.err))
                 break;
             __syncwarp();
-            const uint32_t bar = smem_addr(&bars[st]);
+            const uint32_t bar = smem_addr(&bars[st]), kt = smem_addr(ring + (size_t)st * T::STAGE);
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::STAGE);
             __syncwarp();
-            if (lane < boxes) {
-                const uint32_t kt = smem_addr(ring + (size_t)st * T::STAGE) + (uint32_t)(lane * boxr * 128);
-                const int y = p & ((1 << a.page_shift) - 1);
-#pragma unroll
-                for (int bx = 0; bx < D / 64; ++bx) {
-                    tma_page(kt + bx * T::BOX, &map, bx * 64, y, hk, page, a.k_plane, bar);
-                    tma_page(kt + T::BYTES + bx * T::BOX, &map, bx * 64, y, hk, page, a.v_plane, bar);
-                }
-            }
+            load_tile<XKEYS, D>(a, &map, kt, p, hk, a.k_plane, page, bar);
+            load_tile<XKEYS, D>(a, &map, kt + T::BYTES, p, hk, a.v_plane, page, bar);
             __syncwarp();
         }
         // no copy may still be landing in shared memory when the block exits
@@ -562,10 +507,7 @@ cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMa
         return cudaFuncSetAttribute(k_prefix_attn<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<D>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    e = launch_kernel(k_prefix_attn<D, BF>, dim3(grid), dim3(XTHREADS), Tile<D>::SMEM, pdl, s, a, pl, map);
-    if (e != cudaSuccess) return e;
-    const long long warps = (long long)a.rows * a.Hq;
-    return launch_kernel(k_prefix_merge<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, true, s, a, pl);
+    return launch_kernel(k_prefix_attn<D, BF>, dim3(grid), dim3(XTHREADS), Tile<D>::SMEM, pdl, s, a, pl, map);
 }
 
 }  // namespace
@@ -578,24 +520,35 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     const int cap = max_parts(a.rows, a.Hq);
+    const long long head_rows = (long long)a.rows * a.G;
+    // The tensor-memory kernel for the shared parts: from TC_ROWS rows a head
+    // on, where they are bound by the products, and prefixes of several tiles.
+    // (A negative scale would turn its maximum into a minimum.)
+    const bool tc = head_rows >= TC_ROWS && a.shared >= TC_SHARED && a.c_log2 >= 0.0f;
+    const bool pair = head_rows > TC_KEYS;
+    const int key = tc ? TC_KEYS : XKEYS, tile_rows = !tc ? XROWS : pair ? 2 * TC_KEYS : TC_KEYS;
     PrefixPlan pl;
-    pl.s0 = a.shared / XKEYS * XKEYS;
-    pl.ptiles = (int)(((long long)a.rows * a.G + XROWS - 1) / XROWS);
+    pl.s0 = a.shared / key * key;
+    pl.ptiles = (int)((head_rows + tile_rows - 1) / tile_rows);
     pl.stiles = (int)(((long long)a.max_rows * a.G + XROWS - 1) / XROWS);
-    // about two blocks per SM for each kind of part, whole tiles, and at most
-    // `cap` parts in all (half of them for each kind)
-    auto cut = [&](long long positions, long long blocks, int most, int &n, int &chunk) {
-        long long want = (2LL * sms + blocks - 1) / blocks;
+    // whole tiles, and at most `cap` parts in all (half of them for each kind)
+    auto cut = [&](long long positions, long long want, int most, int tile, int &n, int &chunk) {
         if (want > most) want = most;
         if (want < 1) want = 1;
         long long len = (positions + want - 1) / want;
-        len = (len + XKEYS - 1) / XKEYS * XKEYS;
-        if (len < XKEYS) len = XKEYS;
+        len = (len + tile - 1) / tile * tile;
+        if (len < tile) len = tile;
         chunk = (int)len;
         n = (int)((positions + len - 1) / len);
     };
-    cut(pl.s0, (long long)a.Hkv * pl.ptiles, cap / 2, pl.np, pl.pchunk);
-    cut((long long)a.max_len - pl.s0, (long long)a.Hkv * a.B * pl.stiles, cap / 2, pl.ns, pl.schunk);
+    const long long pblocks = (long long)a.Hkv * pl.ptiles, sblocks = (long long)a.Hkv * a.B * pl.stiles;
+    if (!tc) {  // about two blocks per SM
+        cut(pl.s0, (2LL * sms + pblocks - 1) / pblocks, cap / 2, key, pl.np, pl.pchunk);
+    } else {    // one block per SM, in as few rounds as the tiles allow
+        cut(pl.s0, sms / pblocks, pair ? cap / 2 : cap / 4, key, pl.np, pl.pchunk);
+        if (!pair) pl.np *= 2;  // each block's two streams are parts of their own
+    }
+    cut((long long)a.max_len - pl.s0, (2LL * sms + sblocks - 1) / sblocks, cap / 2, XKEYS, pl.ns, pl.schunk);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
@@ -604,14 +557,26 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     CUtensorMap map;
     cudaError_t e = pool_map(&map, c, D, a.type, XKEYS);
     if (e != cudaSuccess) return e;
-    const long long grid = (long long)a.Hkv * ((long long)pl.np * pl.ptiles + (long long)a.B * pl.ns * pl.stiles);
+    if (tc) {
+        CUtensorMap wide;
+        e = pool_map(&wide, c, D, a.type, TC_KEYS);
+        if (e != cudaSuccess) return e;
+        e = launch_prefix_tc(a, pl, wide, D, pdl, s);
+        if (e != cudaSuccess) return e;
+        pdl = true;
+    }
+    a.own_only = tc;
+    const long long grid = (tc ? 0 : pblocks * pl.np) + sblocks * pl.ns;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const bool bf = a.type == HQ_BF16;
     if (D == 128)
-        return bf ? launch_t<128, true>(a, pl, map, (unsigned)grid, pdl, s)
-                  : launch_t<128, false>(a, pl, map, (unsigned)grid, pdl, s);
-    return bf ? launch_t<64, true>(a, pl, map, (unsigned)grid, pdl, s)
-              : launch_t<64, false>(a, pl, map, (unsigned)grid, pdl, s);
+        e = bf ? launch_t<128, true>(a, pl, map, (unsigned)grid, pdl, s) : launch_t<128, false>(a, pl, map, (unsigned)grid, pdl, s);
+    else
+        e = bf ? launch_t<64, true>(a, pl, map, (unsigned)grid, pdl, s) : launch_t<64, false>(a, pl, map, (unsigned)grid, pdl, s);
+    if (e != cudaSuccess) return e;
+    const dim3 merge((unsigned)(((long long)a.rows * a.Hq + 7) / 8));
+    return D == 128 ? launch_kernel(k_prefix_merge<128>, merge, dim3(256), 0, true, s, a, pl)
+                    : launch_kernel(k_prefix_merge<64>, merge, dim3(256), 0, true, s, a, pl);
 }
 
 }  // namespace hq

@@ -1,0 +1,399 @@
+// k_prefix_tc.cu -- the shared parts of the prefix attention on the
+// fifth-generation tensor cores (tcgen05), for batches with many rows.
+//
+// Over the shared positions the batch is one dense attention without a mask:
+// all rows that read one key/value head (rows * G of them) against the prefix.
+// With enough rows it is bound by the tensor cores, not by memory, and the
+// warp-level MMAs of k_prefix.cu reach only a third of their rate.
+//
+// A thread block works on two streams at once, each with its own 128-row
+// query tile, its 128 columns of scores and its output accumulator in tensor
+// memory (2 x (128 + 128) columns: all 512):
+//   S = Q K^T        both operands in shared memory
+//   P = exp2(c S - c m), rounded to the cache's type, written over S
+//   O += P V         P from tensor memory, V from shared memory
+// While one stream is in its softmax the tensor core works for the other.
+// PAIR: the streams are two query tiles against the same positions; otherwise
+// (at most 128 rows) one query tile against alternating tiles of positions.
+//   warps 0-3, 4-7  softmax of stream 0, 1: a thread owns one row, so maximum
+//                   and sum need no exchange between lanes
+//   warp 8          K and V tiles by TMA into a ring of four slots
+//   warp 9          issues the MMAs (one thread); warps 10, 11 only fill the
+//                   warpgroup whose registers go to the softmax
+// The reference maximum m of a row is raised only when a score exceeds it by
+// 2^8 or more in the exponent's units: then O is scaled by the softmax warps
+// themselves, between two products; P stays below 2^8, far from fp16's end, and
+// the sums stay exact ratios.  A block writes its unnormalized outputs, m and
+// sums; k_prefix_merge puts the parts together.
+//
+// The wait for S(j + 1) also orders the scaling of O behind P V(j): MMAs of
+// one thread complete in order, and P V(j) is issued before S(j + 1).
+#include "hq_tc.cuh"
+#include "prefix_common.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int CR = 128;       // rows of a query tile, positions of a K/V tile
+constexpr int CSLOTS = 4;     // ring slots, each one K or one V tile
+constexpr int CTHREADS = 384;
+// Registers: three warpgroups start with the 168 that 384 threads allow; the
+// third gives up 96 a thread, the softmax warpgroups take 48 each (2 * 216 +
+// 72 = 3 * 168): a row's 128 scores then stay in registers.
+constexpr int CREG_SOFTMAX = 216, CREG_REST = 72;
+constexpr float LAZY = 8.0f;  // base-2 units a score may exceed the reference maximum by
+
+template <int D>
+struct TcTile {
+    static constexpr int BOX = CR * 128;          // 128 rows x 64 dimensions
+    static constexpr int BYTES = (D / 64) * BOX;
+    static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256;
+};
+
+// D[128 x N] (+)= A[128 x 16] * B[16 x N], A and B in shared memory, fp32 D.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: 8 x 128-byte atoms,
+// `sbo` bytes between the atoms of consecutive groups of 8 rows (K-major: rows
+// of the operand; MN-major: steps along K), `lbo` between blocks of 64
+// elements along MN (MN-major only).
+__device__ __forceinline__ uint64_t desc_swz128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: 128 x N, fp32 D, A and B fp16 or bf16; B K-major
+// (scores) or MN-major (V as it lies in the cache).
+template <bool BF>
+__host__ __device__ constexpr uint32_t idesc_of(int N, bool b_mn) {
+    return (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+template <int D, bool BF, bool PAIR>
+__global__ void __launch_bounds__(CTHREADS, 1)
+    k_prefix_tc(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
+    using T = TcTile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *s_q = sm, *s_ring = sm + 2 * T::BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(s_ring + CSLOTS * T::BYTES);
+    const uint32_t full = smem_addr(bars), empty = full + 8 * CSLOTS, sfull = empty + 8 * CSLOTS, pready = sfull + 16,
+                   ofull = pready + 16, qready = ofull + 16;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * CSLOTS + 7);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < CSLOTS; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(sfull + 8 * w, 1);
+            mbar_init(pready + 8 * w, 4);
+            mbar_init(ofull + 8 * w, 1);
+        }
+        mbar_init(qready, 8);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(smem_addr(s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    int unit = blockIdx.x;
+    const int hk = unit % a.Hkv;
+    unit /= a.Hkv;
+    const int rt = unit % pl.ptiles, split = unit / pl.ptiles;
+    const int k0 = split * pl.pchunk, k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
+    const Seq seq = first_live(a);
+    const int ntiles = seq.live ? (k1 - k0) / CR : 0;  // no row of the batch uses this part: nothing to do
+    const int nrows = a.rows * a.G;
+
+    if (warp < 8) {
+        // ------------------------------------------------------- softmax ---
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CREG_SOFTMAX));
+        const int w = warp >> 2, r = threadIdx.x & 127;               // stream, row of its tile
+        const int row = PAIR ? (2 * rt + w) * CR + r : rt * CR + r;   // row among all rows of this head
+        const int part = PAIR ? split : 2 * split + w;
+        const size_t at = ((size_t)part * a.rows + row / a.G) * a.Hq + hk * a.G + row % a.G;
+        const int n = PAIR ? ntiles : (ntiles - w + 1) / 2;
+        bool ok = true;
+        if (ntiles > 0) {
+            // the query rows, swizzled as the tensor core reads them
+            if (PAIR || w == 0) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(a.q) +
+                    (row < nrows ? (size_t)(row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
+                uint8_t *dst = s_q + w * T::BYTES;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * T::BOX + swz128(r, c & 7)) =
+                        row < nrows ? src[c] : make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qready);
+        }
+        const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+        const uint32_t tS = lane_base + w * 128, tO = lane_base + 256 + w * 128;
+        const float c = a.c_log2;
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            if (ok) ok = mbar_wait_bounded(sfull + 8 * w, (uint32_t)(j & 1), a.err);
+            __syncwarp();
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
+            tmem_wait_ld();
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (j == 0) {
+                m = top;
+            } else {
+                const bool raise = (top - m) * c > LAZY;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float mn = raise ? top : m;
+                    const float al = raise ? ex2((m - mn) * c) : 1.0f;
+                    m = mn;
+                    l *= al;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        float o[32];
+                        uint32_t u[32];
+                        tmem_ld32(tO + 32 * i, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * al);
+                        tmem_st32(tO + 32 * i, u);
+                    }
+                }
+            }
+            const float mc = m == -INFINITY ? 0.0f : m * c;
+            const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
+            f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float x, y;
+                    f2_split(f2_fma(f2_make(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), cc, mm), x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    sum[i & 1] = f2_add(sum[i & 1], f2_make(x, y));
+                    p[i] = pack16<BF>(x, y);
+                }
+                tmem_st32(tS + 32 * h, p);
+            }
+            float x0, x1, x2, x3;
+            f2_split(sum[0], x0, x1);
+            f2_split(sum[1], x2, x3);
+            l += (x0 + x1) + (x2 + x3);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pready + 8 * w);
+        }
+        if (n > 0) {
+            if (ok) ok = mbar_wait_bounded(ofull + 8 * w, 0u, a.err);
+            __syncwarp();
+            tc_fence_after();
+        }
+        float4 *dst = reinterpret_cast<float4 *>(a.ws_o + at * D);
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float o[32];
+                tmem_ld32(tO + 32 * i, o);
+                tmem_wait_ld();
+                if (row < nrows)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+        }
+        // a stream without a tile (or without a finite score) adds nothing
+        if (row < nrows)
+            *reinterpret_cast<float2 *>(a.ws_ml + at * 2) =
+                make_float2(l == 0.0f ? -INFINITY : m == -INFINITY ? 0.0f : m * c, l);
+        tc_fence_before();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREG_REST));
+    }
+    if (warp == 8) {
+        // ---------------------------------------------------------- K, V ---
+        // the order in which the MMAs use them: PAIR K0 V0 K1 V1 ...; else
+        // K0 K1 V0 K2 V1 K3 ...
+        const int32_t *row = a.table + (size_t)(seq.live ? seq.slot : 0) * a.max_pages;
+        int i = 0;
+        bool ok = true;
+        auto put = [&](int tile, int plane) {
+            const int p = k0 + tile * CR, st = i % CSLOTS;
+            const int page = lookup_page<CR>(a, row, p, k1);
+            if (ok && i >= CSLOTS)
+                ok = mbar_wait_bounded(empty + 8 * st, (uint32_t)((i / CSLOTS) & 1) ^ 1u, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)T::BYTES);
+            __syncwarp();
+            load_tile<CR, D>(a, &map, smem_addr(s_ring + st * T::BYTES), p, hk, plane, page, full + 8 * st);
+            __syncwarp();
+            ++i;
+        };
+        if (PAIR) {
+            for (int t = 0; t < ntiles; ++t) {
+                put(t, a.k_plane);
+                put(t, a.v_plane);
+            }
+        } else if (ntiles > 0) {
+            put(0, a.k_plane);
+            if (ntiles > 1) put(1, a.k_plane);
+            for (int t = 0; t < ntiles; ++t) {
+                put(t, a.v_plane);
+                if (t + 2 < ntiles) put(t + 2, a.k_plane);
+            }
+        }
+        // no copy may still be landing in shared memory when the block exits
+        for (int j = i > CSLOTS ? i - CSLOTS : 0; j < i; ++j)
+            mbar_wait_bounded(full + 8 * (j % CSLOTS), (uint32_t)((j / CSLOTS) & 1), a.err);
+    } else if (warp == 9 && lane == 0 && ntiles > 0) {
+        // ---------------------------------------------------------- MMAs ---
+        constexpr uint32_t id_s = idesc_of<BF>(CR, false), id_o = idesc_of<BF>(D, true);
+        bool ok = mbar_wait_bounded(qready, 0u, a.err);
+        int use = 0;  // ring uses so far
+        auto next = [&]() -> int {  // the slot of the next K or V tile, arrived
+            const int st = use % CSLOTS;
+            if (ok) ok = mbar_wait_bounded(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
+            ++use;
+            return st;
+        };
+        auto scores = [&](int w, int st) {  // S_w = Q K^T
+            const uint32_t q = smem_addr(s_q + (PAIR ? w : 0) * T::BYTES), k = smem_addr(s_ring + st * T::BYTES);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t o = (uint32_t)(ks >> 2) * T::BOX + (uint32_t)(ks & 3) * 32;
+                tc_mma_ss(tmem + w * 128, desc_swz128(q + o, 16, 1024), desc_swz128(k + o, 16, 1024), id_s, ks > 0);
+            }
+            tc_commit(sfull + 8 * w);
+        };
+        auto product = [&](int w, int st, int j) {  // O_w += P_w V
+            if (ok) ok = mbar_wait_bounded(pready + 8 * w, (uint32_t)(j & 1), a.err);
+            tc_fence_after();
+            const uint32_t v = smem_addr(s_ring + st * T::BYTES);
+#pragma unroll
+            for (int ks = 0; ks < CR / 16; ++ks)
+                tc_mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8,
+                              desc_swz128(v + (uint32_t)ks * 2048, T::BOX, 1024), id_o, j > 0 || ks > 0);
+        };
+        if (PAIR) {
+            int kst = next();
+            scores(0, kst);
+            scores(1, kst);
+            tc_commit(empty + 8 * kst);
+            for (int j = 0; j < ntiles; ++j) {
+                const bool more = j + 1 < ntiles;
+                const int vst = next();
+                product(0, vst, j);
+                if (more) {
+                    kst = next();
+                    scores(0, kst);
+                } else {
+                    tc_commit(ofull);
+                }
+                product(1, vst, j);
+                tc_commit(empty + 8 * vst);
+                if (more) {
+                    scores(1, kst);
+                    tc_commit(empty + 8 * kst);
+                } else {
+                    tc_commit(ofull + 8);
+                }
+            }
+        } else {
+            for (int w = 0; w < 2 && w < ntiles; ++w) {
+                const int st = next();
+                scores(w, st);
+                tc_commit(empty + 8 * st);
+            }
+            for (int t = 0; t < ntiles; ++t) {
+                const int w = t & 1, vst = next();
+                product(w, vst, t >> 1);
+                tc_commit(empty + 8 * vst);
+                if (t + 2 < ntiles) {
+                    const int st = next();
+                    scores(w, st);
+                    tc_commit(empty + 8 * st);
+                } else {
+                    tc_commit(ofull + 8 * w);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF, bool PAIR>
+cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> configured[CACHE_DEVICES];
+    int done = 0;
+    e = cached_per_device(configured, dev, &done, [&](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(k_prefix_tc<D, BF, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)TcTile<D>::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    const int splits = PAIR ? pl.np : pl.np / 2;
+    return launch_kernel(k_prefix_tc<D, BF, PAIR>, dim3((unsigned)(a.Hkv * pl.ptiles * splits)), dim3(CTHREADS),
+                         TcTile<D>::SMEM, pdl, s, a, pl, map);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, int D, bool pdl,
+                             cudaStream_t s) {
+    const bool bf = a.type == HQ_BF16, pair = (long long)a.rows * a.G > CR;
+    if (D == 128) {
+        if (pair) return bf ? launch_t<128, true, true>(a, pl, map, pdl, s) : launch_t<128, false, true>(a, pl, map, pdl, s);
+        return bf ? launch_t<128, true, false>(a, pl, map, pdl, s) : launch_t<128, false, false>(a, pl, map, pdl, s);
+    }
+    if (pair) return bf ? launch_t<64, true, true>(a, pl, map, pdl, s) : launch_t<64, false, true>(a, pl, map, pdl, s);
+    return bf ? launch_t<64, true, false>(a, pl, map, pdl, s) : launch_t<64, false, false>(a, pl, map, pdl, s);
+}
+
+}  // namespace hq

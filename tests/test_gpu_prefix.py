@@ -364,3 +364,62 @@ def test_on_a_side_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert hq.hq_workspace_status(ws) == hq.HQ_OK
     t.check(out)
+
+
+MANY_ROWS = [  # batch, most rows, shared, own positions up to, Hq, Hkv, D, page, type: rows enough for the tensor-memory kernel
+    (20, 1, 700, 40, 32, 8, 128, 16, F16), (32, 1, 512, 9, 8, 2, 128, 64, BF16), (65, 1, 640, 0, 2, 2, 64, 32, F16),
+    (33, 1, 4096, 20, 12, 3, 64, 128, BF16), (13, 9, 900, 5, 8, 8, 128, 256, F16), (3, 128, 1300, 200, 8, 8, 128, 16, BF16),
+    (5, 100, 515, 7, 6, 2, 64, 16, F16), (70, 2, 2049, 64, 40, 8, 128, 32, F16), (24, 16, 6000, 30, 32, 4, 128, 64, BF16),
+]
+
+
+@pytest.mark.parametrize("B,m,shared,own,Hq,Hkv,D,ps,dtype", MANY_ROWS)
+def test_many_rows_match_64_bits(B, m, shared, own, Hq, Hkv, D, ps, dtype):
+    rows = [m] + spread(B - 1, 1, m, B)
+    lens = [shared + own + m] + [shared + x + r for x, r in zip(spread(B - 1, 0, own, B + 1), rows[1:])]
+    t = Batch(lens, rows, shared, Hq, Hkv, D, ps, dtype, seed=B + m)
+    got = t.run()
+    assert t.status == hq.HQ_OK
+    t.check(got)
+    assert torch.equal(got, t.run(flags=hq.HQ_LAUNCH_PDL))
+    t.check(t.run(shared=shared // 2 + 1))
+
+
+@pytest.mark.parametrize("B,rising", [(20, True), (20, False), (80, True), (80, False)])
+def test_scores_that_rise_or_fall_along_the_prefix(B, rising):
+    """The running maximum moves at every tile, by a little and by a lot."""
+    t = Batch([1500 + b % 7 for b in range(B)], [1] * B, 1400, 8, 2, 128, 16, F16, seed=B)
+    pages = t.cache.table[0, :1400 // 16].long()
+    ramp = torch.linspace(0.0, 6.0, len(pages), device=DEV)
+    ramp = ramp if rising else ramp.flip(0)
+    t.cache.pool[2, pages] = (t.cache.pool[2, pages].float() * ramp.view(-1, 1, 1, 1)).half()
+    got = t.run()
+    assert t.status == hq.HQ_OK
+    t.check(got)
+
+
+def test_nan_in_the_prefix_reaches_every_row_of_its_head():
+    for B in (20, 80):
+        t = Batch([800] * B, [1] * B, 700, 8, 2, 128, 16, BF16, seed=B)
+        t.cache.pool[1, int(t.cache.table[0, 20]), 1, 3, 5] = float("nan")
+        got = t.run()
+        assert bool(torch.isnan(got[:, 4:, 5]).all()) and bool(torch.isfinite(got[:, :4].float()).all())
+        assert bool(torch.isfinite(got[:, 4:, :5].float()).all())
+
+
+def test_a_negative_scale_with_many_rows():
+    t = Batch([900 + b for b in range(70)], [1] * 70, 800, 8, 2, 128, 32, F16, seed=3)
+    t.scale = -0.1
+    got = t.run()
+    t.q, t.scale = -t.q, 0.1
+    t.check(got)
+
+
+def test_inactive_sequences_among_many_rows():
+    lens = [0 if b % 5 == 0 else 700 + b for b in range(60)]
+    t = Batch(lens, [2] * 60, 600, 8, 2, 128, 16, F16, seed=4)
+    got = t.run()
+    assert t.status == hq.HQ_OK
+    t.check(got)
+    t.cache.lens.zero_()  # none left: the prefix has no table to be read through
+    assert not t.run(max_len=700).any() and t.status == hq.HQ_OK
