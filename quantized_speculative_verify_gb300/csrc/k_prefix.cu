@@ -18,28 +18,31 @@
 // Per block: one producer warp brings each 64-position tile of K and V with
 // TMA tiled copies (a page, or 64 positions of it, per box, in 128-byte
 // swizzle) into a ring of stages; the lanes look the pages up in parallel.
-// Four consumer warps own 16 rows each: S = Q K^T and O += P V on the tensor
-// cores with fp32 accumulation, an online softmax in base-2 units.
+// Four consumer warps form S = Q K^T and O += P V on the tensor cores with fp32
+// accumulation and an online softmax in base-2 units: KW of them share 16 rows
+// and take every KW-th group of 16 positions of a tile (a single token's few
+// rows do not fill more than one warp's MMA), 4 / KW row groups to a block; at
+// the end the warps of a row group merge in shared memory.
 #include "prefix_common.cuh"
 
 namespace hq {
 namespace {
 
-constexpr int XROWS = 64;     // query rows per thread block
 constexpr int XKEYS = 64;     // positions per stage
 constexpr int XSTAGES = 3;
-constexpr int XCW = 4;        // consumer warps, 16 rows each
+constexpr int XCW = 4;        // consumer warps
 constexpr int XTHREADS = (XCW + 1) * 32;
 constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the tensor-memory kernel
 constexpr int TC_ROWS = 65;
 constexpr int TC_SHARED = 512;
+constexpr int MAX_PARTS = 64;   // shared_parts + own_parts
 
 template <int D>
 struct Tile {
     static constexpr int BOX = XKEYS * 128;           // 64 positions x 64 dimensions
     static constexpr int BYTES = (D / 64) * BOX;      // K or V of a stage
     static constexpr int STAGE = 2 * BYTES;
-    static constexpr size_t SMEM = 1024 + (size_t)XSTAGES * STAGE + 2 * XSTAGES * 8 + XROWS * 16 + HQ_MAX_M * 4;
+    static constexpr size_t SMEM = 1024 + (size_t)XSTAGES * STAGE + 2 * XSTAGES * 8 + 64 * 16 + HQ_MAX_M * 4;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
@@ -93,10 +96,12 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
     return (w & e) == e || ((w >> 16) & e) == e;
 }
 
-template <int D, bool BF>
+template <int D, bool BF, int KW>
 __global__ void __launch_bounds__(XTHREADS, 2)
     k_prefix_attn(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
     using T = Tile<D>;
+    constexpr int XROWS = 64 / KW;     // query rows of the block
+    constexpr int NJ = XKEYS / 8 / KW; // this warp's groups of 8 positions in a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + (size_t)XSTAGES * T::STAGE);  // full[S], empty[S]
@@ -177,7 +182,8 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 
     // ---------------------------------------------------------- consumers ---
     const int g8 = lane >> 2, t4 = lane & 3;
-    const int rA = rt * XROWS + warp * 16 + g8, rB = rA + 8;  // this lane's two rows of the part
+    const int kw = warp % KW;                                        // this warp's share of the positions
+    const int rA = rt * XROWS + (warp / KW) * 16 + g8, rB = rA + 8;  // this lane's two rows of the part
     uint32_t qa[D / 16][4];
     {
         const bool vA = rA < nrows, vB = rB < nrows;
@@ -239,31 +245,33 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         const uint32_t kt = smem_addr(ring + (size_t)st * T::STAGE), vt = kt + T::BYTES;
         const int p0 = k0 + i * XKEYS;
 
-        float s[XKEYS / 8][4];
+        // group n of this warp: the 16 positions kw + n * KW of the tile
+        float s[NJ][4];
 #pragma unroll
-        for (int j = 0; j < XKEYS / 8; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-            for (int np = 0; np < XKEYS / 16; ++np) {
+            for (int n = 0; n < NJ / 2; ++n) {
                 uint32_t b0, b1, b2, b3;
-                ldsm4(kt + (uint32_t)((ks >> 2) * T::BOX) + swz128(np * 16 + k_row, 2 * (ks & 3) + k_half), b0, b1, b2, b3);
-                mma_x<BF>(s[2 * np], qa[ks], b0, b1);
-                mma_x<BF>(s[2 * np + 1], qa[ks], b2, b3);
+                ldsm4(kt + (uint32_t)((ks >> 2) * T::BOX) + swz128((kw + n * KW) * 16 + k_row, 2 * (ks & 3) + k_half),
+                      b0, b1, b2, b3);
+                mma_x<BF>(s[2 * n], qa[ks], b0, b1);
+                mma_x<BF>(s[2 * n + 1], qa[ks], b2, b3);
             }
 
         // mask, scale to base-2 units, running maximum
         const bool full = p0 + XKEYS <= tree0 && p0 + XKEYS <= k1;
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < XKEYS / 8; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float x = s[j][e] * a.c_log2;
                 if (!full) {
-                    const int pos = p0 + j * 8 + 2 * t4 + (e & 1);
+                    const int pos = p0 + (kw + (j >> 1) * KW) * 16 + (j & 1) * 8 + 2 * t4 + (e & 1);
                     bool vis = pos < k1;
                     if (vis && pos >= tree0) {
                         const int tn = pos - tree0;
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         }
         float rs[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < XKEYS / 8; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float p = exp2f(s[j][e] - mx[e >> 1]);
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         if (plain) {
             // O += P V: P rounded to the cache's type
 #pragma unroll
-            for (int kk = 0; kk < XKEYS / 16; ++kk) {
+            for (int kk = 0; kk < NJ / 2; ++kk) {
                 uint32_t pa[4];
                 pa[0] = pack2<BF>(s[2 * kk][0], s[2 * kk][1]);
                 pa[1] = pack2<BF>(s[2 * kk][2], s[2 * kk][3]);
@@ -333,21 +341,21 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 #pragma unroll
                 for (int dp = 0; dp < D / 16; ++dp) {
                     uint32_t b0, b1, b2, b3;
-                    ldsm4t(vt + (uint32_t)((dp >> 2) * T::BOX) + swz128(kk * 16 + v_row, 2 * (dp & 3) + v_half), b0, b1,
-                           b2, b3);
+                    ldsm4t(vt + (uint32_t)((dp >> 2) * T::BOX) + swz128((kw + kk * KW) * 16 + v_row, 2 * (dp & 3) + v_half),
+                           b0, b1, b2, b3);
                     mma_x<BF>(o[2 * dp], pa, b0, b1);
                     mma_x<BF>(o[2 * dp + 1], pa, b2, b3);
                 }
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < XKEYS / 8; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
                     const int from = (lane & ~3) | (c >> 1);
                     const float pA = __shfl_sync(0xffffffffu, (c & 1) ? s[j][1] : s[j][0], from);
                     const float pB = __shfl_sync(0xffffffffu, (c & 1) ? s[j][3] : s[j][2], from);
-                    const int r = j * 8 + c;
+                    const int r = (kw + (j >> 1) * KW) * 16 + (j & 1) * 8 + c;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
                         uint32_t w;
@@ -370,11 +378,60 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         if (lane == 0) mbar_arrive(smem_addr(&bars[XSTAGES + st]));
     }
 
-    // this part's unnormalized outputs, maxima and sums
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 1);
         lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 2);
+    }
+    if constexpr (KW > 1) {
+        // The warps of a row group merge through the ring, which nothing
+        // writes any more: every tile has arrived and been read.
+        float *box = reinterpret_cast<float *>(ring);  // [consumer warp][D / 8 * 4 + 4][32 lanes]
+        constexpr int PER = (D / 8 * 4 + 4) * 32;
+        named_barrier(1, XCW * 32);
+        float *mine = box + warp * PER + lane;
+        if (kw > 0) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(j * 4 + e) * 32] = o[j][e];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mine[(D / 2 + h) * 32] = mrun[h];
+                mine[(D / 2 + 2 + h) * 32] = lrun[h];
+            }
+        }
+        named_barrier(1, XCW * 32);
+        if (kw > 0) return;
+        float top[2] = {mrun[0], mrun[1]}, wt[2][KW];
+#pragma unroll
+        for (int k = 1; k < KW; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) top[h] = fmaxf(top[h], mine[k * PER + (D / 2 + h) * 32]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float t = top[h] == -INFINITY ? 0.0f : top[h];  // nothing seen by any: all weights 0
+            wt[h][0] = exp2f(mrun[h] - t);
+            lrun[h] *= wt[h][0];
+#pragma unroll
+            for (int k = 1; k < KW; ++k) {
+                wt[h][k] = exp2f(mine[k * PER + (D / 2 + h) * 32] - t);
+                lrun[h] += wt[h][k] * mine[k * PER + (D / 2 + 2 + h) * 32];
+            }
+            mrun[h] = top[h];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[j][e] *= wt[e >> 1][0];
+#pragma unroll
+                for (int k = 1; k < KW; ++k) o[j][e] += wt[e >> 1][k] * mine[k * PER + (j * 4 + e) * 32];
+            }
+    }
+    // this part's unnormalized outputs, maxima and sums
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
         const int r = h ? rB : rA;
         if (r >= nrows) continue;
         const size_t row = ((size_t)split * a.rows + first + r / a.G) * a.Hq + hk * a.G + r % a.G;
@@ -418,22 +475,57 @@ __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const 
     // own parts that reach into the sequence
     const int parts = !live ? 0 : pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
     const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h;
-    float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.ws_ml[(r0 + p * step) * 2]);
+    // lane p holds part p's (and p + 32's) weight; a part in which the row saw
+    // nothing weighs 0 and is not read
+    static_assert(MAX_PARTS <= 64, "two parts a lane");
+    float m2[2], l2[2], top = -INFINITY, den = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = lane + 32 * i;
+        const float2 ml = p < parts ? *reinterpret_cast<const float2 *>(a.ws_ml + (r0 + p * step) * 2)
+                                    : make_float2(-INFINITY, 0.0f);
+        m2[i] = ml.x;
+        l2[i] = ml.y;
+        top = fmaxf(top, ml.x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    constexpr int E = D / 32;
-    float acc[E], den = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        m2[i] = m2[i] == -INFINITY && l2[i] == 0.0f ? 0.0f : exp2f(m2[i] - top);
+        den += m2[i] * l2[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    constexpr int E = D / 32, BATCH = 8;  // loads in flight
+    float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int p = 0; p < parts; ++p) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + (r0 + p * step) * 2);
-        if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // the row saw nothing in this part
-        const float wt = exp2f(ml.x - top);
-        den += wt * ml.y;
-        const float *src = a.ws_o + (r0 + p * step) * D + lane * E;
+    for (int p0 = 0; p0 < parts; p0 += BATCH) {
+        float v[BATCH][E], wt[BATCH];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wt * src[e];
+        for (int i = 0; i < BATCH; ++i) {
+            const int p = p0 + i;
+            wt[i] = __shfl_sync(0xffffffffu, p & 32 ? m2[1] : m2[0], p & 31);
+            const float *src = a.ws_o + (r0 + p * step) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = 0.0f;
+            if (p < parts && wt[i] != 0.0f) {
+                if constexpr (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src);
+                    v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2 *>(src);
+                    v[i][0] = f.x, v[i][1] = f.y;
+                }
+            } else {
+                wt[i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += wt[i] * v[i][e];
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = parts == 0 ? 0.0f : acc[e] / den;
@@ -488,13 +580,18 @@ cudaError_t pool_map(CUtensorMap *m, const hq_pages &c, int D, int type, int box
 }
 
 // Parts a row may be cut into, for a workspace that does not depend on the
-// lengths: many for few rows (every SM needs a block), few for many.
-int max_parts(int rows, int Hq) {
-    const long long p = (1LL << 16) / ((long long)rows * Hq);
-    return p > 64 ? 64 : p < 8 ? 8 : (int)p;
+// lengths: as many as it takes to give every SM a block.  A block of the
+// shared parts has up to 256 rows, one of the own parts a sequence's.
+int shared_parts(int rows, int Hq) {
+    const long long p = 40960 / ((long long)rows * Hq) + 1;
+    return p > 32 ? 32 : p < 2 ? 2 : (int)p;
+}
+int own_parts(int B, int Hkv) {
+    const long long p = 320 / ((long long)B * Hkv) + 1;
+    return p > 32 ? 32 : (int)p;
 }
 
-template <int D, bool BF>
+template <int D, bool BF, int KW>
 cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, unsigned grid, bool pdl,
                      cudaStream_t s) {
     int dev = 0;
@@ -504,34 +601,45 @@ cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMa
     int done = 0;
     e = cached_per_device(configured, dev, &done, [&](int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(k_prefix_attn<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<D>::SMEM);
+        return cudaFuncSetAttribute(k_prefix_attn<D, BF, KW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<D>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    return launch_kernel(k_prefix_attn<D, BF>, dim3(grid), dim3(XTHREADS), Tile<D>::SMEM, pdl, s, a, pl, map);
+    return launch_kernel(k_prefix_attn<D, BF, KW>, dim3(grid), dim3(XTHREADS), Tile<D>::SMEM, pdl, s, a, pl, map);
+}
+
+template <int D, bool BF>
+cudaError_t launch_kw(int kw, const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, unsigned grid, bool pdl,
+                      cudaStream_t s) {
+    return kw == 4   ? launch_t<D, BF, 4>(a, pl, map, grid, pdl, s)
+           : kw == 2 ? launch_t<D, BF, 2>(a, pl, map, grid, pdl, s)
+                     : launch_t<D, BF, 1>(a, pl, map, grid, pdl, s);
 }
 
 }  // namespace
 
-size_t prefix_workspace_bytes(int rows, int Hq, int D) {
-    return 16 + (size_t)max_parts(rows, Hq) * rows * Hq * (size_t)(D + 2) * 4;
+size_t prefix_workspace_bytes(int B, int rows, int Hq, int Hkv, int D) {
+    return 16 + (size_t)(shared_parts(rows, Hq) + own_parts(B, Hkv)) * rows * Hq * (size_t)(D + 2) * 4;
 }
 
 cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    const int cap = max_parts(a.rows, a.Hq);
+    const int pcap = shared_parts(a.rows, a.Hq), scap = own_parts(a.B, a.Hkv);
     const long long head_rows = (long long)a.rows * a.G;
     // The tensor-memory kernel for the shared parts: from TC_ROWS rows a head
     // on, where they are bound by the products, and prefixes of several tiles.
     // (A negative scale would turn its maximum into a minimum.)
     const bool tc = head_rows >= TC_ROWS && a.shared >= TC_SHARED && a.c_log2 >= 0.0f;
     const bool pair = head_rows > TC_KEYS;
-    const int key = tc ? TC_KEYS : XKEYS, tile_rows = !tc ? XROWS : pair ? 2 * TC_KEYS : TC_KEYS;
+    // warps that share 16 rows, from the rows that the blocks of the other kernel have
+    const long long few = tc ? (long long)a.max_rows * a.G : head_rows;
+    const int kw = few <= 16 ? 4 : few <= 32 ? 2 : 1, xrows = 64 / kw;
+    const int key = tc ? TC_KEYS : XKEYS, tile_rows = !tc ? xrows : pair ? 2 * TC_KEYS : TC_KEYS;
     PrefixPlan pl;
     pl.s0 = a.shared / key * key;
     pl.ptiles = (int)((head_rows + tile_rows - 1) / tile_rows);
-    pl.stiles = (int)(((long long)a.max_rows * a.G + XROWS - 1) / XROWS);
-    // whole tiles, and at most `cap` parts in all (half of them for each kind)
+    pl.stiles = (int)(((long long)a.max_rows * a.G + xrows - 1) / xrows);
+    // whole tiles, and no more parts than the workspace holds
     auto cut = [&](long long positions, long long want, int most, int tile, int &n, int &chunk) {
         if (want > most) want = most;
         if (want < 1) want = 1;
@@ -543,17 +651,17 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     };
     const long long pblocks = (long long)a.Hkv * pl.ptiles, sblocks = (long long)a.Hkv * a.B * pl.stiles;
     if (!tc) {  // about two blocks per SM
-        cut(pl.s0, (2LL * sms + pblocks - 1) / pblocks, cap / 2, key, pl.np, pl.pchunk);
+        cut(pl.s0, (2LL * sms + pblocks - 1) / pblocks, pcap, key, pl.np, pl.pchunk);
     } else {    // one block per SM, in as few rounds as the tiles allow
-        cut(pl.s0, sms / pblocks, pair ? cap / 2 : cap / 4, key, pl.np, pl.pchunk);
+        cut(pl.s0, sms / pblocks, pair ? pcap : pcap / 2, key, pl.np, pl.pchunk);
         if (!pair) pl.np *= 2;  // each block's two streams are parts of their own
     }
-    cut((long long)a.max_len - pl.s0, (2LL * sms + sblocks - 1) / sblocks, cap / 2, XKEYS, pl.ns, pl.schunk);
+    cut((long long)a.max_len - pl.s0, (2LL * sms + sblocks - 1) / sblocks, scap, XKEYS, pl.ns, pl.schunk);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
     a.ws_o = reinterpret_cast<float *>(ws + 16);
-    a.ws_ml = a.ws_o + (size_t)cap * a.rows * a.Hq * D;
+    a.ws_ml = a.ws_o + (size_t)(pcap + scap) * a.rows * a.Hq * D;
     CUtensorMap map;
     cudaError_t e = pool_map(&map, c, D, a.type, XKEYS);
     if (e != cudaSuccess) return e;
@@ -570,9 +678,11 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const bool bf = a.type == HQ_BF16;
     if (D == 128)
-        e = bf ? launch_t<128, true>(a, pl, map, (unsigned)grid, pdl, s) : launch_t<128, false>(a, pl, map, (unsigned)grid, pdl, s);
+        e = bf ? launch_kw<128, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
+               : launch_kw<128, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
     else
-        e = bf ? launch_t<64, true>(a, pl, map, (unsigned)grid, pdl, s) : launch_t<64, false>(a, pl, map, (unsigned)grid, pdl, s);
+        e = bf ? launch_kw<64, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
+               : launch_kw<64, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
     if (e != cudaSuccess) return e;
     const dim3 merge((unsigned)(((long long)a.rows * a.Hq + 7) / 8));
     return D == 128 ? launch_kernel(k_prefix_merge<128>, merge, dim3(256), 0, true, s, a, pl)

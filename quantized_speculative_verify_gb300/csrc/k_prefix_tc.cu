@@ -82,6 +82,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+    return d;
+}
+
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if constexpr (BF) {
@@ -101,9 +107,9 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *s_q = sm, *s_ring = sm + 2 * T::BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(s_ring + CSLOTS * T::BYTES);
-    const uint32_t full = smem_addr(bars), empty = full + 8 * CSLOTS, sfull = empty + 8 * CSLOTS, pready = sfull + 16,
-                   ofull = pready + 16, qready = ofull + 16;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * CSLOTS + 7);
+    const uint32_t full = smem_addr(bars), empty = full + 8 * CSLOTS, sfull = empty + 8 * CSLOTS, phalf = sfull + 16,
+                   pready = phalf + 16, ofull = pready + 16, qready = ofull + 16;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * CSLOTS + 9);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -113,6 +119,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(sfull + 8 * w, 1);
+            mbar_init(phalf + 8 * w, 4);
             mbar_init(pready + 8 * w, 4);
             mbar_init(ofull + 8 * w, 1);
         }
@@ -166,17 +173,24 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         const float c = a.c_log2;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < n; ++j) {
-            if (ok) ok = mbar_wait_bounded(sfull + 8 * w, (uint32_t)(j & 1), a.err);
+            if (ok) ok = mbar_wait_short(sfull + 8 * w, (uint32_t)(j & 1), a.err);
             __syncwarp();
             tc_fence_after();
             float s[128];
+            // each quarter's maximum is taken while the next one is on its way
+            tmem_ld32(tS, s);
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, s + 32 * i);
-            tmem_wait_ld();
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_ld();
+                if (q < 3) tmem_ld32(tS + 32 * (q + 1), s + 32 * (q + 1));
 #pragma unroll
-            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int i = 0; i < 32; i += 4) {
+                    mx[0] = max3(mx[0], s[32 * q + i], s[32 * q + i + 1]);
+                    mx[1] = max3(mx[1], s[32 * q + i + 2], s[32 * q + i + 3]);
+                }
+            }
+            const float top = fmaxf(mx[0], mx[1]);
             if (j == 0) {
                 m = top;
             } else {
@@ -214,6 +228,12 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                     p[i] = pack16<BF>(x, y);
                 }
                 tmem_st32(tS + 32 * h, p);
+                if (h == 0) {  // the product may start on the first half
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(phalf + 8 * w);
+                }
             }
             float x0, x1, x2, x3;
             f2_split(sum[0], x0, x1);
@@ -225,7 +245,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             if (lane == 0) mbar_arrive(pready + 8 * w);
         }
         if (n > 0) {
-            if (ok) ok = mbar_wait_bounded(ofull + 8 * w, 0u, a.err);
+            if (ok) ok = mbar_wait_short(ofull + 8 * w, 0u, a.err);
             __syncwarp();
             tc_fence_after();
         }
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             const int p = k0 + tile * CR, st = i % CSLOTS;
             const int page = lookup_page<CR>(a, row, p, k1);
             if (ok && i >= CSLOTS)
-                ok = mbar_wait_bounded(empty + 8 * st, (uint32_t)((i / CSLOTS) & 1) ^ 1u, a.err);
+                ok = mbar_wait_short(empty + 8 * st, (uint32_t)((i / CSLOTS) & 1) ^ 1u, a.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)T::BYTES);
@@ -285,15 +305,15 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         }
         // no copy may still be landing in shared memory when the block exits
         for (int j = i > CSLOTS ? i - CSLOTS : 0; j < i; ++j)
-            mbar_wait_bounded(full + 8 * (j % CSLOTS), (uint32_t)((j / CSLOTS) & 1), a.err);
+            mbar_wait_short(full + 8 * (j % CSLOTS), (uint32_t)((j / CSLOTS) & 1), a.err);
     } else if (warp == 9 && lane == 0 && ntiles > 0) {
         // ---------------------------------------------------------- MMAs ---
         constexpr uint32_t id_s = idesc_of<BF>(CR, false), id_o = idesc_of<BF>(D, true);
-        bool ok = mbar_wait_bounded(qready, 0u, a.err);
+        bool ok = mbar_wait_short(qready, 0u, a.err);
         int use = 0;  // ring uses so far
         auto next = [&]() -> int {  // the slot of the next K or V tile, arrived
             const int st = use % CSLOTS;
-            if (ok) ok = mbar_wait_bounded(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
+            if (ok) ok = mbar_wait_short(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
             ++use;
             return st;
         };
@@ -307,13 +327,16 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             tc_commit(sfull + 8 * w);
         };
         auto product = [&](int w, int st, int j) {  // O_w += P_w V
-            if (ok) ok = mbar_wait_bounded(pready + 8 * w, (uint32_t)(j & 1), a.err);
-            tc_fence_after();
             const uint32_t v = smem_addr(s_ring + st * T::BYTES);
 #pragma unroll
-            for (int ks = 0; ks < CR / 16; ++ks)
+            for (int ks = 0; ks < CR / 16; ++ks) {
+                if (ks == 0 || ks == CR / 32) {
+                    if (ok) ok = mbar_wait_short((ks ? pready : phalf) + 8 * w, (uint32_t)(j & 1), a.err);
+                    tc_fence_after();
+                }
                 tc_mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8,
                               desc_swz128(v + (uint32_t)ks * 2048, T::BOX, 1024), id_o, j > 0 || ks > 0);
+            }
         };
         if (PAIR) {
             int kst = next();

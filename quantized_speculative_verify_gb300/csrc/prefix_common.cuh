@@ -57,8 +57,8 @@ __device__ __forceinline__ Seq first_live(const PrefixArgs &a) {
 // A warp loads one tile of TILE positions from p0 on of K or V (`plane`) of
 // head hk into `dst` (boxes of 64 dimensions, TILE * 128 bytes each): lane j
 // looks up and loads the j-th run of positions that lie in one page.  `row` is
-// the sequence's table; positions from `end` on and bad pages arrive as zeros.
-// `page` is the lane's page as lookup_page returned it.
+// the sequence's table; runs that start at or past `end` and bad pages arrive
+// as zeros.  `page` is the lane's page as lookup_page returned it.
 template <int TILE>
 __device__ __forceinline__ int lookup_page(const PrefixArgs &a, const int32_t *row, int p0, int end) {
     const int lane = threadIdx.x & 31;
@@ -86,6 +86,13 @@ __device__ __forceinline__ void load_tile(const PrefixArgs &a, const CUtensorMap
     const uint32_t at = dst + (uint32_t)(lane << sh) * 128u;
 #pragma unroll
     for (int bx = 0; bx < D / 64; ++bx) tma_page(at + bx * TILE * 128, map, bx * 64, y, hk, page, plane, bar);
+}
+
+// mbar_wait_bounded for waits that are short and frequent: the clock is read
+// only after the hardware's own waiting (up to a millisecond each) gave up.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, int *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, err);
 }
 
 // Shared parts on the tensor-memory kernel (k_prefix_tc.cu).
