@@ -18,7 +18,7 @@
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread owns one row, so maximum
 //                   and sum need no exchange between lanes
 //   warp 8          K and V tiles by TMA into a ring of four slots
-//   warp 9          issues the MMAs (one thread); warps 10, 11 only fill the
+//   warp 9          issues the MMAs; warps 10, 11 only fill the
 //                   warpgroup whose registers go to the softmax
 // The reference maximum m of a row is raised only when a score exceeds it by
 // 2^8 or more in the exponent's units: then O is scaled by the softmax warps
@@ -50,12 +50,16 @@ struct TcTile {
     static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256;
 };
 
-// D[128 x N] (+)= A[128 x 16] * B[16 x N], A and B in shared memory, fp32 D.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// D[128 x N] (+)= A[128 x 16] * B[16 x N], A and B in shared memory, fp32 D;
+// issued by the lane with `leader` set, executed by the converged warp (the
+// operands stay warp-uniform: one lane in a branch of its own took 3600 cycles
+// for the 32 MMAs of two tiles that the tensor core needs 2048 for).
+__device__ __forceinline__ void tc_mma_ss_if(uint32_t leader, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
 
@@ -306,43 +310,48 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         // no copy may still be landing in shared memory when the block exits
         for (int j = i > CSLOTS ? i - CSLOTS : 0; j < i; ++j)
             mbar_wait_short(full + 8 * (j % CSLOTS), (uint32_t)((j / CSLOTS) & 1), a.err);
-    } else if (warp == 9 && lane == 0 && ntiles > 0) {
+    } else if (warp == 9 && ntiles > 0) {
         // ---------------------------------------------------------- MMAs ---
+        const uint32_t leader = elect_one() ? 1u : 0u;
+        const uint64_t dq = desc_swz128(smem_addr(s_q), 16, 1024), dk = desc_swz128(smem_addr(s_ring), 16, 1024);
+        const uint64_t dv = desc_swz128(smem_addr(s_ring), T::BOX, 1024);  // addresses count in 16 bytes, below bit 14
         constexpr uint32_t id_s = idesc_of<BF>(CR, false), id_o = idesc_of<BF>(D, true);
         bool ok = mbar_wait_short(qready, 0u, a.err);
         int use = 0;  // ring uses so far
         auto next = [&]() -> int {  // the slot of the next K or V tile, arrived
             const int st = use % CSLOTS;
             if (ok) ok = mbar_wait_short(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
+            __syncwarp();
             ++use;
             return st;
         };
         auto scores = [&](int w, int st) {  // S_w = Q K^T
-            const uint32_t q = smem_addr(s_q + (PAIR ? w : 0) * T::BYTES), k = smem_addr(s_ring + st * T::BYTES);
+            const uint64_t q = dq + (uint64_t)((PAIR ? w : 0) * (T::BYTES / 16)), k = dk + (uint64_t)(st * (T::BYTES / 16));
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t o = (uint32_t)(ks >> 2) * T::BOX + (uint32_t)(ks & 3) * 32;
-                tc_mma_ss(tmem + w * 128, desc_swz128(q + o, 16, 1024), desc_swz128(k + o, 16, 1024), id_s, ks > 0);
+                const uint64_t o = (uint64_t)((ks >> 2) * (T::BOX / 16) + (ks & 3) * 2);
+                tc_mma_ss_if(leader, tmem + w * 128, q + o, k + o, id_s, ks > 0);
             }
-            tc_commit(sfull + 8 * w);
+            tc_commit_if(leader, sfull + 8 * w);
         };
         auto product = [&](int w, int st, int j) {  // O_w += P_w V
-            const uint32_t v = smem_addr(s_ring + st * T::BYTES);
+            const uint64_t v = dv + (uint64_t)(st * (T::BYTES / 16));
 #pragma unroll
             for (int ks = 0; ks < CR / 16; ++ks) {
                 if (ks == 0 || ks == CR / 32) {
                     if (ok) ok = mbar_wait_short((ks ? pready : phalf) + 8 * w, (uint32_t)(j & 1), a.err);
+                    __syncwarp();
                     tc_fence_after();
                 }
-                tc_mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8,
-                              desc_swz128(v + (uint32_t)ks * 2048, T::BOX, 1024), id_o, j > 0 || ks > 0);
+                tc_mma_f16_ts_if(leader, tmem + 256 + w * 128, tmem + w * 128 + ks * 8, v + (uint64_t)(ks * 128), id_o,
+                                 j > 0 || ks > 0);
             }
         };
         if (PAIR) {
             int kst = next();
             scores(0, kst);
             scores(1, kst);
-            tc_commit(empty + 8 * kst);
+            tc_commit_if(leader, empty + 8 * kst);
             for (int j = 0; j < ntiles; ++j) {
                 const bool more = j + 1 < ntiles;
                 const int vst = next();
@@ -351,33 +360,33 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                     kst = next();
                     scores(0, kst);
                 } else {
-                    tc_commit(ofull);
+                    tc_commit_if(leader, ofull);
                 }
                 product(1, vst, j);
-                tc_commit(empty + 8 * vst);
+                tc_commit_if(leader, empty + 8 * vst);
                 if (more) {
                     scores(1, kst);
-                    tc_commit(empty + 8 * kst);
+                    tc_commit_if(leader, empty + 8 * kst);
                 } else {
-                    tc_commit(ofull + 8);
+                    tc_commit_if(leader, ofull + 8);
                 }
             }
         } else {
             for (int w = 0; w < 2 && w < ntiles; ++w) {
                 const int st = next();
                 scores(w, st);
-                tc_commit(empty + 8 * st);
+                tc_commit_if(leader, empty + 8 * st);
             }
             for (int t = 0; t < ntiles; ++t) {
                 const int w = t & 1, vst = next();
                 product(w, vst, t >> 1);
-                tc_commit(empty + 8 * vst);
+                tc_commit_if(leader, empty + 8 * vst);
                 if (t + 2 < ntiles) {
                     const int st = next();
                     scores(w, st);
-                    tc_commit(empty + 8 * st);
+                    tc_commit_if(leader, empty + 8 * st);
                 } else {
-                    tc_commit(ofull + 8 * w);
+                    tc_commit_if(leader, ofull + 8 * w);
                 }
             }
         }
