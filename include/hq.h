@@ -610,6 +610,7 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  * parent as in hq_tree_attention (numbered within the sequence), or NULL: a
  * chain (node i - 1 is the parent of node i: the newest tokens of a prompt or
  * a single token).  Query head h reads key/value head h / (Hq / heads).
+ *   Hq        a multiple of heads, at most 65535
  *   cache     row_bytes = 2 D, D = 64 or 128; type HQ_F16 or HQ_BF16;
  *             plane_bytes below 2^40
  *   q         type [rows][Hq][D], rows ldq elements apart, 16-byte aligned rows

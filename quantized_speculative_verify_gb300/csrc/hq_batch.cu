@@ -240,7 +240,7 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
     if (!type16(type) || (out_type != HQ_F32 && out_type != type)) return HQ_ERR_INVALID_ARG;
     if (B < 0 || B > 65535 || rows < 0 || max_rows < 1 || max_rows > HQ_MAX_M) return HQ_ERR_INVALID_ARG;
     if (!starts && (long long)B * max_rows > rows) return HQ_ERR_INVALID_ARG;
-    if (Hq <= 0 || Hq % cache->heads != 0 || (long long)rows * Hq > (1 << 28)) return HQ_ERR_INVALID_ARG;
+    if (Hq <= 0 || Hq > 65535 || Hq % cache->heads != 0 || (long long)rows * Hq > (1 << 28)) return HQ_ERR_INVALID_ARG;
     if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return HQ_ERR_INVALID_ARG;
     if (shared < 0 || max_len < 1 || max_len > 1 << 30 || shared >= max_len ||
         max_len > (long long)cache->max_pages * cache->page_size)

@@ -443,102 +443,119 @@ __global__ void __launch_bounds__(XTHREADS, 2)
     }
 }
 
-// One warp per (row, query head): the parts' maxima and sums, then the
-// weighted sum of their outputs, in ascending order of position.
-template <int D>
+// Merges the parts of `HG` query heads of one row: blockIdx = (row, group of
+// heads).  First the weight of every part, exp2(m - top) over the sum of
+// weight times l, into shared memory; then each thread adds up four dimensions
+// of one head over every PG-th part (PG groups of threads where the heads
+// alone do not fill the block), 8 loads in flight, and the groups add up in
+// order.  What bounds it is the chain of dependent loads (row -> sequence ->
+// maxima -> outputs), so the sequence is found by all threads at once.
+template <int D, int HG>
 __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const PrefixPlan pl) {
+    constexpr int COLS = HG * D / 4;            // float4 columns
+    constexpr int PG = COLS >= 256 ? 1 : 256 / COLS, BATCH = 8;
+    __shared__ float s_w[MAX_PARTS][HG];
+    __shared__ float4 s_acc[PG > 1 ? 256 : 1];
+    __shared__ int s_b;
+    const int tid = threadIdx.x, row = blockIdx.x, h0 = blockIdx.y * HG;
+    if (tid == 0) s_b = -1;
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w >= (long long)a.rows * a.Hq) return;
-    const int row = (int)(w / a.Hq), h = (int)(w % a.Hq);
-    // the sequence the row belongs to: the last one that starts at or before it
-    int b = 0;
+    // the sequence whose rows hold this one (the last, should `starts` repeat it)
     if (a.starts) {
-        int lo = 0, hi = a.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.starts[mid] <= row) lo = mid;
-            else hi = mid;
+        int mine = -1;
+        for (int b = tid; b < a.B; b += 256) {
+            int first, m;
+            batch_rows(a.starts, b, a.rows, a.max_rows, first, m);
+            if (row >= first && row < first + m) mine = b;
         }
-        b = lo;
-    } else {
-        b = row / a.max_rows;
+        if (mine >= 0) atomicMax(&s_b, mine);
+    } else if (tid == 0 && row / a.max_rows < a.B) {
+        s_b = row / a.max_rows;
     }
-    bool live = b < a.B;  // rows past the last sequence's belong to none
-    Seq s = {};
-    if (live) {
-        s = seq_of(a, b);
-        live = s.live && row >= s.first && row < s.first + s.m;
+    __syncthreads();
+    int parts = 0;
+    if (s_b >= 0) {
+        const Seq s = seq_of(a, s_b);
+        // own parts that reach into the sequence
+        if (s.live) parts = pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
     }
-    // own parts that reach into the sequence
-    const int parts = !live ? 0 : pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
-    const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h;
-    // lane p holds part p's (and p + 32's) weight; a part in which the row saw
-    // nothing weighs 0 and is not read
+    const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h0;
+    // weights: a warp per head, two parts a lane
     static_assert(MAX_PARTS <= 64, "two parts a lane");
-    float m2[2], l2[2], top = -INFINITY, den = 0.0f;
+    for (int h = tid >> 5; h < HG; h += 8) {
+        const int lane = tid & 31;
+        const bool in = h0 + h < a.Hq;
+        float m2[2], l2[2], top = -INFINITY, den = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = lane + 32 * i;
-        const float2 ml = p < parts ? *reinterpret_cast<const float2 *>(a.ws_ml + (r0 + p * step) * 2)
-                                    : make_float2(-INFINITY, 0.0f);
-        m2[i] = ml.x;
-        l2[i] = ml.y;
-        top = fmaxf(top, ml.x);
+        for (int i = 0; i < 2; ++i) {
+            const int p = lane + 32 * i;
+            const float2 ml = in && p < parts ? *reinterpret_cast<const float2 *>(a.ws_ml + (r0 + h + p * step) * 2)
+                                              : make_float2(-INFINITY, 0.0f);
+            m2[i] = ml.x;
+            l2[i] = ml.y;
+            top = fmaxf(top, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // a part in which the row saw nothing weighs 0 and is not read
+            m2[i] = m2[i] == -INFINITY && l2[i] == 0.0f ? 0.0f : exp2f(m2[i] - top);
+            den += m2[i] * l2[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane + 32 * i < parts) s_w[lane + 32 * i][h] = m2[i] == 0.0f ? 0.0f : m2[i] / den;
     }
+    __syncthreads();
+    const int pg = PG > 1 ? tid / COLS : 0;
+    for (int c = PG > 1 ? tid % COLS : tid; c < COLS; c += 256) {
+        const int h = c / (D / 4), d = (c % (D / 4)) * 4;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float *src = a.ws_o + (r0 + h) * D + d;
+        for (int p0 = pg; p0 < parts; p0 += PG * BATCH) {
+            float4 v[BATCH];
+            float w[BATCH];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int i = 0; i < BATCH; ++i) {
+                const int p = p0 + i * PG;
+                w[i] = p < parts && h0 + h < a.Hq ? s_w[p][h] : 0.0f;
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (w[i] != 0.0f) v[i] = *reinterpret_cast<const float4 *>(src + (size_t)p * step * D);
+            }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        m2[i] = m2[i] == -INFINITY && l2[i] == 0.0f ? 0.0f : exp2f(m2[i] - top);
-        den += m2[i] * l2[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    constexpr int E = D / 32, BATCH = 8;  // loads in flight
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int p0 = 0; p0 < parts; p0 += BATCH) {
-        float v[BATCH][E], wt[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int p = p0 + i;
-            wt[i] = __shfl_sync(0xffffffffu, p & 32 ? m2[1] : m2[0], p & 31);
-            const float *src = a.ws_o + (r0 + p * step) * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[i][e] = 0.0f;
-            if (p < parts && wt[i] != 0.0f) {
-                if constexpr (E == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(src);
-                    v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2 *>(src);
-                    v[i][0] = f.x, v[i][1] = f.y;
-                }
-            } else {
-                wt[i] = 0.0f;
+            for (int i = 0; i < BATCH; ++i) {
+                acc.x += w[i] * v[i].x;
+                acc.y += w[i] * v[i].y;
+                acc.z += w[i] * v[i].z;
+                acc.w += w[i] * v[i].w;
             }
         }
+        if constexpr (PG > 1) {
+            s_acc[tid] = acc;
+            __syncthreads();
+            if (pg > 0) return;
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += wt[i] * v[i][e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = parts == 0 ? 0.0f : acc[e] / den;
-    const size_t at = (size_t)row * a.ldo + (size_t)h * D + lane * E;
-    if (a.out_type == HQ_F32) {
-        float *o = static_cast<float *>(a.out) + at;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = acc[e];
-    } else {
-        uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at);
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            o[e / 2] = a.out_type == HQ_F16 ? pack2<false>(acc[e], acc[e + 1]) : pack2<true>(acc[e], acc[e + 1]);
+            for (int g = 1; g < PG; ++g) {
+                const float4 v = s_acc[tid + g * COLS];
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
+            }
+        }
+        if (h0 + h >= a.Hq) continue;
+        const size_t at = (size_t)row * a.ldo + (size_t)(h0 + h) * D + d;
+        if (a.out_type == HQ_F32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = acc;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                a.out_type == HQ_F16 ? make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w))
+                                     : make_uint2(pack2<true>(acc.x, acc.y), pack2<true>(acc.z, acc.w));
     }
 }
 
@@ -587,7 +604,7 @@ int shared_parts(int rows, int Hq) {
     return p > 32 ? 32 : p < 2 ? 2 : (int)p;
 }
 int own_parts(int B, int Hkv) {
-    const long long p = 320 / ((long long)B * Hkv) + 1;
+    const long long p = 1280 / ((long long)B * Hkv) + 1;
     return p > 32 ? 32 : (int)p;
 }
 
@@ -613,6 +630,17 @@ cudaError_t launch_kw(int kw, const PrefixArgs &a, const PrefixPlan &pl, const C
     return kw == 4   ? launch_t<D, BF, 4>(a, pl, map, grid, pdl, s)
            : kw == 2 ? launch_t<D, BF, 2>(a, pl, map, grid, pdl, s)
                      : launch_t<D, BF, 1>(a, pl, map, grid, pdl, s);
+}
+
+template <int D>
+cudaError_t launch_merge(const PrefixArgs &a, const PrefixPlan &pl, int sms, cudaStream_t s) {
+    // 8 heads a block where that gives every SM two, fewer heads and more
+    // threads on the parts of each where rows are few
+    auto grid = [&](int hg) { return dim3((unsigned)a.rows, (unsigned)((a.Hq + hg - 1) / hg)); };
+    auto enough = [&](int hg) { return (long long)a.rows * ((a.Hq + hg - 1) / hg) >= 2LL * sms; };
+    if (enough(8)) return launch_kernel(k_prefix_merge<D, 8>, grid(8), dim3(256), 0, true, s, a, pl);
+    if (enough(2)) return launch_kernel(k_prefix_merge<D, 2>, grid(2), dim3(256), 0, true, s, a, pl);
+    return launch_kernel(k_prefix_merge<D, 1>, grid(1), dim3(256), 0, true, s, a, pl);
 }
 
 }  // namespace
@@ -656,7 +684,7 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
         cut(pl.s0, sms / pblocks, pair ? pcap : pcap / 2, key, pl.np, pl.pchunk);
         if (!pair) pl.np *= 2;  // each block's two streams are parts of their own
     }
-    cut((long long)a.max_len - pl.s0, (2LL * sms + sblocks - 1) / sblocks, scap, XKEYS, pl.ns, pl.schunk);
+    cut((long long)a.max_len - pl.s0, (8LL * sms + sblocks - 1) / sblocks, scap, XKEYS, pl.ns, pl.schunk);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
@@ -684,9 +712,7 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
         e = bf ? launch_kw<64, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
                : launch_kw<64, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
     if (e != cudaSuccess) return e;
-    const dim3 merge((unsigned)(((long long)a.rows * a.Hq + 7) / 8));
-    return D == 128 ? launch_kernel(k_prefix_merge<128>, merge, dim3(256), 0, true, s, a, pl)
-                    : launch_kernel(k_prefix_merge<64>, merge, dim3(256), 0, true, s, a, pl);
+    return D == 128 ? launch_merge<128>(a, pl, sms, s) : launch_merge<64>(a, pl, sms, s);
 }
 
 }  // namespace hq
