@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
             const int st = i % XSTAGES, p = k0 + i * XKEYS;
             const int page = lookup_page<XKEYS>(a, row, p, k1);
             if (i >= XSTAGES &&
-                !mbar_wait_bounded(smem_addr(&bars[XSTAGES + st]), (uint32_t)((i / XSTAGES) & 1) ^ 1u, a.err))
+                !mbar_wait_short(smem_addr(&bars[XSTAGES + st]), (uint32_t)((i / XSTAGES) & 1) ^ 1u, a.err))
                 break;
             __syncwarp();
             const uint32_t bar = smem_addr(&bars[st]), kt = smem_addr(ring + (size_t)st * T::STAGE);
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         }
         // no copy may still be landing in shared memory when the block exits
         for (int j = i > XSTAGES ? i - XSTAGES : 0; j < i; ++j)
-            mbar_wait_bounded(smem_addr(&bars[j % XSTAGES]), (uint32_t)((j / XSTAGES) & 1), a.err);
+            mbar_wait_short(smem_addr(&bars[j % XSTAGES]), (uint32_t)((j / XSTAGES) & 1), a.err);
         return;
     }
 
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 
     for (int i = 0; i < ntiles; ++i) {
         const int st = i % XSTAGES;
-        if (ok) ok = mbar_wait_bounded(smem_addr(&bars[st]), (uint32_t)((i / XSTAGES) & 1), a.err);
+        if (ok) ok = mbar_wait_short(smem_addr(&bars[st]), (uint32_t)((i / XSTAGES) & 1), a.err);
         __syncwarp();
         const uint32_t kt = smem_addr(ring + (size_t)st * T::STAGE), vt = kt + T::BYTES;
         const int p0 = k0 + i * XKEYS;
@@ -262,24 +262,36 @@ __global__ void __launch_bounds__(XTHREADS, 2)
                 mma_x<BF>(s[2 * n + 1], qa[ks], b2, b3);
             }
 
-        // mask, scale to base-2 units, running maximum
+        // scale to base-2 units, mask, running maximum.  `sees`: which of the
+        // tile's positions each of this lane's two rows sees (bit = position)
         const bool full = p0 + XKEYS <= tree0 && p0 + XKEYS <= k1;
+        uint64_t sees[2] = {~0ull, ~0ull};
+        if (!full) {
+            const int n = k1 - p0, old = tree0 - p0;  // positions in the part; before the tree
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t *anc = h ? ancB : ancA;
+                uint64_t v = old >= 64 ? ~0ull : old > 0 ? (1ull << old) - 1 : 0ull;
+                if (old < 64) {
+                    const uint64_t lo = anc[0] | (uint64_t)anc[1] << 32, hi = anc[2] | (uint64_t)anc[3] << 32;
+                    if (old >= 0)
+                        v |= lo << old;
+                    else if (old > -64)
+                        v |= lo >> -old | hi << (64 + old);
+                    else
+                        v |= hi >> (-64 - old);  // old > -128: the part ends with the tree
+                }
+                if (n < 64) v &= (1ull << n) - 1;
+                sees[h] = v >> (kw * 16 + 2 * t4);
+            }
+        }
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = s[j][e] * a.c_log2;
-                if (!full) {
-                    const int pos = p0 + (kw + (j >> 1) * KW) * 16 + (j & 1) * 8 + 2 * t4 + (e & 1);
-                    bool vis = pos < k1;
-                    if (vis && pos >= tree0) {
-                        const int tn = pos - tree0;
-                        const uint32_t *anc = (e >> 1) ? ancB : ancA;
-                        vis = (anc[tn >> 5] >> (tn & 31)) & 1u;
-                    }
-                    if (!vis) x = -INFINITY;
-                }
+                const int at = (j >> 1) * KW * 16 + (j & 1) * 8 + (e & 1);  // the position, less kw * 16 + 2 * t4
+                const float x = full || ((sees[e >> 1] >> at) & 1) ? s[j][e] * a.c_log2 : -INFINITY;
                 s[j][e] = x;
                 mx[e >> 1] = fmaxf(mx[e >> 1], x);
             }
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
             const float mnew = fmaxf(mrun[h], mx[h]);
-            alpha[h] = mnew == -INFINITY ? 1.0f : exp2f(mrun[h] - mnew);
+            alpha[h] = mnew == -INFINITY ? 1.0f : ex2(mrun[h] - mnew);
             mx[h] = mnew == -INFINITY ? 0.0f : mnew;  // no visible position yet: probabilities 0
             mrun[h] = mnew;
         }
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float p = exp2f(s[j][e] - mx[e >> 1]);
+                const float p = ex2(s[j][e] - mx[e >> 1]);
                 s[j][e] = p;
                 rs[e >> 1] += p;
             }
@@ -314,54 +326,50 @@ __global__ void __launch_bounds__(XTHREADS, 2)
             }
         }
 
-        // A masked position weighs 0, and 0 times an infinity or NaN is NaN:
-        // where a tile is masked and its values are not all finite, each row
-        // adds the positions it sees one by one.
-        bool plain = true;
-        if (!full) {
-            bool odd = false;
-            for (int x = lane; x < T::BYTES / 16; x += 32) {
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(vt + (uint32_t)x * 16));
-                odd |= nonfinite2<BF>(w[0]) || nonfinite2<BF>(w[1]) || nonfinite2<BF>(w[2]) || nonfinite2<BF>(w[3]);
-            }
-            plain = !__any_sync(0xffffffffu, odd);
-        }
-        if (plain) {
-            // O += P V: P rounded to the cache's type
+        // O += P V: P rounded to the cache's type.  A masked position weighs 0,
+        // and 0 times an infinity or NaN is NaN: in a masked group of 16
+        // positions whose values are not all finite, each row adds the
+        // positions it sees one by one.
 #pragma unroll
-            for (int kk = 0; kk < NJ / 2; ++kk) {
-                uint32_t pa[4];
-                pa[0] = pack2<BF>(s[2 * kk][0], s[2 * kk][1]);
-                pa[1] = pack2<BF>(s[2 * kk][2], s[2 * kk][3]);
-                pa[2] = pack2<BF>(s[2 * kk + 1][0], s[2 * kk + 1][1]);
-                pa[3] = pack2<BF>(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+        for (int kk = 0; kk < NJ / 2; ++kk) {
+            uint32_t pa[4];
+            pa[0] = pack2<BF>(s[2 * kk][0], s[2 * kk][1]);
+            pa[1] = pack2<BF>(s[2 * kk][2], s[2 * kk][3]);
+            pa[2] = pack2<BF>(s[2 * kk + 1][0], s[2 * kk + 1][1]);
+            pa[3] = pack2<BF>(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+            uint32_t v[D / 16][4];
+            const int r0 = (kw + kk * KW) * 16;  // the group's first row of the tile
+            bool odd = false;
+#pragma unroll
+            for (int dp = 0; dp < D / 16; ++dp)
+                ldsm4t(vt + (uint32_t)((dp >> 2) * T::BOX) + swz128(r0 + v_row, 2 * (dp & 3) + v_half), v[dp][0], v[dp][1],
+                       v[dp][2], v[dp][3]);
+            if (!full && (p0 + r0 + 16 > tree0 || p0 + r0 + 16 > k1)) {
+#pragma unroll
+                for (int dp = 0; dp < D / 16; ++dp)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) odd |= nonfinite2<BF>(v[dp][e]);
+                odd = __any_sync(0xffffffffu, odd);
+            }
+            if (!odd) {
 #pragma unroll
                 for (int dp = 0; dp < D / 16; ++dp) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm4t(vt + (uint32_t)((dp >> 2) * T::BOX) + swz128((kw + kk * KW) * 16 + v_row, 2 * (dp & 3) + v_half),
-                           b0, b1, b2, b3);
-                    mma_x<BF>(o[2 * dp], pa, b0, b1);
-                    mma_x<BF>(o[2 * dp + 1], pa, b2, b3);
+                    mma_x<BF>(o[2 * dp], pa, v[dp][0], v[dp][1]);
+                    mma_x<BF>(o[2 * dp + 1], pa, v[dp][2], v[dp][3]);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
+            } else {
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const int from = (lane & ~3) | (c >> 1);
-                    const float pA = __shfl_sync(0xffffffffu, (c & 1) ? s[j][1] : s[j][0], from);
-                    const float pB = __shfl_sync(0xffffffffu, (c & 1) ? s[j][3] : s[j][2], from);
-                    const int r = (kw + (j >> 1) * KW) * 16 + (j & 1) * 8 + c;
+                for (int c = 0; c < 16; ++c) {
+                    const int from = (lane & ~3) | ((c & 7) >> 1);
+                    const float x = c & 8 ? (c & 1 ? s[2 * kk + 1][1] : s[2 * kk + 1][0]) : (c & 1 ? s[2 * kk][1] : s[2 * kk][0]);
+                    const float y = c & 8 ? (c & 1 ? s[2 * kk + 1][3] : s[2 * kk + 1][2]) : (c & 1 ? s[2 * kk][3] : s[2 * kk][2]);
+                    const float pA = __shfl_sync(0xffffffffu, x, from), pB = __shfl_sync(0xffffffffu, y, from);
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
                         uint32_t w;
                         asm volatile("ld.shared.b32 %0, [%1];"
                                      : "=r"(w)
-                                     : "r"(vt + (uint32_t)((n >> 3) * T::BOX) + swz128(r, n & 7) + (uint32_t)t4 * 4));
+                                     : "r"(vt + (uint32_t)((n >> 3) * T::BOX) + swz128(r0 + c, n & 7) + (uint32_t)t4 * 4));
                         const float2 f = unpack2<BF>(w);
                         if (pA != 0.0f) {
                             o[n][0] = fmaf(pA, f.x, o[n][0]);
@@ -373,6 +381,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
                         }
                     }
                 }
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bars[XSTAGES + st]));

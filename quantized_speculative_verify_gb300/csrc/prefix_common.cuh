@@ -30,6 +30,13 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, i
 
 __device__ __forceinline__ uint32_t swz128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// 2^x by the hardware's unit (2 ulp; results below the normal range are 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A sequence of the batch: its slot, rows, length; `live` false where it is
 // empty or its length contradicts the call.
 struct Seq {
