@@ -79,12 +79,13 @@ struct PrefixArgs {
     const void *q;
     void *out;
     const int32_t *seqs, *starts, *parent, *table, *len;
+    const uint8_t *pool;
+    int64_t plane_bytes;
     int *err;
     float *ws_o, *ws_ml;  // [part][row][Hq][D], [part][row][Hq][2]: running maximum (base-2 units), sum
     int64_t ldq, ldo;
     int B, rows, max_rows, Hq, Hkv, G, n_seqs, max_pages, page_shift, n_pages, k_plane, v_plane;
     int shared, max_len, type, out_type;
-    int own_only;    // the shared parts are another kernel's
     float c_log2;  // scale * log2(e)
 };
 size_t prefix_workspace_bytes(int B, int rows, int Hq, int Hkv, int D);

@@ -35,6 +35,7 @@ constexpr int XTHREADS = (XCW + 1) * 32;
 constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the tensor-memory kernel
 constexpr int TC_ROWS = 65;
 constexpr int TC_SHARED = 512;
+constexpr int TC_ROWS_OWN = 33;
 constexpr int MAX_PARTS = 64;   // shared_parts + own_parts
 
 template <int D>
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
     int unit = blockIdx.x;
     const int hk = unit % a.Hkv;
     unit /= a.Hkv;
-    const int nshared = a.own_only ? 0 : pl.np * pl.ptiles;
+    const int nshared = pl.tc_shared ? 0 : pl.np * pl.ptiles;
     int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0;
     if (unit < nshared) {
         split = unit / pl.ptiles;
@@ -662,20 +663,24 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     const int pcap = shared_parts(a.rows, a.Hq), scap = own_parts(a.B, a.Hkv);
-    const long long head_rows = (long long)a.rows * a.G;
-    // The tensor-memory kernel for the shared parts: from TC_ROWS rows a head
-    // on, where they are bound by the products, and prefixes of several tiles.
-    // (A negative scale would turn its maximum into a minimum.)
-    const bool tc = head_rows >= TC_ROWS && a.shared >= TC_SHARED && a.c_log2 >= 0.0f;
-    const bool pair = head_rows > TC_KEYS;
-    // warps that share 16 rows, from the rows that the blocks of the other kernel have
-    const long long few = tc ? (long long)a.max_rows * a.G : head_rows;
-    const int kw = few <= 16 ? 4 : few <= 32 ? 2 : 1, xrows = 64 / kw;
-    const int key = tc ? TC_KEYS : XKEYS, tile_rows = !tc ? xrows : pair ? 2 * TC_KEYS : TC_KEYS;
+    const long long head_rows = (long long)a.rows * a.G, seq_rows = (long long)a.max_rows * a.G;
+    // The tensor-memory kernel takes the shared parts from TC_ROWS rows a head
+    // on, where they are bound by the products, and prefixes of several tiles;
+    // and the own parts of sequences with TC_ROWS_OWN rows a head or more,
+    // which then take a short prefix along.  (A scale below 0 would turn its
+    // maximum into a minimum, a scale of 0 its masks into NaN.)
     PrefixPlan pl;
-    pl.s0 = a.shared / key * key;
-    pl.ptiles = (int)((head_rows + tile_rows - 1) / tile_rows);
-    pl.stiles = (int)(((long long)a.max_rows * a.G + xrows - 1) / xrows);
+    pl.tc_shared = head_rows >= TC_ROWS && a.shared >= TC_SHARED && a.c_log2 > 0.0f;
+    pl.tc_own = seq_rows >= TC_ROWS_OWN && (pl.tc_shared || a.shared < TC_SHARED) && a.c_log2 > 0.0f;
+    const bool pair = head_rows > TC_KEYS;
+    // warps that share 16 rows, from the rows that a block of the other kernel has
+    const long long few = pl.tc_shared ? seq_rows : head_rows;
+    const int kw = few <= 16 ? 4 : few <= 32 ? 2 : 1, xrows = 64 / kw;
+    const int pkey = pl.tc_shared ? TC_KEYS : XKEYS, skey = pl.tc_own ? TC_KEYS : XKEYS;
+    const int prows = !pl.tc_shared ? xrows : pair ? 2 * TC_KEYS : TC_KEYS, srows = pl.tc_own ? TC_KEYS : xrows;
+    pl.s0 = pl.tc_own && !pl.tc_shared ? 0 : a.shared / pkey * pkey;
+    pl.ptiles = (int)((head_rows + prows - 1) / prows);
+    pl.stiles = (int)((seq_rows + srows - 1) / srows);
     // whole tiles, and no more parts than the workspace holds
     auto cut = [&](long long positions, long long want, int most, int tile, int &n, int &chunk) {
         if (want > most) want = most;
@@ -687,40 +692,40 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
         n = (int)((positions + len - 1) / len);
     };
     const long long pblocks = (long long)a.Hkv * pl.ptiles, sblocks = (long long)a.Hkv * a.B * pl.stiles;
-    if (!tc) {  // about two blocks per SM
-        cut(pl.s0, (2LL * sms + pblocks - 1) / pblocks, pcap, key, pl.np, pl.pchunk);
-    } else {    // one block per SM, in as few rounds as the tiles allow
-        cut(pl.s0, sms / pblocks, pair ? pcap : pcap / 2, key, pl.np, pl.pchunk);
-        if (!pair) pl.np *= 2;  // each block's two streams are parts of their own
-    }
-    cut((long long)a.max_len - pl.s0, (8LL * sms + sblocks - 1) / sblocks, scap, XKEYS, pl.ns, pl.schunk);
+    // shared: one block per SM of the tensor-memory kernel in as few rounds as
+    // the tiles allow, two of the other; own: several short ones per SM
+    cut(pl.s0, pl.tc_shared ? sms / pblocks : (2LL * sms + pblocks - 1) / pblocks, pcap, pkey, pl.np, pl.pchunk);
+    cut((long long)a.max_len - pl.s0, ((pl.tc_own ? 2LL : 8LL) * sms + sblocks - 1) / sblocks, scap, skey, pl.ns, pl.schunk);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
     a.ws_o = reinterpret_cast<float *>(ws + 16);
     a.ws_ml = a.ws_o + (size_t)(pcap + scap) * a.rows * a.Hq * D;
+    a.pool = static_cast<const uint8_t *>(c.pool);
+    a.plane_bytes = c.plane_bytes;
+    const bool bf = a.type == HQ_BF16;
     CUtensorMap map;
-    cudaError_t e = pool_map(&map, c, D, a.type, XKEYS);
-    if (e != cudaSuccess) return e;
-    if (tc) {
-        CUtensorMap wide;
-        e = pool_map(&wide, c, D, a.type, TC_KEYS);
+    cudaError_t e;
+    if (pl.tc_shared || pl.tc_own) {
+        e = pool_map(&map, c, D, a.type, TC_KEYS);
         if (e != cudaSuccess) return e;
-        e = launch_prefix_tc(a, pl, wide, D, pdl, s);
+        e = launch_prefix_tc(a, pl, map, D, pdl, s);
         if (e != cudaSuccess) return e;
         pdl = true;
     }
-    a.own_only = tc;
-    const long long grid = (tc ? 0 : pblocks * pl.np) + sblocks * pl.ns;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const bool bf = a.type == HQ_BF16;
-    if (D == 128)
-        e = bf ? launch_kw<128, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
-               : launch_kw<128, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
-    else
-        e = bf ? launch_kw<64, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
-               : launch_kw<64, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
-    if (e != cudaSuccess) return e;
+    if (!pl.tc_own) {  // the own parts are always there
+        e = pool_map(&map, c, D, a.type, XKEYS);
+        if (e != cudaSuccess) return e;
+        const long long grid = (pl.tc_shared ? 0 : pblocks * pl.np) + sblocks * pl.ns;
+        if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        if (D == 128)
+            e = bf ? launch_kw<128, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
+                   : launch_kw<128, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
+        else
+            e = bf ? launch_kw<64, true>(kw, a, pl, map, (unsigned)grid, pdl, s)
+                   : launch_kw<64, false>(kw, a, pl, map, (unsigned)grid, pdl, s);
+        if (e != cudaSuccess) return e;
+    }
     return D == 128 ? launch_merge<128>(a, pl, sms, s) : launch_merge<64>(a, pl, sms, s);
 }
 

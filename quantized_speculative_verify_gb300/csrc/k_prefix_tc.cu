@@ -1,33 +1,42 @@
-// k_prefix_tc.cu -- the shared parts of the prefix attention on the
-// fifth-generation tensor cores (tcgen05), for batches with many rows.
+// k_prefix_tc.cu -- the prefix attention on the fifth-generation tensor cores
+// (tcgen05): the shared parts of batches with many rows, and the own parts of
+// sequences with many rows (draft trees).
 //
 // Over the shared positions the batch is one dense attention without a mask:
 // all rows that read one key/value head (rows * G of them) against the prefix.
 // With enough rows it is bound by the tensor cores, not by memory, and the
-// warp-level MMAs of k_prefix.cu reach only a third of their rate.
+// warp-level MMAs of k_prefix.cu reach a tenth of their rate (170 TFLOP/s).
 //
-// A thread block works on two streams at once, each with its own 128-row
-// query tile, its 128 columns of scores and its output accumulator in tensor
-// memory (2 x (128 + 128) columns: all 512):
+// A thread block works on two streams at once, each with its own 128 columns
+// of scores and its output accumulator in tensor memory (2 x (128 + 128)
+// columns: all 512):
 //   S = Q K^T        both operands in shared memory
 //   P = exp2(c S - c m), rounded to the cache's type, written over S
 //   O += P V         P from tensor memory, V from shared memory
 // While one stream is in its softmax the tensor core works for the other.
-// PAIR: the streams are two query tiles against the same positions; otherwise
-// (at most 128 rows) one query tile against alternating tiles of positions.
+// PAIR: the streams are two 128-row query tiles against the same positions.
+// Otherwise (at most 128 rows; own parts) they are one query tile against
+// alternating tiles of positions, added up at the end through shared memory.
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread owns one row, so maximum
 //                   and sum need no exchange between lanes
 //   warp 8          K and V tiles by TMA into a ring of four slots
-//   warp 9          issues the MMAs; warps 10, 11 only fill the
-//                   warpgroup whose registers go to the softmax
+//   warp 9          issues the MMAs; warps 10, 11 only fill the warpgroup
+//                   whose registers go to the softmax
 // The reference maximum m of a row is raised only when a score exceeds it by
-// 2^8 or more in the exponent's units: then O is scaled by the softmax warps
-// themselves, between two products; P stays below 2^8, far from fp16's end, and
-// the sums stay exact ratios.  A block writes its unnormalized outputs, m and
-// sums; k_prefix_merge puts the parts together.
+// 8 or more in base-2 units: then O is scaled by the softmax warps themselves,
+// between two products; P stays below 2^8, far from fp16's end, and output and
+// sum are relative to the same m.
 //
 // The wait for S(j + 1) also orders the scaling of O behind P V(j): MMAs of
 // one thread complete in order, and P V(j) is issued before S(j + 1).
+//
+// Own parts end with the sequence's draft tree: a row's visible positions of a
+// tile are 128 bits.  A masked position weighs 0, but 0 times an infinity or
+// NaN is NaN: in a masked tile the softmax warps set the non-finite values of
+// V from the tree on to 0 in shared memory before the product may read it, and
+// the rows that see such a value add it at the end from the cache itself.
+#include <type_traits>
+
 #include "hq_tc.cuh"
 #include "prefix_common.cuh"
 
@@ -47,7 +56,7 @@ template <int D>
 struct TcTile {
     static constexpr int BOX = CR * 128;          // 128 rows x 64 dimensions
     static constexpr int BYTES = (D / 64) * BOX;
-    static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256;
+    static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256 + HQ_MAX_M * 4;
 };
 
 // D[128 x N] (+)= A[128 x 16] * B[16 x N], A and B in shared memory, fp32 D;
@@ -97,7 +106,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     }
 }
 
-template <int D, bool BF, bool PAIR>
+// The low n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Sets the infinities and NaN of a pair to 0; whether there was one.
+template <bool BF>
+__device__ __forceinline__ bool clear_nonfinite(uint32_t &x) {
+    constexpr uint32_t e = BF ? 0x7f80u : 0x7c00u;
+    const bool lo = (x & e) == e, hi = ((x >> 16) & e) == e;
+    if (lo) x &= 0xffff0000u;
+    if (hi) x &= 0x0000ffffu;
+    return lo || hi;
+}
+
+enum { PAIR = 0, ALTERNATE = 1, OWN = 2 };  // shared parts: two query tiles, or one; own parts
+
+template <int D, bool BF, int MODE>
 __global__ void __launch_bounds__(CTHREADS, 1)
     k_prefix_tc(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
     using T = TcTile<D>;
@@ -108,6 +132,8 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     const uint32_t full = smem_addr(bars), empty = full + 8 * CSLOTS, sfull = empty + 8 * CSLOTS, phalf = sfull + 16,
                    pready = phalf + 16, ofull = pready + 16, qready = ofull + 16;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * CSLOTS + 9);
+    volatile int *s_odd = reinterpret_cast<int *>(s_tmem + 2);  // [2]: a stream has set values of V to 0
+    int32_t *s_par = reinterpret_cast<int32_t *>(s_tmem + 4);   // [HQ_MAX_M]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -132,30 +158,52 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
 
+    // which part this block is; nothing to do (ntiles 0) where no row uses it
     int unit = blockIdx.x;
     const int hk = unit % a.Hkv;
     unit /= a.Hkv;
-    const int rt = unit % pl.ptiles, split = unit / pl.ptiles;
-    const int k0 = split * pl.pchunk, k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
-    const Seq seq = first_live(a);
-    const int ntiles = seq.live ? (k1 - k0) / CR : 0;  // no row of the batch uses this part: nothing to do
-    const int nrows = a.rows * a.G;
+    constexpr bool own = MODE == OWN, pair = MODE == PAIR;
+    int part, row0, nrows, first = 0, k0, k1, tree0 = 0x7fffffff, nodes = 0, slot = 0, ntiles = 0;
+    if (!own) {
+        part = unit / pl.ptiles;
+        row0 = (unit % pl.ptiles) * (pair ? 2 * CR : CR);
+        nrows = a.rows * a.G;
+        k0 = part * pl.pchunk;
+        k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
+        const Seq s = first_live(a);
+        slot = s.slot;
+        if (s.live) ntiles = (k1 - k0) / CR;
+    } else {
+        const int b = unit / (pl.ns * pl.stiles);
+        unit %= pl.ns * pl.stiles;
+        part = unit / pl.stiles;
+        row0 = (unit % pl.stiles) * CR;
+        const Seq s = seq_of(a, b);
+        first = s.first;
+        nodes = s.m;
+        nrows = s.m * a.G;
+        k0 = pl.s0 + part * pl.schunk;
+        k1 = s.len - k0 > pl.schunk ? k0 + pl.schunk : s.len;
+        slot = s.slot;
+        tree0 = s.len - s.m;
+        part += pl.np;
+        if (s.live && row0 < nrows && k0 < k1) ntiles = (k1 - k0 + CR - 1) / CR;
+    }
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax ---
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CREG_SOFTMAX));
-        const int w = warp >> 2, r = threadIdx.x & 127;               // stream, row of its tile
-        const int row = PAIR ? (2 * rt + w) * CR + r : rt * CR + r;   // row among all rows of this head
-        const int part = PAIR ? split : 2 * split + w;
-        const size_t at = ((size_t)part * a.rows + row / a.G) * a.Hq + hk * a.G + row % a.G;
-        const int n = PAIR ? ntiles : (ntiles - w + 1) / 2;
-        bool ok = true;
         if (ntiles > 0) {
+            const int w = warp >> 2, r = threadIdx.x & 127;  // stream, row of its tile
+            const int row = row0 + (pair ? w * CR : 0) + r;  // row among the part's
+            const size_t at = ((size_t)part * a.rows + first + row / a.G) * a.Hq + hk * a.G + row % a.G;
+            const int n = pair ? ntiles : (ntiles - w + 1) / 2;
+            bool ok = true;
             // the query rows, swizzled as the tensor core reads them
-            if (PAIR || w == 0) {
+            if (pair || w == 0) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(a.q) +
-                    (row < nrows ? (size_t)(row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
+                    (row < nrows ? (size_t)(first + row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
                 uint8_t *dst = s_q + w * T::BYTES;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
@@ -165,114 +213,260 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
-        }
-        const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-        const uint32_t tS = lane_base + w * 128, tO = lane_base + 256 + w * 128;
-        const float c = a.c_log2;
-        float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < n; ++j) {
-            if (ok) ok = mbar_wait_short(sfull + 8 * w, (uint32_t)(j & 1), a.err);
-            __syncwarp();
-            tc_fence_after();
-            float s[128];
-            // each quarter's maximum is taken while the next one is on its way
-            tmem_ld32(tS, s);
-            float mx[2] = {-INFINITY, -INFINITY};
+            // the tree nodes this row sees (without `parent`: a chain)
+            uint32_t anc[4] = {0u, 0u, 0u, 0u};
+            if (own && k1 > tree0) {
+                if (a.parent)
+                    for (int i = threadIdx.x; i < nodes; i += 256) s_par[i] = a.parent[first + i];
+                if (threadIdx.x < 2) s_odd[threadIdx.x] = 0;
+                named_barrier(1, 256);
+                if (row < nrows) {
+                    int cur = row / a.G;
+                    for (int step = 0; step < HQ_MAX_M; ++step) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld();
-                if (q < 3) tmem_ld32(tS + 32 * (q + 1), s + 32 * (q + 1));
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    mx[0] = max3(mx[0], s[32 * q + i], s[32 * q + i + 1]);
-                    mx[1] = max3(mx[1], s[32 * q + i + 2], s[32 * q + i + 3]);
+                        for (int i = 0; i < 4; ++i)
+                            if (cur >> 5 == i) anc[i] |= 1u << (cur & 31);
+                        const int p = cur == 0 ? -1 : a.parent ? s_par[cur] : cur - 1;
+                        if (p < 0 || p >= cur) break;
+                        cur = p;
+                    }
                 }
+                __syncwarp();
             }
-            const float top = fmaxf(mx[0], mx[1]);
-            if (j == 0) {
-                m = top;
-            } else {
-                const bool raise = (top - m) * c > LAZY;
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float mn = raise ? top : m;
-                    const float al = raise ? ex2((m - mn) * c) : 1.0f;
-                    m = mn;
-                    l *= al;
+            const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+            const uint32_t tS = lane_base + w * 128, tO = lane_base + 256 + w * 128;
+            const float c = a.c_log2;
+            float m = -INFINITY, l = 0.0f;
+            // Tile j of this stream.  Masked tiles are a code of their own: the
+            // masks in the common one cost a quarter of its speed.
+            auto step = [&](auto masked, int j) {
+                constexpr bool MASKED = decltype(masked)::value;
+                if (ok) ok = mbar_wait_short(sfull + 8 * w, (uint32_t)(j & 1), a.err);
+                __syncwarp();
+                tc_fence_after();
+                const int tile = pair ? j : 2 * j + w, p0 = k0 + tile * CR;
+                uint32_t sees[4];
+                if constexpr (MASKED) {
+                    // bit i: position p0 + i is before the tree, or a node this row
+                    // sees; and inside the part
+                    const int old = tree0 - p0, in = k1 - p0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t v = bits_below(old - 32 * i);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {  // word x of the nodes starts at bit old + 32 x
+                            const int sh = old + 32 * (x - i);
+                            if (sh >= 0 && sh < 32) v |= anc[x] << sh;
+                            if (sh < 0 && sh > -32) v |= anc[x] >> -sh;
+                        }
+                        sees[i] = v & bits_below(in - 32 * i);
+                    }
+                }
+                float s[128];
+                // each quarter's maximum is taken while the next one is on its way
+                tmem_ld32(tS, s);
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait_ld();
+                    if (q < 3) tmem_ld32(tS + 32 * (q + 1), s + 32 * (q + 1));
+                    if constexpr (MASKED)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[32 * q + i] = (sees[q] >> i) & 1u ? s[32 * q + i] : -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        mx[0] = max3(mx[0], s[32 * q + i], s[32 * q + i + 1]);
+                        mx[1] = max3(mx[1], s[32 * q + i + 2], s[32 * q + i + 3]);
+                    }
+                }
+                const float top = fmaxf(mx[0], mx[1]);
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool raise = (top - m) * c > LAZY;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float mn = raise ? top : m;
+                        const float al = raise ? ex2((m - mn) * c) : 1.0f;
+                        m = mn;
+                        l *= al;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            float o[32];
+                            uint32_t u[32];
+                            tmem_ld32(tO + 32 * i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * al);
+                            tmem_st32(tO + 32 * i, u);
+                        }
+                    }
+                }
+                if constexpr (MASKED) {
+                    // V from the tree on: finite, or set to 0 (see above)
+                    const int use = tile + (tile + 2 < ntiles ? tile + 2 : ntiles), st = use % CSLOTS;
+                    if (ok) ok = mbar_wait_short(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
+                    __syncwarp();
+                    const int lo = tree0 > p0 ? tree0 - p0 : 0;
+                    bool odd = false;
+                    for (int i = lo * (D / 8) + r; i < CR * (D / 8); i += CR) {
+                        const int vr = i / (D / 8), ch = i % (D / 8);
+                        uint4 *x = reinterpret_cast<uint4 *>(s_ring + st * T::BYTES + (ch >> 3) * T::BOX + swz128(vr, ch & 7));
+                        uint4 u = *x;
+                        if (clear_nonfinite<BF>(u.x) | clear_nonfinite<BF>(u.y) | clear_nonfinite<BF>(u.z) |
+                            clear_nonfinite<BF>(u.w)) {
+                            *x = u;
+                            odd = true;
+                        }
+                    }
+                    if (odd) {
+                        s_odd[w] = 1;
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
+                f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float x, y;
+                        f2_split(f2_fma(f2_make(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), cc, mm), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        sum[i & 1] = f2_add(sum[i & 1], f2_make(x, y));
+                        p[i] = pack16<BF>(x, y);
+                    }
+                    tmem_st32(tS + 32 * h, p);
+                    if (h == 0) {  // the product may start on the first half
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(phalf + 8 * w);
+                    }
+                }
+                float x0, x1, x2, x3;
+                f2_split(sum[0], x0, x1);
+                f2_split(sum[1], x2, x3);
+                l += (x0 + x1) + (x2 + x3);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready + 8 * w);
+            };
+            for (int j = 0; j < n; ++j) {
+                const int p0 = k0 + (pair ? j : 2 * j + w) * CR;
+                if (!own || (p0 + CR <= tree0 && p0 + CR <= k1))
+                    step(std::false_type{}, j);
+                else if constexpr (own)
+                    step(std::true_type{}, j);
+            }
+            // a stream's O is complete with its last product; both streams' where
+            // they are added up, through the ring that nothing reads any more
+            for (int x = 0; x < 2; ++x)
+                if (pair ? x == w : x < ntiles) {
+                    if (ok) ok = mbar_wait_short(ofull + 8 * x, 0u, a.err);
+                    __syncwarp();
+                }
+            tc_fence_after();
+            if (l == 0.0f) m = -INFINITY;  // no tile, or no finite score: adds nothing
+            float mb = m == -INFINITY ? -INFINITY : m * c;  // in base-2 units
+            float scale = 1.0f, other = 0.0f;
+            float *box = reinterpret_cast<float *>(s_ring);  // [D][128 rows], then m, l
+            bool odd = false;
+            if (own && k1 > tree0) {
+                if (w)
+                    named_barrier(3, 128);
+                else
+                    named_barrier(2, 128);
+                odd = s_odd[w] != 0;
+            }
+            // O of this thread's row, dimensions 32 i .. 32 i + 31, and what the
+            // masked tiles' non-finite values add to the rows that see them
+            auto load_o = [&](int i, float (&o)[32]) {
+                if (n > 0) {
+                    tmem_ld32(tO + 32 * i, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                }
+                if (!odd) return;
+                for (int t = 0; t < nodes; ++t) {
+                    const int p = tree0 + t;
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (t >> 5 == x) word = anc[x];
+                    if (!((word >> (t & 31)) & 1u) || p < k0 || p >= k1 || (((p - k0) / CR) & 1) != w) continue;
+                    const int page = a.table[(size_t)slot * a.max_pages + (p >> a.page_shift)];
+                    if (page < 0 || page >= a.n_pages) continue;
+                    const int ps = 1 << a.page_shift;
+                    const uint16_t *v = reinterpret_cast<const uint16_t *>(
+                                            a.pool + (size_t)a.v_plane * (size_t)a.plane_bytes +
+                                            (((size_t)page * a.Hkv + hk) * ps + (p & (ps - 1))) * (size_t)(2 * D)) +
+                                        32 * i;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        uint32_t one = v[e];
+                        const float f = BF ? __uint_as_float(one << 16) : __half2float(__ushort_as_half((unsigned short)one));
+                        if (clear_nonfinite<BF>(one)) o[e] += f;
+                    }
+                }
+                __syncwarp();
+            };
+            if (!pair) {
+                if (w == 1) {
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         float o[32];
-                        uint32_t u[32];
-                        tmem_ld32(tO + 32 * i, o);
-                        tmem_wait_ld();
+                        load_o(i, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * al);
-                        tmem_st32(tO + 32 * i, u);
+                        for (int e = 0; e < 32; ++e) box[(32 * i + e) * CR + r] = o[e];
                     }
+                    box[D * CR + r] = mb;
+                    box[(D + 1) * CR + r] = l;
+                }
+                named_barrier(1, 256);
+                if (w == 0) {
+                    const float mo = box[D * CR + r], lo = box[(D + 1) * CR + r];
+                    const float top = fmaxf(mb, mo), t = top == -INFINITY ? 0.0f : top;
+                    scale = ex2(mb - t);
+                    other = ex2(mo - t);
+                    l = scale * l + other * lo;
+                    mb = top;
                 }
             }
-            const float mc = m == -INFINITY ? 0.0f : m * c;
-            const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
-            f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
+            if (pair || w == 0) {
+                float4 *dst = reinterpret_cast<float4 *>(a.ws_o + at * D);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
+                for (int i = 0; i < D / 32; ++i) {
+                    float o[32];
+                    load_o(i, o);
+                    if (row < nrows) {
+                        if (!pair)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float x, y;
-                    f2_split(f2_fma(f2_make(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), cc, mm), x, y);
-                    x = ex2(x);
-                    y = ex2(y);
-                    sum[i & 1] = f2_add(sum[i & 1], f2_make(x, y));
-                    p[i] = pack16<BF>(x, y);
-                }
-                tmem_st32(tS + 32 * h, p);
-                if (h == 0) {  // the product may start on the first half
-                    tmem_wait_st();
-                    tc_fence_before();
+                            for (int e = 0; e < 32; ++e) o[e] = scale * o[e] + other * box[(32 * i + e) * CR + r];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(phalf + 8 * w);
                 }
+                if (row < nrows) *reinterpret_cast<float2 *>(a.ws_ml + at * 2) = make_float2(mb, l);
             }
-            float x0, x1, x2, x3;
-            f2_split(sum[0], x0, x1);
-            f2_split(sum[1], x2, x3);
-            l += (x0 + x1) + (x2 + x3);
-            tmem_wait_st();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pready + 8 * w);
         }
-        if (n > 0) {
-            if (ok) ok = mbar_wait_short(ofull + 8 * w, 0u, a.err);
-            __syncwarp();
-            tc_fence_after();
-        }
-        float4 *dst = reinterpret_cast<float4 *>(a.ws_o + at * D);
-        if (n > 0) {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float o[32];
-                tmem_ld32(tO + 32 * i, o);
-                tmem_wait_ld();
-                if (row < nrows)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-        }
-        // a stream without a tile (or without a finite score) adds nothing
-        if (row < nrows)
-            *reinterpret_cast<float2 *>(a.ws_ml + at * 2) =
-                make_float2(l == 0.0f ? -INFINITY : m == -INFINITY ? 0.0f : m * c, l);
-        tc_fence_before();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CREG_REST));
     }
     if (warp == 8) {
         // ---------------------------------------------------------- K, V ---
-        // the order in which the MMAs use them: PAIR K0 V0 K1 V1 ...; else
+        // the order in which the MMAs use them: pair K0 V0 K1 V1 ...; else
         // K0 K1 V0 K2 V1 K3 ...
-        const int32_t *row = a.table + (size_t)(seq.live ? seq.slot : 0) * a.max_pages;
+        const int32_t *row = a.table + (size_t)(ntiles > 0 ? slot : 0) * a.max_pages;
         int i = 0;
         bool ok = true;
         auto put = [&](int tile, int plane) {
@@ -288,7 +482,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             __syncwarp();
             ++i;
         };
-        if (PAIR) {
+        if constexpr (pair) {
             for (int t = 0; t < ntiles; ++t) {
                 put(t, a.k_plane);
                 put(t, a.v_plane);
@@ -320,7 +514,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             return st;
         };
         auto scores = [&](int w, int st) {  // S_w = Q K^T
-            const uint64_t q = dq + (uint64_t)((PAIR ? w : 0) * (T::BYTES / 16)), k = dk + (uint64_t)(st * (T::BYTES / 16));
+            const uint64_t q = dq + (uint64_t)((pair ? w : 0) * (T::BYTES / 16)), k = dk + (uint64_t)(st * (T::BYTES / 16));
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t o = (uint64_t)((ks >> 2) * (T::BOX / 16) + (ks & 3) * 2);
@@ -341,7 +535,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                                  j > 0 || ks > 0);
             }
         };
-        if (PAIR) {
+        if constexpr (pair) {
             int kst = next();
             scores(0, kst);
             scores(1, kst);
@@ -391,8 +585,8 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool BF, bool PAIR>
-cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+template <int D, bool BF, int MODE>
+cudaError_t launch_mode(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -400,26 +594,34 @@ cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMa
     int done = 0;
     e = cached_per_device(configured, dev, &done, [&](int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(k_prefix_tc<D, BF, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(k_prefix_tc<D, BF, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)TcTile<D>::SMEM);
     });
     if (e != cudaSuccess) return e;
-    const int splits = PAIR ? pl.np : pl.np / 2;
-    return launch_kernel(k_prefix_tc<D, BF, PAIR>, dim3((unsigned)(a.Hkv * pl.ptiles * splits)), dim3(CTHREADS),
-                         TcTile<D>::SMEM, pdl, s, a, pl, map);
+    const long long grid = a.Hkv * (MODE == OWN ? (long long)a.B * pl.ns * pl.stiles : (long long)pl.np * pl.ptiles);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_kernel(k_prefix_tc<D, BF, MODE>, dim3((unsigned)grid), dim3(CTHREADS), TcTile<D>::SMEM, pdl, s, a, pl,
+                         map);
+}
+
+template <int D, bool BF>
+cudaError_t launch_modes(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+    if (pl.tc_shared) {
+        const cudaError_t e = (long long)a.rows * a.G > CR ? launch_mode<D, BF, PAIR>(a, pl, map, pdl, s)
+                                                           : launch_mode<D, BF, ALTERNATE>(a, pl, map, pdl, s);
+        if (e != cudaSuccess) return e;
+        pdl = true;
+    }
+    return pl.tc_own ? launch_mode<D, BF, OWN>(a, pl, map, pdl, s) : cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_tc(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, int D, bool pdl,
                              cudaStream_t s) {
-    const bool bf = a.type == HQ_BF16, pair = (long long)a.rows * a.G > CR;
-    if (D == 128) {
-        if (pair) return bf ? launch_t<128, true, true>(a, pl, map, pdl, s) : launch_t<128, false, true>(a, pl, map, pdl, s);
-        return bf ? launch_t<128, true, false>(a, pl, map, pdl, s) : launch_t<128, false, false>(a, pl, map, pdl, s);
-    }
-    if (pair) return bf ? launch_t<64, true, true>(a, pl, map, pdl, s) : launch_t<64, false, true>(a, pl, map, pdl, s);
-    return bf ? launch_t<64, true, false>(a, pl, map, pdl, s) : launch_t<64, false, false>(a, pl, map, pdl, s);
+    const bool bf = a.type == HQ_BF16;
+    if (D == 128) return bf ? launch_modes<128, true>(a, pl, map, pdl, s) : launch_modes<128, false>(a, pl, map, pdl, s);
+    return bf ? launch_modes<64, true>(a, pl, map, pdl, s) : launch_modes<64, false>(a, pl, map, pdl, s);
 }
 
 }  // namespace hq

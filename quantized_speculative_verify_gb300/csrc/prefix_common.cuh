@@ -15,6 +15,7 @@ struct PrefixPlan {
     int np, pchunk;     // shared parts of a row, positions each
     int ns, schunk;     // own parts of a row, positions each
     int ptiles, stiles; // row tiles: all rows, one sequence's rows
+    int tc_shared, tc_own;  // which kind the tensor-memory kernel takes
 };
 
 // Tiled copy (dimension, row in page, head, page, plane) into shared memory.
@@ -102,7 +103,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, i
     return mbar_wait_bounded(bar, parity, err);
 }
 
-// Shared parts on the tensor-memory kernel (k_prefix_tc.cu).
+// The parts that the plan gives to the tensor-memory kernel (k_prefix_tc.cu).
 cudaError_t launch_prefix_tc(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, int D, bool pdl,
                              cudaStream_t s);
 

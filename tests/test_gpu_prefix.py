@@ -423,3 +423,51 @@ def test_inactive_sequences_among_many_rows():
     t.check(got)
     t.cache.lens.zero_()  # none left: the prefix has no table to be read through
     assert not t.run(max_len=700).any() and t.status == hq.HQ_OK
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 65504.0])
+@pytest.mark.parametrize("dtype,D,ps,shared,B", [(F16, 128, 16, 70, 3), (BF16, 64, 128, 700, 20), (F16, 128, 64, 1000, 9)])
+def test_what_no_row_sees_does_not_matter_to_large_trees(fill, dtype, D, ps, shared, B):
+    rows = [60] + spread(B - 1, 1, 60, 1)
+    lens = [shared + n + m for n, m in zip(spread(B, 0, 300, 2), rows)]
+    t = Batch(lens, rows, shared, 8, 2, D, ps, dtype, seed=10, fill=fill)
+    got = t.run()
+    assert t.status == hq.HQ_OK and bool(torch.isfinite(got.float()).all())
+    t.check(got)
+
+
+@pytest.mark.parametrize("dtype,m,Hq", [(F16, 100, 8), (BF16, 40, 2), (F16, 128, 2), (BF16, 13, 16)])
+def test_nonfinite_branches_of_large_trees_reach_only_their_own_rows(dtype, m, Hq):
+    rng = np.random.default_rng(m)
+    for node, plane, x in ((1, 1, float("nan")), (m // 2, 1, float("inf")), (3, 2, float("nan")), (m - 1, 1, float("-inf"))):
+        s = Batch([600 + m, 600], [m, 3], 560 if m % 2 else 100, Hq, 2, 128, 32, dtype, seed=m)
+        pos = 600 + node
+        s.cache.pool[plane, int(s.cache.table[0, pos // 32]), 1, pos % 32, 7] = x
+        got = s.run()
+        hit = [i for i in range(m) if pos in s.visible(0, i)]
+        free = {(0, i) for i in range(m) if i not in hit} | {(1, i) for i in range(3)}
+        assert hit and s.status == hq.HQ_OK
+        h = Hq // 2
+        s.check(got, rows=set(list(free)[:40]))
+        assert bool(torch.isfinite(got[:, :h].float()).all())
+        out = torch.tensor([i not in hit for i in range(m)], device=DEV)
+        assert bool(torch.isfinite(got[:m][out].float()).all())
+        for i in hit:
+            assert not torch.isfinite(got[i, h:, 7]).any()
+            if plane == 1:
+                assert bool(torch.isfinite(got[i, h:, :7].float()).all())
+
+
+@pytest.mark.parametrize("B,m,shared,own,Hq,Hkv,D,ps,dtype", [
+    (1, 33, 0, 0, 4, 4, 128, 16, F16), (2, 128, 0, 900, 8, 2, 128, 64, BF16), (50, 9, 600, 260, 8, 2, 64, 16, F16),
+    (4, 128, 2000, 5, 64, 2, 128, 128, BF16), (6, 40, 511, 128, 5, 5, 128, 32, F16), (3, 17, 512, 127, 16, 8, 64, 256, BF16),
+])
+def test_large_trees_match_64_bits(B, m, shared, own, Hq, Hkv, D, ps, dtype):
+    rows = [m] + spread(B - 1, 1, m, B)
+    lens = [shared + own + m] + [shared + x + r for x, r in zip(spread(B - 1, 0, own, B + 1), rows[1:])]
+    for tree in (True, False):
+        t = Batch(lens, rows, shared, Hq, Hkv, D, ps, dtype, seed=B + m, tree=tree)
+        got = t.run()
+        assert t.status == hq.HQ_OK
+        t.check(got)
+        assert torch.equal(got, t.run())
