@@ -8,6 +8,7 @@ libhq.so is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -167,8 +168,16 @@ def _ptr(t) -> int | None:
     raise TypeError(f"device memory expected, cannot pass {type(t).__name__} as a device pointer")
 
 
+# The current stream's handle without making a torch.cuda.Stream object of it:
+# 0.1 us instead of 3.7 us a call (Grace host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -479,6 +488,8 @@ def delta_commit(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: t
 
 
 # ---------------------------------------------------- a batch of requests ---
+# These are called once or more a layer, so their checks are written to cost a
+# few microseconds: messages are formatted only when they are raised.
 def _type(t) -> int:
     """The library's element type of a tensor (fp32 where there is none)."""
     if t is None:
@@ -493,6 +504,10 @@ def _rows(t, cols: int, what: str) -> int:
     """The distance in elements between the rows of a tensor whose last dimensions are `cols` contiguous elements."""
     if t is None:
         return cols
+    if t.is_contiguous():
+        if t.numel() != t.shape[0] * cols:
+            raise ValueError(f"{what}: rows of {cols} elements expected, got shape {tuple(t.shape)}")
+        return cols
     n = 1
     for d in range(t.dim() - 1, 0, -1):  # the dimensions that make up one row
         if t.shape[d] != 1 and t.stride(d) != n:
@@ -503,15 +518,20 @@ def _rows(t, cols: int, what: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else cols
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
 def _dense(t, dtype, shape, what: str) -> None:
     """A contiguous tensor of the given type and shape, or None."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what}: contiguous {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _shaped(t, shape, what: str) -> None:
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _room(t, need: int, what: str) -> None:
+    if t.numel() * t.element_size() < need:
+        raise ValueError(f"{what} is too small: {need} bytes needed")
 
 
 def hq_add_norm_quant(desc, x, x_type: int, ldx: int, residual, residual_out, r_type: int, ldr: int, weight, eps: float,
@@ -531,23 +551,30 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     bf16, rows any 16-byte-aligned distance apart; residual may be None (the
     norm of x alone) and any output may be None; residual_out may be residual
     itself.  weight fp32 [K]."""
-    M, K = x.shape
-    _need(K == desc.K, f"add_norm_quant: x has {K} features, the layer {desc.K}")
-    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (h, "h")):
-        _need(t is None or tuple(t.shape) == (M, K), f"add_norm_quant: {what} must be [{M}][{K}]")
+    shape = x.shape
+    M, K = shape
+    if K != desc.K:
+        raise ValueError(f"add_norm_quant: x has {K} features, the layer {desc.K}")
+    _shaped(residual, shape, "add_norm_quant: residual")
+    _shaped(residual_out, shape, "add_norm_quant: residual_out")
+    _shaped(h, shape, "add_norm_quant: h")
     _dense(weight, torch.float32, (K,), "add_norm_quant: weight")
-    _dense(qx, torch.int8, (M, K), "add_norm_quant: qx")
-    _dense(gsum, torch.int32, (M, K // desc.group), "add_norm_quant: gsum")
+    _dense(qx, torch.int8, shape, "add_norm_quant: qx")
     _dense(sx, torch.float32, (M,), "add_norm_quant: sx")
-    _need(qop is None or qop.numel() * qop.element_size() >= hq_act_operand_bytes(desc, M), "add_norm_quant: qop is too small")
+    if gsum is not None:
+        _dense(gsum, torch.int32, (M, K // desc.group), "add_norm_quant: gsum")
+    if qop is not None:
+        _room(qop, hq_act_operand_bytes(desc, M), "add_norm_quant: qop")
     r = residual if residual is not None else residual_out
-    if residual is not None and residual_out is not None:
-        _need(residual.dtype == residual_out.dtype and (M < 2 or residual.stride(0) == residual_out.stride(0)),
-              "add_norm_quant: residual and residual_out need the same type and stride")
-    hq_add_norm_quant(desc, x, _type(x), _rows(x, K, "x"), residual, residual_out, _type(r), _rows(r, K, "residual"),
-                      weight, eps, M, signs, h, _type(h), _rows(h, K, "h"), qx, gsum, qop, sx, flags, stream)
+    ldr = _rows(r, K, "residual")
+    if residual is not None and residual_out is not None and residual_out is not residual and (
+            residual.dtype != residual_out.dtype or _rows(residual_out, K, "residual_out") != ldr):
+        raise ValueError("add_norm_quant: residual and residual_out need the same type and stride")
+    hq_add_norm_quant(desc, x, _type(x), _rows(x, K, "x"), residual, residual_out, _type(r), ldr, weight, eps, M, signs,
+                      h, _type(h), _rows(h, K, "h"), qx, gsum, qop, sx, flags, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def hq_lora_workspace_bytes(M: int, r_max: int) -> int:
     return int(load().hq_lora_workspace_bytes(int(M), int(r_max)))
 
@@ -575,12 +602,14 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     _dense(scale, torch.float32, (n,), "lora_apply: scale")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.float32, device=x.device)
-    for t, what in ((base, "base"), (Y, "Y")):
-        _need(t is None or (tuple(t.shape) == (M, N) and t.dtype == torch.float32), f"lora_apply: {what} must be fp32 [{M}][{N}]")
+    _shaped(base, (M, N), "lora_apply: base")
+    _shaped(Y, (M, N), "lora_apply: Y")
+    if Y.dtype != torch.float32 or (base is not None and base.dtype != torch.float32):
+        raise ValueError("lora_apply: base and Y must be fp32")
     need = hq_lora_workspace_bytes(M, r)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _need(workspace.numel() * workspace.element_size() >= need, "lora_apply: the workspace is too small")
+    _room(workspace, need, "lora_apply: the workspace")
     hq_lora_apply(x, _type(x), _rows(x, K, "x"), M, K, N, A, B, _type(A), n, r, ids, ranks, scale, base,
                   _rows(base, N, "base"), Y, _rows(Y, N, "Y"), workspace, flags, stream)
     return Y
@@ -594,13 +623,17 @@ class PagedCache:
 
     def __init__(self, pool: torch.Tensor, ref: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
         planes, pages, heads, page_size, dim = pool.shape
-        _need(pool.dtype in (torch.float16, torch.bfloat16), f"PagedCache: fp16 or bf16 expected, got {pool.dtype}")
-        _need(pool[0].is_contiguous(), "PagedCache: the pages of a plane must be contiguous")
+        if pool.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"PagedCache: fp16 or bf16 expected, got {pool.dtype}")
+        if not pool[0].is_contiguous():
+            raise ValueError("PagedCache: the pages of a plane must be contiguous")
+        if table.dim() != 2:
+            raise ValueError("PagedCache: table must be [sequences][max_pages]")
         _dense(ref, torch.int32, (pages,), "PagedCache: ref")
-        _dense(table, torch.int32, tuple(table.shape), "PagedCache: table")
-        _need(table.dim() == 2, "PagedCache: table must be [sequences][max_pages]")
+        _dense(table, torch.int32, table.shape, "PagedCache: table")
         _dense(lens, torch.int32, (table.shape[0],), "PagedCache: lens")
         self.pool, self.ref, self.table, self.lens = pool, ref, table, lens
+        self.type = TYPES[pool.dtype]
         self.status = torch.zeros(4, dtype=torch.int32, device=pool.device)
         plane_bytes = (pool.stride(0) if planes > 1 else pool[0].numel()) * 2
         self.c = hq_pages(0, 0, 0, 0, 0, 0, plane_bytes, planes, pages, table.shape[0], table.shape[1], page_size, heads,
@@ -612,6 +645,7 @@ class PagedCache:
         for f, t in (("pool", pool), ("ref", ref), ("table", table), ("len", lens), ("status", self.status),
                      ("scratch", self.scratch)):
             setattr(self.c, f, _ptr(t))
+        self.heads, self.dim, self.n_seqs = heads, dim, table.shape[0]
 
     @classmethod
     def empty(cls, planes: int, pages: int, heads: int, page_size: int, dim: int, sequences: int, max_pages: int,
@@ -624,8 +658,8 @@ class PagedCache:
 
 def _list(t, n, what: str) -> int:
     """The length of an int32 list; n: the length it must have, if any."""
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n),
-          f"{what}: contiguous int32 [{'n' if n is None else n}] expected, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{what}: contiguous int32 [{'n' if n is None else n}] expected, got {t.dtype} {tuple(t.shape)}")
     return t.shape[0]
 
 
@@ -657,11 +691,12 @@ def pages_compact(cache: PagedCache, seqs: torch.Tensor, base: torch.Tensor, kee
     n = _list(seqs, None, "pages_compact: seqs")
     _list(base, n, "pages_compact: base")
     _list(n_keep, n, "pages_compact: n_keep")
-    _need(keep.dtype == torch.int32 and keep.dim() == 2 and keep.shape[0] == n and keep.shape[1] >= 1 and
-          (keep.shape[1] == 1 or keep.stride(1) == 1), f"pages_compact: keep must be int32 [{n}][1 or more]")
-    ld = keep.stride(0) if n > 1 else keep.shape[1]
-    _check(load().hq_pages_compact(cache.c, _ptr(seqs), _ptr(base), _ptr(keep), ld, keep.shape[1], _ptr(n_keep), n,
-                                   flags, _stream(stream)), "hq_pages_compact")
+    if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != n or keep.shape[1] < 1 or (
+            keep.shape[1] > 1 and keep.stride(1) != 1):
+        raise ValueError(f"pages_compact: keep must be int32 [{n}][1 or more]")
+    width = keep.shape[1]
+    _check(load().hq_pages_compact(cache.c, _ptr(seqs), _ptr(base), _ptr(keep), keep.stride(0) if n > 1 else width, width,
+                                   _ptr(n_keep), n, flags, _stream(stream)), "hq_pages_compact")
 
 
 def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: int = 0, stream=None) -> None:
@@ -674,16 +709,17 @@ def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: i
 def _batch(cache: PagedCache, rows: int, starts, max_rows: int, seqs, what: str) -> int:
     """The number of sequences of a batch of rows."""
     if starts is not None:
-        B = _list(starts, None, f"{what}: starts") - 1
-        _need(B >= 0, f"{what}: starts is empty")
+        B = _list(starts, None, what) - 1
+        if B < 0:
+            raise ValueError(f"{what}: starts is empty")
     elif seqs is not None:
         B = seqs.shape[0]
     else:
         B = rows // max_rows
     if seqs is not None:
-        _list(seqs, B, f"{what}: seqs")
-    else:
-        _need(0 <= B <= cache.c.n_seqs, f"{what}: {B} sequences, the cache has {cache.c.n_seqs}")
+        _list(seqs, B, what)
+    elif B > cache.n_seqs:
+        raise ValueError(f"{what}: {B} sequences, the cache has {cache.n_seqs}")
     return B
 
 
@@ -692,13 +728,14 @@ def pages_write(cache: PagedCache, k_plane: int, v_plane: int, k: torch.Tensor, 
     """Writes the newest rows of sequences (rows starts[b] .. starts[b + 1] of k
     and v [rows][heads][dim], fp32 or the cache's type) at the end of their
     positions (hq_pages_write); starts None: max_rows rows each."""
-    rows, c = k.shape[0], cache.c
-    _need(v.shape[0] == rows and v.dtype == k.dtype, "pages_write: k and v need the same rows and type")
-    B = _batch(cache, rows, starts, max_rows, seqs, "pages_write")
-    cols = c.heads * (c.row_bytes // 2)
-    _check(load().hq_pages_write(c, k_plane, v_plane, _ptr(k), _ptr(v), _type(k), _rows(k, cols, "k"),
-                                 _rows(v, cols, "v"), _type(cache.pool), _ptr(seqs), _ptr(starts), B, rows, max_rows,
-                                 flags, _stream(stream)), "hq_pages_write")
+    rows = k.shape[0]
+    if v.shape[0] != rows or v.dtype != k.dtype:
+        raise ValueError("pages_write: k and v need the same rows and type")
+    B = _batch(cache, rows, starts, max_rows, seqs, "pages_write: starts and seqs")
+    cols = cache.heads * cache.dim
+    _check(load().hq_pages_write(cache.c, k_plane, v_plane, _ptr(k), _ptr(v), _type(k), _rows(k, cols, "k"),
+                                 _rows(v, cols, "v"), cache.type, _ptr(seqs), _ptr(starts), B, rows, max_rows, flags,
+                                 _stream(stream)), "hq_pages_write")
 
 
 def pages_status(cache: PagedCache, stream=None) -> int:
@@ -706,6 +743,7 @@ def pages_status(cache: PagedCache, stream=None) -> int:
     return int(load().hq_pages_status(cache.c, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def hq_prefix_attention_workspace_bytes(B: int, rows: int, max_rows: int, Hq: int, Hkv: int, D: int) -> int:
     return int(load().hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, Hkv, D))
 
@@ -719,21 +757,21 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     rows each) are its newest positions, a draft tree with `parent` (int32
     [rows]; None: a chain).  max_len: at least every sequence's length.  out
     [rows][Hq][D] of the cache's type or fp32; workspace: zeroed once."""
-    rows, Hq, D = q.shape
-    c = cache.c
-    _need(D * 2 == c.row_bytes and q.dtype == cache.pool.dtype,
-          f"prefix_attention: q must be {cache.pool.dtype} [rows][heads][{c.row_bytes // 2}]")
-    B = _batch(cache, rows, starts, max_rows, seqs, "prefix_attention")
+    shape = q.shape
+    rows, Hq, D = shape
+    if D != cache.dim or q.dtype != cache.pool.dtype:
+        raise ValueError(f"prefix_attention: q must be {cache.pool.dtype} [rows][heads][{cache.dim}]")
+    B = _batch(cache, rows, starts, max_rows, seqs, "prefix_attention: starts and seqs")
     if parent is not None:
         _list(parent, rows, "prefix_attention: parent")
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=q.dtype, device=q.device)
-    _need(tuple(out.shape) == (rows, Hq, D), f"prefix_attention: out must be [{rows}][{Hq}][{D}]")
-    need = hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, c.heads, D)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    _shaped(out, shape, "prefix_attention: out")
+    need = hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, cache.heads, D)
     if workspace is None:
         workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
-    _need(workspace.numel() * workspace.element_size() >= need, "prefix_attention: the workspace is too small")
-    _check(load().hq_prefix_attention(c, k_plane, v_plane, _type(q), _ptr(q), _rows(q, Hq * D, "q"), _ptr(seqs),
+    _room(workspace, need, "prefix_attention: the workspace")
+    _check(load().hq_prefix_attention(cache.c, k_plane, v_plane, cache.type, _ptr(q), _rows(q, Hq * D, "q"), _ptr(seqs),
                                       _ptr(starts), B, rows, max_rows, _ptr(parent), Hq, shared, max_len, scale,
                                       _ptr(out), _type(out), _rows(out, Hq * D, "out"), _ptr(workspace), flags,
                                       _stream(stream)), "hq_prefix_attention")
