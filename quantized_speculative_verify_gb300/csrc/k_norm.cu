@@ -9,9 +9,14 @@
 // sum of squares and the largest |z| are reduced together, with one barrier,
 // where norming first and rotating after needs two.
 //
-// One thread block per row; a thread holds octets of 8 consecutive features
+// One thread block per row at a time; a thread holds octets of 8 consecutive features
 // (one 16-byte load of 16-bit values, two of fp32), so butterfly strides 1, 2
 // and 4 stay inside the thread and strides 8 and 16 are two lane exchanges.
+// With more rows than resident blocks a block takes several rows in turn: the
+// next row's loads are issued before the reduction of the current one, and
+// weight and signs stay in registers.  (One row per block left the memory idle
+// during the reductions: 8190 rows of 8192, all bf16, 232 us = 2.6 TB/s; the
+// loop: 154 us = 3.9 TB/s, then bound by issue slots.)
 // Everything is fp32 until the outputs: residual_out, h and the codes are
 // rounded once each.
 #include "act_common.cuh"
@@ -20,22 +25,36 @@
 namespace hq {
 namespace {
 
-// 8 consecutive values of a row of type `type` (uniform over the block).
-__device__ __forceinline__ void load8(const void *row, int type, int octet, float (&v)[8]) {
+// 8 consecutive values of a row of type `type` (uniform over the block) as
+// they lie in memory, and as floats.
+struct Raw {
+    uint4 u, v;  // v: fp32 only
+};
+__device__ __forceinline__ Raw load_raw(const void *row, int type, int octet) {
+    Raw r;
     if (type == HQ_F32) {
-        const float4 *p = static_cast<const float4 *>(row) + 2 * (size_t)octet;
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        const uint4 *p = static_cast<const uint4 *>(row) + 2 * (size_t)octet;
+        r.u = p[0];
+        r.v = p[1];
+    } else {
+        r.u = static_cast<const uint4 *>(row)[octet];
+        r.v = make_uint4(0, 0, 0, 0);
+    }
+    return r;
+}
+__device__ __forceinline__ void widen(const Raw &r, int type, float (&f)[8]) {
+    const uint32_t w[8] = {r.u.x, r.u.y, r.u.z, r.u.w, r.v.x, r.v.y, r.v.z, r.v.w};
+    if (type == HQ_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
         return;
     }
-    const uint4 u = static_cast<const uint4 *>(row)[octet];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = type == HQ_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i]))
+        const float2 x = type == HQ_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[i]))
                                         : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
     }
 }
 
@@ -66,9 +85,10 @@ __device__ __forceinline__ const void *row_of(const void *p, int type, int64_t l
 
 template <int V, int T>
 __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
-    __shared__ float s_sum[T / 32], s_max[T / 32];
+    __shared__ float s_sum[2][T / 32], s_max[2][T / 32];  // by the parity of the row's turn
     __shared__ int s_gs[MAX_K / 16];  // group sums of this row
-    const int row = blockIdx.x, MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+    int row = blockIdx.x;
+    const int MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
     const int K = a.K, G = a.G, n8 = K >> 3;
     const bool quant = a.sx != nullptr;
 
@@ -113,165 +133,195 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[j][i] = 0.0f;
         if (idx < n8) {
-            load8(a.weight, HQ_F32, idx, w[j]);
+            widen(load_raw(a.weight, HQ_F32, idx), HQ_F32, w[j]);
             if (quant) sg[j] = (__ldg(a.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu;
         }
     }
     pdl_wait();
     const bool need_gs = a.gsum != nullptr || (a.qop != nullptr && a.sums != 0);
-    if (need_gs)
-        for (int g = tid; g < ngk; g += T) s_gs[g] = 0;
-
-    const void *xr = row_of(a.x, a.x_type, a.ldx, row);
-    const void *rr = a.res ? row_of(a.res, a.r_type, a.ldr, row) : nullptr;
-    void *ro = a.res_out ? const_cast<void *>(row_of(a.res_out, a.r_type, a.ldr, row)) : nullptr;
-    float v[V][8];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-        if (idx >= n8) continue;
-        load8(xr, a.x_type, idx, v[j]);
-        if (rr) {
-            float r[8];
-            load8(rr, a.r_type, idx, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] += r[i];
-        }
-    }
-    pdl_launch_dependents();
-    float ss = 0.0f, amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-        if (ro && idx < n8) store8(ro, a.r_type, idx, v[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            ss = fmaf(v[j][i], v[j][i], ss);
-            v[j][i] *= w[j][i];
-        }
-    }
-    // z: the rotated w * s
-    float z[V][8];
-    if (quant) {
-        const float c = __int_as_float((int)HADAMARD_SCALE_BITS);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[j][i] = flip(v[j][i], (sg[j] >> i) & 1u);
-#pragma unroll
-            for (int st = 1; st <= 4; st <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if ((i & st) == 0) {
-                        const float p = z[j][i], q = z[j][i + st];
-                        z[j][i] = p + q;
-                        z[j][i + st] = p - q;
-                    }
-#pragma unroll
-            for (int lb = 1; lb <= 2; lb <<= 1) {
-                const bool up = (lane & lb) != 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[j][i] = bfly_x(z[j][i], lb, up);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[j][i] *= c;
-                amax = fmaxf(amax, fabsf(z[j][i]));
-            }
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    }
-    if (lane == 0) {
-        s_sum[tid >> 5] = ss;
-        s_max[tid >> 5] = amax;
-    }
-    __syncthreads();
-    ss = lane < T / 32 ? s_sum[lane] : 0.0f;
-    amax = lane < T / 32 ? s_max[lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    }
-    // an all-zero row with eps = 0 gives zeros; NaN and infinities reach sx and h
-    const float d = ss / (float)K + a.eps;
-    const float rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
-    if (a.h) {
-        void *hr = const_cast<void *>(row_of(a.h, a.h_type, a.ldh, row));
+    Raw xn[V], rn[V];  // the next row
+    auto fetch = [&](int r) {
+        const void *xr = row_of(a.x, a.x_type, a.ldx, r);
+        const void *rr = a.res ? row_of(a.res, a.r_type, a.ldr, r) : nullptr;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int idx = tid + j * T;
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[j][i] * rstd;
-            if (idx < n8) store8(hr, a.h_type, idx, y);
+            xn[j].u = xn[j].v = rn[j].u = rn[j].v = make_uint4(0, 0, 0, 0);
+            if (idx >= n8) continue;
+            xn[j] = load_raw(xr, a.x_type, idx);
+            if (rr) rn[j] = load_raw(rr, a.r_type, idx);
         }
-    }
-    if (!quant) return;
-    if (tid == 0) a.sx[row] = rstd * (amax / 127.0f);
-    const float inv = amax == 0.0f ? 0.0f : 127.0f / amax;
-
-    int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
-    const int width = G / 8 < 32 ? G / 8 : 32;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-        int q[8], gs = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            q[i] = idx < n8 ? min(127, max(-127, __float2int_rn(z[j][i] * inv))) : 0;
-            gs += q[i];
+    };
+    constexpr bool AHEAD = V == 1;  // more octets a thread leave no registers for the next row
+    for (int turn = 0; row < a.M; ++turn, row += MT) {
+        if (need_gs) {
+            if (turn) __syncthreads();  // the last row's sums have been read
+            for (int g = tid; g < ngk; g += T) s_gs[g] = 0;
         }
-        if (qr && idx < n8) {
-            uint32_t lo = 0, hi = 0;
+        if (!AHEAD || turn == 0) fetch(row);
+        void *ro = a.res_out ? const_cast<void *>(row_of(a.res_out, a.r_type, a.ldr, row)) : nullptr;
+        float v[V][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo |= (uint32_t)(q[i] & 255) << (8 * i);
-                hi |= (uint32_t)(q[i + 4] & 255) << (8 * i);
+        for (int j = 0; j < V; ++j) {
+            float r[8];
+            widen(xn[j], a.x_type, v[j]);
+            widen(rn[j], a.r_type, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+        }
+        if (AHEAD && row + MT < a.M) fetch(row + MT);
+        pdl_launch_dependents();
+        float ss = 0.0f, amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int idx = tid + j * T;
+            if (ro && idx < n8) store8(ro, a.r_type, idx, v[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                ss = fmaf(v[j][i], v[j][i], ss);
+                v[j][i] *= w[j][i];
             }
-            reinterpret_cast<uint2 *>(qr)[idx] = make_uint2(lo, hi);
         }
-        if (a.qop && idx < n8pad) {
-            uint4 c16 = make_uint4(0, 0, 0, 0);
-            uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-            if (a.e4) {
-                digits4(q[0], q[1], q[2], q[3], lo.x, hi.x);
-                digits4(q[4], q[5], q[6], q[7], lo.y, hi.y);
-            } else {
-                uint32_t h[4];
+        // z: the rotated w * s
+        float z[V][8];
+        if (quant) {
+            const float c = __int_as_float((int)HADAMARD_SCALE_BITS);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[j][i] = flip(v[j][i], (sg[j] >> i) & 1u);
+#pragma unroll
+                for (int st = 1; st <= 4; st <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if ((i & st) == 0) {
+                            const float p = z[j][i], q = z[j][i + st];
+                            z[j][i] = p + q;
+                            z[j][i + st] = p - q;
+                        }
+#pragma unroll
+                for (int lb = 1; lb <= 2; lb <<= 1) {
+                    // lower lane a + b, upper lane a - b: one exact multiply-add
+                    const float sign = (lane & lb) != 0 ? -1.0f : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[j][i] = fmaf(sign, z[j][i], __shfl_xor_sync(0xffffffffu, z[j][i], lb));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    z[j][i] *= c;
+                    amax = fmaxf(amax, fabsf(z[j][i]));
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        }
+        if (lane == 0) {
+            s_sum[turn & 1][tid >> 5] = ss;
+            s_max[turn & 1][tid >> 5] = amax;
+        }
+        __syncthreads();
+        ss = lane < T / 32 ? s_sum[turn & 1][lane] : 0.0f;
+        amax = lane < T / 32 ? s_max[turn & 1][lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        }
+        // an all-zero row with eps = 0 gives zeros; NaN and infinities reach sx and h
+        const float d = ss / (float)K + a.eps;
+        const float rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
+        if (a.h) {
+            void *hr = const_cast<void *>(row_of(a.h, a.h_type, a.ldh, row));
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int idx = tid + j * T;
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = v[j][i] * rstd;
+                if (idx < n8) store8(hr, a.h_type, idx, y);
+            }
+        }
+        if (!quant) continue;
+        if (tid == 0) a.sx[row] = rstd * (amax / 127.0f);
+        const float inv = amax == 0.0f ? 0.0f : 127.0f / amax;
+
+        int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
+        const int width = G / 8 < 32 ? G / 8 : 32;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int idx = tid + j * T;
+            int q[8], gs = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // |z| <= amax: the product rounds to at most 127 (NaN to 0)
+                q[i] = idx < n8 ? __float2int_rn(z[j][i] * inv) : 0;
+                gs += q[i];
+            }
+            if (qr && idx < n8) {
+                uint32_t lo = 0, hi = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const __half2 p = __halves2half2(__int2half_rn(q[2 * i]), __int2half_rn(q[2 * i + 1]));
-                    h[i] = *reinterpret_cast<const uint32_t *>(&p);
+                    lo |= (uint32_t)(q[i] & 255) << (8 * i);
+                    hi |= (uint32_t)(q[i + 4] & 255) << (8 * i);
                 }
-                c16 = make_uint4(h[0], h[1], h[2], h[3]);
+                reinterpret_cast<uint2 *>(qr)[idx] = make_uint2(lo, hi);
             }
-            put(idx, c16, lo, hi);
+            if (a.qop && idx < n8pad) {
+                uint4 c16 = make_uint4(0, 0, 0, 0);
+                uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
+                if (a.e4) {
+                    digits4(q[0], q[1], q[2], q[3], lo.x, hi.x);
+                    digits4(q[4], q[5], q[6], q[7], lo.y, hi.y);
+                } else {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 p = __halves2half2(__int2half_rn(q[2 * i]), __int2half_rn(q[2 * i + 1]));
+                        h[i] = *reinterpret_cast<const uint32_t *>(&p);
+                    }
+                    c16 = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                put(idx, c16, lo, hi);
+            }
+            // a group's G / 8 threads are consecutive lanes (G = 16: two lanes)
+            if (need_gs) {
+                for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
+                if (idx < n8 && (lane & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / G], gs);
+            }
         }
-        // a group's G / 8 threads are consecutive lanes (G = 16: two lanes)
-        if (need_gs) {
-            for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
-            if (idx < n8 && (lane & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / G], gs);
+        if (!need_gs) continue;
+        __syncthreads();
+        for (int g = tid; g < ngp; g += T) {
+            const int v2 = g < ngk ? s_gs[g] : 0;
+            if (a.gsum && g < ngk) a.gsum[(size_t)row * ngk + g] = v2;
+            if (a.qop && a.sums) put_sum(g, (float)v2);
         }
-    }
-    if (!need_gs) return;
-    __syncthreads();
-    for (int g = tid; g < ngp; g += T) {
-        const int v2 = g < ngk ? s_gs[g] : 0;
-        if (a.gsum && g < ngk) a.gsum[(size_t)row * ngk + g] = v2;
-        if (a.qop && a.sums) put_sum(g, (float)v2);
     }
 }
 
 template <int V, int T>
 cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
-    return launch_kernel(k_add_norm_quant<V, T>, dim3((unsigned)(a.qop ? act_rows(a.M) : a.M)), dim3(T), 0, pdl, s, a);
+    int grid = a.M;
+    if (a.qop) {
+        grid = act_rows(a.M);  // one block per row of the operand, padding included
+    } else {
+        const int sms = device_sm_count();
+        if (sms <= 0) return cudaErrorNoDevice;
+        int dev = 0, per_sm = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        static std::atomic<int> resident[CACHE_DEVICES];
+        e = cached_per_device(resident, dev, &per_sm, [&](int *v) {
+            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k_add_norm_quant<V, T>, T, 0);
+        });
+        if (e != cudaSuccess) return e;
+        const int most = sms * (per_sm > 0 ? per_sm : 1);
+        if (grid > most) grid = most;
+    }
+    return launch_kernel(k_add_norm_quant<V, T>, dim3((unsigned)grid), dim3(T), 0, pdl, s, a);
 }
 
 }  // namespace
