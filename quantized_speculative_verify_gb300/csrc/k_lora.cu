@@ -7,21 +7,26 @@
 // thread) and takes every gridDim.y-th, so no list is built on the host, ids
 // may come in any order, and an item reads its adapter once.
 //
-// k_lora_shrink: a cluster of 8 thread blocks per item splits K; every warp
-// forms 16 x 64 partial sums with m16n8k16 MMAs straight from global memory.
-// The sum over k does not care in which order the k are taken as long as both
-// operands agree, so a lane's 16-byte loads of 8 consecutive k serve two MMA
-// steps as they are.  Warps add up in shared memory, the blocks through the
-// cluster's distributed shared memory, in a fixed order.
+// k_lora_shrink, items of three rows and more: a cluster of 8 thread blocks
+// splits K; every warp forms 16 x 64 partial sums with m16n8k16 MMAs straight
+// from global memory.  The sum over k does not care in which order the k are
+// taken as long as both operands agree, so a lane's 16-byte loads of 8
+// consecutive k serve two MMA steps as they are.  Warps add up in shared
+// memory, the blocks through the cluster's distributed shared memory, in a
+// fixed order.  Items of one or two rows (a token per request): the cluster's
+// blocks split the ranks instead, a warp takes one row of A over all of K with
+// multiply-adds, eight 512-byte loads in flight, and nothing is left to add up
+// but its lanes.  (With K split, the items of a row each waited for two cluster
+// barriers: 97 rows of rank 16 to 64, K = 12288: 45 us instead of 33.)
 // k_lora_expand: each warp forms 16 rows x 32 outputs with the same MMAs over
-// the rank and adds base.
-// Items of one or two rows (a token per request) use multiply-adds on the same
-// loads instead: an MMA takes 16 rows' time whatever it is given, and the
-// loads, not the products, should be what bounds them.
+// the rank, or with multiply-adds where the item has one or two rows, and adds
+// base.  (A thread per output column with t in shared memory, fp32 products
+// and the next item's loads in flight took 28 us instead of 21 for 97 rows and
+// 34 instead of 21 for 128 rows of 24576 outputs: its reads of t bound it.)
 //
 // Exactness: products of two 16-bit values are exact in fp32.  Where the
-// operand's type is not the adapter's (fp32 activations, and t, which is kept
-// in fp32), the value enters as three bf16 terms whose sum is the value
+// MMAs' operand is not of the adapter's type (fp32 activations, and t, which
+// is kept in fp32), the value enters as three bf16 terms whose sum is the value
 // (8 significant bits each), an fp16 weight as two.
 #include <cooperative_groups.h>
 
@@ -85,19 +90,25 @@ struct Items {
     int number[HQ_MAX_M];  // its number among the rows of its adapter
     int lead[HQ_MAX_M];    // the first row of each item
     int row[LR];           // the rows of the current item
+    int rank[HQ_MAX_M];    // of the row's adapter
+    float scale[HQ_MAX_M];
     int warp_count[HQ_MAX_M / 32];
     int n;
 };
 
-__device__ void find_items(Items &it, const int32_t *ids, int M, int n_adapters) {
+__device__ void find_items(Items &it, const LoraArgs &a) {
+    const int M = a.M;
     const int t = threadIdx.x;
     int id = -2;  // no row
     if (t < HQ_MAX_M) {
         if (t < M) {
-            id = ids[t];
-            if (id < 0 || id >= n_adapters) id = -1;
+            id = a.ids[t];
+            if (id < 0 || id >= a.n_adapters) id = -1;
         }
         it.id[t] = id;
+        int r = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;
+        it.rank[t] = r < 0 ? 0 : r > a.r_max ? a.r_max : r;
+        it.scale[t] = id >= 0 && a.scale ? a.scale[id] : 1.0f;
     }
     __syncthreads();
     bool lead = false;
@@ -129,8 +140,8 @@ __device__ void find_items(Items &it, const int32_t *ids, int M, int n_adapters)
     __syncthreads();
 }
 
-// The rows of item i into it.row; their number.  (The block has finished with
-// the item before: the barrier comes first.)
+// The rows of item i into it.row; their number.  (The barriers also
+// separate the block's work on the items before and after.)
 __device__ int item_rows(Items &it, int i, int M) {
     const int t = threadIdx.x, lead = it.lead[i], id = it.id[lead], part = it.number[lead] / LR;
     const bool mine = t < M && t < HQ_MAX_M && it.id[t] == id && it.number[t] / LR == part;
@@ -138,11 +149,6 @@ __device__ int item_rows(Items &it, int i, int M) {
     if (mine) it.row[it.number[t] % LR] = t;
     __syncthreads();
     return n;
-}
-
-__device__ __forceinline__ int rank_of(const LoraArgs &a, int id) {
-    const int r = a.ranks ? a.ranks[id] : a.r_max;
-    return r < 0 ? 0 : r > a.r_max ? a.r_max : r;
 }
 
 // 8 consecutive values of x as MMA words: one 16-byte load where the types
@@ -215,14 +221,102 @@ __device__ __forceinline__ void wide_w(const uint4 &u, float (&f)[8]) {
     }
 }
 
+// Items of one or two rows: t[row] for the 8 ranks of this block's share, one a
+// warp, over all of K, in chunks of 2048 k: x in shared memory as fp32 (the
+// first and last four of each eight apart, which keeps its 16-byte reads free
+// of bank conflicts), the next chunk's loads in flight during the products.
+template <bool WBF>
+__device__ __forceinline__ void shrink_few(const LoraArgs &a, const int *rows, int nr, int id, int rank, int r0, int part,
+                                           float *s_x, bool &waited) {
+    constexpr int NB = 8, CH = NB * 256;
+    static_assert(CH == LWARPS * 32 * 8, "a thread brings 8 values of x a chunk");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int j = part * (LG / LCL) + warp;  // this warp's rank of the group
+    const bool live = j < rank;
+    const int xb = type_bytes(a.x_type);
+    const uint8_t *xr[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        xr[m] = static_cast<const uint8_t *>(a.x) + (size_t)rows[m < nr ? m : 0] * (size_t)a.ldx * xb;
+    const uint8_t *Ar = static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + (live ? j : 0)) * (size_t)a.K * 2;
+    uint4 b[NB];
+    float x[2][8];
+    auto load_b = [&](int k0) {
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+            const int k = k0 + h * 256 + lane * 8;
+            b[h] = live && k < a.K ? *reinterpret_cast<const uint4 *>(Ar + (size_t)k * 2) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto load_x = [&](int k0) {
+        const int k = k0 + tid * 8;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[m][e] = 0.0f;
+            if (m < nr && k < a.K) wide8(xr[m] + (size_t)k * xb, a.x_type, x[m]);
+        }
+    };
+    load_b(0);
+    if (!waited) {
+        pdl_wait();
+        waited = true;
+    }
+    load_x(0);
+    float sum[2][4] = {};
+    for (int k0 = 0; k0 < a.K; k0 += CH) {
+        __syncthreads();  // the chunk before has been used
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float4 *>(s_x + (m * 2 + h) * (CH / 2) + tid * 4) =
+                    make_float4(x[m][4 * h], x[m][4 * h + 1], x[m][4 * h + 2], x[m][4 * h + 3]);
+        __syncthreads();
+        uint4 c[NB];
+#pragma unroll
+        for (int h = 0; h < NB; ++h) c[h] = b[h];
+        if (k0 + CH < a.K) {
+            load_b(k0 + CH);
+            load_x(k0 + CH);
+        }
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+            float w[8];
+            wide_w<WBF>(c[h], w);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (m == 1 && nr == 1) break;
+                const float4 u = *reinterpret_cast<const float4 *>(s_x + m * CH + (h * 32 + lane) * 4);
+                const float4 v = *reinterpret_cast<const float4 *>(s_x + m * CH + CH / 2 + (h * 32 + lane) * 4);
+                sum[m][0] = fmaf(w[0], u.x, sum[m][0]);
+                sum[m][1] = fmaf(w[1], u.y, sum[m][1]);
+                sum[m][2] = fmaf(w[2], u.z, sum[m][2]);
+                sum[m][3] = fmaf(w[3], u.w, sum[m][3]);
+                sum[m][0] = fmaf(w[4], v.x, sum[m][0]);
+                sum[m][1] = fmaf(w[5], v.y, sum[m][1]);
+                sum[m][2] = fmaf(w[6], v.z, sum[m][2]);
+                sum[m][3] = fmaf(w[7], v.w, sum[m][3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float v = (sum[m][0] + sum[m][1]) + (sum[m][2] + sum[m][3]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0 && live && m < nr) a.t[(size_t)rows[m] * a.r_max + r0 + j] = v;
+    }
+}
+
 template <bool WBF, bool SAME>
-__global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32) k_lora_shrink(const LoraArgs a) {
+__global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_lora_shrink(const LoraArgs a) {
     __shared__ __align__(16) Items it;
-    __shared__ float s_part[LWARPS][LR][LG + 4];
+    __shared__ __align__(16) float s_part[LWARPS][LR][LG + 4];
     cg::cluster_group cluster = cg::this_cluster();
     const int part = blockIdx.x, r0 = blockIdx.z * LG;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    find_items(it, a.ids, a.M, a.n_adapters);
+    find_items(it, a);
     pdl_launch_dependents();
     const int xb = type_bytes(a.x_type);
     const int units = (a.K + 31) / 32;
@@ -230,120 +324,74 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32) k_lor
     bool waited = false;
     for (int i = blockIdx.y; i < it.n; i += gridDim.y) {  // the same for the whole cluster
         const int id = it.id[it.lead[i]];
-        const int rank = id < 0 ? 0 : rank_of(a, id) - r0;
+        const int rank = it.rank[it.lead[i]] - r0;
         if (rank <= 0) continue;
         const int nr = item_rows(it, i, a.M);
+        const int *rows = it.row;
+        if (nr <= 2) {  // the blocks of such items do not meet
+            if (part * (LG / LCL) < rank) shrink_few<WBF>(a, rows, nr, id, rank, r0, part, &s_part[0][0][0], waited);
+            continue;
+        }
         const int nt = rank >= LG ? LG / 8 : (rank + 7) / 8;
         const uint8_t *Aw = static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + g) * (size_t)a.K * 2;
-        const uint8_t *xA = static_cast<const uint8_t *>(a.x) + (size_t)it.row[g < nr ? g : 0] * (size_t)a.ldx * xb;
-        const uint8_t *xB = static_cast<const uint8_t *>(a.x) + (size_t)it.row[g + 8 < nr ? g + 8 : 0] * (size_t)a.ldx * xb;
+        const uint8_t *xA = static_cast<const uint8_t *>(a.x) + (size_t)rows[g < nr ? g : 0] * (size_t)a.ldx * xb;
+        const uint8_t *xB = static_cast<const uint8_t *>(a.x) + (size_t)rows[g + 8 < nr ? g + 8 : 0] * (size_t)a.ldx * xb;
         float acc[LG / 8][4];
 #pragma unroll
         for (int j = 0; j < LG / 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-        if (nr <= 2) {
-            // lane (g, t4): ranks 8 j + g, k = 8 t4 .. 8 t4 + 7 of each unit
-            const uint8_t *x0 = static_cast<const uint8_t *>(a.x) + (size_t)it.row[0] * (size_t)a.ldx * xb;
-            const uint8_t *x1 = static_cast<const uint8_t *>(a.x) + (size_t)it.row[nr - 1] * (size_t)a.ldx * xb;
-            for (int u = u0 + warp; u < u1; u += LWARPS) {
-                const int k = u * 32 + t4 * 8;
-                const bool live = k < a.K;
-                uint4 b[LG / 8];
+        constexpr int NX = SAME ? 1 : 3;
+        for (int u = u0 + warp; u < u1; u += LWARPS) {
+            const int k = u * 32 + t4 * 8;
+            const bool live = k < a.K;
+            uint4 b[LG / 8];
 #pragma unroll
-                for (int j = 0; j < LG / 8; ++j)
-                    b[j] = j < nt && live && j * 8 + g < rank
-                               ? *reinterpret_cast<const uint4 *>(Aw + ((size_t)j * 8 * a.K + k) * 2)
-                               : make_uint4(0, 0, 0, 0);
-                if (!waited) {
-                    pdl_wait();
-                    waited = true;
-                }
-                float x[2][8] = {};
-                if (live) {
-                    wide8(x0 + (size_t)k * xb, a.x_type, x[0]);
-                    if (nr == 2) wide8(x1 + (size_t)k * xb, a.x_type, x[1]);
-                }
-#pragma unroll
-                for (int j = 0; j < LG / 8; ++j) {
-                    if (j >= nt) break;
-                    float w[8];
-                    wide_w<WBF>(b[j], w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[j][e & 1] = fmaf(w[e], x[0][e], acc[j][e & 1]);
-                    if (nr == 2)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[j][2 + (e & 1)] = fmaf(w[e], x[1][e], acc[j][2 + (e & 1)]);
-                }
-            }
+            for (int j = 0; j < LG / 8; ++j)
+                b[j] = j < nt && live && j * 8 + g < rank
+                           ? *reinterpret_cast<const uint4 *>(Aw + ((size_t)j * 8 * a.K + k) * 2)
+                           : make_uint4(0, 0, 0, 0);
             if (!waited) {
                 pdl_wait();
                 waited = true;
             }
+            uint32_t p[NX][4], q[NX][4];
+            load_x<SAME>(a, xA, k, live && g < nr, p);
+            load_x<SAME>(a, xB, k, live && g + 8 < nr, q);
 #pragma unroll
             for (int j = 0; j < LG / 8; ++j) {
                 if (j >= nt) break;
+                const uint32_t w[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    float v = acc[j][2 * m] + acc[j][2 * m + 1];
-                    v += __shfl_xor_sync(0xffffffffu, v, 1);
-                    v += __shfl_xor_sync(0xffffffffu, v, 2);
-                    if (t4 == 0) s_part[warp][m][j * 8 + g] = v;
-                }
-            }
-        } else {
-            constexpr int NX = SAME ? 1 : 3;
-            for (int u = u0 + warp; u < u1; u += LWARPS) {
-                const int k = u * 32 + t4 * 8;
-                const bool live = k < a.K;
-                uint4 b[LG / 8];
+                for (int st = 0; st < 2; ++st)
 #pragma unroll
-                for (int j = 0; j < LG / 8; ++j)
-                    b[j] = j < nt && live && j * 8 + g < rank
-                               ? *reinterpret_cast<const uint4 *>(Aw + ((size_t)j * 8 * a.K + k) * 2)
-                               : make_uint4(0, 0, 0, 0);
-                if (!waited) {
-                    pdl_wait();
-                    waited = true;
-                }
-                uint32_t p[NX][4], q[NX][4];
-                load_x<SAME>(a, xA, k, live && g < nr, p);
-                load_x<SAME>(a, xB, k, live && g + 8 < nr, q);
-#pragma unroll
-                for (int j = 0; j < LG / 8; ++j) {
-                    if (j >= nt) break;
-                    const uint32_t w[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
-#pragma unroll
-                    for (int st = 0; st < 2; ++st)
-#pragma unroll
-                        for (int x = 0; x < NX; ++x) {
-                            const uint32_t x4[4] = {p[x][2 * st], q[x][2 * st], p[x][2 * st + 1], q[x][2 * st + 1]};
-                            if constexpr (SAME || WBF) {
-                                mma16<WBF>(acc[j], x4, w[2 * st], w[2 * st + 1]);
-                            } else {
-                                uint32_t h0[2], h1[2];
-                                split_half(w[2 * st], h0);
-                                split_half(w[2 * st + 1], h1);
-                                mma16<true>(acc[j], x4, h0[0], h1[0]);
-                                mma16<true>(acc[j], x4, h0[1], h1[1]);
-                            }
+                    for (int x = 0; x < NX; ++x) {
+                        const uint32_t x4[4] = {p[x][2 * st], q[x][2 * st], p[x][2 * st + 1], q[x][2 * st + 1]};
+                        if constexpr (SAME || WBF) {
+                            mma16<WBF>(acc[j], x4, w[2 * st], w[2 * st + 1]);
+                        } else {
+                            uint32_t h0[2], h1[2];
+                            split_half(w[2 * st], h0);
+                            split_half(w[2 * st + 1], h1);
+                            mma16<true>(acc[j], x4, h0[0], h1[0]);
+                            mma16<true>(acc[j], x4, h0[1], h1[1]);
                         }
-                }
+                    }
             }
-            if (!waited) {
-                pdl_wait();
-                waited = true;
-            }
+        }
+        if (!waited) {
+            pdl_wait();
+            waited = true;
+        }
 #pragma unroll
-            for (int j = 0; j < LG / 8; ++j) {
-                if (j >= nt) break;
-                float *d = &s_part[warp][g][j * 8 + 2 * t4];
-                d[0] = acc[j][0];
-                d[1] = acc[j][1];
-                float *e = &s_part[warp][g + 8][j * 8 + 2 * t4];
-                e[0] = acc[j][2];
-                e[1] = acc[j][3];
-            }
+        for (int j = 0; j < LG / 8; ++j) {
+            if (j >= nt) break;
+            float *d = &s_part[warp][g][j * 8 + 2 * t4];
+            d[0] = acc[j][0];
+            d[1] = acc[j][1];
+            float *e = &s_part[warp][g + 8][j * 8 + 2 * t4];
+            e[0] = acc[j][2];
+            e[1] = acc[j][3];
         }
         __syncthreads();
         const int cols = nt * 8, elems = nr * cols;
@@ -361,7 +409,7 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32) k_lor
             float v = 0.0f;
 #pragma unroll
             for (int b = 0; b < LCL; ++b) v += *cluster.map_shared_rank(&s_part[0][m][c], b);
-            a.t[(size_t)it.row[m] * a.r_max + r0 + c] = v;
+            a.t[(size_t)rows[m] * a.r_max + r0 + c] = v;
         }
         cluster.sync();  // the others may still be reading this block's sums
     }
@@ -372,7 +420,7 @@ template <bool WBF>
 __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
     __shared__ __align__(16) Items it;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    find_items(it, a.ids, a.M, a.n_adapters);
+    find_items(it, a);
     pdl_launch_dependents();
     const long long n0 = (long long)blockIdx.x * LCOLS + warp * LNT * 8;
     // pairs of outputs where every row starts at an 8-byte boundary
@@ -383,9 +431,9 @@ __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
         const int id = it.id[it.lead[i]];
         if (id < 0 && a.base == a.Y) continue;  // no adapter, in place: nothing to change
         const int nr = item_rows(it, i, a.M);
-        const int rank = id < 0 ? 0 : rank_of(a, id);
+        const int rank = it.rank[it.lead[i]];
         const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
-        const float sc = id >= 0 && a.scale ? a.scale[id] : 1.0f;
+        const float sc = it.scale[it.lead[i]];
         float acc[LNT][4];
 #pragma unroll
         for (int j = 0; j < LNT; ++j)
@@ -536,8 +584,8 @@ cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s)
     const bool bf = w_type == HQ_BF16, same = a.x_type == w_type;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    // items in turn: enough clusters for four blocks an SM, enough blocks for
-    // eight (a block without an item costs a microsecond all the same)
+    // items in turn: clusters for four blocks an SM; the expand's blocks all at
+    // once (two an SM), each with its next item's loads in flight
     const int rg = (a.r_max + LG - 1) / LG, tiles = (int)(((long long)a.N + LCOLS - 1) / LCOLS);
     auto least = [&](long long want) { return (unsigned)(want < 1 ? 1 : want < a.M ? want : a.M); };
     const dim3 grid(LCL, least((4LL * sms / LCL + rg - 1) / rg), (unsigned)rg), block(LWARPS * 32);
