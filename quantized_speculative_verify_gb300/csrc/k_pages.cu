@@ -265,47 +265,145 @@ __global__ void __launch_bounds__(PT) k_pages_extend(const hq_pages c, const int
     pdl_launch_dependents();
 }
 
+// What k_pages_compact knows of its sequences, in shared memory.
+struct Compact {
+    int seq[PMAX], len[PMAX], base[PMAX], nk[PMAX], d0[PMAX], fresh[PMAX], first[PMAX], job[PMAX];
+    int warp[32];
+    int bad, most;
+};
+
+// The page passes of the compaction, G lanes a sequence (8 where every sequence
+// changes few pages, else 32).
+template <int G>
+struct PagePasses {
+    // lane of the group, its bits in the warp, sequences side by side
+    int lane, sub;
+    uint32_t mask;
+    __device__ PagePasses() {
+        const int l = threadIdx.x & 31;
+        lane = l & (G - 1);
+        sub = threadIdx.x / G;
+        mask = G == 32 ? ~0u : ((1u << (G & 31)) - 1u) << (l & ~(G - 1));
+    }
+    __device__ static bool moves(const Compact &s, int i) { return s.nk[i] >= 0 && s.d0[i] < s.nk[i]; }
+
+    // fresh pages of each sequence: those of its changed pages that are shared
+    __device__ void count(const hq_pages &c, Compact &s, int n, bool bad) const {
+        const int ps = c.page_size;
+        for (int i = sub; i < n; i += PT / G) {
+            int k = 0;
+            if (!bad && moves(s, i)) {
+                const int p1 = pages_of(s.base[i] + 1 + s.nk[i], ps);
+                const int32_t *row = c.table + (size_t)s.seq[i] * c.max_pages;
+                for (int p = (s.base[i] + 1 + s.d0[i]) / ps + lane; p < p1; p += G) {
+                    const int page = row[p];
+                    k += page_ok(c, page) && c.ref[page] > 1;
+                }
+            }
+#pragma unroll
+            for (int o = G / 2; o > 0; o >>= 1) k += __shfl_xor_sync(mask, k, o);
+            if (lane == 0) s.fresh[i] = k;
+        }
+    }
+    // Notes the old pages and the new ones.  Which pages are shared is decided
+    // for all before any count changes: a page held by two listed sequences is
+    // shared for both.
+    __device__ void note(const hq_pages &c, const Compact &s, int n) const {
+        const int ps = c.page_size;
+        const int32_t *list = list_of(c);
+        for (int i = sub; i < n; i += PT / G) {
+            if (s.nk[i] < 0) continue;
+            int32_t *row = c.table + (size_t)s.seq[i] * c.max_pages;
+            const int p1 = pages_of(s.base[i] + 1 + s.nk[i], ps), q1 = pages_of(s.len[i], ps);
+            const bool mv = s.job[i] >= 0;
+            const int lo = mv ? (s.base[i] + 1 + s.d0[i]) / ps : p1;
+            int32_t *o = mv ? old_table(c, s.job[i]) : nullptr;
+            int k = s.first[i];
+            for (int p0 = lo; p0 < q1; p0 += G) {
+                const int p = p0 + lane;
+                int page = -1;
+                if (p < q1) {
+                    page = row[p];
+                    if (!page_ok(c, page)) row[p] = page = -1;  // below -1 only -2 - (a page) from here on
+                    if (mv) o[p] = page;
+                }
+                const bool fresh = mv && p < p1 && page >= 0 && c.ref[page] > 1;
+                const uint32_t m = __ballot_sync(mask, fresh) & mask;
+                if (fresh) row[p] = -2 - list[k + __popc(m & ((1u << (threadIdx.x & 31)) - 1u))];
+                if (fresh && p == lo) jobs_of(c)[s.job[i]].p0 = lo * ps;
+                k += __popc(m);
+            }
+        }
+    }
+    __device__ void apply(const hq_pages &c, const Compact &s, int n) const {
+        const int ps = c.page_size;
+        for (int i = sub; i < n; i += PT / G) {
+            if (s.nk[i] < 0) continue;
+            int32_t *row = c.table + (size_t)s.seq[i] * c.max_pages;
+            const int end = s.base[i] + 1 + s.nk[i], p1 = pages_of(end, ps), q1 = pages_of(s.len[i], ps);
+            const bool mv = s.job[i] >= 0;
+            const int lo = mv ? (s.base[i] + 1 + s.d0[i]) / ps : p1;
+            const int32_t *o = mv ? old_table(c, s.job[i]) : row;
+            for (int p = lo + lane; p < q1; p += G) {
+                const int now = row[p];
+                int gone = -1;  // the page this sequence gives up here
+                if (now <= -2) {
+                    gone = o[p];
+                    row[p] = -2 - now;
+                    c.ref[-2 - now] = 1;
+                } else if (p >= p1) {
+                    gone = now;
+                    row[p] = -1;
+                }
+                if (gone >= 0) atomicSub(&c.ref[gone], 1);
+            }
+            if (lane == 0) c.len[s.seq[i]] = end;
+        }
+    }
+};
+
 __global__ void __cluster_dims__(PCL, 1, 1) __launch_bounds__(PT)
     k_pages_compact(const hq_pages c, const int32_t *seqs, const int32_t *base, const int32_t *keep, int ldkeep,
                     int max_keep, const int32_t *n_keep, int n) {
     __shared__ uint32_t s_bits[PSEQ / 32];
-    __shared__ int s_warp[32];
-    __shared__ int s_seq[PMAX], s_len[PMAX], s_base[PMAX], s_nk[PMAX], s_d0[PMAX], s_bad;
-    __shared__ int s_fresh[PMAX], s_first[PMAX], s_job[PMAX];
+    __shared__ Compact s;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, ps = c.page_size;
     for (int i = tid; i < PSEQ / 32; i += PT) s_bits[i] = 0;
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s.bad = s.most = 0;
     pdl_wait();
     __syncthreads();
+    int span = 0;
     if (tid < n) {
-        const int s = seqs[tid], b = base[tid], k = n_keep[tid];
+        const int q = seqs[tid], b = base[tid], k = n_keep[tid];
         int len = 0;
-        bool bad = !first_use(c, s, s_bits);
+        bool bad = !first_use(c, q, s_bits);
         if (!bad && k >= 0) {
-            len = c.len[s];
+            len = c.len[q];
             bad = !len_ok(c, len) || b < -1 || b >= len || k > max_keep || k > len - 1 - b;
         }
-        if (bad) s_bad = 1;
-        s_seq[tid] = s;
-        s_base[tid] = b;
-        s_nk[tid] = bad ? -1 : k;
-        s_len[tid] = len;
-        s_d0[tid] = k < 0 ? 0 : k;
+        if (bad) s.bad = 1;
+        s.seq[tid] = q;
+        s.base[tid] = b;
+        s.nk[tid] = bad ? -1 : k;
+        s.len[tid] = len;
+        s.d0[tid] = k < 0 ? 0 : k;
+        if (!bad && k >= 0) {
+            atomicMax(&s.most, k);
+            span = pages_of(len, ps) - (b + 1) / ps;  // pages it may look at
+        }
     }
-    __syncthreads();
+    const bool few = !__syncthreads_or(span > 16);
     // Every kept position: ascending, inside the sequence; d0 = the first that
     // moves.  The cluster's warps share the lists in runs of 32.
-    const int warp = (int)(blockIdx.x * PT + tid) >> 5, warps = PCL * PT / 32;
-    for (int i = 0; i < n; ++i) {
-        const int nk = s_nk[i], b = s_base[i], len = s_len[i];
+    const int warp = (int)(blockIdx.x * PT + tid) >> 5, warps = PCL * PT / 32, runs = (s.most + 31) / 32;
+    for (int w = warp; w < n * runs; w += warps) {
+        const int i = w / runs, d = (w % runs) * 32 + lane;
+        if (d >= s.nk[i]) continue;
         const int32_t *kp = keep + (size_t)i * ldkeep;
-        // start at another warp for each sequence: short lists spread over the warps
-        for (int d = ((warp + i) % warps) * 32 + lane; d < nk; d += warps * 32) {
-            const int k = kp[d], before = d ? kp[d - 1] : 0;
-            if (k <= before || k > len - 1 - b) s_bad = 1;
-            if (k != d + 1) atomicMin(&s_d0[i], d);
-        }
+        const int k = kp[d], before = d ? kp[d - 1] : 0;
+        if (k <= before || k > s.len[i] - 1 - s.base[i]) s.bad = 1;
+        if (k != d + 1) atomicMin(&s.d0[i], d);
     }
     cluster.sync();
     if (blockIdx.x != 0) {
@@ -314,41 +412,31 @@ __global__ void __cluster_dims__(PCL, 1, 1) __launch_bounds__(PT)
         return;
     }
     bool bad = false;
-    if (tid < PCL) bad = *cluster.map_shared_rank(&s_bad, tid) != 0;
+    if (tid < PCL) bad = *cluster.map_shared_rank(&s.bad, tid) != 0;
     if (tid < n) {
-        int d0 = s_d0[tid];
+        int d0 = s.d0[tid];
+#pragma unroll
         for (int r = 1; r < PCL; ++r) {
-            const int v = cluster.map_shared_rank(s_d0, r)[tid];
+            const int v = cluster.map_shared_rank(s.d0, r)[tid];
             d0 = v < d0 ? v : d0;
         }
-        s_d0[tid] = d0;
+        s.d0[tid] = d0;
     }
     bad = __syncthreads_or(bad);
     cluster.sync();
-    Job *jobs = jobs_of(c);
-    int32_t *list = list_of(c);
 
-    // fresh pages of each sequence: those of its changed pages that are shared
-    for (int i = tid >> 5; i < n; i += PT / 32) {
-        int count = 0;
-        if (!bad && s_nk[i] >= 0 && s_d0[i] < s_nk[i]) {
-            const int p1 = pages_of(s_base[i] + 1 + s_nk[i], ps);
-            const int32_t *row = c.table + (size_t)s_seq[i] * c.max_pages;
-            for (int p = (s_base[i] + 1 + s_d0[i]) / ps + lane; p < p1; p += 32) {
-                const int page = row[p];
-                count += page_ok(c, page) && c.ref[page] > 1;
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
-        if (lane == 0) s_fresh[i] = count;
-    }
+    const PagePasses<8> narrow;
+    const PagePasses<32> wide;
+    if (few)
+        narrow.count(c, s, n, bad);
+    else
+        wide.count(c, s, n, bad);
     __syncthreads();
     int first, job;
-    const int want = block_scan(tid < n ? s_fresh[tid] : 0, s_warp, first);
-    const bool moves = !bad && tid < n && s_nk[tid] >= 0 && s_d0[tid] < s_nk[tid];
-    const int njobs = block_scan(moves ? 1 : 0, s_warp, job);
-    const bool enough = !bad && find_free(c, want, list, s_warp);
+    const int want = block_scan(tid < n ? s.fresh[tid] : 0, s.warp, first);
+    const bool moves = !bad && tid < n && PagePasses<32>::moves(s, tid);
+    const int njobs = block_scan(moves ? 1 : 0, s.warp, job);
+    const bool enough = !bad && find_free(c, want, list_of(c), s.warp);
     if (tid == 0) {
         *jobs_count(c) = enough ? njobs : 0;
         if (!enough) set_status(c, bad ? HQ_ERR_INVALID_ARG : HQ_ERR_NO_PAGES);
@@ -358,63 +446,24 @@ __global__ void __cluster_dims__(PCL, 1, 1) __launch_bounds__(PT)
         return;
     }
     if (tid < n) {
-        s_first[tid] = first;
-        s_job[tid] = moves ? job : -1;
+        s.first[tid] = first;
+        s.job[tid] = moves ? job : -1;
         if (moves) {
-            const int from = s_base[tid] + 1 + s_d0[tid], end = s_base[tid] + 1 + s_nk[tid];
-            jobs[job] = Job{s_seq[tid], from, end, from, s_base[tid], s_len[tid],
-                            s_fresh[tid] == pages_of(end, ps) - from / ps, tid};
-        }
-    }
-    // Which pages are shared is decided for all before any count changes: a
-    // page held by two listed sequences is shared for both.
-    __syncthreads();
-    for (int i = tid >> 5; i < n; i += PT / 32) {
-        if (s_nk[i] < 0) continue;
-        int32_t *row = c.table + (size_t)s_seq[i] * c.max_pages;
-        const int p1 = pages_of(s_base[i] + 1 + s_nk[i], ps), q1 = pages_of(s_len[i], ps);
-        const bool mv = s_job[i] >= 0;
-        const int lo = mv ? (s_base[i] + 1 + s_d0[i]) / ps : p1;
-        int32_t *o = mv ? old_table(c, s_job[i]) : nullptr;
-        int k = s_first[i];
-        for (int p0 = lo; p0 < q1; p0 += 32) {
-            const int p = p0 + lane;
-            int page = -1;
-            if (p < q1) {
-                page = row[p];
-                if (!page_ok(c, page)) row[p] = page = -1;  // below -1 only -2 - (a page) from here on
-                if (mv) o[p] = page;
-            }
-            const bool fresh = mv && p < p1 && page >= 0 && c.ref[page] > 1;
-            const uint32_t m = __ballot_sync(0xffffffffu, fresh);
-            if (fresh) row[p] = -2 - list[k + __popc(m & ((1u << lane) - 1u))];
-            if (fresh && p == lo) jobs[s_job[i]].p0 = lo * ps;
-            k += __popc(m);
+            const int from = s.base[tid] + 1 + s.d0[tid], end = s.base[tid] + 1 + s.nk[tid];
+            jobs_of(c)[job] = Job{s.seq[tid], from, end, from, s.base[tid], s.len[tid],
+                                  s.fresh[tid] == pages_of(end, ps) - from / ps, tid};
         }
     }
     __syncthreads();
-    for (int i = tid >> 5; i < n; i += PT / 32) {
-        if (s_nk[i] < 0) continue;
-        int32_t *row = c.table + (size_t)s_seq[i] * c.max_pages;
-        const int end = s_base[i] + 1 + s_nk[i], p1 = pages_of(end, ps), q1 = pages_of(s_len[i], ps);
-        const bool mv = s_job[i] >= 0;
-        const int lo = mv ? (s_base[i] + 1 + s_d0[i]) / ps : p1;
-        const int32_t *o = mv ? old_table(c, s_job[i]) : row;
-        for (int p = lo + lane; p < q1; p += 32) {
-            const int now = row[p];
-            int gone = -1;  // the page this sequence gives up here
-            if (now <= -2) {
-                gone = o[p];
-                row[p] = -2 - now;
-                c.ref[-2 - now] = 1;
-            } else if (p >= p1) {
-                gone = now;
-                row[p] = -1;
-            }
-            if (gone >= 0) atomicSub(&c.ref[gone], 1);
-        }
-        if (lane == 0) c.len[s_seq[i]] = end;
-    }
+    if (few)
+        narrow.note(c, s, n);
+    else
+        wide.note(c, s, n);
+    __syncthreads();
+    if (few)
+        narrow.apply(c, s, n);
+    else
+        wide.apply(c, s, n);
     pdl_launch_dependents();
 }
 
