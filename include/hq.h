@@ -625,7 +625,10 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  *   out       out_type [rows][Hq][D], rows ldo elements apart, 16-byte aligned
  *             rows; out_type is `type` or HQ_F32
  *   workspace hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq,
- *             heads, D) bytes, 16-byte aligned, its first 16 bytes zeroed once
+ *             heads, D) bytes, 16-byte aligned, its first 16 bytes zeroed
+ *             once; the size grows with rows and max_rows and does not depend
+ *             on B or the lengths, so one workspace of the largest rows and
+ *             max_rows serves every call of these heads in turn
  * A row of an empty sequence (len 0), and a row that no sequence claims, is
  * zero.  A length that contradicts shared, m_b or max_len makes the
  * sequence's rows zero, a table entry outside [0, n_pages) makes its

@@ -88,7 +88,7 @@ struct PrefixArgs {
     int shared, max_len, type, out_type;
     float c_log2;  // scale * log2(e)
 };
-size_t prefix_workspace_bytes(int B, int rows, int Hq, int Hkv, int D);
+size_t prefix_workspace_bytes(int rows, int max_rows, int Hq, int Hkv, int D);
 cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s);
 
 #ifdef __CUDACC__

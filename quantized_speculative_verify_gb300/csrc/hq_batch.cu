@@ -227,7 +227,7 @@ size_t hq_prefix_attention_workspace_bytes(int32_t B, int32_t rows, int32_t max_
     if (B <= 0 || B > 65535 || rows <= 0 || max_rows <= 0 || max_rows > HQ_MAX_M || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0)
         return 0;
     if ((D != 64 && D != 128) || (long long)rows * Hq > (1 << 28)) return 0;
-    return hq::prefix_workspace_bytes(B, rows, Hq, Hkv, D);
+    return hq::prefix_workspace_bytes(rows, max_rows, Hq, Hkv, D);
 }
 
 int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32_t type, const void *q,

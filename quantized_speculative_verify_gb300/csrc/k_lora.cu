@@ -88,17 +88,42 @@ __device__ __forceinline__ void split_half(uint32_t w, uint32_t (&t)[2]) {
 struct Items {
     int id[HQ_MAX_M];      // the row's adapter, -1 for none
     int number[HQ_MAX_M];  // its number among the rows of its adapter
-    int lead[HQ_MAX_M];    // the first row of each item
-    int row[LR];           // the rows of the current item
+    int size[HQ_MAX_M];    // rows of its adapter
     int rank[HQ_MAX_M];    // of the row's adapter
     float scale[HQ_MAX_M];
+    int lead[HQ_MAX_M];    // the first row of each item
+    int rows[HQ_MAX_M];    // rows of each item
+    int mate[HQ_MAX_M];    // the second row of the item that a row leads
+    int unit0[HQ_MAX_M + 1];  // k_lora_shrink: the few-row items' shares before each item
+    int row[LR];           // the rows of the current item of three rows or more
     int warp_count[HQ_MAX_M / 32];
     int n;
 };
 
+// Sum over the first HQ_MAX_M threads before this one; `total` over all.
+__device__ int sum_below(Items &it, int v, int &total) {
+    const int t = threadIdx.x, lane = t & 31;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (t < HQ_MAX_M && lane == 31) it.warp_count[t >> 5] = x;
+    __syncthreads();
+    int below = x - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < HQ_MAX_M / 32; ++w) {
+        if (w < (t >> 5)) below += it.warp_count[w];
+        total += it.warp_count[w];
+    }
+    return below;
+}
+
 __device__ void find_items(Items &it, const LoraArgs &a) {
-    const int M = a.M;
-    const int t = threadIdx.x;
+    const int M = a.M, t = threadIdx.x;
     int id = -2;  // no row
     if (t < HQ_MAX_M) {
         if (t < M) {
@@ -113,29 +138,33 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
     __syncthreads();
     bool lead = false;
     if (t < HQ_MAX_M) {
-        int n = 0;
+        int n = 0, all = 0, last = 0;
         const int4 *v = reinterpret_cast<const int4 *>(it.id);
 #pragma unroll 8
         for (int j = 0; j < HQ_MAX_M / 4; ++j) {
-            const int4 x = v[j];
-            n += (x.x == id && 4 * j < t) + (x.y == id && 4 * j + 1 < t) + (x.z == id && 4 * j + 2 < t) +
-                 (x.w == id && 4 * j + 3 < t);
+            const int4 q = v[j];
+            const int x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool same = x[e] == id, before = same && 4 * j + e < t;
+                all += same;
+                n += before;
+                last = before ? 4 * j + e : last;
+            }
         }
         it.number[t] = n;
+        it.size[t] = all;
         lead = t < M && n % LR == 0;
+        if (t < M && n % LR == 1) it.mate[last] = t;
     }
-    const uint32_t b = __ballot_sync(0xffffffffu, lead);
-    if (t < HQ_MAX_M && (t & 31) == 0) it.warp_count[t >> 5] = __popc(b);
+    int total;
+    const int at = sum_below(it, lead ? 1 : 0, total);
+    if (lead) it.lead[at] = t;
+    if (t == 0) it.n = total;
     __syncthreads();
-    if (t < HQ_MAX_M) {
-        int at = __popc(b & ((1u << (t & 31)) - 1u));
-        for (int w = 0; w < (t >> 5); ++w) at += it.warp_count[w];
-        if (lead) it.lead[at] = t;
-    }
-    if (t == 0) {
-        int n = 0;
-        for (int w = 0; w < HQ_MAX_M / 32; ++w) n += it.warp_count[w];
-        it.n = n;
+    if (t < total) {
+        const int l = it.lead[t], left = it.size[l] - it.number[l];
+        it.rows[t] = left < LR ? left : LR;
     }
     __syncthreads();
 }
@@ -144,11 +173,10 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
 // separate the block's work on the items before and after.)
 __device__ int item_rows(Items &it, int i, int M) {
     const int t = threadIdx.x, lead = it.lead[i], id = it.id[lead], part = it.number[lead] / LR;
-    const bool mine = t < M && t < HQ_MAX_M && it.id[t] == id && it.number[t] / LR == part;
-    const int n = __syncthreads_count(mine);
-    if (mine) it.row[it.number[t] % LR] = t;
     __syncthreads();
-    return n;
+    if (t < M && t < HQ_MAX_M && it.id[t] == id && it.number[t] / LR == part) it.row[it.number[t] % LR] = t;
+    __syncthreads();
+    return it.rows[i];
 }
 
 // 8 consecutive values of x as MMA words: one 16-byte load where the types
@@ -226,8 +254,8 @@ __device__ __forceinline__ void wide_w(const uint4 &u, float (&f)[8]) {
 // first and last four of each eight apart, which keeps its 16-byte reads free
 // of bank conflicts), the next chunk's loads in flight during the products.
 template <bool WBF>
-__device__ __forceinline__ void shrink_few(const LoraArgs &a, const int *rows, int nr, int id, int rank, int r0, int part,
-                                           float *s_x, bool &waited) {
+__device__ __forceinline__ void shrink_few(const LoraArgs &a, int row0, int row1, int nr, int id, int rank, int r0,
+                                           int part, float *s_x, bool &waited) {
     constexpr int NB = 8, CH = NB * 256;
     static_assert(CH == LWARPS * 32 * 8, "a thread brings 8 values of x a chunk");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -237,7 +265,7 @@ __device__ __forceinline__ void shrink_few(const LoraArgs &a, const int *rows, i
     const uint8_t *xr[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
-        xr[m] = static_cast<const uint8_t *>(a.x) + (size_t)rows[m < nr ? m : 0] * (size_t)a.ldx * xb;
+        xr[m] = static_cast<const uint8_t *>(a.x) + (size_t)(m ? row1 : row0) * (size_t)a.ldx * xb;
     const uint8_t *Ar = static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + (live ? j : 0)) * (size_t)a.K * 2;
     uint4 b[NB];
     float x[2][8];
@@ -305,7 +333,7 @@ __device__ __forceinline__ void shrink_few(const LoraArgs &a, const int *rows, i
         float v = (sum[m][0] + sum[m][1]) + (sum[m][2] + sum[m][3]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0 && live && m < nr) a.t[(size_t)rows[m] * a.r_max + r0 + j] = v;
+        if (lane == 0 && live && m < nr) a.t[(size_t)(m ? row1 : row0) * a.r_max + r0 + j] = v;
     }
 }
 
@@ -322,16 +350,36 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_
     const int units = (a.K + 31) / 32;
     const int u0 = (int)((long long)units * part / LCL), u1 = (int)((long long)units * (part + 1) / LCL);
     bool waited = false;
+    {
+        // items of one or two rows: their shares of 8 ranks, over all blocks
+        int share = 0, shares;
+        if (tid < it.n && it.rows[tid] <= 2 && it.id[it.lead[tid]] >= 0) {
+            const int rank = it.rank[it.lead[tid]] - r0;
+            share = rank <= 0 ? 0 : rank >= LG ? LG / 8 : (rank + 7) / 8;
+        }
+        const int below = sum_below(it, share, shares);
+        if (tid < HQ_MAX_M) it.unit0[tid] = below;
+        if (tid == 0) it.unit0[HQ_MAX_M] = shares;
+        __syncthreads();
+        for (int u = part + LCL * (int)blockIdx.y; u < shares; u += LCL * gridDim.y) {
+            int lo = 0, hi = HQ_MAX_M;  // the last item that starts at or before u
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (it.unit0[mid] <= u) lo = mid;
+                else hi = mid;
+            }
+            const int lead = it.lead[lo], nr = it.rows[lo];
+            shrink_few<WBF>(a, lead, nr == 2 ? it.mate[lead] : lead, nr, it.id[lead], it.rank[lead] - r0, r0,
+                            u - it.unit0[lo], &s_part[0][0][0], waited);
+        }
+        __syncthreads();
+    }
     for (int i = blockIdx.y; i < it.n; i += gridDim.y) {  // the same for the whole cluster
         const int id = it.id[it.lead[i]];
         const int rank = it.rank[it.lead[i]] - r0;
-        if (rank <= 0) continue;
+        if (rank <= 0 || it.rows[i] <= 2) continue;
         const int nr = item_rows(it, i, a.M);
         const int *rows = it.row;
-        if (nr <= 2) {  // the blocks of such items do not meet
-            if (part * (LG / LCL) < rank) shrink_few<WBF>(a, rows, nr, id, rank, r0, part, &s_part[0][0][0], waited);
-            continue;
-        }
         const int nt = rank >= LG ? LG / 8 : (rank + 7) / 8;
         const uint8_t *Aw = static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + g) * (size_t)a.K * 2;
         const uint8_t *xA = static_cast<const uint8_t *>(a.x) + (size_t)rows[g < nr ? g : 0] * (size_t)a.ldx * xb;
@@ -417,7 +465,7 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_
 }
 
 template <bool WBF>
-__global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
+__global__ void __launch_bounds__(LWARPS * 32, 2) k_lora_expand(const LoraArgs a) {
     __shared__ __align__(16) Items it;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     find_items(it, a);
@@ -426,10 +474,100 @@ __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
     // pairs of outputs where every row starts at an 8-byte boundary
     const bool pairs = (a.N & 1) == 0 && (a.ldy & 1) == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 7) == 0 &&
                        (!a.base || ((a.ldb & 1) == 0 && (reinterpret_cast<uintptr_t>(a.base) & 7) == 0));
-    bool waited = false;
+    // Items of one or two rows first, the warps on their own: lane (g, t4) has
+    // the outputs 8 j + g and the ranks 8 t4 .. 8 t4 + 7 of each 32; the next
+    // item's row pieces of B are on their way during this one's products.
+    {
+        auto next_few = [&](int i) {
+            while (i < it.n && (it.rows[i] > 2 || (it.id[it.lead[i]] < 0 && a.base == a.Y))) i += gridDim.y;
+            return i;
+        };
+        auto load_b = [&](int i, int k0, uint4 (&b)[LNT]) {
+            const int id = it.id[it.lead[i]], k = k0 + t4 * 8, left = it.rank[it.lead[i]] - k;
+            const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
+#pragma unroll
+            for (int j = 0; j < LNT; ++j) {
+                const long long n = n0 + j * 8 + g;
+                b[j] = left > 0 && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
+                                           : make_uint4(0, 0, 0, 0);
+            }
+        };
+        int i = next_few(blockIdx.y);
+        uint4 next[2][LNT];
+        if (i < it.n) {
+            load_b(i, 0, next[0]);
+            load_b(i, 32, next[1]);
+        }
+        pdl_wait();
+        while (i < it.n) {
+            uint4 b[2][LNT];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < LNT; ++j) b[h][j] = next[h][j];
+            const int lead = it.lead[i], nr = it.rows[i], rank = it.rank[lead], cur = i;
+            const int row[2] = {lead, nr == 2 ? it.mate[lead] : lead};
+            const float sc = it.scale[lead];
+            i = next_few(i + gridDim.y);
+            if (i < it.n) {
+                load_b(i, 0, next[0]);
+                load_b(i, 32, next[1]);
+            }
+            const long long nw = n0 + t4 * 8 + g;  // the output this lane writes
+            float base[2], acc[LNT][2] = {};
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                base[m] = a.base && m < nr && nw < a.N ? a.base[(size_t)row[m] * a.ldb + nw] : 0.0f;
+            for (int k0 = 0; k0 < rank; k0 += 64) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + 32 * h + t4 * 8, left = rank - k;
+                    if (k0 > 0) load_b(cur, k0 + 32 * h, b[h]);
+                    float t[2][8];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        float4 u = make_float4(0, 0, 0, 0), v = u;
+                        if (m < nr && left > 0) {
+                            const float4 *tr = reinterpret_cast<const float4 *>(a.t + (size_t)row[m] * a.r_max + k);
+                            u = tr[0];
+                            v = tr[1];
+                        }
+                        const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) t[m][e] = e < left ? f[e] : 0.0f;  // past the rank: not written
+                    }
+#pragma unroll
+                    for (int j = 0; j < LNT; ++j) {
+                        float w[8];
+                        wide_w<WBF>(b[h][j], w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = e < left ? w[e] : 0.0f;  // what lies past the rank is not used
+                            acc[j][0] = fmaf(x, t[0][e], acc[j][0]);
+                            acc[j][1] = fmaf(x, t[1][e], acc[j][1]);
+                        }
+                    }
+                }
+            }
+            // the four lanes of an output add up; lane t4 writes output 8 t4 + g
+            static_assert(LNT == 4, "one output a lane");
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float mine = 0.0f;
+#pragma unroll
+                for (int j = 0; j < LNT; ++j) {
+                    float v = acc[j][m];
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    if (t4 == j) mine = v;
+                }
+                if (m < nr && nw < a.N) a.Y[(size_t)row[m] * a.ldy + nw] = rank > 0 ? base[m] + sc * mine : base[m];
+            }
+        }
+    }
     for (int i = blockIdx.y; i < it.n; i += gridDim.y) {
         const int id = it.id[it.lead[i]];
-        if (id < 0 && a.base == a.Y) continue;  // no adapter, in place: nothing to change
+        if (it.rows[i] <= 2 || (id < 0 && a.base == a.Y)) continue;  // done; no adapter, in place: nothing to change
         const int nr = item_rows(it, i, a.M);
         const int rank = it.rank[it.lead[i]];
         const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
@@ -453,31 +591,6 @@ __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
                     for (int x = 0; x < 4; ++x) w[x] = 2 * x + 1 < left ? w[x] : 2 * x < left ? w[x] & 0xffffu : 0u;
                     b[j] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            }
-            if (!waited) {
-                pdl_wait();
-                waited = true;
-            }
-            if (nr <= 2) {
-                // lane (g, t4): outputs 8 j + g, ranks 8 t4 .. 8 t4 + 7 of the 32
-                float t[2][8];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float *tr = a.t + (size_t)it.row[m < nr ? m : 0] * a.r_max + k;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[m][e] = m < nr && e < left ? tr[e] : 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < LNT; ++j) {
-                    float w[8];
-                    wide_w<WBF>(b[j], w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[j][0] = fmaf(w[e], t[0][e], acc[j][0]);
-                        acc[j][1] = fmaf(w[e], t[1][e], acc[j][1]);
-                    }
-                }
-                continue;
             }
             uint32_t p[3][4], q[3][4];
 #pragma unroll
@@ -512,31 +625,6 @@ __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
                     }
                 }
             }
-        }
-        if (!waited) {
-            pdl_wait();
-            waited = true;
-        }
-        if (nr <= 2) {
-            // the four lanes of an output add up; lane t4 writes output 8 t4 + g
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float mine = 0.0f;
-#pragma unroll
-                for (int j = 0; j < LNT; ++j) {
-                    float v = acc[j][m];
-                    v += __shfl_xor_sync(0xffffffffu, v, 1);
-                    v += __shfl_xor_sync(0xffffffffu, v, 2);
-                    if (t4 == j) mine = v;
-                }
-                static_assert(LNT == 4, "one output a lane");
-                const long long n = n0 + t4 * 8 + g;
-                if (m >= nr || n >= a.N) continue;
-                const size_t r = (size_t)it.row[m];
-                const float base = a.base ? a.base[r * a.ldb + n] : 0.0f;
-                a.Y[r * a.ldy + n] = rank > 0 ? base + sc * mine : base;
-            }
-            continue;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -575,7 +663,6 @@ __global__ void __launch_bounds__(LWARPS * 32) k_lora_expand(const LoraArgs a) {
             }
         }
     }
-    if (!waited) pdl_wait();
 }
 
 }  // namespace
@@ -584,11 +671,10 @@ cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s)
     const bool bf = w_type == HQ_BF16, same = a.x_type == w_type;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    // items in turn: clusters for four blocks an SM; the expand's blocks all at
-    // once (two an SM), each with its next item's loads in flight
+    // items in turn by as many blocks as are resident at once, two an SM
     const int rg = (a.r_max + LG - 1) / LG, tiles = (int)(((long long)a.N + LCOLS - 1) / LCOLS);
     auto least = [&](long long want) { return (unsigned)(want < 1 ? 1 : want < a.M ? want : a.M); };
-    const dim3 grid(LCL, least((4LL * sms / LCL + rg - 1) / rg), (unsigned)rg), block(LWARPS * 32);
+    const dim3 grid(LCL, least((2LL * sms / LCL + rg - 1) / rg), (unsigned)rg), block(LWARPS * 32);
     cudaError_t e;
     if (bf)
         e = same ? launch_kernel(k_lora_shrink<true, true>, grid, block, 0, pdl, s, a)
@@ -597,7 +683,7 @@ cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s)
         e = same ? launch_kernel(k_lora_shrink<false, true>, grid, block, 0, pdl, s, a)
                  : launch_kernel(k_lora_shrink<false, false>, grid, block, 0, pdl, s, a);
     if (e != cudaSuccess) return e;
-    const dim3 eg((unsigned)tiles, least((8LL * sms + tiles - 1) / tiles));
+    const dim3 eg((unsigned)tiles, least((2LL * sms + tiles - 1) / tiles));
     // the expand always follows the shrink programmatically: it loads its
     // weights while the shrink runs
     return bf ? launch_kernel(k_lora_expand<true>, eg, block, 0, true, s, a)

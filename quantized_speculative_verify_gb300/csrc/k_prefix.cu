@@ -36,7 +36,7 @@ constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the t
 constexpr int TC_ROWS = 65;
 constexpr int TC_SHARED = 512;
 constexpr int TC_ROWS_OWN = 33;
-constexpr int MAX_PARTS = 64;   // shared_parts + own_parts
+constexpr int MAX_PARTS = 64;   // shared_parts + own_parts, at most 32 each
 
 template <int D>
 struct Tile {
@@ -606,16 +606,23 @@ cudaError_t pool_map(CUtensorMap *m, const hq_pages &c, int D, int type, int box
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Parts a row may be cut into, for a workspace that does not depend on the
-// lengths: as many as it takes to give every SM a block.  A block of the
-// shared parts has up to 256 rows, one of the own parts a sequence's.
-int shared_parts(int rows, int Hq) {
-    const long long p = 40960 / ((long long)rows * Hq) + 1;
+// Partial results (rows x heads x parts) the workspace holds, for a size that
+// does not depend on the lengths or on B and grows with rows and max_rows: as
+// many parts as it takes to give every SM a block, up to 32 of each kind.  A
+// block of the shared parts has up to 256 rows of the n = rows * Hq; the own
+// parts of B >= rows / max_rows sequences are wanted for 1280 blocks in all.
+long long shared_slots(long long n) { return 32 * n < 40960 + 2 * n ? 32 * n : 40960 + 2 * n; }
+long long own_slots(long long n, int max_rows, int G) {
+    const long long want = 1280LL * max_rows * G + n;
+    return 32 * n < want ? 32 * n : want;
+}
+int shared_parts(long long n) {
+    const long long p = 40960 / n + 1;
     return p > 32 ? 32 : p < 2 ? 2 : (int)p;
 }
-int own_parts(int B, int Hkv) {
-    const long long p = 1280 / ((long long)B * Hkv) + 1;
-    return p > 32 ? 32 : (int)p;
+int own_parts(long long n, int B, int max_rows, int Hkv, int G) {
+    const long long p = 1280 / ((long long)B * Hkv) + 1, room = own_slots(n, max_rows, G) / n;
+    return (int)(p < room ? p : room);
 }
 
 template <int D, bool BF, int KW>
@@ -655,14 +662,16 @@ cudaError_t launch_merge(const PrefixArgs &a, const PrefixPlan &pl, int sms, cud
 
 }  // namespace
 
-size_t prefix_workspace_bytes(int B, int rows, int Hq, int Hkv, int D) {
-    return 16 + (size_t)(shared_parts(rows, Hq) + own_parts(B, Hkv)) * rows * Hq * (size_t)(D + 2) * 4;
+size_t prefix_workspace_bytes(int rows, int max_rows, int Hq, int Hkv, int D) {
+    const long long n = (long long)rows * Hq;
+    return 16 + (size_t)(shared_slots(n) + own_slots(n, max_rows, Hq / Hkv)) * (size_t)(D + 2) * 4;
 }
 
 cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    const int pcap = shared_parts(a.rows, a.Hq), scap = own_parts(a.B, a.Hkv);
+    const long long n = (long long)a.rows * a.Hq;
+    const int pcap = shared_parts(n), scap = own_parts(n, a.B, a.max_rows, a.Hkv, a.G);
     const long long head_rows = (long long)a.rows * a.G, seq_rows = (long long)a.max_rows * a.G;
     // The tensor-memory kernel takes the shared parts from TC_ROWS rows a head
     // on, where they are bound by the products, and prefixes of several tiles;
@@ -700,7 +709,7 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
     a.ws_o = reinterpret_cast<float *>(ws + 16);
-    a.ws_ml = a.ws_o + (size_t)(pcap + scap) * a.rows * a.Hq * D;
+    a.ws_ml = a.ws_o + (size_t)(pcap + scap) * n * D;
     a.pool = static_cast<const uint8_t *>(c.pool);
     a.plane_bytes = c.plane_bytes;
     const bool bf = a.type == HQ_BF16;

@@ -210,3 +210,12 @@ def test_prefix_attention_refuses_bad_arguments():
     assert size(2, 6, 4, 4, 2, 128) > 16
     for z in ((0, 6, 4, 4, 2, 128), (2, 0, 4, 4, 2, 128), (2, 6, 129, 4, 2, 128), (2, 6, 4, 5, 2, 128), (2, 6, 4, 4, 2, 96)):
         assert size(*z) == 0, z
+
+
+def test_prefix_attention_workspace_serves_smaller_calls():
+    size = hq.hq_prefix_attention_workspace_bytes
+    for Hq, Hkv, D in ((32, 8, 128), (8, 8, 64), (64, 1, 128), (40, 5, 64)):
+        for m in (1, 5, 16, 128):
+            sizes = [size(1, rows, m, Hq, Hkv, D) for rows in range(1, 700, 3)]
+            assert sizes == sorted(sizes)
+            assert size(7, 50, m, Hq, Hkv, D) == size(50, 50, m, Hq, Hkv, D) <= size(1, 50, min(128, m + 1), Hq, Hkv, D)
