@@ -553,6 +553,8 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     itself.  weight fp32 [K]."""
     shape = x.shape
     M, K = shape
+    if x.dtype not in TYPES:
+        raise TypeError(f"add_norm_quant: fp32, fp16 or bf16 expected, got {x.dtype}")
     if K != desc.K:
         raise ValueError(f"add_norm_quant: x has {K} features, the layer {desc.K}")
     _shaped(residual, shape, "add_norm_quant: residual")
@@ -570,8 +572,12 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     if residual is not None and residual_out is not None and residual_out is not residual and (
             residual.dtype != residual_out.dtype or _rows(residual_out, K, "residual_out") != ldr):
         raise ValueError("add_norm_quant: residual and residual_out need the same type and stride")
-    hq_add_norm_quant(desc, x, _type(x), _rows(x, K, "x"), residual, residual_out, _type(r), ldr, weight, eps, M, signs,
-                      h, _type(h), _rows(h, K, "h"), qx, gsum, qop, sx, flags, stream)
+    ldx, ldh = _rows(x, K, "x"), _rows(h, K, "h")
+    rc = load().hq_add_norm_quant(ctypes.byref(desc), _ptr(x), _type(x), ldx, _ptr(residual), _ptr(residual_out), _type(r),
+                                  ldr, _ptr(weight), eps, M, _ptr(signs), _ptr(h), _type(h), ldh, _ptr(qx), _ptr(gsum),
+                                  _ptr(qop), _ptr(sx), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_add_norm_quant")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -610,8 +616,11 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _room(workspace, need, "lora_apply: the workspace")
-    hq_lora_apply(x, _type(x), _rows(x, K, "x"), M, K, N, A, B, _type(A), n, r, ids, ranks, scale, base,
-                  _rows(base, N, "base"), Y, _rows(Y, N, "Y"), workspace, flags, stream)
+    rc = load().hq_lora_apply(_ptr(x), _type(x), _rows(x, K, "x"), M, K, N, _ptr(A), _ptr(B), _type(A), n, r, _ptr(ids),
+                              _ptr(ranks), _ptr(scale), _ptr(base), _rows(base, N, "base"), _ptr(Y), _rows(Y, N, "Y"),
+                              _ptr(workspace), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_lora_apply")
     return Y
 
 
