@@ -27,6 +27,11 @@
  * hq_delta_commit).  Source: the same page, section "Verifying a draft tree
  * without restoring model state".
  *
+ * For a batch of requests there are the residual addition and norm in front of
+ * a layer (hq_add_norm_quant), low-rank adapters beside it (hq_lora_apply), a
+ * paged key/value cache (hq_pages_*) and attention over it that reads a shared
+ * prefix once (hq_prefix_attention).
+ *
  * Conventions
  *   - Row-major everywhere.  X is [M][K], W is [N][K], Y = X W^T is [M][N].
  *   - Pointers are DEVICE pointers unless their name ends in _host.  The
