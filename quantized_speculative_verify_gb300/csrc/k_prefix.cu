@@ -36,6 +36,7 @@ constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the t
 constexpr int TC_ROWS = 65;
 constexpr int TC_SHARED = 512;
 constexpr int TC_ROWS_OWN = 33;
+constexpr int OWN_POS = 160, OWN_POS_TC = 35;
 constexpr int MAX_PARTS = 64;   // shared_parts + own_parts, at most 32 each
 
 template <int D>
@@ -119,14 +120,19 @@ __global__ void __launch_bounds__(XTHREADS, 2)
     }
     __syncthreads();
     pdl_launch_dependents();
-    pdl_wait();
+    // Behind the tensor-memory kernel nothing is waited for: each of its blocks
+    // has itself waited for the call's inputs before this kernel may start, and
+    // the SMs that it leaves idle, or is done with, begin here at once.  Only
+    // this grid's end, which the merge waits for, must not come before its end.
+    const bool last = pl.tc_shared && blockIdx.x == gridDim.x - 1;
+    if (!pl.tc_shared) pdl_wait();
 
-    // which part this block is
+    // which part this block is; nothing to do (ntiles 0) where no row uses it
     int unit = blockIdx.x;
     const int hk = unit % a.Hkv;
     unit /= a.Hkv;
     const int nshared = pl.tc_shared ? 0 : pl.np * pl.ptiles;
-    int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0;
+    int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0, ntiles = 0;
     if (unit < nshared) {
         split = unit / pl.ptiles;
         rt = unit % pl.ptiles;
@@ -135,8 +141,8 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         k0 = split * pl.pchunk;
         k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
         const Seq s = first_live(a);
-        if (!s.live) return;  // no row of the batch uses this part
         slot = s.slot;
+        if (s.live) ntiles = (k1 - k0) / XKEYS;
     } else {
         unit -= nshared;
         const int b = unit / (pl.ns * pl.stiles);
@@ -144,7 +150,6 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         split = unit / pl.stiles;
         rt = unit % pl.stiles;
         const Seq s = seq_of(a, b);
-        if (!s.live || rt * XROWS >= s.m * a.G) return;
         first = s.first;
         nodes = s.m;
         nrows = s.m * a.G;
@@ -153,9 +158,13 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         slot = s.slot;
         tree0 = s.len - s.m;
         split += pl.np;
-        if (k0 >= k1) return;  // past the sequence's end: the merge does not look here
+        // (past the sequence's end the merge does not look)
+        if (s.live && rt * XROWS < nrows && k0 < k1) ntiles = (k1 - k0 + XKEYS - 1) / XKEYS;
     }
-    const int ntiles = (k1 - k0 + XKEYS - 1) / XKEYS;
+    if (ntiles == 0) {
+        if (last) pdl_wait();
+        return;
+    }
 
     if (warp == XCW) {
         // ------------------------------------------------------ producer ---
@@ -178,6 +187,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         // no copy may still be landing in shared memory when the block exits
         for (int j = i > XSTAGES ? i - XSTAGES : 0; j < i; ++j)
             mbar_wait_short(smem_addr(&bars[j % XSTAGES]), (uint32_t)((j / XSTAGES) & 1), a.err);
+        if (last) pdl_wait();
         return;
     }
 
@@ -701,10 +711,27 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
         n = (int)((positions + len - 1) / len);
     };
     const long long pblocks = (long long)a.Hkv * pl.ptiles, sblocks = (long long)a.Hkv * a.B * pl.stiles;
-    // shared: one block per SM of the tensor-memory kernel in as few rounds as
-    // the tiles allow, two of the other; own: several short ones per SM
-    cut(pl.s0, pl.tc_shared ? sms / pblocks : (2LL * sms + pblocks - 1) / pblocks, pcap, pkey, pl.np, pl.pchunk);
-    cut((long long)a.max_len - pl.s0, ((pl.tc_own ? 2LL : 8LL) * sms + sblocks - 1) / sblocks, scap, skey, pl.ns, pl.schunk);
+    long long want = (2LL * sms + pblocks - 1) / pblocks;
+    if (pl.tc_shared) {
+        // At most one block of the tensor-memory kernel per SM.  The SMs that
+        // are left over work on the own parts meanwhile, so a few blocks less
+        // end earlier than all: the count with the least estimated time, in
+        // units of a block's tile (1.6 us).  In that time an SM reads OWN_POS
+        // own positions of a head, and all of them together, bound by memory,
+        // two thirds as many each; sequences have half the largest length.
+        const long long tiles = pl.s0 / TC_KEYS, own = sblocks * (a.max_len - pl.s0) / (2 * (pl.tc_own ? OWN_POS_TC : OWN_POS));
+        long long best = -1;
+        for (long long np = 1; np <= pcap && (np == 1 || np * pblocks <= sms); ++np) {
+            const long long t = (tiles + np - 1) / np, rest = own - (sms - pblocks * np) * t;
+            const long long cost = 2 * sms * t + (rest > 0 ? 3 * rest : 0);
+            if (best < 0 || cost < best) {
+                best = cost;
+                want = np;
+            }
+        }
+    }
+    cut(pl.s0, want, pcap, pkey, pl.np, pl.pchunk);
+    cut((long long)a.max_len - pl.s0, ((pl.tc_own ? 2LL : 4LL) * sms + sblocks - 1) / sblocks, scap, skey, pl.ns, pl.schunk);
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(ws);

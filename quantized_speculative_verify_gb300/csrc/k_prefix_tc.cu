@@ -155,7 +155,12 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    pdl_wait();
+    // Own parts behind shared ones start on the SMs that those leave idle, or
+    // are done with: each of their blocks has itself waited for the call's
+    // inputs before these may start.  Only this grid's end, which the merge
+    // waits for, must not come before theirs (see the end).
+    const bool behind = MODE == OWN && pl.tc_shared;
+    if (!behind) pdl_wait();
     pdl_launch_dependents();
 
     // which part this block is; nothing to do (ntiles 0) where no row uses it
@@ -583,6 +588,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 9) tmem_dealloc(tmem, 512);
+    if (behind && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 template <int D, bool BF, int MODE>
