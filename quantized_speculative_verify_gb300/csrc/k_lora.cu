@@ -84,7 +84,7 @@ __device__ __forceinline__ void split_half(uint32_t w, uint32_t (&t)[2]) {
     t[1] = pack_bf16(isinf(h0) ? 0.0f : f.x - h0, isinf(h1) ? 0.0f : f.y - h1);
 }
 
-// The items of the batch.  All threads of the block call find(), then rows().
+// The items of the batch, found by all threads of the block.
 struct Items {
     int id[HQ_MAX_M];      // the row's adapter, -1 for none
     int number[HQ_MAX_M];  // its number among the rows of its adapter
@@ -95,7 +95,8 @@ struct Items {
     int rows[HQ_MAX_M];    // rows of each item
     int mate[HQ_MAX_M];    // the second row of the item that a row leads
     int unit0[HQ_MAX_M + 1];  // k_lora_shrink: the few-row items' shares before each item
-    int row[LR];           // the rows of the current item of three rows or more
+    int at[HQ_MAX_M];      // the item that a row leads
+    uint8_t row[HQ_MAX_M][LR];  // the rows of each item
     int warp_count[HQ_MAX_M / 32];
     int n;
 };
@@ -124,21 +125,22 @@ __device__ int sum_below(Items &it, int v, int &total) {
 
 __device__ void find_items(Items &it, const LoraArgs &a) {
     const int M = a.M, t = threadIdx.x;
-    int id = -2;  // no row
+    int id = -2, rank = 0;  // no row
+    float scale = 1.0f;
     if (t < HQ_MAX_M) {
         if (t < M) {
             id = a.ids[t];
             if (id < 0 || id >= a.n_adapters) id = -1;
         }
         it.id[t] = id;
-        int r = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;
-        it.rank[t] = r < 0 ? 0 : r > a.r_max ? a.r_max : r;
-        it.scale[t] = id >= 0 && a.scale ? a.scale[id] : 1.0f;
+        rank = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;  // on their way during the compares
+        if (id >= 0 && a.scale) scale = a.scale[id];
     }
     __syncthreads();
     bool lead = false;
+    int n = 0, first = t;  // rows of the same adapter before this one; the first of its item
     if (t < HQ_MAX_M) {
-        int n = 0, all = 0, last = 0;
+        int all = 0, last = 0;
         const int4 *v = reinterpret_cast<const int4 *>(it.id);
 #pragma unroll 8
         for (int j = 0; j < HQ_MAX_M / 4; ++j) {
@@ -148,35 +150,33 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
             for (int e = 0; e < 4; ++e) {
                 const bool same = x[e] == id, before = same && 4 * j + e < t;
                 all += same;
+                first = before && n % LR == 0 ? 4 * j + e : first;
                 n += before;
                 last = before ? 4 * j + e : last;
             }
         }
         it.number[t] = n;
         it.size[t] = all;
+        it.rank[t] = rank < 0 ? 0 : rank > a.r_max ? a.r_max : rank;
+        it.scale[t] = scale;
         lead = t < M && n % LR == 0;
+        if (lead) first = t;
         if (t < M && n % LR == 1) it.mate[last] = t;
     }
     int total;
     const int at = sum_below(it, lead ? 1 : 0, total);
-    if (lead) it.lead[at] = t;
+    if (lead) {
+        it.lead[at] = t;
+        it.at[t] = at;
+    }
     if (t == 0) it.n = total;
     __syncthreads();
+    if (t < M) it.row[it.at[first]][n % LR] = (uint8_t)t;
     if (t < total) {
         const int l = it.lead[t], left = it.size[l] - it.number[l];
         it.rows[t] = left < LR ? left : LR;
     }
     __syncthreads();
-}
-
-// The rows of item i into it.row; their number.  (The barriers also
-// separate the block's work on the items before and after.)
-__device__ int item_rows(Items &it, int i, int M) {
-    const int t = threadIdx.x, lead = it.lead[i], id = it.id[lead], part = it.number[lead] / LR;
-    __syncthreads();
-    if (t < M && t < HQ_MAX_M && it.id[t] == id && it.number[t] / LR == part) it.row[it.number[t] % LR] = t;
-    __syncthreads();
-    return it.rows[i];
 }
 
 // 8 consecutive values of x as MMA words: one 16-byte load where the types
@@ -378,8 +378,8 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_
         const int id = it.id[it.lead[i]];
         const int rank = it.rank[it.lead[i]] - r0;
         if (rank <= 0 || it.rows[i] <= 2) continue;
-        const int nr = item_rows(it, i, a.M);
-        const int *rows = it.row;
+        const int nr = it.rows[i];
+        const uint8_t *rows = it.row[i];
         const int nt = rank >= LG ? LG / 8 : (rank + 7) / 8;
         const uint8_t *Aw = static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + g) * (size_t)a.K * 2;
         const uint8_t *xA = static_cast<const uint8_t *>(a.x) + (size_t)rows[g < nr ? g : 0] * (size_t)a.ldx * xb;
@@ -467,6 +467,9 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_
 template <bool WBF>
 __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a) {
     __shared__ __align__(16) Items it;
+    // t of an item, a step of 64 ranks, as three bf16 terms (16-byte pieces
+    // swizzled by row: the lanes' reads are free of bank conflicts)
+    __shared__ __align__(16) uint16_t s_t[3][LR][64];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     find_items(it, a);
     pdl_launch_dependents();
@@ -561,72 +564,108 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             }
         }
     }
-    for (int i = blockIdx.y; i < it.n; i += gridDim.y) {
-        const int id = it.id[it.lead[i]];
-        if (it.rows[i] <= 2 || (id < 0 && a.base == a.Y)) continue;  // done; no adapter, in place: nothing to change
-        const int nr = item_rows(it, i, a.M);
-        const int rank = it.rank[it.lead[i]];
+    // Items of three rows and more, in steps of 64 ranks: the block splits t
+    // into its three terms once, in shared memory, and the next step's B and t
+    // are on their way during the last additions of this one.
+    auto next_many = [&](int i) {
+        while (i < it.n && (it.rows[i] <= 2 || (it.id[it.lead[i]] < 0 && a.base == a.Y))) i += gridDim.y;
+        return i;
+    };
+    uint4 b[2][LNT];
+    auto load_b = [&](int i, int k0) {
+        const int id = it.id[it.lead[i]], rank = it.rank[it.lead[i]];
         const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
-        const float sc = it.scale[it.lead[i]];
-        float acc[LNT][4];
 #pragma unroll
-        for (int j = 0; j < LNT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-        for (int k0 = 0; k0 < rank; k0 += 32) {
-            const int k = k0 + t4 * 8, left = rank - k;  // ranks left from this lane's first on
-            uint4 b[LNT];
+        for (int c = 0; c < 2; ++c) {
+            const int k = k0 + c * 32 + t4 * 8;
 #pragma unroll
             for (int j = 0; j < LNT; ++j) {
                 const long long n = n0 + j * 8 + g;
-                b[j] = left > 0 && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
-                                           : make_uint4(0, 0, 0, 0);
-                if (left > 0 && left < 8) {  // what lies past the rank is not used
-                    uint32_t w[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+                b[c][j] = k < rank && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
+                                              : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    const int tm = tid >> 4, tk = (tid & 15) * 4;  // the row and ranks of t that this thread brings
+    auto load_t = [&](int i, int k0) {
+        return tm < it.rows[i] && k0 + tk < it.rank[it.lead[i]]
+                   ? *reinterpret_cast<const float4 *>(a.t + (size_t)it.row[i][tm] * a.r_max + k0 + tk)
+                   : make_float4(0, 0, 0, 0);
+    };
+    const int sw = (tk >> 3 ^ tm & 7) * 8 + (tk & 4);  // where it lies in the row
+    int i = next_many(blockIdx.y), k0 = 0;
+    float4 tv = make_float4(0, 0, 0, 0);
+    if (i < it.n) {
+        load_b(i, 0);
+        tv = load_t(i, 0);
+    }
+    float acc[LNT][4];
+#pragma unroll
+    for (int j = 0; j < LNT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+    while (i < it.n) {
+        const int nr = it.rows[i], rank = it.rank[it.lead[i]], cur = i;
+        const float sc = it.scale[it.lead[i]];
+        const bool end = k0 + 64 >= rank;
+        {
+            const int left = rank - k0 - tk;  // past the rank nothing is used
+            uint32_t u[3], v[3];
+            split3(left > 0 ? tv.x : 0.0f, left > 1 ? tv.y : 0.0f, u);
+            split3(left > 2 ? tv.z : 0.0f, left > 3 ? tv.w : 0.0f, v);
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+                *reinterpret_cast<uint2 *>(&s_t[x][tm][sw]) = make_uint2(u[x], v[x]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int left = rank - k0 - c * 32 - t4 * 8;  // ranks left from this lane's first on
+            if (k0 + c * 32 >= rank) break;
+            if (left > 0 && left < 8)
+#pragma unroll
+                for (int j = 0; j < LNT; ++j) {
+                    uint32_t w[4] = {b[c][j].x, b[c][j].y, b[c][j].z, b[c][j].w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) w[x] = 2 * x + 1 < left ? w[x] : 2 * x < left ? w[x] & 0xffffu : 0u;
-                    b[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    b[c][j] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            }
-            uint32_t p[3][4], q[3][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int m = g + 8 * h;
-                const float *tr = a.t + (size_t)it.row[m < nr ? m : 0] * a.r_max + k;
+            for (int x = 0; x < 3; ++x) {
+                const uint4 p = *reinterpret_cast<const uint4 *>(&s_t[x][g][(c * 4 + t4 ^ g) * 8]);
+                const uint4 q = *reinterpret_cast<const uint4 *>(&s_t[x][g + 8][(c * 4 + t4 ^ g) * 8]);
+                const uint32_t xa[4] = {p.x, q.x, p.y, q.y}, xb[4] = {p.z, q.z, p.w, q.w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float f0 = m < nr && 2 * x < left ? tr[2 * x] : 0.0f;
-                    const float f1 = m < nr && 2 * x + 1 < left ? tr[2 * x + 1] : 0.0f;
-                    uint32_t s[3];
-                    split3(f0, f1, s);
+                for (int j = 0; j < LNT; ++j) {
+                    if constexpr (WBF) {
+                        mma16<true>(acc[j], xa, b[c][j].x, b[c][j].y);
+                        mma16<true>(acc[j], xb, b[c][j].z, b[c][j].w);
+                    } else {
 #pragma unroll
-                    for (int y = 0; y < 3; ++y) (h ? q : p)[y][x] = s[y];
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < LNT; ++j) {
-                const uint32_t w[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    uint32_t h0[2] = {w[2 * st], 0}, h1[2] = {w[2 * st + 1], 0};
-                    if constexpr (!WBF) {
-                        split_half(w[2 * st], h0);
-                        split_half(w[2 * st + 1], h1);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) {
-                        const uint32_t x4[4] = {p[x][2 * st], q[x][2 * st], p[x][2 * st + 1], q[x][2 * st + 1]};
-                        mma16<true>(acc[j], x4, h0[0], h1[0]);
-                        if constexpr (!WBF) mma16<true>(acc[j], x4, h0[1], h1[1]);
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t h0[2], h1[2];
+                            split_half(st ? b[c][j].z : b[c][j].x, h0);
+                            split_half(st ? b[c][j].w : b[c][j].y, h1);
+                            mma16<true>(acc[j], st ? xb : xa, h0[0], h1[0]);
+                            mma16<true>(acc[j], st ? xb : xa, h0[1], h1[1]);
+                        }
                     }
                 }
             }
         }
+        __syncthreads();  // the next step writes s_t
+        k0 = end ? 0 : k0 + 64;
+        if (end) i = next_many(i + gridDim.y);
+        if (i < it.n) {
+            load_b(i, k0);
+            tv = load_t(i, k0);
+        }
+        if (!end) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int m = g + 8 * h;
             if (m >= nr) continue;
-            const size_t r = (size_t)it.row[m];
+            const size_t r = it.row[cur][m];
             float2 base[LNT];
 #pragma unroll
             for (int j = 0; j < LNT; ++j) {
@@ -645,19 +684,24 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             for (int j = 0; j < LNT; ++j) {
                 const long long n = n0 + j * 8 + 2 * t4;
                 if (n >= a.N) continue;
+                float2 y = base[j];
                 if (rank > 0) {
-                    base[j].x += sc * acc[j][2 * h];
-                    base[j].y += sc * acc[j][2 * h + 1];
+                    y.x += sc * acc[j][2 * h];
+                    y.y += sc * acc[j][2 * h + 1];
                 }
                 float *d = a.Y + r * a.ldy + n;
                 if (pairs) {
-                    *reinterpret_cast<float2 *>(d) = base[j];
+                    *reinterpret_cast<float2 *>(d) = y;
                 } else {
-                    d[0] = base[j].x;
-                    if (n + 1 < a.N) d[1] = base[j].y;
+                    d[0] = y.x;
+                    if (n + 1 < a.N) d[1] = y.y;
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < LNT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
     }
 }
 
@@ -681,7 +725,7 @@ cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s)
         e = same ? launch_kernel(k_lora_shrink<false, true>, grid, block, 0, pdl, s, a)
                  : launch_kernel(k_lora_shrink<false, false>, grid, block, 0, pdl, s, a);
     if (e != cudaSuccess) return e;
-    const dim3 eg((unsigned)tiles, least((3LL * sms + tiles - 1) / tiles));
+    const dim3 eg((unsigned)tiles, least(3LL * sms / tiles));
     // the expand always follows the shrink programmatically: it loads its
     // weights while the shrink runs
     return bf ? launch_kernel(k_lora_expand<true>, eg, block, 0, true, s, a)
