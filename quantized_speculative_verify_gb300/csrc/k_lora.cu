@@ -41,6 +41,8 @@ constexpr int LR = 16;        // rows per item
 constexpr int LG = 64;        // ranks per block of the shrink
 constexpr int LCL = 8;        // thread blocks per cluster (parts of K)
 constexpr int LWARPS = 8;
+constexpr int LTAB = 2 * HQ_MAX_M;  // places of a hash table of a batch's adapters, at most half full
+static_assert(LTAB == LWARPS * 32 && HQ_MAX_M == 128, "a thread a place, a row a bit");
 constexpr int LNT = 4;        // 8-column tiles per warp of the expand
 constexpr int LCOLS = LWARPS * LNT * 8;
 
@@ -87,18 +89,19 @@ __device__ __forceinline__ void split_half(uint32_t w, uint32_t (&t)[2]) {
 // The items of the batch, found by all threads of the block.
 struct Items {
     int id[HQ_MAX_M];      // the row's adapter, -1 for none
-    int number[HQ_MAX_M];  // its number among the rows of its adapter
-    int size[HQ_MAX_M];    // rows of its adapter
     int rank[HQ_MAX_M];    // of the row's adapter
     float scale[HQ_MAX_M];
     int lead[HQ_MAX_M];    // the first row of each item
     int rows[HQ_MAX_M];    // rows of each item
     int mate[HQ_MAX_M];    // the second row of the item that a row leads
     int unit0[HQ_MAX_M + 1];  // k_lora_shrink: the few-row items' shares before each item
-    int at[HQ_MAX_M];      // the item that a row leads
     uint8_t row[HQ_MAX_M][LR];  // the rows of each item
     int warp_count[HQ_MAX_M / 32];
     int n;
+    // the batch's adapters, hashed: id, rows (a bit each), items
+    int key[LTAB];
+    uint4 mask[LTAB];
+    uint8_t item[LTAB][HQ_MAX_M / LR];
 };
 
 // Sum over the first HQ_MAX_M threads before this one; `total` over all.
@@ -123,59 +126,70 @@ __device__ int sum_below(Items &it, int v, int &total) {
     return below;
 }
 
+// (A hash table instead of comparing every row with every other: xNEWx)
 __device__ void find_items(Items &it, const LoraArgs &a) {
-    const int M = a.M, t = threadIdx.x;
-    int id = -2, rank = 0;  // no row
+    const int M = a.M, t = threadIdx.x, w = t >> 5;
+    const uint32_t below = (1u << (t & 31)) - 1;
+    it.key[t] = -2;
+    it.mask[t] = make_uint4(0, 0, 0, 0);
+    int id = -2, rank = 0, place = 0;
     float scale = 1.0f;
-    if (t < HQ_MAX_M) {
-        if (t < M) {
-            id = a.ids[t];
-            if (id < 0 || id >= a.n_adapters) id = -1;
-        }
-        it.id[t] = id;
-        rank = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;  // on their way during the compares
+    if (t < M) {
+        id = a.ids[t];
+        if (id < 0 || id >= a.n_adapters) id = -1;
+    }
+    __syncthreads();
+    if (t < M) {
+        rank = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;  // on its way meanwhile
         if (id >= 0 && a.scale) scale = a.scale[id];
+        place = (int)(((uint32_t)id * 2654435761u) >> 16) & (LTAB - 1);
+        for (int probe = 0; probe < LTAB; ++probe) {
+            const int old = atomicCAS(&it.key[place], -2, id);
+            if (old == -2 || old == id) break;
+            place = (place + 1) & (LTAB - 1);
+        }
+        atomicOr(reinterpret_cast<uint32_t *>(&it.mask[place]) + w, 1u << (t & 31));
     }
     __syncthreads();
     bool lead = false;
-    int n = 0, first = t;  // rows of the same adapter before this one; the first of its item
+    int n = 0, size = 0;
     if (t < HQ_MAX_M) {
-        int all = 0, last = 0;
-        const int4 *v = reinterpret_cast<const int4 *>(it.id);
-#pragma unroll 8
-        for (int j = 0; j < HQ_MAX_M / 4; ++j) {
-            const int4 q = v[j];
-            const int x[4] = {q.x, q.y, q.z, q.w};
+        if (t < M) {
+            const uint4 m4 = it.mask[place];
+            const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
+            int last = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool same = x[e] == id, before = same && 4 * j + e < t;
-                all += same;
-                first = before && n % LR == 0 ? 4 * j + e : first;
-                n += before;
-                last = before ? 4 * j + e : last;
+            for (int i = 0; i < 4; ++i) {
+                size += __popc(m[i]);
+                const uint32_t before = i < w ? m[i] : i == w ? m[i] & below : 0u;
+                n += __popc(before);
+                if (before) last = 32 * i + 31 - __clz(before);
             }
+            lead = n % LR == 0;
+            if (n % LR == 1) it.mate[last] = t;
+            it.id[t] = id;
+            it.rank[t] = rank < 0 ? 0 : rank > a.r_max ? a.r_max : rank;
+            it.scale[t] = scale;
         }
-        it.number[t] = n;
-        it.size[t] = all;
-        it.rank[t] = rank < 0 ? 0 : rank > a.r_max ? a.r_max : rank;
-        it.scale[t] = scale;
-        lead = t < M && n % LR == 0;
-        if (lead) first = t;
-        if (t < M && n % LR == 1) it.mate[last] = t;
+        const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+        if ((t & 31) == 0) it.warp_count[w] = (int)leads;
     }
-    int total;
-    const int at = sum_below(it, lead ? 1 : 0, total);
+    __syncthreads();
+    int total = 0, at = 0;
+#pragma unroll
+    for (int i = 0; i < HQ_MAX_M / 32; ++i) {
+        const uint32_t leads = (uint32_t)it.warp_count[i];
+        at += i < w ? __popc(leads) : i == w ? __popc(leads & below) : 0;
+        total += __popc(leads);
+    }
     if (lead) {
         it.lead[at] = t;
-        it.at[t] = at;
+        it.rows[at] = size - n < LR ? size - n : LR;
+        it.item[place][n / LR] = (uint8_t)at;
     }
     if (t == 0) it.n = total;
     __syncthreads();
-    if (t < M) it.row[it.at[first]][n % LR] = (uint8_t)t;
-    if (t < total) {
-        const int l = it.lead[t], left = it.size[l] - it.number[l];
-        it.rows[t] = left < LR ? left : LR;
-    }
+    if (t < M) it.row[it.item[place][n / LR]][n % LR] = (uint8_t)t;
     __syncthreads();
 }
 
@@ -474,9 +488,9 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
     find_items(it, a);
     pdl_launch_dependents();
     const long long n0 = (long long)blockIdx.x * LCOLS + warp * LNT * 8;
-    // pairs of outputs where every row starts at an 8-byte boundary
-    const bool pairs = (a.N & 1) == 0 && (a.ldy & 1) == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 7) == 0 &&
-                       (!a.base || ((a.ldb & 1) == 0 && (reinterpret_cast<uintptr_t>(a.base) & 7) == 0));
+    // four outputs at a time where every row starts at a 16-byte boundary
+    const bool quads = (a.N & 3) == 0 && (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0 &&
+                       (!a.base || ((a.ldb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.base) & 15) == 0));
     // Items of one or two rows first, the warps on their own: lane (g, t4) has
     // the outputs 8 j + g and the ranks 8 t4 .. 8 t4 + 7 of each 32; the next
     // item's row pieces of B are on their way during this one's products.
@@ -571,7 +585,10 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
         while (i < it.n && (it.rows[i] <= 2 || (it.id[it.lead[i]] < 0 && a.base == a.Y))) i += gridDim.y;
         return i;
     };
+    // Column c of the MMAs' tile j is output 8 (c / 2) + 2 j + c % 2, so that a
+    // lane's columns of the four tiles are 8 consecutive outputs.
     uint4 b[2][LNT];
+    const long long ny = n0 + t4 * 8;
     auto load_b = [&](int i, int k0) {
         const int id = it.id[it.lead[i]], rank = it.rank[it.lead[i]];
         const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             const int k = k0 + c * 32 + t4 * 8;
 #pragma unroll
             for (int j = 0; j < LNT; ++j) {
-                const long long n = n0 + j * 8 + g;
+                const long long n = n0 + (g >> 1) * 8 + j * 2 + (g & 1);
                 b[c][j] = k < rank && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
                                               : make_uint4(0, 0, 0, 0);
             }
@@ -666,35 +683,37 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             const int m = g + 8 * h;
             if (m >= nr) continue;
             const size_t r = it.row[cur][m];
-            float2 base[LNT];
+            float y[8];
 #pragma unroll
-            for (int j = 0; j < LNT; ++j) {
-                const long long n = n0 + j * 8 + 2 * t4;
-                base[j] = make_float2(0.0f, 0.0f);
-                if (!a.base || n >= a.N) continue;
-                const float *s = a.base + r * a.ldb + n;
-                if (pairs) {
-                    base[j] = *reinterpret_cast<const float2 *>(s);
-                } else {
-                    base[j].x = s[0];
-                    if (n + 1 < a.N) base[j].y = s[1];
+            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+            if (a.base) {
+                const float *s = a.base + r * a.ldb + ny;
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    if (quads) {
+                        if (ny + e < a.N) {
+                            const float4 u = *reinterpret_cast<const float4 *>(s + e);
+                            y[e] = u.x, y[e + 1] = u.y, y[e + 2] = u.z, y[e + 3] = u.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int f = e; f < e + 4; ++f)
+                            if (ny + f < a.N) y[f] = s[f];
+                    }
                 }
             }
+            if (rank > 0)
 #pragma unroll
-            for (int j = 0; j < LNT; ++j) {
-                const long long n = n0 + j * 8 + 2 * t4;
-                if (n >= a.N) continue;
-                float2 y = base[j];
-                if (rank > 0) {
-                    y.x += sc * acc[j][2 * h];
-                    y.y += sc * acc[j][2 * h + 1];
-                }
-                float *d = a.Y + r * a.ldy + n;
-                if (pairs) {
-                    *reinterpret_cast<float2 *>(d) = y;
+                for (int e = 0; e < 8; ++e) y[e] += sc * acc[e >> 1][2 * h + (e & 1)];
+            float *d = a.Y + r * a.ldy + ny;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                if (quads) {
+                    if (ny + e < a.N) *reinterpret_cast<float4 *>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 } else {
-                    d[0] = y.x;
-                    if (n + 1 < a.N) d[1] = y.y;
+#pragma unroll
+                    for (int f = e; f < e + 4; ++f)
+                        if (ny + f < a.N) d[f] = y[f];
                 }
             }
         }
