@@ -9,14 +9,24 @@
 // sum of squares and the largest |z| are reduced together, with one barrier,
 // where norming first and rotating after needs two.
 //
-// One thread block per row at a time; a thread holds octets of 8 consecutive features
-// (one 16-byte load of 16-bit values, two of fp32), so butterfly strides 1, 2
-// and 4 stay inside the thread and strides 8 and 16 are two lane exchanges.
-// With more rows than resident blocks a block takes several rows in turn: the
-// next row's loads are issued before the reduction of the current one, and
-// weight and signs stay in registers.  (One row per block left the memory idle
-// during the reductions: 8190 rows of 8192, all bf16, 232 us = 2.6 TB/s; the
-// loop: 154 us = 3.9 TB/s, then bound by issue slots.)
+// The 1/sqrt(32) enters sx alone: the codes are rint(127 z / max|z|) for any
+// factor of z.  w holds the weight with the feature's sign, so the butterfly
+// starts from the product, and h takes the sign back.
+//
+// One thread block per row at a time; a thread holds octets of 8 consecutive
+// features (one 16-byte load of 16-bit values, two of fp32), so butterfly
+// strides 1, 2 and 4 stay inside the thread and strides 8 and 16 are two lane
+// exchanges.  What bounds it: few rows, the chain load - reduction - store (128
+// rows of 8192: 6.8 us, 6.3 of which one row takes).  With more rows than
+// resident blocks a block takes several in turn, weight and signs stay in
+// registers and each thread copies its share of the next three rows into a ring
+// in shared memory.  Then the instructions bound it, not the memory: 8190 rows
+// of 8192, all bf16, 111 us = 5.4 TB/s at 400 instructions a warp and row, four
+// fifths of the issue slots used.  On the way there: one row per block 232 us
+// (the memory idle during reductions); a loop with the next row in registers
+// 148; the ring 145; types known at compile time 115; the largest value by one
+// instruction 111.  The types are known where x, residual and h are all of one
+// 16-bit type; any others take the general code (145 us in that case).
 // Everything is fp32 until the outputs: residual_out, h and the codes are
 // rounded once each.
 #include "act_common.cuh"
@@ -58,11 +68,15 @@ __device__ __forceinline__ void widen(const Raw &r, int type, float (&f)[8]) {
     }
 }
 
-__device__ __forceinline__ void store8(void *row, int type, int octet, const float (&v)[8]) {
+// `signs`: bit i set, value i is negated.
+__device__ __forceinline__ void store8(void *row, int type, int octet, const float (&v)[8], uint32_t signs = 0) {
     if (type == HQ_F32) {
         float4 *p = static_cast<float4 *>(row) + 2 * (size_t)octet;
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = flip(v[i], (signs >> i) & 1u);
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
         return;
     }
     uint32_t w[4];
@@ -75,22 +89,56 @@ __device__ __forceinline__ void store8(void *row, int type, int octet, const flo
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
+        // the pair's signs: its two bits, 15 apart after the product
+        w[i] ^= (((signs >> (2 * i)) & 3u) * 0x40008000u) & 0x80008000u;
     }
     static_cast<uint4 *>(row)[octet] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The largest value of the warp's lanes (NaN only if all are).
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four integers in [-128, 127] as bytes, x0 lowest.
+__device__ __forceinline__ uint32_t pack_s8(int x0, int x1, int x2, int x3) {
+    uint32_t hi, d;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(x3), "r"(x2));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(x1), "r"(x0), "r"(hi));
+    return d;
 }
 
 __device__ __forceinline__ const void *row_of(const void *p, int type, int64_t ld, int row) {
     return static_cast<const uint8_t *>(p) + (size_t)row * (size_t)ld * type_bytes(type);
 }
 
-template <int V, int T>
+// Copies of 16 bytes into shared memory that the thread waits for by groups, in
+// the order in which it committed them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+constexpr int NSTAGES = 3;            // rows in the ring
+constexpr int NORM_SMEM = 220 << 10;  // shared memory of an SM's blocks
+constexpr int NORM_FIXED = 18 << 10;  // of which a block needs beside its ring, with the system's 1 KB
+
+// RING: 0, or rows through the ring (no operand is written): of any types, or
+// x, residual and h all of one 16-bit type.
+enum { DIRECT = 0, RING_ANY = 1, RING_F16 = 2, RING_BF16 = 3 };
+template <int V, int T, int RING>
 __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
+    extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][16-byte piece of a thread's share][thread]
     __shared__ float s_sum[2][T / 32], s_max[2][T / 32];  // by the parity of the row's turn
     __shared__ int s_gs[MAX_K / 16];  // group sums of this row
     int row = blockIdx.x;
     const int MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
     const int K = a.K, G = a.G, n8 = K >> 3;
     const bool quant = a.sx != nullptr;
+    constexpr int ONE = RING == RING_F16 ? HQ_F16 : RING == RING_BF16 ? HQ_BF16 : -1;
+    const int x_type = ONE >= 0 ? ONE : a.x_type, r_type = ONE >= 0 ? ONE : a.r_type, h_type = ONE >= 0 ? ONE : a.h_type;
+    const float inv_k = 1.0f / (float)K;
 
     // the operand's layout (hq_internal.cuh): K tiles of code blocks, then group sums
     const int n8pad = act_blocks(K) * (ACT_BLOCK / 8);
@@ -123,7 +171,8 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
         return;
     }
 
-    // weight and signs are not outputs of the kernel before this one
+    // weight and signs are not outputs of the kernel before this one.  w: the
+    // weight with the feature's sign, sg: the signs
     float w[V][8];
     uint32_t sg[V];
 #pragma unroll
@@ -136,46 +185,90 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             widen(load_raw(a.weight, HQ_F32, idx), HQ_F32, w[j]);
             if (quant) sg[j] = (__ldg(a.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[j][i] = flip(w[j][i], (sg[j] >> i) & 1u);
     }
     pdl_wait();
-    const bool need_gs = a.gsum != nullptr || (a.qop != nullptr && a.sums != 0);
-    Raw xn[V], rn[V];  // the next row
+    const bool need_gs = a.gsum != nullptr || (RING == DIRECT && a.qop != nullptr && a.sums != 0);
+    Raw xn[V], rn[V];
     auto fetch = [&](int r) {
-        const void *xr = row_of(a.x, a.x_type, a.ldx, r);
-        const void *rr = a.res ? row_of(a.res, a.r_type, a.ldr, r) : nullptr;
+        const void *xr = row_of(a.x, x_type, a.ldx, r);
+        const void *rr = a.res ? row_of(a.res, r_type, a.ldr, r) : nullptr;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int idx = tid + j * T;
             xn[j].u = xn[j].v = rn[j].u = rn[j].v = make_uint4(0, 0, 0, 0);
             if (idx >= n8) continue;
-            xn[j] = load_raw(xr, a.x_type, idx);
-            if (rr) rn[j] = load_raw(rr, a.r_type, idx);
+            xn[j] = load_raw(xr, x_type, idx);
+            if (rr) rn[j] = load_raw(rr, r_type, idx);
         }
     };
-    constexpr bool AHEAD = V == 1;  // more octets a thread leave no registers for the next row
+    // The ring: each thread copies, waits for and reads its own octets only.
+    const int xu = x_type == HQ_F32 ? 2 : 1, ru = ONE < 0 && !a.res ? 0 : r_type == HQ_F32 ? 2 : 1;
+    const uint32_t stage_bytes = (uint32_t)(V * (xu + ru) * T * 16);
+    auto issue = [&](int r, int st) {
+        if (r < a.M) {
+            const uint8_t *xr = static_cast<const uint8_t *>(row_of(a.x, x_type, a.ldx, r));
+            const uint8_t *rr = ru ? static_cast<const uint8_t *>(row_of(a.res, r_type, a.ldr, r)) : nullptr;
+            uint32_t d = smem_addr(s_ring) + (uint32_t)st * stage_bytes + (uint32_t)tid * 16;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int idx = tid + j * T;
+                if (idx < n8) {
+                    cp_async16(d, xr + (size_t)idx * xu * 16);
+                    if (xu == 2) cp_async16(d + T * 16, xr + (size_t)idx * 32 + 16);
+                    if (ru) cp_async16(d + xu * T * 16, rr + (size_t)idx * ru * 16);
+                    if (ru == 2) cp_async16(d + (xu + 1) * T * 16, rr + (size_t)idx * 32 + 16);
+                }
+                d += (xu + ru) * T * 16;
+            }
+        }
+        cp_async_commit();
+    };
+    auto take = [&](int st) {
+        const uint8_t *d = s_ring + (size_t)st * stage_bytes + (size_t)tid * 16;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            xn[j].u = xn[j].v = rn[j].u = rn[j].v = make_uint4(0, 0, 0, 0);
+            if (tid + j * T < n8) {
+                xn[j].u = *reinterpret_cast<const uint4 *>(d);
+                if (xu == 2) xn[j].v = *reinterpret_cast<const uint4 *>(d + T * 16);
+                if (ru) rn[j].u = *reinterpret_cast<const uint4 *>(d + xu * T * 16);
+                if (ru == 2) rn[j].v = *reinterpret_cast<const uint4 *>(d + (xu + 1) * T * 16);
+            }
+            d += (xu + ru) * T * 16;
+        }
+    };
+    int stage = 0;
+    if constexpr (RING != DIRECT)
+        for (int i = 0; i < NSTAGES; ++i) issue(row + i * MT, i);
     for (int turn = 0; row < a.M; ++turn, row += MT) {
         if (need_gs) {
             if (turn) __syncthreads();  // the last row's sums have been read
             for (int g = tid; g < ngk; g += T) s_gs[g] = 0;
         }
-        if (!AHEAD || turn == 0) fetch(row);
-        void *ro = a.res_out ? const_cast<void *>(row_of(a.res_out, a.r_type, a.ldr, row)) : nullptr;
+        if constexpr (RING != DIRECT) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(NSTAGES - 1) : "memory");
+            take(stage);
+        } else {
+            fetch(row);
+        }
+        void *ro = a.res_out ? const_cast<void *>(row_of(a.res_out, r_type, a.ldr, row)) : nullptr;
         float v[V][8];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float r[8];
-            widen(xn[j], a.x_type, v[j]);
-            widen(rn[j], a.r_type, r);
+            widen(xn[j], x_type, v[j]);
+            widen(rn[j], r_type, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[j][i] += r[i];
         }
-        if (AHEAD && row + MT < a.M) fetch(row + MT);
         pdl_launch_dependents();
         float ss = 0.0f, amax = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int idx = tid + j * T;
-            if (ro && idx < n8) store8(ro, a.r_type, idx, v[j]);
+            if (ro && idx < n8) store8(ro, r_type, idx, v[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 ss = fmaf(v[j][i], v[j][i], ss);
@@ -185,11 +278,10 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
         // z: the rotated w * s
         float z[V][8];
         if (quant) {
-            const float c = __int_as_float((int)HADAMARD_SCALE_BITS);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[j][i] = flip(v[j][i], (sg[j] >> i) & 1u);
+                for (int i = 0; i < 8; ++i) z[j][i] = v[j][i];
 #pragma unroll
                 for (int st = 1; st <= 4; st <<= 1)
 #pragma unroll
@@ -207,45 +299,42 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
                     for (int i = 0; i < 8; ++i) z[j][i] = fmaf(sign, z[j][i], __shfl_xor_sync(0xffffffffu, z[j][i], lb));
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    z[j][i] *= c;
-                    amax = fmaxf(amax, fabsf(z[j][i]));
-                }
+                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(z[j][i]));
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        }
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        amax = warp_max(amax);
         if (lane == 0) {
             s_sum[turn & 1][tid >> 5] = ss;
             s_max[turn & 1][tid >> 5] = amax;
         }
         __syncthreads();
+        if constexpr (RING != DIRECT) {  // what the thread took has been used
+            issue(row + NSTAGES * MT, stage);
+            if (++stage == NSTAGES) stage = 0;
+        }
         ss = lane < T / 32 ? s_sum[turn & 1][lane] : 0.0f;
         amax = lane < T / 32 ? s_max[turn & 1][lane] : 0.0f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        }
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        amax = warp_max(amax);
         // an all-zero row with eps = 0 gives zeros; NaN and infinities reach sx and h
-        const float d = ss / (float)K + a.eps;
+        const float d = ss * inv_k + a.eps;
         const float rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
         if (a.h) {
-            void *hr = const_cast<void *>(row_of(a.h, a.h_type, a.ldh, row));
+            void *hr = const_cast<void *>(row_of(a.h, h_type, a.ldh, row));
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int idx = tid + j * T;
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = v[j][i] * rstd;
-                if (idx < n8) store8(hr, a.h_type, idx, y);
+                if (idx < n8) store8(hr, h_type, idx, y, sg[j]);
             }
         }
         if (!quant) continue;
-        if (tid == 0) a.sx[row] = rstd * (amax / 127.0f);
+        if (tid == 0) a.sx[row] = rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f);
         const float inv = amax == 0.0f ? 0.0f : 127.0f / amax;
 
         int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
@@ -258,18 +347,10 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             for (int i = 0; i < 8; ++i) {
                 // |z| <= amax: the product rounds to at most 127 (NaN to 0)
                 q[i] = idx < n8 ? __float2int_rn(z[j][i] * inv) : 0;
-                gs += q[i];
             }
-            if (qr && idx < n8) {
-                uint32_t lo = 0, hi = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    lo |= (uint32_t)(q[i] & 255) << (8 * i);
-                    hi |= (uint32_t)(q[i + 4] & 255) << (8 * i);
-                }
-                reinterpret_cast<uint2 *>(qr)[idx] = make_uint2(lo, hi);
-            }
-            if (a.qop && idx < n8pad) {
+            if (qr && idx < n8)
+                reinterpret_cast<uint2 *>(qr)[idx] = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+            if (RING == DIRECT && a.qop && idx < n8pad) {
                 uint4 c16 = make_uint4(0, 0, 0, 0);
                 uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
                 if (a.e4) {
@@ -288,6 +369,8 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             }
             // a group's G / 8 threads are consecutive lanes (G = 16: two lanes)
             if (need_gs) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gs += q[i];
                 for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
                 if (idx < n8 && (lane & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / G], gs);
             }
@@ -304,24 +387,34 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
 
 template <int V, int T>
 cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
-    int grid = a.M;
-    if (a.qop) {
-        grid = act_rows(a.M);  // one block per row of the operand, padding included
-    } else {
-        const int sms = device_sm_count();
-        if (sms <= 0) return cudaErrorNoDevice;
-        int dev = 0, per_sm = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        static std::atomic<int> resident[CACHE_DEVICES];
-        e = cached_per_device(resident, dev, &per_sm, [&](int *v) {
-            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k_add_norm_quant<V, T>, T, 0);
-        });
-        if (e != cudaSuccess) return e;
-        const int most = sms * (per_sm > 0 ? per_sm : 1);
-        if (grid > most) grid = most;
-    }
-    return launch_kernel(k_add_norm_quant<V, T>, dim3((unsigned)grid), dim3(T), 0, pdl, s, a);
+    if (a.qop)  // one block per row of the operand, padding included
+        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)act_rows(a.M)), dim3(T), 0, pdl, s, a);
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorNoDevice;
+    int dev = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> resident[CACHE_DEVICES];
+    e = cached_per_device(resident, dev, &per_sm, [&](int *v) {
+        for (auto f : {k_add_norm_quant<V, T, RING_ANY>, k_add_norm_quant<V, T, RING_F16>, k_add_norm_quant<V, T, RING_BF16>}) {
+            const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM - NORM_FIXED);
+            if (r != cudaSuccess) return r;
+        }
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k_add_norm_quant<V, T, RING_ANY>, T, 0);
+    });
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) per_sm = 1;
+    // the ring where blocks take several rows and its rows fit
+    const int row_bytes = V * T * 8 * (type_bytes(a.x_type) + (a.res ? type_bytes(a.r_type) : 0));
+    const int ring = NSTAGES * row_bytes;
+    const long long most = (long long)sms * per_sm;
+    if (a.M <= most || ring > NORM_SMEM / per_sm - NORM_FIXED)
+        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)a.M), dim3(T), 0, pdl, s, a);
+    const bool one = a.x_type != HQ_F32 && a.res && a.r_type == a.x_type && (!a.h || a.h_type == a.x_type);
+    auto f = !one ? k_add_norm_quant<V, T, RING_ANY>
+             : a.x_type == HQ_F16 ? k_add_norm_quant<V, T, RING_F16>
+                                  : k_add_norm_quant<V, T, RING_BF16>;
+    return launch_kernel(f, dim3((unsigned)most), dim3(T), (size_t)ring, pdl, s, a);
 }
 
 }  // namespace
