@@ -117,6 +117,42 @@ def test_norm_of_many_rows_without_an_operand(M, K):
     check(x, r, w, signs, 1e-6, out, h, qx, sx)
 
 
+@pytest.mark.parametrize("M,K,G,xt,rt,ht,pad", [
+    (3001, 1024, 32, F16, F16, F16, 0), (2500, 736, 16, F32, BF16, F16, 24), (1300, 4096, 64, BF16, F32, BF16, 0),
+    (700, 8192, 128, F32, F32, F32, 8), (400, 16384, 64, BF16, BF16, BF16, 16), (1200, 2048, 32, BF16, None, F16, 0),
+    (2100, 96, 32, BF16, BF16, F32, 0), (200, 16384, 32, F32, F32, BF16, 0)])
+def test_norm_of_many_rows_of_every_type_in_place(M, K, G, xt, rt, ht, pad):
+    x, r, w, signs = make(M, K, xt, rt or F32, seed=M + K, pad=pad)
+    d = hq.make_desc(K, 128, G, "w4")
+    r0 = r.clone() if rt else None
+    h = torch.full((M, K + 8), 7.0, dtype=ht, device=DEV)
+    qx, sx, gs = Guarded((M, K), torch.int8, DEV), Guarded((M,), F32, DEV), Guarded((M, K // G), torch.int32, DEV)
+    hq.add_norm_quant(d, x, r if rt else None, w, signs_dev(signs), 1e-5, residual_out=r if rt else None, h=h[:, :K],
+                      qx=qx.t, gsum=gs.t, sx=sx.t)
+    torch.cuda.synchronize()
+    for t in (qx, sx, gs):
+        t.check()
+    check(x, r0, w, signs, 1e-5, r if rt else None, h[:, :K], qx.t, sx.t)
+    assert bool((h[:, K:] == 7.0).all())
+    assert torch.equal(gs.t, qx.t.view(M, K // G, G).to(torch.int32).sum(2, dtype=torch.int32))
+
+
+def test_norm_degenerate_rows_among_many():
+    """Zero, NaN and infinite rows stay by themselves where a block takes several rows."""
+    M, K = 1500, 2048
+    x, r, w, signs = make(M, K, BF16, BF16, seed=9, spread=1.0)
+    x[700], r[700] = 0, 0
+    x[3, 17] = float("nan")
+    r[1499, 2000] = float("inf")
+    d = hq.make_desc(K, 128, 32, "w4")
+    h, qx, sx = torch.empty_like(x), torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), 0.0, h=h, qx=qx, sx=sx)
+    assert not h[700].any() and not qx[700].any() and float(sx[700]) == 0.0
+    assert not torch.isfinite(sx[3]) and not torch.isfinite(sx[1499])
+    keep = [i for i in range(M) if i not in (3, 700, 1499)]
+    check(x[keep], r[keep], w, signs, 0.0, None, h[keep], qx[keep], sx[keep])
+
+
 def test_norm_strided_rows_and_in_place_residual():
     M, K = 9, 736
     x, r, w, signs = make(M, K, F32, BF16, seed=5, pad=24)
