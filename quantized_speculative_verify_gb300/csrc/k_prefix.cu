@@ -119,13 +119,13 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         fence_mbar_init();
     }
     __syncthreads();
-    pdl_launch_dependents();
     // Behind the tensor-memory kernel nothing is waited for: each of its blocks
     // has itself waited for the call's inputs before this kernel may start, and
     // the SMs that it leaves idle, or is done with, begin here at once.  Only
     // this grid's end, which the merge waits for, must not come before its end.
     const bool last = pl.tc_shared && blockIdx.x == gridDim.x - 1;
     if (!pl.tc_shared) pdl_wait();
+    pdl_launch_dependents();  // after the wait: the merge reads lengths before its own
 
     // which part this block is; nothing to do (ntiles 0) where no row uses it
     int unit = blockIdx.x;
@@ -481,8 +481,9 @@ __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const 
     if (tid == 0) s_b = -1;
     __syncthreads();
     pdl_launch_dependents();
-    pdl_wait();
-    // the sequence whose rows hold this one (the last, should `starts` repeat it)
+    // The inputs of the call are complete: the kernels before this one have
+    // waited for them before they let it start.  Only their results are not.
+    // The sequence whose rows hold this one (the last, should `starts` repeat it)
     if (a.starts) {
         int mine = -1;
         for (int b = tid; b < a.B; b += 256) {
@@ -501,6 +502,7 @@ __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const 
         // own parts that reach into the sequence
         if (s.live) parts = pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
     }
+    pdl_wait();
     const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h0;
     // weights: a warp per head, two parts a lane
     static_assert(MAX_PARTS <= 64, "two parts a lane");

@@ -56,7 +56,7 @@ template <int D>
 struct TcTile {
     static constexpr int BOX = CR * 128;          // 128 rows x 64 dimensions
     static constexpr int BYTES = (D / 64) * BOX;
-    static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256 + HQ_MAX_M * 4;
+    static constexpr size_t SMEM = 1024 + (size_t)(2 + CSLOTS) * BYTES + 256;
 };
 
 // D[128 x N] (+)= A[128 x 16] * B[16 x N], A and B in shared memory, fp32 D;
@@ -119,9 +119,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t &x) {
     return lo || hi;
 }
 
-enum { PAIR = 0, ALTERNATE = 1, OWN = 2 };  // shared parts: two query tiles, or one; own parts
-
-template <int D, bool BF, int MODE>
+template <int D, bool BF, bool PAIR>
 __global__ void __launch_bounds__(CTHREADS, 1)
     k_prefix_tc(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
     using T = TcTile<D>;
@@ -132,8 +130,6 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     const uint32_t full = smem_addr(bars), empty = full + 8 * CSLOTS, sfull = empty + 8 * CSLOTS, phalf = sfull + 16,
                    pready = phalf + 16, ofull = pready + 16, qready = ofull + 16;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 2 * CSLOTS + 9);
-    volatile int *s_odd = reinterpret_cast<int *>(s_tmem + 2);  // [2]: a stream has set values of V to 0
-    int32_t *s_par = reinterpret_cast<int32_t *>(s_tmem + 4);   // [HQ_MAX_M]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -150,50 +146,24 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         mbar_init(qready, 8);
         fence_mbar_init();
     }
+    pdl_wait();
+    // (columns are taken after the wait: a kernel before this one may want them)
     if (warp == 9) tmem_alloc(smem_addr(s_tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    // Own parts behind shared ones start on the SMs that those leave idle, or
-    // are done with: each of their blocks has itself waited for the call's
-    // inputs before these may start.  Only this grid's end, which the merge
-    // waits for, must not come before theirs (see the end).
-    const bool behind = MODE == OWN && pl.tc_shared;
-    if (!behind) pdl_wait();
     pdl_launch_dependents();
 
-    // which part this block is; nothing to do (ntiles 0) where no row uses it
+    // which part this block is
     int unit = blockIdx.x;
     const int hk = unit % a.Hkv;
     unit /= a.Hkv;
-    constexpr bool own = MODE == OWN, pair = MODE == PAIR;
-    int part, row0, nrows, first = 0, k0, k1, tree0 = 0x7fffffff, nodes = 0, slot = 0, ntiles = 0;
-    if (!own) {
-        part = unit / pl.ptiles;
-        row0 = (unit % pl.ptiles) * (pair ? 2 * CR : CR);
-        nrows = a.rows * a.G;
-        k0 = part * pl.pchunk;
-        k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
-        const Seq s = first_live(a);
-        slot = s.slot;
-        if (s.live) ntiles = (k1 - k0) / CR;
-    } else {
-        const int b = unit / (pl.ns * pl.stiles);
-        unit %= pl.ns * pl.stiles;
-        part = unit / pl.stiles;
-        row0 = (unit % pl.stiles) * CR;
-        const Seq s = seq_of(a, b);
-        first = s.first;
-        nodes = s.m;
-        nrows = s.m * a.G;
-        k0 = pl.s0 + part * pl.schunk;
-        k1 = s.len - k0 > pl.schunk ? k0 + pl.schunk : s.len;
-        slot = s.slot;
-        tree0 = s.len - s.m;
-        part += pl.np;
-        if (s.live && row0 < nrows && k0 < k1) ntiles = (k1 - k0 + CR - 1) / CR;
-    }
+    constexpr bool pair = PAIR;
+    const int part = unit / pl.ptiles, row0 = (unit % pl.ptiles) * (pair ? 2 * CR : CR), nrows = a.rows * a.G;
+    const int k0 = part * pl.pchunk, k1 = k0 + pl.pchunk < pl.s0 ? k0 + pl.pchunk : pl.s0;
+    const Seq seq = first_live(a);
+    const int ntiles = seq.live ? (k1 - k0) / CR : 0;  // no live sequence: no row uses this part
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax ---
@@ -201,14 +171,14 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         if (ntiles > 0) {
             const int w = warp >> 2, r = threadIdx.x & 127;  // stream, row of its tile
             const int row = row0 + (pair ? w * CR : 0) + r;  // row among the part's
-            const size_t at = ((size_t)part * a.rows + first + row / a.G) * a.Hq + hk * a.G + row % a.G;
+            const size_t at = ((size_t)part * a.rows + row / a.G) * a.Hq + hk * a.G + row % a.G;
             const int n = pair ? ntiles : (ntiles - w + 1) / 2;
             bool ok = true;
             // the query rows, swizzled as the tensor core reads them
             if (pair || w == 0) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(a.q) +
-                    (row < nrows ? (size_t)(first + row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
+                    (row < nrows ? (size_t)(row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
                 uint8_t *dst = s_q + w * T::BYTES;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
@@ -218,55 +188,14 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
-            // the tree nodes this row sees (without `parent`: a chain)
-            uint32_t anc[4] = {0u, 0u, 0u, 0u};
-            if (own && k1 > tree0) {
-                if (a.parent)
-                    for (int i = threadIdx.x; i < nodes; i += 256) s_par[i] = a.parent[first + i];
-                if (threadIdx.x < 2) s_odd[threadIdx.x] = 0;
-                named_barrier(1, 256);
-                if (row < nrows) {
-                    int cur = row / a.G;
-                    for (int step = 0; step < HQ_MAX_M; ++step) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (cur >> 5 == i) anc[i] |= 1u << (cur & 31);
-                        const int p = cur == 0 ? -1 : a.parent ? s_par[cur] : cur - 1;
-                        if (p < 0 || p >= cur) break;
-                        cur = p;
-                    }
-                }
-                __syncwarp();
-            }
             const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
             const uint32_t tS = lane_base + w * 128, tO = lane_base + 256 + w * 128;
             const float c = a.c_log2;
             float m = -INFINITY, l = 0.0f;
-            // Tile j of this stream.  Masked tiles are a code of their own: the
-            // masks in the common one cost a quarter of its speed.
-            auto step = [&](auto masked, int j) {
-                constexpr bool MASKED = decltype(masked)::value;
+            for (int j = 0; j < n; ++j) {
                 if (ok) ok = mbar_wait_short(sfull + 8 * w, (uint32_t)(j & 1), a.err);
                 __syncwarp();
                 tc_fence_after();
-                const int tile = pair ? j : 2 * j + w, p0 = k0 + tile * CR;
-                uint32_t sees[4];
-                if constexpr (MASKED) {
-                    // bit i: position p0 + i is before the tree, or a node this row
-                    // sees; and inside the part
-                    const int old = tree0 - p0, in = k1 - p0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v = bits_below(old - 32 * i);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {  // word x of the nodes starts at bit old + 32 x
-                            const int sh = old + 32 * (x - i);
-                            if (sh >= 0 && sh < 32) v |= anc[x] << sh;
-                            if (sh < 0 && sh > -32) v |= anc[x] >> -sh;
-                        }
-                        sees[i] = v & bits_below(in - 32 * i);
-                    }
-                }
                 float s[128];
                 // each quarter's maximum is taken while the next one is on its way
                 tmem_ld32(tS, s);
@@ -275,9 +204,6 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                 for (int q = 0; q < 4; ++q) {
                     tmem_wait_ld();
                     if (q < 3) tmem_ld32(tS + 32 * (q + 1), s + 32 * (q + 1));
-                    if constexpr (MASKED)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[32 * q + i] = (sees[q] >> i) & 1u ? s[32 * q + i] : -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         mx[0] = max3(mx[0], s[32 * q + i], s[32 * q + i + 1]);
@@ -305,29 +231,6 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                             tmem_st32(tO + 32 * i, u);
                         }
                     }
-                }
-                if constexpr (MASKED) {
-                    // V from the tree on: finite, or set to 0 (see above)
-                    const int use = tile + (tile + 2 < ntiles ? tile + 2 : ntiles), st = use % CSLOTS;
-                    if (ok) ok = mbar_wait_short(full + 8 * st, (uint32_t)((use / CSLOTS) & 1), a.err);
-                    __syncwarp();
-                    const int lo = tree0 > p0 ? tree0 - p0 : 0;
-                    bool odd = false;
-                    for (int i = lo * (D / 8) + r; i < CR * (D / 8); i += CR) {
-                        const int vr = i / (D / 8), ch = i % (D / 8);
-                        uint4 *x = reinterpret_cast<uint4 *>(s_ring + st * T::BYTES + (ch >> 3) * T::BOX + swz128(vr, ch & 7));
-                        uint4 u = *x;
-                        if (clear_nonfinite<BF>(u.x) | clear_nonfinite<BF>(u.y) | clear_nonfinite<BF>(u.z) |
-                            clear_nonfinite<BF>(u.w)) {
-                            *x = u;
-                            odd = true;
-                        }
-                    }
-                    if (odd) {
-                        s_odd[w] = 1;
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * c;
                 const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
@@ -360,13 +263,6 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pready + 8 * w);
-            };
-            for (int j = 0; j < n; ++j) {
-                const int p0 = k0 + (pair ? j : 2 * j + w) * CR;
-                if (!own || (p0 + CR <= tree0 && p0 + CR <= k1))
-                    step(std::false_type{}, j);
-                else if constexpr (own)
-                    step(std::true_type{}, j);
             }
             // a stream's O is complete with its last product; both streams' where
             // they are added up, through the ring that nothing reads any more
@@ -380,16 +276,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
             float mb = m == -INFINITY ? -INFINITY : m * c;  // in base-2 units
             float scale = 1.0f, other = 0.0f;
             float *box = reinterpret_cast<float *>(s_ring);  // [D][128 rows], then m, l
-            bool odd = false;
-            if (own && k1 > tree0) {
-                if (w)
-                    named_barrier(3, 128);
-                else
-                    named_barrier(2, 128);
-                odd = s_odd[w] != 0;
-            }
-            // O of this thread's row, dimensions 32 i .. 32 i + 31, and what the
-            // masked tiles' non-finite values add to the rows that see them
+            // O of this thread's row, dimensions 32 i .. 32 i + 31
             auto load_o = [&](int i, float (&o)[32]) {
                 if (n > 0) {
                     tmem_ld32(tO + 32 * i, o);
@@ -398,29 +285,6 @@ __global__ void __launch_bounds__(CTHREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.0f;
                 }
-                if (!odd) return;
-                for (int t = 0; t < nodes; ++t) {
-                    const int p = tree0 + t;
-                    uint32_t word = 0;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (t >> 5 == x) word = anc[x];
-                    if (!((word >> (t & 31)) & 1u) || p < k0 || p >= k1 || (((p - k0) / CR) & 1) != w) continue;
-                    const int page = a.table[(size_t)slot * a.max_pages + (p >> a.page_shift)];
-                    if (page < 0 || page >= a.n_pages) continue;
-                    const int ps = 1 << a.page_shift;
-                    const uint16_t *v = reinterpret_cast<const uint16_t *>(
-                                            a.pool + (size_t)a.v_plane * (size_t)a.plane_bytes +
-                                            (((size_t)page * a.Hkv + hk) * ps + (p & (ps - 1))) * (size_t)(2 * D)) +
-                                        32 * i;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        uint32_t one = v[e];
-                        const float f = BF ? __uint_as_float(one << 16) : __half2float(__ushort_as_half((unsigned short)one));
-                        if (clear_nonfinite<BF>(one)) o[e] += f;
-                    }
-                }
-                __syncwarp();
             };
             if (!pair) {
                 if (w == 1) {
@@ -471,7 +335,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
         // ---------------------------------------------------------- K, V ---
         // the order in which the MMAs use them: pair K0 V0 K1 V1 ...; else
         // K0 K1 V0 K2 V1 K3 ...
-        const int32_t *row = a.table + (size_t)(ntiles > 0 ? slot : 0) * a.max_pages;
+        const int32_t *row = a.table + (size_t)(ntiles > 0 ? seq.slot : 0) * a.max_pages;
         int i = 0;
         bool ok = true;
         auto put = [&](int tile, int plane) {
@@ -588,37 +452,377 @@ __global__ void __launch_bounds__(CTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// The own parts of draft trees: one query tile (at most 128 rows of a sequence)
+// against its own positions, few tiles of them, so what counts is how fast a
+// part starts and ends.  Two thread blocks an SM (half the tensor memory, a K
+// and a V tile, 192 threads each) hide that in one another; there is one stream
+// of tiles, whose scores are read twice from tensor memory instead of being
+// held in registers, and warps whose 32 rows are all past the tile's end leave
+// out the softmax.
+//   warps 0-3 softmax, warp 4 K and V tiles, warp 5 the MMAs
+constexpr int OTHREADS = 192;
+constexpr size_t OSMEM = 1024 + 3 * (size_t)TcTile<128>::BYTES + 128 + HQ_MAX_M * 4;  // D = 64: as much, two blocks an SM
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(OTHREADS, 2)
+    k_prefix_own(const PrefixArgs a, const PrefixPlan pl, const __grid_constant__ CUtensorMap map) {
+    using T = TcTile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *s_q = sm, *s_k = sm + T::BYTES, *s_v = sm + 2 * T::BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + 3 * T::BYTES);
+    const uint32_t kfull = smem_addr(bars), kempty = kfull + 8, vfull = kfull + 16, vempty = kfull + 24, sfull = kfull + 32,
+                   phalf = kfull + 40, pready = kfull + 48, ofull = kfull + 56, qready = kfull + 64;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(bars + 9);
+    volatile int *s_odd = reinterpret_cast<int *>(s_tmem + 1);  // values of V have been set to 0
+    int32_t *s_par = reinterpret_cast<int32_t *>(s_tmem + 2);   // [HQ_MAX_M]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 9; ++i) mbar_init(kfull + 8 * i, i == 5 || i == 6 || i == 8 ? 4 : 1);
+        *s_odd = 0;
+        fence_mbar_init();
+    }
+    // Behind shared parts nothing is waited for: each of their blocks has itself
+    // waited for the call's inputs, and taken its tensor memory, before these
+    // may start, and the SMs that they leave idle, or are done with, begin here
+    // at once.  Only this grid's end, which the merge waits for, must not come
+    // before theirs (see the end).
+    const bool behind = pl.tc_shared;
+    if (!behind) pdl_wait();
+    if (warp == 5) tmem_alloc(smem_addr(s_tmem), 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;  // 128 columns of scores, then O
+    pdl_launch_dependents();
+
+    // which part this block is; nothing to do (ntiles 0) where no row uses it
+    int unit = blockIdx.x;
+    const int hk = unit % a.Hkv;
+    unit /= a.Hkv;
+    const int b = unit / (pl.ns * pl.stiles);
+    unit %= pl.ns * pl.stiles;
+    const int part = unit / pl.stiles, row0 = (unit % pl.stiles) * CR;
+    const Seq seq = seq_of(a, b);
+    const int first = seq.first, nodes = seq.m, nrows = seq.m * a.G, slot = seq.slot, tree0 = seq.len - seq.m;
+    const int k0 = pl.s0 + part * pl.schunk, k1 = seq.len - k0 > pl.schunk ? k0 + pl.schunk : seq.len;
+    const int ntiles = seq.live && row0 < nrows && k0 < k1 ? (k1 - k0 + CR - 1) / CR : 0;
+
+    if (warp < 4 && ntiles > 0) {
+        // ------------------------------------------------------- softmax ---
+        const int r = threadIdx.x, row = row0 + r;  // row of the tile, among the sequence's
+        const bool idle = row0 + warp * 32 >= nrows;
+        bool ok = true;
+        {
+            // the query rows, swizzled as the tensor core reads them
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const uint16_t *>(a.q) +
+                (row < nrows ? (size_t)(first + row / a.G) * a.ldq + (size_t)(hk * a.G + row % a.G) * D : 0));
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(s_q + (c >> 3) * T::BOX + swz128(r, c & 7)) =
+                    row < nrows ? src[c] : make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+        // the tree nodes this row sees (without `parent`: a chain)
+        uint32_t anc[4] = {0u, 0u, 0u, 0u};
+        if (k1 > tree0) {
+            if (a.parent) {
+                for (int i = r; i < nodes; i += 128) s_par[i] = a.parent[first + i];
+                named_barrier(1, 128);
+            }
+            if (row < nrows) {
+                int cur = row / a.G;
+                for (int step = 0; step < HQ_MAX_M; ++step) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (cur >> 5 == i) anc[i] |= 1u << (cur & 31);
+                    const int p = cur == 0 ? -1 : a.parent ? s_par[cur] : cur - 1;
+                    if (p < 0 || p >= cur) break;
+                    cur = p;
+                }
+            }
+            __syncwarp();
+        }
+        const uint32_t tS = tmem + ((uint32_t)warp << 21), tO = tS + 128;  // this warp's 32 lanes
+        const float c = a.c_log2;
+        float m = -INFINITY, l = 0.0f;
+        // masked tiles are a code of their own: the masks slow the common one down
+        auto step = [&](auto masked, int j) {
+            constexpr bool MASKED = decltype(masked)::value;
+            const int p0 = k0 + j * CR;
+            if (ok) ok = mbar_wait_short(sfull, (uint32_t)(j & 1), a.err);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t sees[4];
+            if constexpr (MASKED) {
+                // bit i: position p0 + i is before the tree, or a node this row
+                // sees; and inside the part
+                const int old = tree0 - p0, in = k1 - p0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v = bits_below(old - 32 * i);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {  // word x of the nodes starts at bit old + 32 x
+                        const int sh = old + 32 * (x - i);
+                        if (sh >= 0 && sh < 32) v |= anc[x] << sh;
+                        if (sh < 0 && sh > -32) v |= anc[x] >> -sh;
+                    }
+                    sees[i] = v & bits_below(in - 32 * i);
+                }
+            }
+            auto scores = [&](int q, float (&s)[32]) {
+                tmem_ld32(tS + 32 * q, s);
+                tmem_wait_ld();
+                if constexpr (MASKED)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[i] = (sees[q] >> i) & 1u ? s[i] : -INFINITY;
+            };
+            if (!idle) {
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float s[32];
+                    scores(q, s);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        mx[0] = max3(mx[0], s[i], s[i + 1]);
+                        mx[1] = max3(mx[1], s[i + 2], s[i + 3]);
+                    }
+                }
+                const float top = fmaxf(mx[0], mx[1]);
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool raise = (top - m) * c > LAZY;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float mn = raise ? top : m;
+                        const float al = raise ? ex2((m - mn) * c) : 1.0f;
+                        m = mn;
+                        l *= al;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            float o[32];
+                            uint32_t u[32];
+                            tmem_ld32(tO + 32 * i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * al);
+                            tmem_st32(tO + 32 * i, u);
+                        }
+                    }
+                }
+            }
+            if constexpr (MASKED) {
+                // V from the tree on: finite, or set to 0 (see above)
+                if (ok) ok = mbar_wait_short(vfull, (uint32_t)(j & 1), a.err);
+                __syncwarp();
+                const int lo = tree0 > p0 ? tree0 - p0 : 0;
+                bool odd = false;
+                for (int i = lo * (D / 8) + r; i < CR * (D / 8); i += CR) {
+                    const int vr = i / (D / 8), ch = i % (D / 8);
+                    uint4 *x = reinterpret_cast<uint4 *>(s_v + (ch >> 3) * T::BOX + swz128(vr, ch & 7));
+                    uint4 u = *x;
+                    if (clear_nonfinite<BF>(u.x) | clear_nonfinite<BF>(u.y) | clear_nonfinite<BF>(u.z) |
+                        clear_nonfinite<BF>(u.w)) {
+                        *x = u;
+                        odd = true;
+                    }
+                }
+                if (odd) {
+                    *s_odd = 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+            }
+            const float mc = m == -INFINITY ? 0.0f : m * c;
+            const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
+            f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!idle) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float s[32];
+                        scores(2 * h + q, s);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x, y;
+                            f2_split(f2_fma(f2_make(s[2 * i], s[2 * i + 1]), cc, mm), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            sum[i & 1] = f2_add(sum[i & 1], f2_make(x, y));
+                            p[16 * q + i] = pack16<BF>(x, y);
+                        }
+                    }
+                    tmem_st32(tS + 32 * h, p);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(h ? pready : phalf);  // the product may start on the first half
+            }
+            float x0, x1, x2, x3;
+            f2_split(sum[0], x0, x1);
+            f2_split(sum[1], x2, x3);
+            l += (x0 + x1) + (x2 + x3);
+        };
+        for (int j = 0; j < ntiles; ++j) {
+            const int p0 = k0 + j * CR;
+            if (p0 + CR <= tree0 && p0 + CR <= k1)
+                step(std::false_type{}, j);
+            else
+                step(std::true_type{}, j);
+        }
+        if (ok) ok = mbar_wait_short(ofull, 0u, a.err);
+        __syncwarp();
+        tc_fence_after();
+        if (k1 > tree0) named_barrier(1, 128);
+        const bool odd = k1 > tree0 && *s_odd != 0;
+        if (l == 0.0f) m = -INFINITY;  // no finite score: adds nothing
+        if (!idle) {
+            const size_t at = ((size_t)(pl.np + part) * a.rows + first + row / a.G) * a.Hq + hk * a.G + row % a.G;
+            float4 *dst = reinterpret_cast<float4 *>(a.ws_o + at * D);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float o[32];
+                tmem_ld32(tO + 32 * i, o);
+                tmem_wait_ld();
+                if (odd) {  // what the masked tiles' non-finite values add to the rows that see them
+                    for (int t = 0; t < nodes; ++t) {
+                        const int p = tree0 + t;
+                        uint32_t word = 0;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (t >> 5 == x) word = anc[x];
+                        if (!((word >> (t & 31)) & 1u) || p < k0 || p >= k1) continue;
+                        const int page = a.table[(size_t)slot * a.max_pages + (p >> a.page_shift)];
+                        if (page < 0 || page >= a.n_pages) continue;
+                        const int ps = 1 << a.page_shift;
+                        const uint16_t *v = reinterpret_cast<const uint16_t *>(
+                                                a.pool + (size_t)a.v_plane * (size_t)a.plane_bytes +
+                                                (((size_t)page * a.Hkv + hk) * ps + (p & (ps - 1))) * (size_t)(2 * D)) +
+                                            32 * i;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            uint32_t one = v[e];
+                            const float f = BF ? __uint_as_float(one << 16) : __half2float(__ushort_as_half((unsigned short)one));
+                            if (clear_nonfinite<BF>(one)) o[e] += f;
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (row < nrows)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[8 * i + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                __syncwarp();
+            }
+            if (row < nrows)
+                *reinterpret_cast<float2 *>(a.ws_ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
+        }
+        tc_fence_before();
+    } else if (warp == 4) {
+        // ---------------------------------------------------------- K, V ---
+        const int32_t *row = a.table + (size_t)(ntiles > 0 ? slot : 0) * a.max_pages;
+        bool ok = true;
+        int nk = 0, nv = 0;
+        auto put = [&](int tile, int plane, uint8_t *dst, uint32_t fb, uint32_t eb, int &n) {
+            const int p = k0 + tile * CR;
+            const int page = lookup_page<CR>(a, row, p, k1);
+            if (ok && tile > 0) ok = mbar_wait_short(eb, (uint32_t)(tile & 1) ^ 1u, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)T::BYTES);
+            __syncwarp();
+            load_tile<CR, D>(a, &map, smem_addr(dst), p, hk, plane, page, fb);
+            __syncwarp();
+            ++n;
+        };
+        for (int t = 0; t < ntiles; ++t) {
+            put(t, a.k_plane, s_k, kfull, kempty, nk);
+            put(t, a.v_plane, s_v, vfull, vempty, nv);
+        }
+        // no copy may still be landing in shared memory when the block exits
+        if (nk > 0) mbar_wait_short(kfull, (uint32_t)((nk - 1) & 1), a.err);
+        if (nv > 0) mbar_wait_short(vfull, (uint32_t)((nv - 1) & 1), a.err);
+    } else if (warp == 5 && ntiles > 0) {
+        // ---------------------------------------------------------- MMAs ---
+        const uint32_t leader = elect_one() ? 1u : 0u;
+        const uint64_t dq = desc_swz128(smem_addr(s_q), 16, 1024), dk = desc_swz128(smem_addr(s_k), 16, 1024);
+        const uint64_t dv = desc_swz128(smem_addr(s_v), T::BOX, 1024);
+        constexpr uint32_t id_s = idesc_of<BF>(CR, false), id_o = idesc_of<BF>(D, true);
+        bool ok = mbar_wait_short(qready, 0u, a.err);
+        for (int j = 0; j < ntiles; ++j) {
+            // S = Q K^T.  (The products of the tile before, which read P where S
+            // goes, were issued first and complete first.)
+            if (ok) ok = mbar_wait_short(kfull, (uint32_t)(j & 1), a.err);
+            __syncwarp();
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t o = (uint64_t)((ks >> 2) * (T::BOX / 16) + (ks & 3) * 2);
+                tc_mma_ss_if(leader, tmem, dq + o, dk + o, id_s, ks > 0);
+            }
+            tc_commit_if(leader, sfull);
+            tc_commit_if(leader, kempty);
+            // O += P V
+            if (ok) ok = mbar_wait_short(vfull, (uint32_t)(j & 1), a.err);
+#pragma unroll
+            for (int ks = 0; ks < CR / 16; ++ks) {
+                if (ks == 0 || ks == CR / 32) {
+                    if (ok) ok = mbar_wait_short(ks ? pready : phalf, (uint32_t)(j & 1), a.err);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+                tc_mma_f16_ts_if(leader, tmem + 128, tmem + ks * 8, dv + (uint64_t)(ks * 128), id_o, j > 0 || ks > 0);
+            }
+            tc_commit_if(leader, vempty);
+        }
+        tc_commit_if(leader, ofull);
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem, 256);
     if (behind && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
-template <int D, bool BF, int MODE>
-cudaError_t launch_mode(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+template <class F>
+cudaError_t launch_part(F f, std::atomic<int> (&configured)[CACHE_DEVICES], long long grid, int threads, size_t smem, const PrefixArgs &a,
+                        const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> configured[CACHE_DEVICES];
     int done = 0;
     e = cached_per_device(configured, dev, &done, [&](int *v) {
         *v = 1;
-        return cudaFuncSetAttribute(k_prefix_tc<D, BF, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)TcTile<D>::SMEM);
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    const long long grid = a.Hkv * (MODE == OWN ? (long long)a.B * pl.ns * pl.stiles : (long long)pl.np * pl.ptiles);
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_kernel(k_prefix_tc<D, BF, MODE>, dim3((unsigned)grid), dim3(CTHREADS), TcTile<D>::SMEM, pdl, s, a, pl,
-                         map);
+    return launch_kernel(f, dim3((unsigned)grid), dim3(threads), smem, pdl, s, a, pl, map);
 }
 
 template <int D, bool BF>
-cudaError_t launch_modes(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+cudaError_t launch_parts(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, bool pdl, cudaStream_t s) {
+    static std::atomic<int> pair[CACHE_DEVICES], single[CACHE_DEVICES], own[CACHE_DEVICES];
     if (pl.tc_shared) {
-        const cudaError_t e = (long long)a.rows * a.G > CR ? launch_mode<D, BF, PAIR>(a, pl, map, pdl, s)
-                                                           : launch_mode<D, BF, ALTERNATE>(a, pl, map, pdl, s);
+        const long long grid = (long long)a.Hkv * pl.np * pl.ptiles;
+        const cudaError_t e =
+            (long long)a.rows * a.G > CR
+                ? launch_part(k_prefix_tc<D, BF, true>, pair, grid, CTHREADS, TcTile<D>::SMEM, a, pl, map, pdl, s)
+                : launch_part(k_prefix_tc<D, BF, false>, single, grid, CTHREADS, TcTile<D>::SMEM, a, pl, map, pdl, s);
         if (e != cudaSuccess) return e;
         pdl = true;
     }
-    return pl.tc_own ? launch_mode<D, BF, OWN>(a, pl, map, pdl, s) : cudaSuccess;
+    if (!pl.tc_own) return cudaSuccess;
+    return launch_part(k_prefix_own<D, BF>, own, (long long)a.Hkv * a.B * pl.ns * pl.stiles, OTHREADS, OSMEM, a, pl, map, pdl, s);
 }
 
 }  // namespace
@@ -626,8 +830,8 @@ cudaError_t launch_modes(const PrefixArgs &a, const PrefixPlan &pl, const CUtens
 cudaError_t launch_prefix_tc(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, int D, bool pdl,
                              cudaStream_t s) {
     const bool bf = a.type == HQ_BF16;
-    if (D == 128) return bf ? launch_modes<128, true>(a, pl, map, pdl, s) : launch_modes<128, false>(a, pl, map, pdl, s);
-    return bf ? launch_modes<64, true>(a, pl, map, pdl, s) : launch_modes<64, false>(a, pl, map, pdl, s);
+    if (D == 128) return bf ? launch_parts<128, true>(a, pl, map, pdl, s) : launch_parts<128, false>(a, pl, map, pdl, s);
+    return bf ? launch_parts<64, true>(a, pl, map, pdl, s) : launch_parts<64, false>(a, pl, map, pdl, s);
 }
 
 }  // namespace hq
