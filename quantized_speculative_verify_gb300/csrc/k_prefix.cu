@@ -10,7 +10,7 @@
 // them.  The parts of a row:
 //   - the shared positions, in whole tiles of 64: all rows of the batch that
 //     read one key/value head (rows * G of them) are one matrix, cut into
-//     tiles of 64 rows; long prefixes are split further;
+//     tiles of rows; long prefixes are split further;
 //   - the sequence's own positions (with what the shared ones leave over of a
 //     tile), for the sequence's own rows only.
 // Shared tiles have no mask at all; the own positions end with the tree.
@@ -22,7 +22,12 @@
 // accumulation and an online softmax in base-2 units: KW of them share 16 rows
 // and take every KW-th group of 16 positions of a tile (a single token's few
 // rows do not fill more than one warp's MMA), 4 / KW row groups to a block; at
-// the end the warps of a row group merge in shared memory.
+// the end the warps of a row group merge in shared memory.  What bounds it is
+// memory where there are many blocks: 128 sequences' own positions, 270 MB in 50
+// us = 5.4 TB/s (beside the shared parts: less, see launch_prefix_attention);
+// the chain sequence - page - tile - merge where there are few: 4 rows, 1000
+// shared and up to 200 own positions, 11 us for both kernels.
+// Many rows go to the tensor-memory kernels of k_prefix_tc.cu.
 #include "prefix_common.cuh"
 
 namespace hq {
@@ -32,10 +37,22 @@ constexpr int XKEYS = 64;     // positions per stage
 constexpr int XSTAGES = 3;
 constexpr int XCW = 4;        // consumer warps
 constexpr int XTHREADS = (XCW + 1) * 32;
-constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the tensor-memory kernel
-constexpr int TC_ROWS = 65;
-constexpr int TC_SHARED = 512;
-constexpr int TC_ROWS_OWN = 33;
+constexpr int TC_KEYS = 128;    // positions (and query rows) of a tile of the tensor-memory kernels
+// Times below: whole calls replayed from a graph, cold L2 cache, 32 query and 8
+// key/value heads of 128, bf16.
+// From TC_ROWS rows a head on, and with at least one of its tiles, the shared
+// parts go to the tensor-memory kernel.  With it and without: 32 rows on 4096
+// shared positions 23.7 us both; 48 on 1000 24 and 27; 64 on 32768 50 and 79;
+// 256 on 4096 46 and 79.
+constexpr int TC_ROWS = 33;
+// From TC_ROWS_OWN rows a head on so do a sequence's own parts.  16 sequences of
+// 700 own positions behind 2048 shared: 16 rows 37 and 34 us; 20 rows 35 and 37;
+// 32 rows 37 and 40; 48 rows 38 and 47.  A lone tree takes its prefix along: 32
+// rows on 2048 + 700 positions 19 us, 22 with the prefix apart.
+constexpr int TC_ROWS_OWN = 17;
+// In the time of one tile of the shared parts' tensor-memory kernel (1.6 us) an
+// SM takes about this many own positions of a head, in k_prefix_attn and in
+// k_prefix_own.
 constexpr int OWN_POS = 160, OWN_POS_TC = 35;
 constexpr int MAX_PARTS = 64;   // shared_parts + own_parts, at most 32 each
 
@@ -403,7 +420,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 1);
         lrun[h] += __shfl_xor_sync(0xffffffffu, lrun[h], 2);
     }
-    if constexpr (KW > 1) {
+    {
         // The warps of a row group merge through the ring, which nothing
         // writes any more: every tile has arrived and been read.
         float *box = reinterpret_cast<float *>(ring);  // [consumer warp][D / 8 * 4 + 4][32 lanes]
@@ -469,7 +486,8 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 // of one head over every PG-th part (PG groups of threads where the heads
 // alone do not fill the block), 8 loads in flight, and the groups add up in
 // order.  What bounds it is the chain of dependent loads (row -> sequence ->
-// maxima -> outputs), so the sequence is found by all threads at once.
+// maxima -> outputs): the sequence is found by all threads at once and before
+// the wait for the parts.  551 rows of 32 heads in 3 parts, 27 MB: 13 us.
 template <int D, int HG>
 __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const PrefixPlan pl) {
     constexpr int COLS = HG * D / 4;            // float4 columns
@@ -656,17 +674,16 @@ cudaError_t launch_t(const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMa
 template <int D, bool BF>
 cudaError_t launch_kw(int kw, const PrefixArgs &a, const PrefixPlan &pl, const CUtensorMap &map, unsigned grid, bool pdl,
                       cudaStream_t s) {
-    return kw == 4   ? launch_t<D, BF, 4>(a, pl, map, grid, pdl, s)
-           : kw == 2 ? launch_t<D, BF, 2>(a, pl, map, grid, pdl, s)
-                     : launch_t<D, BF, 1>(a, pl, map, grid, pdl, s);
+    return kw == 4 ? launch_t<D, BF, 4>(a, pl, map, grid, pdl, s) : launch_t<D, BF, 2>(a, pl, map, grid, pdl, s);
 }
 
 template <int D>
 cudaError_t launch_merge(const PrefixArgs &a, const PrefixPlan &pl, int sms, cudaStream_t s) {
-    // 8 heads a block where that gives every SM two, fewer heads and more
-    // threads on the parts of each where rows are few
+    // 8 heads a block where that gives every SM one, fewer heads and more
+    // threads on the parts of each where rows are few.  Whole calls with 8, 2
+    // and 1 heads: 64 rows 36, 38, 40 us; 4 rows 21.6, 16.5, 15.5 us.
     auto grid = [&](int hg) { return dim3((unsigned)a.rows, (unsigned)((a.Hq + hg - 1) / hg)); };
-    auto enough = [&](int hg) { return (long long)a.rows * ((a.Hq + hg - 1) / hg) >= 2LL * sms; };
+    auto enough = [&](int hg) { return (long long)a.rows * ((a.Hq + hg - 1) / hg) >= sms; };
     if (enough(8)) return launch_kernel(k_prefix_merge<D, 8>, grid(8), dim3(256), 0, true, s, a, pl);
     if (enough(2)) return launch_kernel(k_prefix_merge<D, 2>, grid(2), dim3(256), 0, true, s, a, pl);
     return launch_kernel(k_prefix_merge<D, 1>, grid(1), dim3(256), 0, true, s, a, pl);
@@ -685,21 +702,22 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     const long long n = (long long)a.rows * a.Hq;
     const int pcap = shared_parts(n), scap = own_parts(n, a.B, a.max_rows, a.Hkv, a.G);
     const long long head_rows = (long long)a.rows * a.G, seq_rows = (long long)a.max_rows * a.G;
-    // The tensor-memory kernel takes the shared parts from TC_ROWS rows a head
-    // on, where they are bound by the products, and prefixes of several tiles;
-    // and the own parts of sequences with TC_ROWS_OWN rows a head or more,
-    // which then take a short prefix along.  (A scale below 0 would turn its
-    // maximum into a minimum, a scale of 0 its masks into NaN.)
+    // Which kernel takes which parts: see TC_ROWS.  A short prefix goes with the
+    // own parts; so does the prefix of a lone draft tree.  (In the tensor-memory
+    // kernels a scale below 0 would turn the maximum into a minimum, a scale of
+    // 0 the masks into NaN.)
     PrefixPlan pl;
-    pl.tc_shared = head_rows >= TC_ROWS && a.shared >= TC_SHARED && a.c_log2 > 0.0f;
-    pl.tc_own = seq_rows >= TC_ROWS_OWN && (pl.tc_shared || a.shared < TC_SHARED) && a.c_log2 > 0.0f;
-    const bool pair = head_rows > TC_KEYS;
-    // warps that share 16 rows, from the rows that a block of the other kernel has
-    const long long few = pl.tc_shared ? seq_rows : head_rows;
-    const int kw = few <= 16 ? 4 : few <= 32 ? 2 : 1, xrows = 64 / kw;
+    pl.tc_shared = head_rows >= TC_ROWS && a.shared >= TC_KEYS && a.c_log2 > 0.0f;
+    pl.tc_own = seq_rows >= TC_ROWS_OWN && (pl.tc_shared || a.shared < TC_KEYS || a.B == 1) && a.c_log2 > 0.0f;
+    const bool split = pl.tc_shared || (!pl.tc_own && a.shared >= TC_KEYS), pair = head_rows > TC_KEYS;
+    // Warps that share 16 rows, from the rows that a block of the other kernel
+    // has.  64 sequences of 2000 positions: 16 rows each 108 us with four, 114
+    // with two (one: 204); 32 rows each 128 and 120.
+    const long long few = split && !pl.tc_shared ? head_rows : seq_rows;
+    const int kw = few <= 16 ? 4 : 2, xrows = 64 / kw;
     const int pkey = pl.tc_shared ? TC_KEYS : XKEYS, skey = pl.tc_own ? TC_KEYS : XKEYS;
     const int prows = !pl.tc_shared ? xrows : pair ? 2 * TC_KEYS : TC_KEYS, srows = pl.tc_own ? TC_KEYS : xrows;
-    pl.s0 = pl.tc_own && !pl.tc_shared ? 0 : a.shared / pkey * pkey;
+    pl.s0 = split ? a.shared / pkey * pkey : 0;
     pl.ptiles = (int)((head_rows + prows - 1) / prows);
     pl.stiles = (int)((seq_rows + srows - 1) / srows);
     // whole tiles, and no more parts than the workspace holds
@@ -716,11 +734,12 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
     long long want = (2LL * sms + pblocks - 1) / pblocks;
     if (pl.tc_shared) {
         // At most one block of the tensor-memory kernel per SM.  The SMs that
-        // are left over work on the own parts meanwhile, so a few blocks less
-        // end earlier than all: the count with the least estimated time, in
-        // units of a block's tile (1.6 us).  In that time an SM reads OWN_POS
-        // own positions of a head, and all of them together, bound by memory,
-        // two thirds as many each; sequences have half the largest length.
+        // are left over work on the own parts meanwhile, so fewer blocks than
+        // SMs can end earlier: the count with the least estimated time, in units
+        // of a block's tile.  All SMs together, bound by memory, take own parts
+        // at two thirds of a single one's rate; sequences have half the largest
+        // length.  (128 rows, 32768 shared and up to 1024 own positions: 144
+        // blocks 113 us, 112 106, 96 and 80 96, 64 112.)
         const long long tiles = pl.s0 / TC_KEYS, own = sblocks * (a.max_len - pl.s0) / (2 * (pl.tc_own ? OWN_POS_TC : OWN_POS));
         long long best = -1;
         for (long long np = 1; np <= pcap && (np == 1 || np * pblocks <= sms); ++np) {
