@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
     unit /= a.Hkv;
     const int nshared = pl.tc_shared ? 0 : pl.np * pl.ptiles;
     int split, rt, first, nrows, k0, k1, slot, tree0 = 0x7fffffff, nodes = 0, ntiles = 0;
+    int early = -1;  // the producer's table entries of the first tile
     if (unit < nshared) {
         split = unit / pl.ptiles;
         rt = unit % pl.ptiles;
@@ -166,11 +167,12 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         unit %= pl.ns * pl.stiles;
         split = unit / pl.stiles;
         rt = unit % pl.stiles;
+        k0 = pl.s0 + split * pl.schunk;
+        if (warp == XCW) early = early_entry<XKEYS>(a, b, k0);
         const Seq s = seq_of(a, b);
         first = s.first;
         nodes = s.m;
         nrows = s.m * a.G;
-        k0 = pl.s0 + split * pl.schunk;
         k1 = s.len - k0 > pl.schunk ? k0 + pl.schunk : s.len;
         slot = s.slot;
         tree0 = s.len - s.m;
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         int i = 0;
         for (; i < ntiles; ++i) {
             const int st = i % XSTAGES, p = k0 + i * XKEYS;
-            const int page = lookup_page<XKEYS>(a, row, p, k1);
+            const int page = i == 0 && nodes > 0 ? checked_page<XKEYS>(a, early, p, k1) : lookup_page<XKEYS>(a, row, p, k1);
             if (i >= XSTAGES &&
                 !mbar_wait_short(smem_addr(&bars[XSTAGES + st]), (uint32_t)((i / XSTAGES) & 1) ^ 1u, a.err))
                 break;

@@ -513,9 +513,12 @@ __global__ void __launch_bounds__(OTHREADS, 2)
     const int b = unit / (pl.ns * pl.stiles);
     unit %= pl.ns * pl.stiles;
     const int part = unit / pl.stiles, row0 = (unit % pl.stiles) * CR;
+    const int k0 = pl.s0 + part * pl.schunk;
+    int early = -1;  // the table entries of the first tile
+    if (warp == 4) early = early_entry<CR>(a, b, k0);
     const Seq seq = seq_of(a, b);
     const int first = seq.first, nodes = seq.m, nrows = seq.m * a.G, slot = seq.slot, tree0 = seq.len - seq.m;
-    const int k0 = pl.s0 + part * pl.schunk, k1 = seq.len - k0 > pl.schunk ? k0 + pl.schunk : seq.len;
+    const int k1 = seq.len - k0 > pl.schunk ? k0 + pl.schunk : seq.len;
     const int ntiles = seq.live && row0 < nrows && k0 < k1 ? (k1 - k0 + CR - 1) / CR : 0;
 
     if (warp < 4 && ntiles > 0) {
@@ -742,7 +745,7 @@ __global__ void __launch_bounds__(OTHREADS, 2)
         int nk = 0, nv = 0;
         auto put = [&](int tile, int plane, uint8_t *dst, uint32_t fb, uint32_t eb, int &n) {
             const int p = k0 + tile * CR;
-            const int page = lookup_page<CR>(a, row, p, k1);
+            const int page = tile == 0 ? checked_page<CR>(a, early, p, k1) : lookup_page<CR>(a, row, p, k1);
             if (ok && tile > 0) ok = mbar_wait_short(eb, (uint32_t)(tile & 1) ^ 1u, a.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;

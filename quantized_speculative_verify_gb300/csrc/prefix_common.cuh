@@ -68,20 +68,36 @@ __device__ __forceinline__ Seq first_live(const PrefixArgs &a) {
 // the sequence's table; runs that start at or past `end` and bad pages arrive
 // as zeros.  `page` is the lane's page as lookup_page returned it.
 template <int TILE>
-__device__ __forceinline__ int lookup_page(const PrefixArgs &a, const int32_t *row, int p0, int end) {
+__device__ __forceinline__ int page_entry(const PrefixArgs &a, const int32_t *row, int p0, int end) {
     const int lane = threadIdx.x & 31;
     constexpr int SHIFT = TILE == 128 ? 7 : 6;
     const int sh = a.page_shift < SHIFT ? a.page_shift : SHIFT;
     const int p = p0 + (lane << sh);
-    int page = a.n_pages;  // outside the map: zeros
-    if (lane < (TILE >> sh) && p < end) {
-        page = row[p >> a.page_shift];
-        if (page < 0 || page >= a.n_pages) {
-            atomicExch(a.err, DEV_ERR_ARG);
-            page = a.n_pages;
-        }
+    return lane < (TILE >> sh) && p < end ? row[p >> a.page_shift] : a.n_pages;
+}
+template <int TILE>
+__device__ __forceinline__ int checked_page(const PrefixArgs &a, int page, int p0, int end) {
+    const int lane = threadIdx.x & 31;
+    constexpr int SHIFT = TILE == 128 ? 7 : 6;
+    const int sh = a.page_shift < SHIFT ? a.page_shift : SHIFT;
+    if (lane >= (TILE >> sh) || p0 + (lane << sh) >= end) return a.n_pages;  // outside the map: zeros
+    if (page < 0 || page >= a.n_pages) {
+        atomicExch(a.err, DEV_ERR_ARG);
+        return a.n_pages;
     }
     return page;
+}
+template <int TILE>
+__device__ __forceinline__ int lookup_page(const PrefixArgs &a, const int32_t *row, int p0, int end) {
+    return checked_page<TILE>(a, page_entry<TILE>(a, row, p0, end), p0, end);
+}
+// The table entries of the first tile of a sequence's part, on their way beside
+// its length (which tells where they end) instead of after it.
+template <int TILE>
+__device__ __forceinline__ int early_entry(const PrefixArgs &a, int b, int p0) {
+    const int slot = a.seqs ? a.seqs[b] : b;
+    if (slot < 0 || slot >= a.n_seqs) return a.n_pages;
+    return page_entry<TILE>(a, a.table + (size_t)slot * a.max_pages, p0, a.max_pages << a.page_shift);
 }
 template <int TILE, int D>
 __device__ __forceinline__ void load_tile(const PrefixArgs &a, const CUtensorMap *map, uint32_t dst, int p0, int hk,

@@ -150,6 +150,9 @@ def _check(rc: int, what: str) -> None:
         raise HQError(rc, what)
 
 
+_Tensor = torch.Tensor
+
+
 def _ptr(t) -> int | None:
     """A device-pointer argument: None, a raw address (int), or a CUDA tensor
     (which must live on the current device: the library launches there; not
@@ -157,7 +160,11 @@ def _ptr(t) -> int | None:
     arrays are refused: the kernels read and write device memory, and on a
     system whose GPU can reach host memory a host buffer would not fault but
     run silently on host memory."""
-    if t is None:
+    # (isinstance with torch.Tensor runs its metaclass's check: 0.3 us)
+    if type(t) is _Tensor:
+        if t.is_cuda:
+            return t.data_ptr()
+    elif t is None:
         return None
     if isinstance(t, int):
         return t
