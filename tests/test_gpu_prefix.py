@@ -471,3 +471,23 @@ def test_large_trees_match_64_bits(B, m, shared, own, Hq, Hkv, D, ps, dtype):
         assert t.status == hq.HQ_OK
         t.check(got)
         assert torch.equal(got, t.run())
+
+
+@pytest.mark.parametrize("B,m,shared,own,Hq,Hkv,D,ps,dtype", [
+    (1, 16, 2000, 300, 2, 2, 128, 16, F16), (1, 17, 2000, 300, 2, 2, 128, 16, F16), (1, 5, 5000, 0, 8, 2, 64, 128, BF16),
+    (8, 1, 128, 50, 8, 2, 128, 64, BF16), (9, 1, 128, 50, 8, 2, 128, 64, BF16), (9, 1, 127, 50, 8, 2, 128, 64, BF16),
+    (33, 1, 129, 0, 1, 1, 64, 16, F16), (32, 1, 129, 300, 1, 1, 64, 16, F16), (2, 8, 100, 900, 4, 1, 128, 32, F16),
+    (2, 4, 900, 900, 4, 1, 128, 32, F16), (2, 17, 130, 700, 1, 1, 64, 32, BF16), (128, 1, 3000, 1000, 8, 2, 128, 64, BF16),
+    (48, 16, 1234, 700, 8, 2, 128, 32, F16), (70, 1, 0, 1500, 8, 2, 128, 16, F16), (20, 6, 256, 1, 16, 4, 64, 16, BF16),
+])
+def test_sizes_where_another_kernel_takes_over(B, m, shared, own, Hq, Hkv, D, ps, dtype):
+    rows = [m] + spread(B - 1, 1, m, B)
+    lens = [shared + own + m] + [shared + x + r for x, r in zip(spread(B - 1, 0, own, B + 1), rows[1:])]
+    t = Batch(lens, rows, shared, Hq, Hkv, D, ps, dtype, seed=B + m + shared)
+    got = t.run().clone()
+    assert t.status == hq.HQ_OK
+    t.check(got)
+    ws = Guarded((hq.hq_prefix_attention_workspace_bytes(B, t.starts[-1], m, Hq, Hkv, D),), torch.uint8, DEV, fill=0)
+    for flags in (0, hq.HQ_LAUNCH_PDL, hq.HQ_LAUNCH_PDL):  # one workspace, calls on each other's heels
+        assert torch.equal(got, t.run(flags=flags, workspace=ws))
+    assert t.status == hq.HQ_OK
