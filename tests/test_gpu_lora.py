@@ -148,3 +148,34 @@ def test_lora_on_a_side_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     check(Y, x, A, B, ids, None, scale, base)
+
+
+@pytest.mark.parametrize("step", [1, 256, 65536, 77777])
+def test_lora_ids_from_a_large_pool(step):
+    """Ids far apart, many of them in the same places of a hash table, twice and five times each."""
+    M, K, N, r = 128, 32, 40, 8
+    n = min(128 * step, 400000)
+    x, A, B, base, scale, g = make(M, K, N, n, r, BF16, BF16, seed=step)
+    pool = (torch.arange(128, device=DEV) * step) % n
+    ids = pool[torch.randint(0, 64, (M,), generator=g, device=DEV)].to(torch.int32)
+    ids[torch.randperm(M, generator=g, device=DEV)[:20]] = ids[0].clone()
+    ids[5], ids[77] = -7, n  # none
+    Y = hq.lora_apply(x, A, B, ids, None, scale, base=base)
+    check(Y, x, A, B, ids, None, scale, base)
+
+
+@pytest.mark.parametrize("wt", [F16, BF16])
+def test_lora_does_not_touch_what_is_past_a_rank_with_many_rows(wt):
+    M, K, N, r = 60, 96, 70, 136
+    x, A, B, base, scale, g = make(M, K, N, 4, r, F32, wt, seed=14)
+    ranks = torch.tensor([5, 0, 70, 131], dtype=torch.int32, device=DEV)
+    for a, k in enumerate(ranks.tolist()):
+        A[a, k:] = float("nan")
+        B[a, :, k:] = float("nan")
+    ids = (torch.arange(M, device=DEV) % 5 - 1).to(torch.int32)
+    x[0] = float("nan")  # no adapter
+    x[8] = float("inf")  # its own row only
+    Y = hq.lora_apply(x, A, B, ids, ranks, scale, base=base)
+    good = [i for i in range(M) if i != 8]
+    check(Y[good], x[good], A, B, ids[good], ranks, scale, base[good])
+    assert not torch.isfinite(Y[8]).any()
