@@ -150,7 +150,7 @@ def _check(rc: int, what: str) -> None:
         raise HQError(rc, what)
 
 
-_Tensor = torch.Tensor
+_Tensor, _INT32 = torch.Tensor, torch.int32
 
 
 def _ptr(t) -> int | None:
@@ -181,9 +181,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_cuda_ready = False  # once true it stays so
+
+
 def _stream(stream) -> int | None:
+    global _cuda_ready
     if stream is None:
+        if _cuda_ready:
+            return _raw_stream(_current_device())
         if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
+            _cuda_ready = True
             return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
@@ -525,6 +532,11 @@ def _rows(t, cols: int, what: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else cols
 
 
+def _pitch(t, cols: int, what: str) -> int:
+    """_rows of a tensor whose shape [rows][cols] has been checked."""
+    return cols if t is None or t.is_contiguous() else _rows(t, cols, what)
+
+
 def _dense(t, dtype, shape, what: str) -> None:
     """A contiguous tensor of the given type and shape, or None."""
     if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
@@ -537,7 +549,7 @@ def _shaped(t, shape, what: str) -> None:
 
 
 def _room(t, need: int, what: str) -> None:
-    if t.numel() * t.element_size() < need:
+    if t.nbytes < need:
         raise ValueError(f"{what} is too small: {need} bytes needed")
 
 
@@ -560,12 +572,14 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     itself.  weight fp32 [K]."""
     shape = x.shape
     M, K = shape
-    if x.dtype not in TYPES:
+    x_type = TYPES.get(x.dtype)
+    if x_type is None:
         raise TypeError(f"add_norm_quant: fp32, fp16 or bf16 expected, got {x.dtype}")
     if K != desc.K:
         raise ValueError(f"add_norm_quant: x has {K} features, the layer {desc.K}")
     _shaped(residual, shape, "add_norm_quant: residual")
-    _shaped(residual_out, shape, "add_norm_quant: residual_out")
+    if residual_out is not residual:
+        _shaped(residual_out, shape, "add_norm_quant: residual_out")
     _shaped(h, shape, "add_norm_quant: h")
     _dense(weight, torch.float32, (K,), "add_norm_quant: weight")
     _dense(qx, torch.int8, shape, "add_norm_quant: qx")
@@ -575,12 +589,12 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     if qop is not None:
         _room(qop, hq_act_operand_bytes(desc, M), "add_norm_quant: qop")
     r = residual if residual is not None else residual_out
-    ldr = _rows(r, K, "residual")
+    ldr = _pitch(r, K, "residual")
     if residual is not None and residual_out is not None and residual_out is not residual and (
-            residual.dtype != residual_out.dtype or _rows(residual_out, K, "residual_out") != ldr):
+            residual.dtype != residual_out.dtype or _pitch(residual_out, K, "residual_out") != ldr):
         raise ValueError("add_norm_quant: residual and residual_out need the same type and stride")
-    ldx, ldh = _rows(x, K, "x"), _rows(h, K, "h")
-    rc = load().hq_add_norm_quant(ctypes.byref(desc), _ptr(x), _type(x), ldx, _ptr(residual), _ptr(residual_out), _type(r),
+    ldx, ldh = _pitch(x, K, "x"), _pitch(h, K, "h")
+    rc = load().hq_add_norm_quant(ctypes.byref(desc), _ptr(x), x_type, ldx, _ptr(residual), _ptr(residual_out), _type(r),
                                   ldr, _ptr(weight), eps, M, _ptr(signs), _ptr(h), _type(h), ldh, _ptr(qx), _ptr(gsum),
                                   _ptr(qop), _ptr(sx), flags, _stream(stream))
     if rc != HQ_OK:
@@ -613,18 +627,20 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     _dense(ids, torch.int32, (M,), "lora_apply: ids")
     _dense(ranks, torch.int32, (n,), "lora_apply: ranks")
     _dense(scale, torch.float32, (n,), "lora_apply: scale")
+    shape = (M, N)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=x.device)
-    _shaped(base, (M, N), "lora_apply: base")
-    _shaped(Y, (M, N), "lora_apply: Y")
+        Y = torch.empty(shape, dtype=torch.float32, device=x.device)
+    if base is not Y:
+        _shaped(base, shape, "lora_apply: base")
+    _shaped(Y, shape, "lora_apply: Y")
     if Y.dtype != torch.float32 or (base is not None and base.dtype != torch.float32):
         raise ValueError("lora_apply: base and Y must be fp32")
     need = hq_lora_workspace_bytes(M, r)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _room(workspace, need, "lora_apply: the workspace")
-    rc = load().hq_lora_apply(_ptr(x), _type(x), _rows(x, K, "x"), M, K, N, _ptr(A), _ptr(B), _type(A), n, r, _ptr(ids),
-                              _ptr(ranks), _ptr(scale), _ptr(base), _rows(base, N, "base"), _ptr(Y), _rows(Y, N, "Y"),
+    rc = load().hq_lora_apply(_ptr(x), _type(x), _pitch(x, K, "x"), M, K, N, _ptr(A), _ptr(B), _type(A), n, r, _ptr(ids),
+                              _ptr(ranks), _ptr(scale), _ptr(base), _pitch(base, N, "base"), _ptr(Y), _pitch(Y, N, "Y"),
                               _ptr(workspace), flags, _stream(stream))
     if rc != HQ_OK:
         raise HQError(rc, "hq_lora_apply")
@@ -674,9 +690,10 @@ class PagedCache:
 
 def _list(t, n, what: str) -> int:
     """The length of an int32 list; n: the length it must have, if any."""
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what}: contiguous int32 [{'n' if n is None else n}] expected, got {t.dtype} {tuple(t.shape)}")
-    return t.shape[0]
+    shape = t.shape
+    if t.dtype is not _INT32 or len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
+        raise ValueError(f"{what}: contiguous int32 [{'n' if n is None else n}] expected, got {t.dtype} {tuple(shape)}")
+    return shape[0]
 
 
 def pages_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: int = 0, stream=None) -> None:
@@ -787,8 +804,8 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     if workspace is None:
         workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
     _room(workspace, need, "prefix_attention: the workspace")
-    _check(load().hq_prefix_attention(cache.c, k_plane, v_plane, cache.type, _ptr(q), _rows(q, Hq * D, "q"), _ptr(seqs),
+    _check(load().hq_prefix_attention(cache.c, k_plane, v_plane, cache.type, _ptr(q), Hq * D if q.is_contiguous() else _rows(q, Hq * D, "q"), _ptr(seqs),
                                       _ptr(starts), B, rows, max_rows, _ptr(parent), Hq, shared, max_len, scale,
-                                      _ptr(out), _type(out), _rows(out, Hq * D, "out"), _ptr(workspace), flags,
+                                      _ptr(out), _type(out), Hq * D if out.is_contiguous() else _rows(out, Hq * D, "out"), _ptr(workspace), flags,
                                       _stream(stream)), "hq_prefix_attention")
     return out
