@@ -23,6 +23,9 @@ constexpr int PT = 1024;       // threads of each
 constexpr int PMAX = 1024;     // entries of a list
 constexpr int PSEQ = 8192;     // sequences of a cache (bits of the duplicate check)
 constexpr int MOVE_BATCH = 8;  // rows a thread has in flight
+constexpr int MOVE_RUN = 128;
+constexpr size_t NOWHERE = ~(size_t)0;
+static_assert(MOVE_RUN % MOVE_BATCH == 0 && MOVE_RUN <= 256, "whole batches, a thread a position");
 
 // One sequence whose rows move: positions [p0, end); position p comes from p
 // itself where p < from, else from base + keep[p - base - 1].  Old pages are
@@ -468,12 +471,14 @@ __global__ void __cluster_dims__(PCL, 1, 1) __launch_bounds__(PT)
 }
 
 // Moves the rows of the jobs: blockIdx = (column block, job, run of positions).
-// A thread owns one 16-byte column of one head and plane and takes positions
-// in ascending order, MOVE_BATCH loads in flight.  Rows only move down, and a
+// The block looks up where the positions lie, MOVE_RUN at a time; a thread owns
+// one 16-byte column of one head and plane and takes positions in ascending
+// order, MOVE_BATCH loads in flight.  Rows only move down, and a
 // page that is both read and written belongs to this sequence alone, so within
 // a column no row is overwritten before it has been read; where every
 // destination page is fresh the positions are also split over blockIdx.z.
 __global__ void __launch_bounds__(256) k_pages_move(const hq_pages c, const int32_t *keep, int ldkeep, int runs) {
+    __shared__ size_t s_from[MOVE_RUN], s_to[MOVE_RUN];
     pdl_launch_dependents();
     pdl_wait();
     if ((int)blockIdx.y >= *jobs_count(c)) return;
@@ -483,7 +488,6 @@ __global__ void __launch_bounds__(256) k_pages_move(const hq_pages c, const int3
     const int32_t *kp = keep ? keep + (size_t)j.item * ldkeep : nullptr;  // extend moves nothing past `from`
     const int units = c.row_bytes / 16, columns = c.n_planes * c.heads * units;
     const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= columns) return;
     int p0 = j.p0, p1 = j.end;
     if (j.whole) {
         const int per = ((p1 - p0 + runs - 1) / runs + MOVE_BATCH - 1) / MOVE_BATCH * MOVE_BATCH;
@@ -496,24 +500,36 @@ __global__ void __launch_bounds__(256) k_pages_move(const hq_pages c, const int3
     const size_t page_bytes = (size_t)c.heads * c.page_size * c.row_bytes;
     uint8_t *at = static_cast<uint8_t *>(c.pool) + (size_t)plane * c.plane_bytes +
                   (size_t)head * c.page_size * c.row_bytes + (size_t)unit * 16;
-    for (int p = p0; p < p1; p += MOVE_BATCH) {
-        uint4 v[MOVE_BATCH];
-        uint8_t *to[MOVE_BATCH];
-#pragma unroll
-        for (int b = 0; b < MOVE_BATCH; ++b) {
-            to[b] = nullptr;
-            const int q = p + b;
-            if (q >= p1) continue;
-            const int src = q < j.from ? q : j.base + kp[q - j.base - 1];
-            if (src < q || src >= j.old_len) continue;  // cannot happen: the lists were checked
-            const int a = old[src / c.page_size], z = now[q / c.page_size];
-            if (!page_ok(c, a) || !page_ok(c, z)) continue;
-            to[b] = at + (size_t)z * page_bytes + (size_t)(q % c.page_size) * c.row_bytes;
-            v[b] = *reinterpret_cast<const uint4 *>(at + (size_t)a * page_bytes + (size_t)(src % c.page_size) * c.row_bytes);
+    for (int p = p0; p < p1; p += MOVE_RUN) {
+        const int n = p1 - p < MOVE_RUN ? p1 - p : MOVE_RUN;
+        __syncthreads();  // the places of the run before have been used
+        if ((int)threadIdx.x < MOVE_RUN) {
+            const int q = p + threadIdx.x;
+            size_t from = 0, to = NOWHERE;
+            if (q < p1) {
+                const int src = q < j.from ? q : j.base + kp[q - j.base - 1];
+                if (src >= q && src < j.old_len) {  // always: the lists were checked
+                    const int x = old[src / c.page_size], z = now[q / c.page_size];
+                    if (page_ok(c, x) && page_ok(c, z)) {
+                        from = (size_t)x * page_bytes + (size_t)(src % c.page_size) * c.row_bytes;
+                        to = (size_t)z * page_bytes + (size_t)(q % c.page_size) * c.row_bytes;
+                    }
+                }
+            }
+            s_from[threadIdx.x] = from;
+            s_to[threadIdx.x] = to;
         }
+        __syncthreads();
+        if (col >= columns) continue;
+        for (int i = 0; i < n; i += MOVE_BATCH) {
+            uint4 v[MOVE_BATCH];
 #pragma unroll
-        for (int b = 0; b < MOVE_BATCH; ++b)
-            if (to[b]) *reinterpret_cast<uint4 *>(to[b]) = v[b];
+            for (int b = 0; b < MOVE_BATCH; ++b)  // (past the run: s_to says nowhere)
+                if (s_to[i + b] != NOWHERE) v[b] = *reinterpret_cast<const uint4 *>(at + s_from[i + b]);
+#pragma unroll
+            for (int b = 0; b < MOVE_BATCH; ++b)
+                if (s_to[i + b] != NOWHERE) *reinterpret_cast<uint4 *>(at + s_to[i + b]) = v[b];
+        }
     }
 }
 
@@ -541,7 +557,8 @@ __global__ void __launch_bounds__(256) k_pages_copy(const hq_pages c, const int3
     }
 }
 
-// One thread block per row: blockIdx = (row of a sequence, sequence, K or V).
+// One thread block per row, its K and its V: blockIdx = (row of a sequence,
+// sequence).  The row is on its way while its place is looked up.
 __global__ void __launch_bounds__(128) k_pages_write(const hq_pages c, const WriteArgs w) {
     pdl_launch_dependents();
     pdl_wait();
@@ -549,27 +566,21 @@ __global__ void __launch_bounds__(128) k_pages_write(const hq_pages c, const Wri
     int first, m;
     batch_rows(w.starts, b, w.rows, w.max_rows, first, m);
     if (i >= m) return;
-    const int seq = w.seqs ? w.seqs[b] : b;
-    int page = -1, p = 0;
-    if (seq >= 0 && seq < c.n_seqs) {
-        const int len = c.len[seq];
-        p = len - m + i;
-        if (len_ok(c, len) && p >= 0) page = c.table[(size_t)seq * c.max_pages + p / c.page_size];
-    }
-    if (!page_ok(c, page)) {
-        if (threadIdx.x == 0 && blockIdx.z == 0) set_status(c, HQ_ERR_INVALID_ARG);
-        return;
-    }
-    const int units = c.row_bytes / 16;
-    const uint8_t *src = static_cast<const uint8_t *>(blockIdx.z ? w.v : w.k) +
-                         (size_t)(first + i) * (size_t)(blockIdx.z ? w.ldv : w.ldk) * type_bytes(w.in_type);
-    uint8_t *dst = static_cast<uint8_t *>(c.pool) + (size_t)(blockIdx.z ? w.v_plane : w.k_plane) * c.plane_bytes +
-                   (size_t)page * c.heads * c.page_size * c.row_bytes + (size_t)(p % c.page_size) * c.row_bytes;
-    for (int u = threadIdx.x; u < c.heads * units; u += 128) {
-        uint4 o;
-        if (w.in_type == HQ_F32) {
-            const float4 x = reinterpret_cast<const float4 *>(src)[2 * u], y = reinterpret_cast<const float4 *>(src)[2 * u + 1];
-            const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    const int units = c.row_bytes / 16, n = c.heads * units;
+    const uint8_t *src[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        src[x] = static_cast<const uint8_t *>(x ? w.v : w.k) +
+                 (size_t)(first + i) * (size_t)(x ? w.ldv : w.ldk) * type_bytes(w.in_type);
+    auto load = [&](int u, uint4 (&o)[2]) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (w.in_type != HQ_F32) {
+                o[x] = reinterpret_cast<const uint4 *>(src[x])[u];
+                continue;
+            }
+            const float4 y = reinterpret_cast<const float4 *>(src[x])[2 * u], z = reinterpret_cast<const float4 *>(src[x])[2 * u + 1];
+            const float f[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -581,11 +592,31 @@ __global__ void __launch_bounds__(128) k_pages_write(const hq_pages c, const Wri
                     h[e] = *reinterpret_cast<const uint32_t *>(&t);
                 }
             }
-            o = make_uint4(h[0], h[1], h[2], h[3]);
-        } else {
-            o = reinterpret_cast<const uint4 *>(src)[u];
+            o[x] = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        *reinterpret_cast<uint4 *>(dst + (size_t)(u / units) * c.page_size * c.row_bytes + (size_t)(u % units) * 16) = o;
+    };
+    uint4 o[2];
+    int u = threadIdx.x;
+    if (u < n) load(u, o);
+    const int seq = w.seqs ? w.seqs[b] : b;
+    int page = -1, p = 0;
+    if (seq >= 0 && seq < c.n_seqs) {
+        const int len = c.len[seq];
+        p = len - m + i;
+        if (len_ok(c, len) && p >= 0) page = c.table[(size_t)seq * c.max_pages + p / c.page_size];
+    }
+    if (!page_ok(c, page)) {
+        if (threadIdx.x == 0) set_status(c, HQ_ERR_INVALID_ARG);
+        return;
+    }
+    uint8_t *dst = static_cast<uint8_t *>(c.pool) + (size_t)page * c.heads * c.page_size * c.row_bytes +
+                   (size_t)(p % c.page_size) * c.row_bytes;
+    while (u < n) {
+        const size_t at = (size_t)(u / units) * c.page_size * c.row_bytes + (size_t)(u % units) * 16;
+        *reinterpret_cast<uint4 *>(dst + (size_t)w.k_plane * c.plane_bytes + at) = o[0];
+        *reinterpret_cast<uint4 *>(dst + (size_t)w.v_plane * c.plane_bytes + at) = o[1];
+        u += 128;
+        if (u < n) load(u, o);
     }
 }
 
@@ -636,7 +667,7 @@ cudaError_t launch_pages_copy(const hq_pages &c, const int32_t *src, const int32
 }
 
 cudaError_t launch_pages_write(const hq_pages &c, const WriteArgs &w, bool pdl, cudaStream_t s) {
-    return launch_kernel(k_pages_write, dim3((unsigned)w.max_rows, (unsigned)w.B, 2), dim3(128), 0, pdl, s, c, w);
+    return launch_kernel(k_pages_write, dim3((unsigned)w.max_rows, (unsigned)w.B), dim3(128), 0, pdl, s, c, w);
 }
 
 }  // namespace hq
