@@ -9,6 +9,14 @@
 // which is a scan over the counts (the lowest free pages, in the lists'
 // order): one block does it and writes a job list, and a second kernel,
 // launched programmatically, moves the rows of all planes.
+//
+// What bounds them: the table operations, chains of dependent loads and
+// barriers (4 requests of 57 pages / 96 branches of 126: free 4.8 / 7.2 us, fork
+// 4.5 / 5.9, extend 6.4 / 7.0, compact 8.8 / 9.7; 6 sequences of 500 pages cut to
+// half: compact 25); the write of 4 / 96 sequences' 16 rows takes 4.5 / 6.5 us.
+// The move is bound by memory: 6 x 8000 rows of 16 planes and 8 heads of 128,
+// 2.4 GB read and written in 377 us = 6.4 TB/s (427 us with every thread looking
+// its places up by itself).
 #include <cooperative_groups.h>
 
 #include "batch.cuh"
