@@ -589,19 +589,22 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
     // Column c of the MMAs' tile j is output 8 (c / 2) + 2 j + c % 2, so that a
     // lane's columns of the four tiles are 8 consecutive outputs.
     uint4 b[2][LNT];
-    const long long ny = n0 + t4 * 8;
+    const long long ny = n0 + t4 * 8, nb = n0 + (g >> 1) * 8 + (g & 1);
+    uint32_t cols = 0;  // bit j: this lane's row of B for tile j is there
+#pragma unroll
+    for (int j = 0; j < LNT; ++j) cols |= nb + j * 2 < a.N ? 1u << j : 0u;
+    const bool y4[2] = {ny < a.N, ny + 4 < a.N};  // where quads
+    const size_t b_lane = ((size_t)nb * a.r_max + t4 * 8) * 2, b_adapter = (size_t)a.N * a.r_max * 2;
     auto load_b = [&](int i, int k0) {
-        const int id = it.id[it.lead[i]], rank = it.rank[it.lead[i]];
-        const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
+        const int id = it.id[it.lead[i]], left = it.rank[it.lead[i]] - k0 - t4 * 8;
+        const uint8_t *p = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * b_adapter + b_lane + (size_t)k0 * 2;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int k = k0 + c * 32 + t4 * 8;
+        for (int j = 0; j < LNT; ++j) {
 #pragma unroll
-            for (int j = 0; j < LNT; ++j) {
-                const long long n = n0 + (g >> 1) * 8 + j * 2 + (g & 1);
-                b[c][j] = k < rank && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
-                                              : make_uint4(0, 0, 0, 0);
-            }
+            for (int c = 0; c < 2; ++c)
+                b[c][j] = left > c * 32 && ((cols >> j) & 1u) ? *reinterpret_cast<const uint4 *>(p + c * 64)
+                                                              : make_uint4(0, 0, 0, 0);
+            p += 4 * a.r_max;
         }
     };
     const int tm = tid >> 4, tk = (tid & 15) * 4;  // the row and ranks of t that this thread brings
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
                     if (quads) {
-                        if (ny + e < a.N) {
+                        if (y4[e >> 2]) {
                             const float4 u = *reinterpret_cast<const float4 *>(s + e);
                             y[e] = u.x, y[e + 1] = u.y, y[e + 2] = u.z, y[e + 3] = u.w;
                         }
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
                 if (quads) {
-                    if (ny + e < a.N) *reinterpret_cast<float4 *>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    if (y4[e >> 2]) *reinterpret_cast<float4 *>(d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
                 } else {
 #pragma unroll
                     for (int f = e; f < e + 4; ++f)
