@@ -264,6 +264,14 @@ __device__ __forceinline__ void wide_w(const uint4 &u, float (&f)[8]) {
     }
 }
 
+// Of 8 values of 16 bits the first `left`, zeros behind them.
+__device__ __forceinline__ uint4 below_rank(const uint4 &u, int left) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) w[x] = 2 * x + 1 < left ? w[x] : 2 * x < left ? w[x] & 0xffffu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Items of one or two rows: t[row] for the 8 ranks of this block's share, one a
 // warp, over all of K, in chunks of 2048 k: x in shared memory as fp32 (the
 // first and last four of each eight apart, which keeps its 16-byte reads free
@@ -500,14 +508,18 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             while (i < it.n && (it.rows[i] > 2 || (it.id[it.lead[i]] < 0 && a.base == a.Y))) i += gridDim.y;
             return i;
         };
+        const long long nb = n0 + g;
+        uint32_t cols = 0;  // bit j: this lane's output 8 j + g is there
+#pragma unroll
+        for (int j = 0; j < LNT; ++j) cols |= nb + j * 8 < a.N ? 1u << j : 0u;
+        const size_t b_lane = ((size_t)nb * a.r_max + t4 * 8) * 2, b_adapter = (size_t)a.N * a.r_max * 2;
         auto load_b = [&](int i, int k0, uint4 (&b)[LNT]) {
-            const int id = it.id[it.lead[i]], k = k0 + t4 * 8, left = it.rank[it.lead[i]] - k;
-            const uint8_t *Bw = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * a.N * (size_t)a.r_max * 2;
+            const int id = it.id[it.lead[i]], left = it.rank[it.lead[i]] - k0 - t4 * 8;
+            const uint8_t *p = static_cast<const uint8_t *>(a.B) + (size_t)(id < 0 ? 0 : id) * b_adapter + b_lane + (size_t)k0 * 2;
 #pragma unroll
             for (int j = 0; j < LNT; ++j) {
-                const long long n = n0 + j * 8 + g;
-                b[j] = left > 0 && n < a.N ? *reinterpret_cast<const uint4 *>(Bw + ((size_t)n * a.r_max + k) * 2)
-                                           : make_uint4(0, 0, 0, 0);
+                b[j] = left > 0 && ((cols >> j) & 1u) ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+                p += 16 * a.r_max;
             }
         };
         int i = next_few(blockIdx.y);
@@ -547,20 +559,26 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
                         u = tr[0];
                         v = tr[1];
                     }
-                    const float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+                    t[m][0] = u.x, t[m][1] = u.y, t[m][2] = u.z, t[m][3] = u.w;
+                    t[m][4] = v.x, t[m][5] = v.y, t[m][6] = v.z, t[m][7] = v.w;
+                }
+                if (left < 8) {  // past the rank t is not written and B not used
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) t[m][e] = e < left ? f[e] : 0.0f;  // past the rank: not written
+                    for (int e = 0; e < 8; ++e) {
+                        if (e >= left) t[0][e] = t[1][e] = 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < LNT; ++j) b[j] = below_rank(b[j], left);
                 }
 #pragma unroll
                 for (int j = 0; j < LNT; ++j) {
                     float w[8];
                     wide_w<WBF>(b[j], w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float x = e < left ? w[e] : 0.0f;  // what lies past the rank is not used
-                        acc[j][0] = fmaf(x, t[0][e], acc[j][0]);
-                        acc[j][1] = fmaf(x, t[1][e], acc[j][1]);
-                    }
+                    for (int e = 0; e < 8; ++e) acc[j][0] = fmaf(w[e], t[0][e], acc[j][0]);
+                    if (nr == 2)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[j][1] = fmaf(w[e], t[1][e], acc[j][1]);
                 }
             }
             // the four lanes of an output add up; lane t4 writes output 8 t4 + g
@@ -645,12 +663,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             if (k0 + c * 32 >= rank) break;
             if (left > 0 && left < 8)
 #pragma unroll
-                for (int j = 0; j < LNT; ++j) {
-                    uint32_t w[4] = {b[c][j].x, b[c][j].y, b[c][j].z, b[c][j].w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = 2 * x + 1 < left ? w[x] : 2 * x < left ? w[x] & 0xffffu : 0u;
-                    b[c][j] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int j = 0; j < LNT; ++j) b[c][j] = below_rank(b[c][j], left);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 const uint4 p = *reinterpret_cast<const uint4 *>(&s_t[x][g][(c * 4 + t4 ^ g) * 8]);
