@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 template <int D, int HG>
 __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const PrefixPlan pl) {
     constexpr int COLS = HG * D / 4;            // float4 columns
-    constexpr int PG = COLS >= 256 ? 1 : 256 / COLS, BATCH = 8;
+    constexpr int PG = COLS >= 256 ? 1 : 256 / COLS, BATCH = HG == 8 ? 4 : 8;
     __shared__ float s_w[MAX_PARTS][HG];
     __shared__ float4 s_acc[PG > 1 ? 256 : 1];
     __shared__ int s_b;
