@@ -19,14 +19,17 @@
 // exchanges.  What bounds it: few rows, the chain load - reduction - store (128
 // rows of 8192: 6.8 us, 6.3 of which one row takes).  With more rows than
 // resident blocks a block takes several in turn, weight and signs stay in
-// registers and each thread copies its share of the next three rows into a ring
+// registers and each thread copies its share of the next two rows into a ring
 // in shared memory.  Then the instructions bound it, not the memory: 8190 rows
 // of 8192, all bf16, 111 us = 5.4 TB/s at 400 instructions a warp and row, four
 // fifths of the issue slots used.  On the way there: one row per block 232 us
 // (the memory idle during reductions); a loop with the next row in registers
 // 148; the ring 145; types known at compile time 115; the largest value by one
-// instruction 111.  The types are known where x, residual and h are all of one
-// 16-bit type; any others take the general code (145 us in that case).
+// instruction 111.  (Two octets a thread and half the threads: 106 in bf16, but
+// 240 instead of 183 with x in fp32.)  The types are known where
+// residual and h are of one 16-bit type and x of the same or fp32 (8192 rows of
+// 8192, x in fp32, the others in bf16: 161 us, 183 in the general code, which
+// any other types take).
 // Everything is fp32 until the outputs: residual_out, h and the codes are
 // rounded once each.
 #include "act_common.cuh"
@@ -120,13 +123,16 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-constexpr int NSTAGES = 3;            // rows in the ring
+// Rows in the ring.  Two and three, 8192 rows: of 1024 in bf16 21.6 and 23.6 us,
+// of 8192 in bf16 114 both, of 12288 in fp32 and bf16 321 and (three do not fit) 400.
+constexpr int NSTAGES = 2;
 constexpr int NORM_SMEM = 220 << 10;  // shared memory of an SM's blocks
 constexpr int NORM_FIXED = 18 << 10;  // of which a block needs beside its ring, with the system's 1 KB
 
 // RING: 0, or rows through the ring (no operand is written): of any types, or
-// x, residual and h all of one 16-bit type.
-enum { DIRECT = 0, RING_ANY = 1, RING_F16 = 2, RING_BF16 = 3 };
+// residual and h of one 16-bit type and x of the same or fp32 (a projection's
+// output).
+enum { DIRECT = 0, RING_ANY = 1, RING_F16 = 2, RING_BF16 = 3, RING_F32_F16 = 4, RING_F32_BF16 = 5 };
 template <int V, int T, int RING>
 __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
     extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][16-byte piece of a thread's share][thread]
@@ -136,8 +142,9 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
     const int MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
     const int K = a.K, G = a.G, n8 = K >> 3;
     const bool quant = a.sx != nullptr;
-    constexpr int ONE = RING == RING_F16 ? HQ_F16 : RING == RING_BF16 ? HQ_BF16 : -1;
-    const int x_type = ONE >= 0 ? ONE : a.x_type, r_type = ONE >= 0 ? ONE : a.r_type, h_type = ONE >= 0 ? ONE : a.h_type;
+    constexpr int ONE = RING == RING_F16 || RING == RING_F32_F16 ? HQ_F16 : RING == RING_BF16 || RING == RING_F32_BF16 ? HQ_BF16 : -1;
+    const int x_type = RING >= RING_F32_F16 ? HQ_F32 : ONE >= 0 ? ONE : a.x_type;
+    const int r_type = ONE >= 0 ? ONE : a.r_type, h_type = ONE >= 0 ? ONE : a.h_type;
     const float inv_k = 1.0f / (float)K;
 
     // the operand's layout (hq_internal.cuh): K tiles of code blocks, then group sums
@@ -396,7 +403,8 @@ cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     static std::atomic<int> resident[CACHE_DEVICES];
     e = cached_per_device(resident, dev, &per_sm, [&](int *v) {
-        for (auto f : {k_add_norm_quant<V, T, RING_ANY>, k_add_norm_quant<V, T, RING_F16>, k_add_norm_quant<V, T, RING_BF16>}) {
+        for (auto f : {k_add_norm_quant<V, T, RING_ANY>, k_add_norm_quant<V, T, RING_F16>, k_add_norm_quant<V, T, RING_BF16>,
+                       k_add_norm_quant<V, T, RING_F32_F16>, k_add_norm_quant<V, T, RING_F32_BF16>}) {
             const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM - NORM_FIXED);
             if (r != cudaSuccess) return r;
         }
@@ -407,13 +415,16 @@ cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
     // the ring where blocks take several rows and its rows fit
     const int row_bytes = V * T * 8 * (type_bytes(a.x_type) + (a.res ? type_bytes(a.r_type) : 0));
     const int ring = NSTAGES * row_bytes;
+    while (per_sm > 1 && ring > NORM_SMEM / per_sm - NORM_FIXED) --per_sm;
     const long long most = (long long)sms * per_sm;
     if (a.M <= most || ring > NORM_SMEM / per_sm - NORM_FIXED)
         return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)a.M), dim3(T), 0, pdl, s, a);
-    const bool one = a.x_type != HQ_F32 && a.res && a.r_type == a.x_type && (!a.h || a.h_type == a.x_type);
-    auto f = !one ? k_add_norm_quant<V, T, RING_ANY>
-             : a.x_type == HQ_F16 ? k_add_norm_quant<V, T, RING_F16>
-                                  : k_add_norm_quant<V, T, RING_BF16>;
+    const bool one = a.res && a.r_type != HQ_F32 && (!a.h || a.h_type == a.r_type), wide = a.x_type == HQ_F32;
+    auto f = k_add_norm_quant<V, T, RING_ANY>;
+    if (one && a.r_type == HQ_F16 && (wide || a.x_type == HQ_F16))
+        f = wide ? k_add_norm_quant<V, T, RING_F32_F16> : k_add_norm_quant<V, T, RING_F16>;
+    else if (one && a.r_type == HQ_BF16 && (wide || a.x_type == HQ_BF16))
+        f = wide ? k_add_norm_quant<V, T, RING_F32_BF16> : k_add_norm_quant<V, T, RING_BF16>;
     return launch_kernel(f, dim3((unsigned)most), dim3(T), (size_t)ring, pdl, s, a);
 }
 

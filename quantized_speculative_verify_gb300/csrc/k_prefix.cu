@@ -486,10 +486,11 @@ __global__ void __launch_bounds__(XTHREADS, 2)
 // heads).  First the weight of every part, exp2(m - top) over the sum of
 // weight times l, into shared memory; then each thread adds up four dimensions
 // of one head over every PG-th part (PG groups of threads where the heads
-// alone do not fill the block), 8 loads in flight, and the groups add up in
+// alone do not fill the block), 8 loads in flight (4 where rows are many), and the groups add up in
 // order.  What bounds it is the chain of dependent loads (row -> sequence ->
 // maxima -> outputs): the sequence is found by all threads at once and before
-// the wait for the parts.  551 rows of 32 heads in 3 parts, 27 MB: 13 us.
+// the wait for the parts.  551 rows of 32 heads in 3 parts, 27 MB: 11.5
+// us (13.3 with 8 parts in flight for all; 13 with 16 heads a block).
 template <int D, int HG>
 __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const PrefixPlan pl) {
     constexpr int COLS = HG * D / 4;            // float4 columns

@@ -218,3 +218,18 @@ def test_norm_on_a_side_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     check(x, r, w, signs, 1e-5, out, h, qx, sx)
+
+
+@pytest.mark.parametrize("M,K,t,pad", [(1000, 8192, F16, 0), (2600, 640, BF16, 16), (1500, 4096, BF16, 0), (333, 12288, F16, 8)])
+def test_norm_of_many_rows_behind_an_fp32_projection(M, K, t, pad):
+    x, r, w, signs = make(M, K, F32, t, seed=M, pad=pad)
+    d = hq.make_desc(K, 128, 32, "w8")
+    out, h, qx, sx = (Guarded((M, K), t, DEV), Guarded((M, K), t, DEV), Guarded((M, K), torch.int8, DEV), Guarded((M,), F32, DEV))
+    if pad:  # residual_out shares the residual's stride
+        hq.add_norm_quant(d, x, r, w, signs_dev(signs), 1e-6, h=h.t, qx=qx.t, sx=sx.t)
+    else:
+        hq.add_norm_quant(d, x, r, w, signs_dev(signs), 1e-6, residual_out=out.t, h=h.t, qx=qx.t, sx=sx.t)
+    torch.cuda.synchronize()
+    for g in (out, h, qx, sx):
+        g.check()
+    check(x, r, w, signs, 1e-6, None if pad else out.t, h.t, qx.t, sx.t)
