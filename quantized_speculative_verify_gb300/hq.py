@@ -7,6 +7,7 @@ libhq.so is missing or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -198,6 +199,26 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _on(stream):
+    """The stream of a call as the current one: what a call allocates, fills or
+    copies for itself belongs to the stream that it launches on, in its order
+    (given back, the memory goes to that stream's next allocations, not to the
+    current stream's while the kernels still use it)."""
+    if stream is None or _stream(stream) == _stream(None):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
+def _new(shape, dtype, device, stream, fill=torch.empty) -> torch.Tensor:
+    """A buffer that a call makes for itself or its caller (see _on).  The
+    caller may use it, and let go of it, on the current stream as well."""
+    with _on(stream):
+        t = fill(shape, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def make_desc(K: int, N: int, group: int, fmt) -> hq_layer_desc:
     return hq_layer_desc(int(K), int(N), int(group), FORMATS.get(fmt, fmt) if isinstance(fmt, str) else int(fmt))
 
@@ -325,9 +346,10 @@ def pack_layer(W: torch.Tensor, group: int, fmt, signs_host: np.ndarray, stream=
     nbytes = hq_packed_bytes(desc)
     if nbytes == 0:
         raise HQError(HQ_ERR_INVALID_ARG, "hq_packed_bytes")
-    blob = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+    blob = _new(nbytes, torch.uint8, W.device, stream)
     signs = torch.from_numpy(signs_host.astype(np.int32, copy=False).view(np.int32)).to(W.device)
-    hq_pack_weights(desc, W.contiguous(), signs, blob, stream)
+    with _on(stream):
+        hq_pack_weights(desc, W.contiguous(), signs, blob, stream)
     return PackedLayer(desc, blob, signs)
 
 
@@ -357,10 +379,11 @@ def pack_fused(Ws: list, group: int, fmt, signs_host: np.ndarray, stream=None) -
     if nbytes == 0:
         raise HQError(HQ_ERR_INVALID_ARG, "hq_packed_bytes")
     dev = Ws[0].device
-    blob = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    blob = _new(nbytes, torch.uint8, dev, stream)
     signs = torch.from_numpy(signs_host.astype(np.int32, copy=False).view(np.int32)).to(dev)
-    for W, o in zip(Ws, offsets):
-        hq_pack_weights_at(desc, o, W.shape[0], W.contiguous(), signs, blob, stream)
+    with _on(stream):
+        for W, o in zip(Ws, offsets):
+            hq_pack_weights_at(desc, o, W.shape[0], W.contiguous(), signs, blob, stream)
     return FusedLayer(PackedLayer(desc, blob, signs), widths, offsets)
 
 
@@ -385,9 +408,9 @@ def workspace(desc: hq_layer_desc, M: int, device) -> torch.Tensor:
 def unpack(layer: PackedLayer, stream=None):
     N, K, G = layer.N, layer.K, layer.group
     dev = layer.blob.device
-    codes = torch.empty((N, K), dtype=torch.uint8, device=dev)
-    scales = torch.empty((N, K // G), dtype=torch.float32, device=dev)
-    zeros = torch.empty((N, K // G), dtype=torch.uint8, device=dev) if layer.fmt == HQ_W4_ASYM else None
+    codes = _new((N, K), torch.uint8, dev, stream)
+    scales = _new((N, K // G), torch.float32, dev, stream)
+    zeros = _new((N, K // G), torch.uint8, dev, stream) if layer.fmt == HQ_W4_ASYM else None
     hq_unpack_codes(layer.desc, layer.blob, codes, scales, zeros, stream)
     return codes, scales, zeros
 
@@ -397,10 +420,11 @@ def verify_linear(layer: PackedLayer, X: torch.Tensor, ws: torch.Tensor, Y: torc
     """Y = dequant(int GEMM(quant(rotate(X)), packed W)): the two kernels in sequence."""
     M, K = X.shape
     if bufs is None:
-        bufs = act_buffers(layer.desc, M, X.device, int8_codes=False)
+        with _on(stream):
+            bufs = act_buffers(layer.desc, M, X.device, int8_codes=False)
     qx, gsum, qop, sx = bufs
     if Y is None:
-        Y = torch.empty((M, layer.N), dtype=torch.float32, device=X.device)
+        Y = _new((M, layer.N), torch.float32, X.device, stream)
     hq_rotate_quant_act(layer.desc, X, M, layer.signs, qx, gsum, qop, sx, flags & HQ_LAUNCH_PDL, stream)
     hq_verify_gemm(layer.desc, layer.blob, qop, sx, M, Y, partials, ws, flags, stream)
     return Y
@@ -421,10 +445,10 @@ def tree_accept(logits: torch.Tensor, parent: torch.Tensor, tokens: torch.Tensor
     """Greedy tokens, accepted path, number accepted and bonus token of a draft tree (device tensors)."""
     M, V = logits.shape
     dev = logits.device
-    greedy = torch.empty(M, dtype=torch.int32, device=dev)
-    path = torch.empty(M, dtype=torch.int32, device=dev)
-    out = torch.empty(2, dtype=torch.int32, device=dev)
-    ws = torch.empty(hq_tree_accept_workspace_bytes(M, V), dtype=torch.uint8, device=dev)
+    greedy = _new(M, torch.int32, dev, stream)
+    path = _new(M, torch.int32, dev, stream)
+    out = _new(2, torch.int32, dev, stream)
+    ws = _new(hq_tree_accept_workspace_bytes(M, V), torch.uint8, dev, stream)
     hq_tree_accept(logits, M, V, parent, tokens, greedy, path, out[0:1], out[1:2], ws, flags, stream)
     return greedy, path, out
 
@@ -456,9 +480,9 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     M, Hq, D = q.shape
     Hkv, cap, _ = k_cache.shape
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((M, Hq, D), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.zeros(hq_tree_attention_workspace_bytes(Hkv), dtype=torch.uint8, device=q.device)
+        workspace = _new(hq_tree_attention_workspace_bytes(Hkv), torch.uint8, q.device, stream, torch.zeros)
     hq_tree_attention(q, k_cache, v_cache, cap, L, M, Hq, Hkv, D, parent, scale, out, workspace, flags, stream)
     return out
 
@@ -489,7 +513,7 @@ def delta_tree(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.T
     state [H][D][D] is only read.  q, k, v fp32 [M][H][D]; alpha, beta [M][H]."""
     M, H, D = q.shape
     if out is None:
-        out = torch.empty((M, H, D), dtype=torch.float32, device=q.device)
+        out = _new((M, H, D), torch.float32, q.device, stream)
     hq_delta_tree(state, q, k, v, alpha, beta, parent, M, H, D, out, flags, stream)
     return out
 
@@ -629,7 +653,7 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     _dense(scale, torch.float32, (n,), "lora_apply: scale")
     shape = (M, N)
     if Y is None:
-        Y = torch.empty(shape, dtype=torch.float32, device=x.device)
+        Y = _new(shape, torch.float32, x.device, stream)
     if base is not Y:
         _shaped(base, shape, "lora_apply: base")
     _shaped(Y, shape, "lora_apply: Y")
@@ -637,7 +661,7 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
         raise ValueError("lora_apply: base and Y must be fp32")
     need = hq_lora_workspace_bytes(M, r)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new(need, torch.uint8, x.device, stream)
     _room(workspace, need, "lora_apply: the workspace")
     rc = load().hq_lora_apply(_ptr(x), _type(x), _pitch(x, K, "x"), M, K, N, _ptr(A), _ptr(B), _type(A), n, r, _ptr(ids),
                               _ptr(ranks), _ptr(scale), _ptr(base), _pitch(base, N, "base"), _ptr(Y), _pitch(Y, N, "Y"),
@@ -798,11 +822,11 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     if parent is not None:
         _list(parent, rows, "prefix_attention: parent")
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _new(shape, q.dtype, q.device, stream)
     _shaped(out, shape, "prefix_attention: out")
     need = hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, cache.heads, D)
     if workspace is None:
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 16), torch.uint8, q.device, stream, torch.zeros)
     _room(workspace, need, "prefix_attention: the workspace")
     _check(load().hq_prefix_attention(cache.c, k_plane, v_plane, cache.type, _ptr(q), Hq * D if q.is_contiguous() else _rows(q, Hq * D, "q"), _ptr(seqs),
                                       _ptr(starts), B, rows, max_rows, _ptr(parent), Hq, shared, max_len, scale,
