@@ -593,7 +593,7 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
     of act_buffers).  x, residual, residual_out and h: [M][K], fp32, fp16 or
     bf16, rows any 16-byte-aligned distance apart; residual may be None (the
     norm of x alone) and any output may be None; residual_out may be residual
-    itself.  weight fp32 [K]."""
+    itself.  weight fp32 [K]; signs int32 [K / 32] (hq_make_signs, on the device)."""
     shape = x.shape
     M, K = shape
     x_type = TYPES.get(x.dtype)
@@ -606,6 +606,7 @@ def add_norm_quant(desc: hq_layer_desc, x: torch.Tensor, residual, weight: torch
         _shaped(residual_out, shape, "add_norm_quant: residual_out")
     _shaped(h, shape, "add_norm_quant: h")
     _dense(weight, torch.float32, (K,), "add_norm_quant: weight")
+    _dense(signs, torch.int32, (K // 32,), "add_norm_quant: signs")
     _dense(qx, torch.int8, shape, "add_norm_quant: qx")
     _dense(sx, torch.float32, (M,), "add_norm_quant: sx")
     if gsum is not None:

@@ -57,6 +57,17 @@ def test_norm_binding_checks_shapes_before_the_library():
         hq.add_norm_quant(d, x, None, w, None, h=x)
 
 
+@pytest.mark.parametrize("signs", [torch.zeros(7, dtype=torch.int32), torch.zeros(9, dtype=torch.int32),
+                                   torch.zeros(8), torch.zeros((2, 4), dtype=torch.int32),
+                                   torch.zeros(16, dtype=torch.int32)[::2]])
+def test_norm_binding_checks_the_signs(signs):
+    """A word per 32 features: a shorter vector would be read past its end."""
+    d = hq.make_desc(256, 256, 32, "w4")
+    x = torch.zeros((3, 256))
+    with pytest.raises(ValueError, match="signs"):
+        hq.add_norm_quant(d, x, None, torch.zeros(256), signs, qx=torch.zeros((3, 256), dtype=torch.int8), sx=torch.zeros(3))
+
+
 def lora_call(**kw):
     a = dict(x=FAKE, xt=hq.HQ_F32, ldx=256, M=4, K=256, N=100, A=FAKE, B=FAKE, wt=hq.HQ_F16, n=3, r=16, ids=FAKE,
              ranks=FAKE, scale=FAKE, base=FAKE, ldb=100, Y=FAKE + 4096, ldy=100, ws=FAKE, flags=0)
