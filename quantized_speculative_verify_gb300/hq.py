@@ -676,7 +676,15 @@ class PagedCache:
     """A paged key/value cache (hq_pages) over the caller's tensors: pool
     [planes][pages][heads][page_size][dim] (fp16 or bf16), ref int32 [pages],
     table int32 [sequences][max_pages], lens int32 [sequences].  `empty` makes
-    one without sequences."""
+    one without sequences.  The library holds the tensors' addresses: their
+    contents may be changed in place, the attributes themselves stay."""
+
+    _held = frozenset(("pool", "ref", "table", "lens", "status", "scratch", "c"))
+
+    def __setattr__(self, name, value):
+        if name in self._held and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"PagedCache.{name} is held by its address: change it in place, or make a new PagedCache")
+        object.__setattr__(self, name, value)
 
     def __init__(self, pool: torch.Tensor, ref: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
         planes, pages, heads, page_size, dim = pool.shape

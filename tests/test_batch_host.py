@@ -193,6 +193,21 @@ def test_paged_cache_binding_checks():
         hq.PagedCache(z((2, 4, 1, 16, 64), dtype=torch.float16), z(4, **i), z((2, 2), **i), z(2, **i))
 
 
+def test_a_paged_cache_keeps_the_tensors_whose_addresses_it_holds(monkeypatch):
+    monkeypatch.setattr(hq, "_ptr", lambda t: t.data_ptr())
+    i = dict(dtype=torch.int32)
+    cache = hq.PagedCache(torch.zeros((2, 4, 1, 16, 64), dtype=torch.float16), torch.zeros(4, **i), torch.zeros((2, 2), **i),
+                          torch.zeros(2, **i))
+    was = {k: getattr(cache, k) for k in ("pool", "ref", "table", "lens", "status", "scratch")}
+    for k, t in was.items():
+        with pytest.raises(AttributeError, match=k):
+            setattr(cache, k, t.clone())
+        assert getattr(cache, k) is t
+    cache.lens += 3  # in place
+    cache.lens[1] = 5
+    assert cache.lens.tolist() == [3, 5] and cache.lens is was["lens"] and cache.c.len == cache.lens.data_ptr()
+
+
 def test_prefix_attention_refuses_bad_arguments():
     lib = hq.load()
 
