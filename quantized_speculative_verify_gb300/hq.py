@@ -774,6 +774,8 @@ def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: i
 
 def _batch(cache: PagedCache, rows: int, starts, max_rows: int, seqs, what: str) -> int:
     """The number of sequences of a batch of rows."""
+    if max_rows < 1:
+        raise ValueError(f"{what}: max_rows must be at least 1, got {max_rows}")
     if starts is not None:
         B = _list(starts, None, what) - 1
         if B < 0:

@@ -208,6 +208,19 @@ def test_a_paged_cache_keeps_the_tensors_whose_addresses_it_holds(monkeypatch):
     assert cache.lens.tolist() == [3, 5] and cache.lens is was["lens"] and cache.c.len == cache.lens.data_ptr()
 
 
+@pytest.mark.parametrize("max_rows", [0, -1])
+def test_binding_refuses_batches_without_rows_a_sequence(monkeypatch, max_rows):
+    monkeypatch.setattr(hq, "_ptr", lambda t: t.data_ptr())
+    i = dict(dtype=torch.int32)
+    cache = hq.PagedCache(torch.zeros((2, 4, 1, 16, 64), dtype=torch.float16), torch.zeros(4, **i), torch.zeros((2, 2), **i),
+                          torch.zeros(2, **i))
+    x = torch.zeros((4, 1, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="max_rows"):
+        hq.pages_write(cache, 0, 1, x, x, None, max_rows)
+    with pytest.raises(ValueError, match="max_rows"):
+        hq.prefix_attention(cache, 0, 1, x, None, max_rows, 0, 16, 0.1)
+
+
 def test_prefix_attention_refuses_bad_arguments():
     lib = hq.load()
 
