@@ -634,8 +634,8 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  *             once; the size grows with rows and max_rows and does not depend
  *             on B or the lengths, so one workspace of the largest rows and
  *             max_rows serves every call of these heads in turn
- * A row of an empty sequence (len 0), and a row that no sequence claims, is
- * zero.  A length that contradicts shared, m_b or max_len makes the
+ * B = 0 or rows = 0: no-op (out is not written).  A row of an empty sequence
+ * (len 0), and a row that no sequence claims, is zero.  A length that contradicts shared, m_b or max_len makes the
  * sequence's rows zero, a table entry outside [0, n_pages) makes its
  * positions read as zeros; both set the error word (hq_workspace_status:
  * HQ_ERR_INVALID_ARG).  Rows past a sequence's length, other branches of the

@@ -835,6 +835,9 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     if out is None:
         out = _new(shape, q.dtype, q.device, stream)
     _shaped(out, shape, "prefix_attention: out")
+    if B == 0 and out.is_cuda:  # the library's call does nothing then, but no sequence claims these rows
+        with _on(stream):
+            return out.zero_()
     need = hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq, cache.heads, D)
     if workspace is None:
         workspace = _new(max(need, 16), torch.uint8, q.device, stream, torch.zeros)

@@ -491,3 +491,14 @@ def test_sizes_where_another_kernel_takes_over(B, m, shared, own, Hq, Hkv, D, ps
     for flags in (0, hq.HQ_LAUNCH_PDL, hq.HQ_LAUNCH_PDL):  # one workspace, calls on each other's heels
         assert torch.equal(got, t.run(flags=flags, workspace=ws))
     assert t.status == hq.HQ_OK
+
+
+def test_a_batch_of_no_sequences_claims_no_row():
+    t = Batch([80], [3], 32, 8, 2, 128, 16, F16, seed=7)
+    for stream in (None, torch.cuda.Stream()):
+        out = torch.full_like(t.q, 5.0)
+        torch.cuda.synchronize()
+        got = hq.prefix_attention(t.cache, 2, 1, t.q, ints([0]), 3, 32, 80, t.scale, out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert got is out and not out.any()
+    assert not hq.prefix_attention(t.cache, 2, 1, t.q, ints([0]), 3, 32, 80, t.scale).any()
