@@ -514,8 +514,8 @@ int hq_lora_apply(const void *x, int32_t x_type, int64_t ldx, int32_t M, int32_t
  *   table   int32 [n_seqs][max_pages]: position p of sequence s lies in row
  *           p % page_size of page table[s][p / page_size]; unused entries -1
  *   len     int32 [n_seqs]: positions held (0 = an empty slot)
- *   status  int32, zeroed once: the first error of a page operation since it
- *           was last read (hq_pages_status)
+ *   status  int32, zeroed once: the first error of a page operation or of
+ *           hq_prefix_attention since it was last read (hq_pages_status)
  *   scratch hq_pages_scratch_bytes(&cache) bytes, 16-byte aligned: one call at
  *           a time
  * page_size is 16, 32, 64, 128 or 256; row_bytes a multiple of 16 up to 4096;
@@ -604,7 +604,8 @@ int hq_pages_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, cons
                    const int32_t *starts, int32_t B, int32_t rows, int32_t max_rows, uint32_t flags, void *stream);
 
 /* Synchronizes `stream`, then reads and clears the cache's status word:
- * HQ_OK, HQ_ERR_INVALID_ARG or HQ_ERR_NO_PAGES. */
+ * HQ_OK, HQ_ERR_INVALID_ARG, HQ_ERR_NO_PAGES or (hq_prefix_attention)
+ * HQ_ERR_TIMEOUT. */
 int hq_pages_status(const hq_pages *cache, void *stream);
 
 /* Attention of a batch over a paged cache whose sequences share their first
@@ -638,7 +639,9 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  * (len 0), and a row that no sequence claims, is zero.  A length that contradicts shared, m_b or max_len makes the
  * sequence's rows zero, a table entry outside [0, n_pages) makes its
  * positions read as zeros; both set the error word (hq_workspace_status:
- * HQ_ERR_INVALID_ARG).  Rows past a sequence's length, other branches of the
+ * HQ_ERR_INVALID_ARG).  A call that ends with the error word set, by itself or
+ * by an earlier call, enters it in the cache's status word too
+ * (hq_pages_status).  Rows past a sequence's length, other branches of the
  * tree and other sequences' pages do not influence a row, whatever they hold
  * (infinities and NaN included).  Scores, softmax statistics and outputs are
  * accumulated in fp32; the probabilities are rounded to `type` for the

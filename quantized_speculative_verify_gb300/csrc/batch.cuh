@@ -81,7 +81,7 @@ struct PrefixArgs {
     const int32_t *seqs, *starts, *parent, *table, *len;
     const uint8_t *pool;
     int64_t plane_bytes;
-    int *err;
+    int *err, *status;  // the workspace's error word, the cache's status word
     float *ws_o, *ws_ml;  // [part][row][Hq][D], [part][row][Hq][2]: running maximum (base-2 units), sum
     int64_t ldq, ldo;
     int B, rows, max_rows, Hq, Hkv, G, n_seqs, max_pages, page_shift, n_pages, k_plane, v_plane;

@@ -262,6 +262,7 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
     a.parent = parent;
     a.table = cache->table;
     a.len = cache->len;
+    a.status = cache->status;
     a.ldq = ldq;
     a.ldo = ldo;
     a.B = B;

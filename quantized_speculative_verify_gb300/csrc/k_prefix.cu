@@ -524,6 +524,10 @@ __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const 
         if (s.live) parts = pl.np + (s.len - pl.s0 + pl.schunk - 1) / pl.schunk;
     }
     pdl_wait();
+    // what went wrong in the parts reaches the cache's status word as well, for
+    // callers that keep no workspace of their own
+    const bool reports = tid == 0 && blockIdx.x == 0 && blockIdx.y == 0;
+    const int wrong = reports ? *static_cast<volatile int *>(a.err) : 0;
     const size_t step = (size_t)a.rows * a.Hq, r0 = (size_t)row * a.Hq + h0;
     // weights: a warp per head, two parts a lane
     static_assert(MAX_PARTS <= 64, "two parts a lane");
@@ -600,6 +604,8 @@ __global__ void __launch_bounds__(256) k_prefix_merge(const PrefixArgs a, const 
                 a.out_type == HQ_F16 ? make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w))
                                      : make_uint2(pack2<true>(acc.x, acc.y), pack2<true>(acc.z, acc.w));
     }
+    if (reports && wrong != 0)
+        atomicCAS(a.status, 0, wrong == DEV_ERR_TIMEOUT ? (int)HQ_ERR_TIMEOUT : (int)HQ_ERR_INVALID_ARG);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -807,7 +807,7 @@ def pages_write(cache: PagedCache, k_plane: int, v_plane: int, k: torch.Tensor, 
 
 
 def pages_status(cache: PagedCache, stream=None) -> int:
-    """Synchronizes; the first error of a page operation since the last call (HQ_OK if none), cleared."""
+    """Synchronizes; the first error of a page operation or of prefix_attention since the last call (HQ_OK if none), cleared."""
     return int(load().hq_pages_status(cache.c, _stream(stream)))
 
 
@@ -824,7 +824,9 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     cache's type: sequence b's rows starts[b] .. starts[b + 1] (None: max_rows
     rows each) are its newest positions, a draft tree with `parent` (int32
     [rows]; None: a chain).  max_len: at least every sequence's length.  out
-    [rows][Hq][D] of the cache's type or fp32; workspace: zeroed once."""
+    [rows][Hq][D] of the cache's type or fp32; workspace: zeroed once.  Bad
+    table entries and lengths are reported by hq_workspace_status(workspace)
+    and by pages_status(cache)."""
     shape = q.shape
     rows, Hq, D = shape
     if D != cache.dim or q.dtype != cache.pool.dtype:

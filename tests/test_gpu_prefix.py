@@ -502,3 +502,25 @@ def test_a_batch_of_no_sequences_claims_no_row():
         torch.cuda.synchronize()
         assert got is out and not out.any()
     assert not hq.prefix_attention(t.cache, 2, 1, t.q, ints([0]), 3, 32, 80, t.scale).any()
+
+
+@pytest.mark.parametrize("B,m", [(2, 2), (60, 1), (2, 40)])
+def test_errors_reach_the_cache_without_a_workspace(B, m):
+    t = Batch([300 + b % 5 for b in range(B)], [m] * B, 200, 8, 2, 128, 16, F16, seed=9)
+
+    def run(**kw):
+        a = dict(shared=200, max_len=320, parent=ints(t.parent), seqs=ints(t.slots))
+        a.update(kw)
+        return hq.prefix_attention(t.cache, 2, 1, t.q, ints(t.starts), m, scale=t.scale, **a)
+    t.check(run())
+    assert hq.pages_status(t.cache) == hq.HQ_OK
+    run(max_len=300)  # some sequences are longer
+    assert hq.pages_status(t.cache) == hq.HQ_ERR_INVALID_ARG and hq.pages_status(t.cache) == hq.HQ_OK
+    for at in (3, 15):  # among the shared positions, among the own ones
+        was = int(t.cache.table[0, at])
+        t.cache.table[0, at] = -1
+        run()
+        assert hq.pages_status(t.cache) == hq.HQ_ERR_INVALID_ARG
+        t.cache.table[0, at] = was
+        t.check(run())
+        assert hq.pages_status(t.cache) == hq.HQ_OK
