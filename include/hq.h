@@ -91,8 +91,9 @@ typedef struct {
  * Some inputs are read before that wait, so with this flag they must not be
  * written by the operation launched immediately before in the same stream:
  * the blob (hq_verify_gemm streams the packed weights early), the committed
- * cache positions [0, L) (hq_tree_attention) and the committed state
- * (hq_delta_tree). */
+ * cache positions [0, L) (hq_tree_attention), the committed state
+ * (hq_delta_tree), weight and signs (hq_add_norm_quant), and ids, ranks, A and
+ * B (hq_lora_apply). */
 #define HQ_LAUNCH_PDL 1u
 /* hq_verify_gemm only: combine the thread blocks that share an output in a
  * fixed order, so that results repeat bit for bit from run to run (the blocks
@@ -498,7 +499,7 @@ int hq_add_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, 
  * repeat bit for bit.  Elements of A and B past a rank are not used in any
  * sum.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (ids, ranks, A and B are
  * then read before the wait for the previous kernel, which must not write
- * them).  Launches two kernels. */
+ * them; scale, like x and base, is read after it).  Launches two kernels. */
 size_t hq_lora_workspace_bytes(int32_t M, int32_t r_max);
 int hq_lora_apply(const void *x, int32_t x_type, int64_t ldx, int32_t M, int32_t K, int32_t N, const void *A,
                   const void *B, int32_t w_type, int32_t n_adapters, int32_t r_max, const int32_t *ids,

@@ -90,7 +90,6 @@ __device__ __forceinline__ void split_half(uint32_t w, uint32_t (&t)[2]) {
 struct Items {
     int id[HQ_MAX_M];      // the row's adapter, -1 for none
     int rank[HQ_MAX_M];    // of the row's adapter
-    float scale[HQ_MAX_M];
     int lead[HQ_MAX_M];    // the first row of each item
     int rows[HQ_MAX_M];    // rows of each item
     int mate[HQ_MAX_M];    // the second row of the item that a row leads
@@ -134,7 +133,6 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
     it.key[t] = -2;
     it.mask[t] = make_uint4(0, 0, 0, 0);
     int id = -2, rank = 0, place = 0;
-    float scale = 1.0f;
     if (t < M) {
         id = a.ids[t];
         if (id < 0 || id >= a.n_adapters) id = -1;
@@ -142,7 +140,6 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
     __syncthreads();
     if (t < M) {
         rank = id < 0 ? 0 : a.ranks ? a.ranks[id] : a.r_max;  // on its way meanwhile
-        if (id >= 0 && a.scale) scale = a.scale[id];
         place = (int)(((uint32_t)id * 2654435761u) >> 16) & (LTAB - 1);
         for (int probe = 0; probe < LTAB; ++probe) {
             const int old = atomicCAS(&it.key[place], -2, id);
@@ -170,7 +167,6 @@ __device__ void find_items(Items &it, const LoraArgs &a) {
             if (n % LR == 1) it.mate[last] = t;
             it.id[t] = id;
             it.rank[t] = rank < 0 ? 0 : rank > a.r_max ? a.r_max : rank;
-            it.scale[t] = scale;
         }
         const uint32_t leads = __ballot_sync(0xffffffffu, lead);
         if ((t & 31) == 0) it.warp_count[w] = (int)leads;
@@ -497,6 +493,8 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
     find_items(it, a);
     pdl_launch_dependents();
     const long long n0 = (long long)blockIdx.x * LCOLS + warp * LNT * 8;
+    // an adapter's factor, after the wait only: the kernel before may write it
+    auto scale_of = [&](int id) { return id >= 0 && a.scale ? a.scale[id] : 1.0f; };
     // four outputs at a time where every row starts at a 16-byte boundary
     const bool quads = (a.N & 3) == 0 && (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 15) == 0 &&
                        (!a.base || ((a.ldb & 3) == 0 && (reinterpret_cast<uintptr_t>(a.base) & 15) == 0));
@@ -532,7 +530,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             for (int j = 0; j < LNT; ++j) b[j] = next[j];
             const int lead = it.lead[i], nr = it.rows[i], rank = it.rank[lead], cur = i;
             const int row[2] = {lead, nr == 2 ? it.mate[lead] : lead};
-            const float sc = it.scale[lead];
+            const float sc = scale_of(it.id[lead]);
             i = next_few(i + gridDim.y);
             // what comes after the first 32 ranks: of this item, or the next item's
             if (rank > 32) load_b(cur, 32, next);
@@ -645,7 +643,7 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
     while (i < it.n) {
         const int nr = it.rows[i], rank = it.rank[it.lead[i]], cur = i;
-        const float sc = it.scale[it.lead[i]];
+        const float sc = scale_of(it.id[it.lead[i]]);
         const bool end = k0 + 64 >= rank;
         {
             const int left = rank - k0 - tk;  // past the rank nothing is used

@@ -179,3 +179,24 @@ def test_lora_does_not_touch_what_is_past_a_rank_with_many_rows(wt):
     good = [i for i in range(M) if i != 8]
     check(Y[good], x[good], A, B, ids[good], ranks, scale, base[good])
     assert not torch.isfinite(Y[8]).any()
+
+
+@pytest.mark.parametrize("rows", [1, 5])
+def test_lora_scale_may_come_from_the_kernel_before(rows):
+    """Only ids, ranks and the adapters are read early: the factors of a
+    programmatic launch may be outputs of the launch before it."""
+    M, K, N, n, r = 120, 4096, 9000, 24, 32
+    x, A, B, base, _, g = make(M, K, N, n, r, BF16, BF16, seed=5)
+    ids = ((torch.arange(M, device=DEV) // rows) % n).to(torch.int32)
+    ws = [torch.empty(hq.hq_lora_workspace_bytes(M, r), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    factors = hq.lora_apply(x, A, B, ids, base=base)
+    for at in (0, 8900):  # of the first row, the first and the last block's
+        out = torch.zeros_like(factors)
+        got = torch.empty_like(factors)
+        scale = out[0, at:at + n]
+        torch.cuda.synchronize()
+        hq.lora_apply(x, A, B, ids, base=base, Y=out, workspace=ws[0])
+        hq.lora_apply(x, A, B, ids, scale=scale, base=base, Y=got, workspace=ws[1], flags=hq.HQ_LAUNCH_PDL)
+        torch.cuda.synchronize()
+        assert torch.equal(out, factors)
+        assert torch.equal(got, hq.lora_apply(x, A, B, ids, scale=factors[0, at:at + n].clone(), base=base))
