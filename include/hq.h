@@ -496,8 +496,9 @@ int hq_add_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, 
  * Products of 16-bit values are exact and sums are fp32; fp32 activations (and
  * the products A x, which stay fp32) enter the tensor cores as three bf16
  * terms that together hold them.  Sums are taken in a fixed order: results
- * repeat bit for bit.  Elements of A and B past a rank are not used in any
- * sum.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (ids, ranks, A and B are
+ * repeat bit for bit.  Infinities and NaN give what the formula gives in fp32,
+ * however many rows share an adapter.  Elements of A and B past a rank are not
+ * used in any sum.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (ids, ranks, A and B are
  * then read before the wait for the previous kernel, which must not write
  * them; scale, like x and base, is read after it).  Launches two kernels. */
 size_t hq_lora_workspace_bytes(int32_t M, int32_t r_max);

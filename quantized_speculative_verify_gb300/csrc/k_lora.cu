@@ -27,7 +27,11 @@
 // Exactness: products of two 16-bit values are exact in fp32.  Where the
 // MMAs' operand is not of the adapter's type (fp32 activations, and t, which
 // is kept in fp32), the value enters as three bf16 terms whose sum is the value
-// (8 significant bits each), an fp16 weight as two.
+// (8 significant bits each), an fp16 weight as two.  That holds for finite values
+// up to bf16's largest; beyond it the first term is an infinity, which meets
+// terms that are 0.  Such a sum comes out not finite, whatever the other operand,
+// and is formed again from the values themselves (dot_again), so that a row's
+// result does not depend on how many rows share its adapter.
 #include <cooperative_groups.h>
 
 #include "batch.cuh"
@@ -65,15 +69,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// x = t[0] + t[1] + t[2], each a bf16 (packed in pairs).  An infinity stays
-// in the first term alone.
+// x = t[0] + t[1] + t[2], each a bf16 (packed in pairs); finite x up to bf16's
+// largest value.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t (&t)[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         t[i] = pack_bf16(x0, x1);
         const float h0 = __uint_as_float(t[i] << 16), h1 = __uint_as_float(t[i] & 0xffff0000u);
-        x0 = isinf(h0) ? 0.0f : x0 - h0;
-        x1 = isinf(h1) ? 0.0f : x1 - h1;
+        x0 -= h0;
+        x1 -= h1;
     }
 }
 
@@ -83,7 +87,7 @@ __device__ __forceinline__ void split_half(uint32_t w, uint32_t (&t)[2]) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
     t[0] = pack_bf16(f.x, f.y);
     const float h0 = __uint_as_float(t[0] << 16), h1 = __uint_as_float(t[0] & 0xffff0000u);
-    t[1] = pack_bf16(isinf(h0) ? 0.0f : f.x - h0, isinf(h1) ? 0.0f : f.y - h1);
+    t[1] = pack_bf16(f.x - h0, f.y - h1);
 }
 
 // The items of the batch, found by all threads of the block.
@@ -257,6 +261,35 @@ __device__ __forceinline__ void wide_w(const uint4 &u, float (&f)[8]) {
                             : __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         f[2 * i] = v.x;
         f[2 * i + 1] = v.y;
+    }
+}
+
+// The sum of n products of values of x (type x_type) and of weights as they are,
+// by one thread, 8 at a time (both are allocated in eights): for sums of split
+// terms that came out not finite.
+template <bool WBF>
+__device__ __noinline__ float dot_again(const uint8_t *x, int x_type, const uint8_t *w, int n) {
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < n; k += 8) {
+        float f[8], v[8];
+        wide8(x + (size_t)k * type_bytes(x_type), x_type, f);
+        wide_w<WBF>(*reinterpret_cast<const uint4 *>(w + (size_t)k * 2), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < n) sum = fmaf(v[e], f[e], sum);
+    }
+    return sum;
+}
+
+// A row's n <= 8 neighbouring outputs, the sums formed as in dot_again.
+template <bool WBF>
+__device__ __noinline__ void outputs_again(const float *base, float *y, const float *t, const uint8_t *b, int r_max,
+                                           int rank, float scale, int n) {
+    for (int e = 0; e < n; ++e) {
+        const float add = rank > 0 ? scale * dot_again<WBF>(reinterpret_cast<const uint8_t *>(t), HQ_F32, b, rank) : 0.0f;
+        y[e] = (base ? base[e] : 0.0f) + add;
+        b += (size_t)r_max * 2;
     }
 }
 
@@ -476,6 +509,9 @@ __global__ void __cluster_dims__(LCL, 1, 1) __launch_bounds__(LWARPS * 32, 2) k_
             float v = 0.0f;
 #pragma unroll
             for (int b = 0; b < LCL; ++b) v += *cluster.map_shared_rank(&s_part[0][m][c], b);
+            if (!SAME && !isfinite(v) && c < rank)
+                v = dot_again<WBF>(static_cast<const uint8_t *>(a.x) + (size_t)rows[m] * (size_t)a.ldx * xb, a.x_type,
+                                   static_cast<const uint8_t *>(a.A) + ((size_t)id * a.r_max + r0 + c) * (size_t)a.K * 2, a.K);
             a.t[(size_t)rows[m] * a.r_max + r0 + c] = v;
         }
         cluster.sync();  // the others may still be reading this block's sums
@@ -636,6 +672,10 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
         load_b(i, 0);
         tv = load_t(i, 0);
     }
+    // The item from which on this thread leaves its outputs to the loop at the end
+    // (formed again in here, with what calls keep in registers, they cost every
+    // call 2 us of 19).
+    int again = HQ_MAX_M;
     float acc[LNT][4];
 #pragma unroll
     for (int j = 0; j < LNT; ++j)
@@ -693,10 +733,16 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
             tv = load_t(i, k0);
         }
         if (!end) continue;
+        float odd = 0.0f;  // NaN where a sum is not finite
+#pragma unroll
+        for (int j = 0; j < LNT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd = fmaf(acc[j][e], 0.0f, odd);
+        if (odd != 0.0f && again > cur) again = cur;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int m = g + 8 * h;
-            if (m >= nr) continue;
+            if (m >= nr || again <= cur) continue;
             const size_t r = it.row[cur][m];
             float y[8];
 #pragma unroll
@@ -737,6 +783,16 @@ __global__ void __launch_bounds__(LWARPS * 32, 3) k_lora_expand(const LoraArgs a
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
     }
+    // the first item with a sum that is not finite, and what comes after it
+    for (i = again; i < it.n; i = next_many(i + gridDim.y))
+        for (int h = 0; h < 2; ++h) {
+            if (g + 8 * h >= it.rows[i] || ny >= a.N) continue;
+            const size_t r = it.row[i][g + 8 * h];
+            const int id = it.id[it.lead[i]];
+            outputs_again<WBF>(a.base ? a.base + r * a.ldb + ny : nullptr, a.Y + r * a.ldy + ny, a.t + r * a.r_max,
+                               static_cast<const uint8_t *>(a.B) + ((size_t)(id < 0 ? 0 : id) * a.N + ny) * (size_t)a.r_max * 2,
+                               a.r_max, it.rank[it.lead[i]], scale_of(id), a.N - ny < 8 ? (int)(a.N - ny) : 8);
+        }
 }
 
 }  // namespace

@@ -200,3 +200,76 @@ def test_lora_scale_may_come_from_the_kernel_before(rows):
         torch.cuda.synchronize()
         assert torch.equal(out, factors)
         assert torch.equal(got, hq.lora_apply(x, A, B, ids, scale=factors[0, at:at + n].clone(), base=base))
+
+
+def same_as_64_bits(Y, x, A, B, ids, ranks, base):
+    """check() for rows with infinities: the same infinities and NaN, the finite rows in its bounds."""
+    for m, a in enumerate(ids.tolist()):
+        k = int(ranks[a])
+        ref = base[m].double() + B[a, :, :k].double() @ (A[a, :k].double() @ x[m].double())
+        got = Y[m].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"row {m}"
+        assert torch.equal(torch.where(torch.isinf(ref), ref, 0.0 * base[m]), torch.where(torch.isinf(got), got, 0.0 * base[m])), f"row {m}"
+        if torch.isfinite(ref).all():
+            check(Y[m:m + 1], x[m:m + 1], A, B, ids[m:m + 1], ranks, None, base[m:m + 1])
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 20])
+@pytest.mark.parametrize("xt,wt", [(F32, F16), (F32, BF16), (F16, BF16), (BF16, F16), (F16, F16)])
+@pytest.mark.parametrize("where", ["x", "A", "B"])
+def test_lora_infinities_do_not_depend_on_the_rows_of_an_adapter(rows, xt, wt, where):
+    K, N, r = 520, 150, 8
+    x, A, B, base, _, g = make(rows, K, N, 2, r, xt, wt, seed=rows)
+    A[1] = torch.where(torch.randn((r, K), generator=g, device=DEV) > 0, 0.5, -0.25).to(wt)  # few significant bits
+    A[0] = A[0] + torch.where(A[0] < 0, -0.01, 0.01).to(wt)  # no zeros
+    B += torch.where(B < 0, -0.01, 0.01).to(wt)
+    ranks = torch.tensor([1, 1], dtype=torch.int32, device=DEV)
+    inf = float("inf")
+    if where == "x":
+        x[0, 77] = inf
+        if rows > 1:
+            x[rows // 2, 300] = -inf
+    elif where == "A":
+        x += torch.where(x < 0, -0.01, 0.01).to(xt)
+        A[:, 0, 11] = inf
+    else:
+        B[:, 3, 0], B[:, 149, 0] = inf, -inf
+    for a in (0, 1):
+        ids = torch.full((rows,), a, dtype=torch.int32, device=DEV)
+        Y = hq.lora_apply(x, A, B, ids, ranks, base=base)
+        assert torch.isinf(Y[0]).any() and (where != "B" or torch.isfinite(Y[0]).any())
+        same_as_64_bits(Y, x, A, B, ids, ranks, base)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20])
+@pytest.mark.parametrize("wt", [F16, BF16])
+def test_lora_largest_finite_activations(rows, wt):
+    """fp32 values that round past bf16's largest, as activations and as products A x."""
+    K, N, r = 264, 70, 16
+    x, A, B, base, _, g = make(rows, K, N, 1, r, F32, wt, seed=rows)
+    top = torch.finfo(F32).max
+    x[0, 5] = top
+    A[0, :, 5] = torch.linspace(-1.0, 1.0, r, device=DEV).to(wt)
+    A[0, 0] = 0
+    A[0, 0, 5] = 1.0  # t = the largest value itself
+    B *= 0.01
+    ids, ranks = torch.zeros(rows, dtype=torch.int32, device=DEV), torch.tensor([r], dtype=torch.int32, device=DEV)
+    Y = hq.lora_apply(x, A, B, ids, base=base)
+    assert bool(torch.isfinite(Y).all())
+    check(Y, x, A, B, ids, ranks, None, base)
+
+
+@pytest.mark.parametrize("wt", [F16, BF16])
+def test_lora_infinities_in_place_among_several_adapters(wt):
+    """Each block takes several groups of rows in turn; one in the middle holds the infinities."""
+    M, K, N, n, r = 128, 256, 40000, 8, 24
+    x, A, B, base, _, g = make(M, K, N, n, r, F32, wt, seed=3)
+    ids = (torch.arange(M, device=DEV) // 16).to(torch.int32)
+    ranks = torch.tensor([24, 17, 8, 1, 24, 0, 5, 24], dtype=torch.int32, device=DEV)
+    B[3, ::1000, 0] = float("inf")
+    x[50, 9] = float("-inf")  # of the same adapter
+    x[70, 1] = float("nan")   # of the next
+    Y = base.clone()
+    hq.lora_apply(x, A, B, ids, ranks, base=Y, Y=Y)
+    same_as_64_bits(Y, x, A, B, ids, ranks, base)
+    assert torch.isinf(Y[50]).all() and torch.isinf(Y[49]).sum() == 40 and torch.isnan(Y).any(1).sum() == 1
