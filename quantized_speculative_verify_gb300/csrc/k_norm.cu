@@ -98,10 +98,15 @@ __device__ __forceinline__ void store8(void *row, int type, int octet, const flo
     static_cast<uint4 *>(row)[octet] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The largest value of the warp's lanes (NaN only if all are).
+// The larger value, the largest of the warp's lanes; NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
 __device__ __forceinline__ float warp_max(float x) {
     float y;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
                     for (int i = 0; i < 8; ++i) z[j][i] = fmaf(sign, z[j][i], __shfl_xor_sync(0xffffffffu, z[j][i], lb));
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(z[j][i]));
+                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
             }
         }
 #pragma unroll
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         amax = warp_max(amax);
-        // an all-zero row with eps = 0 gives zeros; NaN and infinities reach sx and h
+        // an all-zero row with eps = 0 gives zeros
         const float d = ss * inv_k + a.eps;
         const float rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
         if (a.h) {
@@ -341,7 +346,11 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             }
         }
         if (!quant) continue;
-        if (tid == 0) a.sx[row] = rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f);
+        // A row with an infinity has sx = NaN, whatever the butterfly made of it
+        // (infinities of both signs cancel to NaN, and 1/rms is 0).
+        if (tid == 0)
+            a.sx[row] = isfinite(ss) ? rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f) : __int_as_float(0x7fffffff);
+        // NaN and infinite maxima leave no code: 0 * z, infinity * 0 and NaN round to 0
         const float inv = amax == 0.0f ? 0.0f : 127.0f / amax;
 
         int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;

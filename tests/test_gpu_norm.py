@@ -233,3 +233,54 @@ def test_norm_of_many_rows_behind_an_fp32_projection(M, K, t, pad):
     for g in (out, h, qx, sx):
         g.check()
     check(x, r, w, signs, 1e-6, None if pad else out.t, h.t, qx.t, sx.t)
+
+
+def outputs(d, x, r, w, signs, eps, qop):
+    """Everything the call writes (qop: with the operand), and a GEMM's output of the operand."""
+    M, K = x.shape
+    h, qx, sx = torch.empty((M, K), device=DEV), torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    gs = torch.empty((M, K // d.group), dtype=torch.int32, device=DEV)
+    op = torch.empty(hq.hq_act_operand_bytes(d, M), dtype=torch.uint8, device=DEV) if qop else None
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), eps, h=h, qx=qx, gsum=gs, qop=op, sx=sx)
+    Y = None
+    if qop:
+        layer = hq.pack_layer(0.02 * torch.randn((128, K), device=DEV), d.group, d.format, signs)
+        Y = torch.empty((M, 128), device=DEV)
+        hq.hq_verify_gemm(layer.desc, layer.blob, op, sx, M, Y, None, hq.workspace(layer.desc, M, DEV), hq.HQ_LAUNCH_EXACT_ORDER)
+    assert torch.equal(gs, qx.view(M, K // d.group, d.group).to(torch.int32).sum(2, dtype=torch.int32))
+    return h, qx, sx, Y
+
+
+NONFINITE = [  # rows, features, group, format, x, residual, operand: direct with either encoding, through the ring
+    (6, 256, 32, "w4", F32, F32, True), (40, 1024, 64, "w4", BF16, F32, True), (100, 512, 128, "w8", F16, BF16, True),
+    (9, 16384, 64, "w8", BF16, BF16, True), (1500, 2048, 32, "w4", BF16, BF16, False), (700, 4096, 64, "w4", F32, F16, False),
+    (900, 736, 32, "w4", F32, F32, False)]
+
+
+@pytest.mark.parametrize("M,K,G,fmt,xt,rt,qop", NONFINITE)
+def test_norm_infinities_of_any_pattern_reach_the_scale(M, K, G, fmt, xt, rt, qop):
+    x, r, w, signs = make(M, K, xt, rt, seed=M, spread=1.0)
+    inf = float("inf")
+    x[0] = inf                              # every block of the row: infinities of both signs after the layer's
+    x[1, 32:36] = inf                       # one block
+    x[2, 64:96] = torch.tensor([inf, -inf], device=DEV).repeat(16).to(xt)
+    x[3, K - 1], r[3, K - 2] = inf, -inf
+    x[4, 40], r[4, 40] = inf, -inf          # their sum is NaN
+    h, qx, sx, Y = outputs(hq.make_desc(K, 128, G, fmt), x, r, w, signs, 1e-6, qop)
+    assert not torch.isfinite(sx[:5]).any() and not qx[:5].any()
+    assert not torch.isfinite(h[torch.arange(5), [0, 33, 70, K - 1, 40]]).any()
+    if qop:
+        assert torch.isnan(Y[:5]).all() and torch.isfinite(Y[5:]).all()
+    check(x[5:], r[5:], w, signs, 1e-6, None, h[5:], qx[5:], sx[5:])
+
+
+@pytest.mark.parametrize("M,K,G,fmt,xt,rt,qop", NONFINITE)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_norm_weights_that_are_not_finite_reach_every_scale(M, K, G, fmt, xt, rt, qop, bad):
+    x, r, w, signs = make(M, K, xt, rt, seed=M, spread=1.0)
+    w[K // 2] = bad
+    h, qx, sx, Y = outputs(hq.make_desc(K, 128, G, fmt), x, r, w, signs, 1e-6, qop)
+    assert not torch.isfinite(sx).any() and not qx.any()
+    assert not torch.isfinite(h[:, K // 2]).any() and torch.isfinite(h[:, :K // 2]).all()
+    if qop:
+        assert not torch.isfinite(Y).any()
