@@ -467,7 +467,9 @@ typedef enum { HQ_F32 = 0, HQ_F16 = 1, HQ_BF16 = 2 } hq_type;
  * too (ldx, ldr, ldh at least K and a multiple of 16 bytes).  An all-zero row
  * has sx = 0 and codes 0.  A row whose sums hold a NaN or an infinity, and a
  * row whose product with the weight does, has a NaN or infinite sx and codes
- * 0, so that a GEMM of it gives NaN.  flags:
+ * 0, so that a GEMM of it gives NaN.  Other rows may be of any size: sums and
+ * codes of very large or small ones are formed in units of a power of two.
+ * flags:
  * HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (weight and signs are then read before
  * the wait for the previous kernel). */
 int hq_add_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, int64_t ldx, const void *residual,

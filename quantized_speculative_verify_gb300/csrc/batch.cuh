@@ -43,6 +43,7 @@ struct NormArgs {
     int x_type, r_type, h_type;
     int M, K, G;
     int rs, e4, sums;  // encoding of the operand (hq_internal.cuh)
+    int keep;          // set by launch_norm
 };
 cudaError_t launch_norm(const NormArgs &a, bool pdl, cudaStream_t s);
 

@@ -118,8 +118,277 @@ __device__ __forceinline__ uint32_t pack_s8(int x0, int x1, int x2, int x3) {
     return d;
 }
 
+// The range in which a row's sum of squares and largest |z| are taken as they
+// are.  Below it squares, or quotients by it, leave fp32's range; a sum of squares
+// that overflows is above it.  Rows outside are formed again (form_again) in units
+// of 2^e, the power of two above their largest |s|: sums and codes of 2^-e s, with
+// eps and 1/rms to match.
+constexpr float SUM_LEAST = 0x1p-80f, MAX_LEAST = 0x1p-110f;
+constexpr float MAX_CODED = 0x1p-120f;  // 127 / it is finite
+// They need the row's inputs once more.  Without a ring, a 16-bit input that
+// residual_out lies over is kept in shared memory (an fp32 residual_out is s itself).
+enum { KEEP_NONE = 0, KEEP_X = 1, KEEP_R = 2 };
+
+// The rotation of a 32-block, without its factor: 8 consecutive values a lane,
+// four lanes a block.
+__device__ __forceinline__ void rotate8(float (&z)[8], int lane) {
+#pragma unroll
+    for (int st = 1; st <= 4; st <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & st) == 0) {
+                const float p = z[i], q = z[i + st];
+                z[i] = p + q;
+                z[i + st] = p - q;
+            }
+#pragma unroll
+    for (int lb = 1; lb <= 2; lb <<= 1) {
+        // lower lane a + b, upper lane a - b: one exact multiply-add
+        const float sign = (lane & lb) != 0 ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = fmaf(sign, z[i], __shfl_xor_sync(0xffffffffu, z[i], lb));
+    }
+}
+
 __device__ __forceinline__ const void *row_of(const void *p, int type, int64_t ld, int row) {
     return static_cast<const uint8_t *>(p) + (size_t)row * (size_t)ld * type_bytes(type);
+}
+
+// A row's codes and group sums, where they go (OPERAND: into the GEMM's operand
+// too, whose layout hq_internal.cuh has: K tiles of code blocks, then group sums).
+template <bool OPERAND>
+struct Codes {
+    const NormArgs &a;
+    int *s_gs;  // group sums of the row, in shared memory
+    int MT, n8, n8pad, bpt, gpt, ngk, ngp, cb, width;
+    size_t tb;
+    bool sums;
+    __device__ __forceinline__ Codes(const NormArgs &a, int K, int G, int MT, int *s_gs) : a(a), s_gs(s_gs), MT(MT) {
+        n8 = K >> 3;
+        n8pad = act_blocks(K) * (ACT_BLOCK / 8);
+        bpt = act_kt(G) / ACT_BLOCK, gpt = act_kt(G) / G, ngk = K / G, ngp = act_ktiles(K, G) * gpt;
+        cb = MT * (a.rs ? ACT_RS_PITCH : 256);
+        tb = (size_t)bpt * cb + (a.sums ? (size_t)gpt * MT * 4 : 0);
+        width = G / 8 < 32 ? G / 8 : 32;
+        sums = a.gsum != nullptr || (OPERAND && a.qop != nullptr && a.sums != 0);
+    }
+    // 8 features from 8 idx on
+    __device__ __forceinline__ void put(int row, int idx, uint4 codes16, uint2 lo, uint2 hi) const {
+        const int f = idx * 8, kb = f / ACT_BLOCK, fb = f % ACT_BLOCK;
+        uint8_t *blk = a.qop + (size_t)(bpt == 1 ? kb : kb >> 1) * tb + (size_t)(bpt == 1 ? 0 : kb & 1) * cb;
+        if (a.rs) {
+            *reinterpret_cast<uint4 *>(blk + (size_t)row * ACT_RS_PITCH + (size_t)fb * 2) = codes16;
+        } else if (a.e4) {
+            uint8_t *d = blk + ((size_t)(fb / 16) * 2 * MT + row) * 16 + (size_t)(fb % 16);
+            *reinterpret_cast<uint2 *>(d) = lo;
+            *reinterpret_cast<uint2 *>(d + (size_t)MT * 16) = hi;
+        } else {
+            *reinterpret_cast<uint4 *>(blk + ((size_t)(fb / 8) * MT + row) * 16) = codes16;
+        }
+    }
+    __device__ __forceinline__ void put_sum(int row, int g, float v) const {
+        reinterpret_cast<float *>(a.qop + (size_t)(g / gpt) * tb + (size_t)bpt * cb)[(size_t)(g % gpt) * MT + row] = v;
+    }
+    template <int T>
+    __device__ __forceinline__ void pad(int row) const {  // a row past the last
+        for (int idx = threadIdx.x; idx < n8pad; idx += T) put(row, idx, make_uint4(0, 0, 0, 0), make_uint2(0, 0), make_uint2(0, 0));
+        if (a.sums)
+            for (int g = threadIdx.x; g < ngp; g += T) put_sum(row, g, 0.0f);
+    }
+    template <int T>
+    __device__ __forceinline__ void clear_sums() const {
+        for (int g = threadIdx.x; g < ngk; g += T) s_gs[g] = 0;
+    }
+    // The codes of an octet of the rotated row; inv: 127 / max|z|.
+    __device__ __forceinline__ void write(int row, int idx, const float (&z)[8], float inv) const {
+        int q[8], gs = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // |z| <= amax, 127 / amax is finite: the product rounds to at most 127
+            q[i] = idx < n8 ? __float2int_rn(z[i] * inv) : 0;
+        }
+        if (a.qx && idx < n8)
+            reinterpret_cast<uint2 *>(a.qx + (size_t)row * a.K)[idx] =
+                make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+        if (OPERAND && a.qop && idx < n8pad) {
+            uint4 c16 = make_uint4(0, 0, 0, 0);
+            uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
+            if (a.e4) {
+                digits4(q[0], q[1], q[2], q[3], lo.x, hi.x);
+                digits4(q[4], q[5], q[6], q[7], lo.y, hi.y);
+            } else {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 p = __halves2half2(__int2half_rn(q[2 * i]), __int2half_rn(q[2 * i + 1]));
+                    h[i] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+                c16 = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            put(row, idx, c16, lo, hi);
+        }
+        // a group's G / 8 threads are consecutive lanes (G = 16: two lanes)
+        if (sums) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gs += q[i];
+            for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
+            if (idx < n8 && (threadIdx.x & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / a.G], gs);
+        }
+    }
+    template <int T>
+    __device__ __forceinline__ void write_sums(int row) const {
+        if (!sums) return;
+        __syncthreads();
+        for (int g = threadIdx.x; g < ngp; g += T) {
+            const int v = g < ngk ? s_gs[g] : 0;
+            if (a.gsum && g < ngk) a.gsum[(size_t)row * ngk + g] = v;
+            if (OPERAND && a.qop && a.sums) put_sum(row, g, (float)v);
+        }
+    }
+};
+
+// 8 weights with the features' signs (sg: the signs).
+__device__ __forceinline__ void load_weight(const NormArgs &a, int idx, float (&w)[8], uint32_t &sg) {
+    sg = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+    if (idx < a.K >> 3) {
+        widen(load_raw(a.weight, HQ_F32, idx), HQ_F32, w);
+        if (a.sx) sg = (__ldg(a.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = flip(w[i], (sg >> i) & 1u);
+}
+
+// A whole row by the block in three passes over its inputs: rows of zeros, rows
+// that are not finite, and those described at SUM_LEAST.  in: the row in the ring,
+// xu and ru pieces an octet; without one (DIRECT), the input that residual_out
+// lies over and has replaced.  s_far: 3 T / 32 floats.
+//
+// It must not take registers from the rows of the common kind: without a ring it
+// is called (1 row of 4096: 3.5 us as before), in the loop over the ring a call
+// costs every row 60 %, so it is inlined there, with the weights read again after
+// it.  8192 rows of 8192 in bf16 take 116 us as before, of 12288 217 instead of
+// 196 (fp32 x: 292 instead of 266).
+template <int T, bool DIRECT>
+__device__ __forceinline__ void form_again(const NormArgs &a, int row, int MT, const uint8_t *in, int xu, int ru, int *s_gs,
+                                           float *s_far) {
+    int tid = threadIdx.x, K = a.K, G = a.G;
+    float eps = a.eps;
+    asm volatile("" : "+r"(tid), "+r"(K), "+r"(G), "+f"(eps));  // nothing of this is worked out ahead, in registers of every row
+    const int lane = tid & 31, n8 = K >> 3;
+    const bool quant = a.sx != nullptr;
+    const Codes<DIRECT> codes(a, K, G, MT, s_gs);
+    const bool s_out = DIRECT && a.res_out && a.r_type == HQ_F32 && (a.res_out == a.res || a.res_out == a.x);
+    auto load = [&](int j, float (&s)[8]) {  // s of octet j T + tid
+        const int idx = j * T + tid;
+        float r[8];
+        Raw x = {}, y = {};
+        if (idx < n8) {
+            if (!DIRECT) {
+                const uint4 *d = reinterpret_cast<const uint4 *>(in) + (size_t)j * (xu + ru) * T + tid;
+                x.u = d[0];
+                if (xu == 2) x.v = d[T];
+                if (ru) y.u = d[xu * T];
+                if (ru == 2) y.v = d[(xu + 1) * T];
+            } else if (s_out) {
+                x = load_raw(row_of(a.res_out, HQ_F32, a.ldr, row), HQ_F32, idx);
+            } else {
+                if (a.keep && a.x == a.res_out) x.u = reinterpret_cast<const uint4 *>(in)[idx];
+                else x = load_raw(row_of(a.x, a.x_type, a.ldx, row), a.x_type, idx);
+                if (a.keep && a.res == a.res_out) y.u = reinterpret_cast<const uint4 *>(in)[idx];
+                else if (a.res) y = load_raw(row_of(a.res, a.r_type, a.ldr, row), a.r_type, idx);
+            }
+        }
+        widen(x, s_out ? HQ_F32 : a.x_type, s);
+        widen(y, a.r_type, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += r[i];
+    };
+    float s[8], u[8], ss = 0.0f, amax = 0.0f, top = 0.0f;
+    uint32_t signs;
+#pragma unroll 1
+    for (int j = 0; j * T < n8; ++j) {
+        load(j, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(s[i]));
+    }
+    top = warp_max(top);
+    if (lane == 0) s_far[tid >> 5] = top;
+    __syncthreads();
+    top = warp_max(lane < T / 32 ? s_far[lane] : 0.0f);
+    float down = 1.0f, rest = 1.0f, rstd = -1.0f;
+    if (top > 0.0f && top < INFINITY) {
+        // 2^(e - 1) <= top < 2^e; 2^-e as two factors, each of them a float
+        const bool small = top < 0x1p-60f;
+        const int e = (__float_as_int(small ? top * 0x1p80f : top) >> 23) - (small ? 206 : 126), half = e / 2;
+        down = __int_as_float((127 - half) << 23);
+        rest = __int_as_float((127 - e + half) << 23);
+        // eps in the units of s^2; where it is all that counts, 1/rms itself
+        const float root = sqrtf(eps), q = root * down * rest;
+        if (q < 0x1p60f)
+            eps = q * q;
+        else
+            rstd = 1.0f / root * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23);
+    }
+#pragma unroll 1
+    for (int j = 0; j * T < n8; ++j) {
+        load(j, s);
+        load_weight(a, j * T + tid, u, signs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[i] = s[i] * down * rest;
+            ss = fmaf(s[i], s[i], ss);
+            s[i] *= u[i];
+        }
+        if (quant) rotate8(s, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(s[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    amax = warp_max(amax);
+    if (lane == 0) {
+        s_far[T / 32 + (tid >> 5)] = ss;
+        s_far[2 * (T / 32) + (tid >> 5)] = amax;
+    }
+    __syncthreads();
+    ss = lane < T / 32 ? s_far[T / 32 + lane] : 0.0f;
+    amax = warp_max(lane < T / 32 ? s_far[2 * (T / 32) + lane] : 0.0f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (rstd < 0.0f) {  // (an all-zero row with eps = 0 gives zeros)
+        const float d = ss * (1.0f / (float)K) + eps;
+        rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
+    }
+    // A row with an infinity has sx = NaN, whatever the butterfly made of it
+    // (infinities of both signs cancel to NaN, and 1/rms is 0).
+    if (quant && tid == 0)
+        a.sx[row] = isfinite(ss) ? rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f) : __int_as_float(0x7fffffff);
+    // No codes for maxima that are 0 (the weight's doing, next to it too), NaN or
+    // infinite: 0 * z, 0 * infinity and NaN round to 0.
+    const float inv = amax >= MAX_CODED ? 127.0f / amax : 0.0f;
+#pragma unroll 1
+    for (int j = 0; j * T < codes.n8pad; ++j) {
+        const int idx = j * T + tid;
+        load(j, s);
+        load_weight(a, idx, u, signs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[i] = s[i] * down * rest * u[i];
+            u[i] = s[i] * rstd;
+        }
+        if (idx < n8 && a.h) store8(const_cast<void *>(row_of(a.h, a.h_type, a.ldh, row)), a.h_type, idx, u, signs);
+        if (!quant) continue;
+        rotate8(s, lane);
+        codes.write(row, idx, s, inv);
+    }
+    codes.template write_sums<T>(row);
+}
+
+template <int T>
+__device__ __noinline__ void form_again_call(const NormArgs &a, int row, int MT, const uint8_t *in, int *s_gs, float *s_far) {
+    form_again<T, true>(a, row, MT, in, 0, 0, s_gs, s_far);
 }
 
 // Copies of 16 bytes into shared memory that the thread waits for by groups, in
@@ -132,53 +401,32 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 // of 8192 in bf16 114 both, of 12288 in fp32 and bf16 321 and (three do not fit) 400.
 constexpr int NSTAGES = 2;
 constexpr int NORM_SMEM = 220 << 10;  // shared memory of an SM's blocks
-constexpr int NORM_FIXED = 18 << 10;  // of which a block needs beside its ring, with the system's 1 KB
+constexpr int NORM_FIXED = 19 << 10;  // of which a block needs beside its ring, with the system's 1 KB
 
 // RING: 0, or rows through the ring (no operand is written): of any types, or
 // residual and h of one 16-bit type and x of the same or fp32 (a projection's
 // output).
 enum { DIRECT = 0, RING_ANY = 1, RING_F16 = 2, RING_BF16 = 3, RING_F32_F16 = 4, RING_F32_BF16 = 5 };
 template <int V, int T, int RING>
-__global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
+__global__ void __launch_bounds__(T, 1024 / T) k_add_norm_quant(const NormArgs a) {
     extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][16-byte piece of a thread's share][thread]
-    __shared__ float s_sum[2][T / 32], s_max[2][T / 32];  // by the parity of the row's turn
+    __shared__ float s_sum[2][T / 32], s_max[2][T / 32];  // by the row's place in the ring
     __shared__ int s_gs[MAX_K / 16];  // group sums of this row
+    __shared__ float s_far[3][T / 32];  // for form_again
+    __shared__ NormArgs s_args;         // for form_again_call
     int row = blockIdx.x;
     const int MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
-    const int K = a.K, G = a.G, n8 = K >> 3;
+    const int K = a.K, n8 = K >> 3;
     const bool quant = a.sx != nullptr;
+    const Codes<RING == DIRECT> codes(a, K, a.G, MT, s_gs);
     constexpr int ONE = RING == RING_F16 || RING == RING_F32_F16 ? HQ_F16 : RING == RING_BF16 || RING == RING_F32_BF16 ? HQ_BF16 : -1;
     const int x_type = RING >= RING_F32_F16 ? HQ_F32 : ONE >= 0 ? ONE : a.x_type;
     const int r_type = ONE >= 0 ? ONE : a.r_type, h_type = ONE >= 0 ? ONE : a.h_type;
     const float inv_k = 1.0f / (float)K;
 
-    // the operand's layout (hq_internal.cuh): K tiles of code blocks, then group sums
-    const int n8pad = act_blocks(K) * (ACT_BLOCK / 8);
-    const int bpt = act_kt(G) / ACT_BLOCK, gpt = act_kt(G) / G, ngk = K / G, ngp = act_ktiles(K, G) * gpt;
-    const int cb = MT * (a.rs ? ACT_RS_PITCH : 256);
-    const size_t tb = (size_t)bpt * cb + (a.sums ? (size_t)gpt * MT * 4 : 0);
-    auto put = [&](int idx, uint4 codes16, uint2 lo, uint2 hi) {  // 8 features from 8 idx on
-        const int f = idx * 8, kb = f / ACT_BLOCK, fb = f % ACT_BLOCK;
-        uint8_t *blk = a.qop + (size_t)(bpt == 1 ? kb : kb >> 1) * tb + (size_t)(bpt == 1 ? 0 : kb & 1) * cb;
-        if (a.rs) {
-            *reinterpret_cast<uint4 *>(blk + (size_t)row * ACT_RS_PITCH + (size_t)fb * 2) = codes16;
-        } else if (a.e4) {
-            uint8_t *d = blk + ((size_t)(fb / 16) * 2 * MT + row) * 16 + (size_t)(fb % 16);
-            *reinterpret_cast<uint2 *>(d) = lo;
-            *reinterpret_cast<uint2 *>(d + (size_t)MT * 16) = hi;
-        } else {
-            *reinterpret_cast<uint4 *>(blk + ((size_t)(fb / 8) * MT + row) * 16) = codes16;
-        }
-    };
-    auto put_sum = [&](int g, float v) {
-        reinterpret_cast<float *>(a.qop + (size_t)(g / gpt) * tb + (size_t)bpt * cb)[(size_t)(g % gpt) * MT + row] = v;
-    };
-
     if (row >= a.M) {  // padding row of the operand
         pdl_wait();
-        for (int idx = tid; idx < n8pad; idx += T) put(idx, make_uint4(0, 0, 0, 0), make_uint2(0, 0), make_uint2(0, 0));
-        if (a.sums)
-            for (int g = tid; g < ngp; g += T) put_sum(g, 0.0f);
+        codes.template pad<T>(row);
         pdl_launch_dependents();
         return;
     }
@@ -188,20 +436,9 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
     float w[V][8];
     uint32_t sg[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-        sg[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[j][i] = 0.0f;
-        if (idx < n8) {
-            widen(load_raw(a.weight, HQ_F32, idx), HQ_F32, w[j]);
-            if (quant) sg[j] = (__ldg(a.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[j][i] = flip(w[j][i], (sg[j] >> i) & 1u);
-    }
+    for (int j = 0; j < V; ++j) load_weight(a, tid + j * T, w[j], sg[j]);
+    if (RING == DIRECT && tid == 0) s_args = a;
     pdl_wait();
-    const bool need_gs = a.gsum != nullptr || (RING == DIRECT && a.qop != nullptr && a.sums != 0);
     Raw xn[V], rn[V];
     auto fetch = [&](int r) {
         const void *xr = row_of(a.x, x_type, a.ldx, r);
@@ -254,10 +491,11 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
     int stage = 0;
     if constexpr (RING != DIRECT)
         for (int i = 0; i < NSTAGES; ++i) issue(row + i * MT, i);
-    for (int turn = 0; row < a.M; ++turn, row += MT) {
-        if (need_gs) {
-            if (turn) __syncthreads();  // the last row's sums have been read
-            for (int g = tid; g < ngk; g += T) s_gs[g] = 0;
+    static_assert(NSTAGES == 2, "a row's sums are read while the next one's are written");
+    for (; row < a.M; row += MT) {
+        if (codes.sums) {
+            if (RING != DIRECT) __syncthreads();  // the last row's sums have been read
+            codes.template clear_sums<T>();
         }
         if constexpr (RING != DIRECT) {
             asm volatile("cp.async.wait_group %0;" ::"n"(NSTAGES - 1) : "memory");
@@ -280,6 +518,7 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int idx = tid + j * T;
+            if (RING == DIRECT && a.keep) reinterpret_cast<uint4 *>(s_ring)[j * T + tid] = a.keep == KEEP_X ? xn[j].u : rn[j].u;
             if (ro && idx < n8) store8(ro, r_type, idx, v[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -294,22 +533,7 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             for (int j = 0; j < V; ++j) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[j][i] = v[j][i];
-#pragma unroll
-                for (int st = 1; st <= 4; st <<= 1)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if ((i & st) == 0) {
-                            const float p = z[j][i], q = z[j][i + st];
-                            z[j][i] = p + q;
-                            z[j][i + st] = p - q;
-                        }
-#pragma unroll
-                for (int lb = 1; lb <= 2; lb <<= 1) {
-                    // lower lane a + b, upper lane a - b: one exact multiply-add
-                    const float sign = (lane & lb) != 0 ? -1.0f : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[j][i] = fmaf(sign, z[j][i], __shfl_xor_sync(0xffffffffu, z[j][i], lb));
-                }
+                rotate8(z[j], lane);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
             }
@@ -318,22 +542,32 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         amax = warp_max(amax);
         if (lane == 0) {
-            s_sum[turn & 1][tid >> 5] = ss;
-            s_max[turn & 1][tid >> 5] = amax;
+            s_sum[RING == DIRECT ? 0 : stage][tid >> 5] = ss;
+            s_max[RING == DIRECT ? 0 : stage][tid >> 5] = amax;
         }
         __syncthreads();
+        ss = lane < T / 32 ? s_sum[RING == DIRECT ? 0 : stage][lane] : 0.0f;
+        amax = lane < T / 32 ? s_max[RING == DIRECT ? 0 : stage][lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        amax = warp_max(amax);
+        if (!(ss >= SUM_LEAST && ss < INFINITY) || (quant && !(amax >= MAX_LEAST && amax < INFINITY))) {
+            if constexpr (RING == DIRECT) {
+                form_again_call<T>(s_args, row, MT, s_ring, s_gs, &s_far[0][0]);
+                return;
+            }
+            form_again<T, false>(a, row, MT, s_ring + (size_t)stage * stage_bytes, xu, ru, s_gs, &s_far[0][0]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) load_weight(a, tid + j * T, w[j], sg[j]);  // (not held meanwhile)
+            issue(row + NSTAGES * MT, stage);
+            if (++stage == NSTAGES) stage = 0;
+            continue;
+        }
         if constexpr (RING != DIRECT) {  // what the thread took has been used
             issue(row + NSTAGES * MT, stage);
             if (++stage == NSTAGES) stage = 0;
         }
-        ss = lane < T / 32 ? s_sum[turn & 1][lane] : 0.0f;
-        amax = lane < T / 32 ? s_max[turn & 1][lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        amax = warp_max(amax);
-        // an all-zero row with eps = 0 gives zeros
-        const float d = ss * inv_k + a.eps;
-        const float rstd = d == 0.0f ? 0.0f : 1.0f / sqrtf(d);
+        const float rstd = 1.0f / sqrtf(ss * inv_k + a.eps);
         if (a.h) {
             void *hr = const_cast<void *>(row_of(a.h, h_type, a.ldh, row));
 #pragma unroll
@@ -346,65 +580,16 @@ __global__ void __launch_bounds__(T) k_add_norm_quant(const NormArgs a) {
             }
         }
         if (!quant) continue;
-        // A row with an infinity has sx = NaN, whatever the butterfly made of it
-        // (infinities of both signs cancel to NaN, and 1/rms is 0).
-        if (tid == 0)
-            a.sx[row] = isfinite(ss) ? rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f) : __int_as_float(0x7fffffff);
-        // NaN and infinite maxima leave no code: 0 * z, infinity * 0 and NaN round to 0
-        const float inv = amax == 0.0f ? 0.0f : 127.0f / amax;
-
-        int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
-        const int width = G / 8 < 32 ? G / 8 : 32;
+        if (tid == 0) a.sx[row] = rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f);
+        const float inv = 127.0f / amax;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int idx = tid + j * T;
-            int q[8], gs = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // |z| <= amax: the product rounds to at most 127 (NaN to 0)
-                q[i] = idx < n8 ? __float2int_rn(z[j][i] * inv) : 0;
-            }
-            if (qr && idx < n8)
-                reinterpret_cast<uint2 *>(qr)[idx] = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
-            if (RING == DIRECT && a.qop && idx < n8pad) {
-                uint4 c16 = make_uint4(0, 0, 0, 0);
-                uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-                if (a.e4) {
-                    digits4(q[0], q[1], q[2], q[3], lo.x, hi.x);
-                    digits4(q[4], q[5], q[6], q[7], lo.y, hi.y);
-                } else {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 p = __halves2half2(__int2half_rn(q[2 * i]), __int2half_rn(q[2 * i + 1]));
-                        h[i] = *reinterpret_cast<const uint32_t *>(&p);
-                    }
-                    c16 = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                put(idx, c16, lo, hi);
-            }
-            // a group's G / 8 threads are consecutive lanes (G = 16: two lanes)
-            if (need_gs) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) gs += q[i];
-                for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
-                if (idx < n8 && (lane & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / G], gs);
-            }
-        }
-        if (!need_gs) continue;
-        __syncthreads();
-        for (int g = tid; g < ngp; g += T) {
-            const int v2 = g < ngk ? s_gs[g] : 0;
-            if (a.gsum && g < ngk) a.gsum[(size_t)row * ngk + g] = v2;
-            if (a.qop && a.sums) put_sum(g, (float)v2);
-        }
+        for (int j = 0; j < V; ++j) codes.write(row, tid + j * T, z[j], inv);
+        codes.template write_sums<T>(row);
     }
 }
 
 template <int V, int T>
 cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
-    if (a.qop)  // one block per row of the operand, padding included
-        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)act_rows(a.M)), dim3(T), 0, pdl, s, a);
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
     int dev = 0, per_sm = 0;
@@ -413,7 +598,7 @@ cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
     static std::atomic<int> resident[CACHE_DEVICES];
     e = cached_per_device(resident, dev, &per_sm, [&](int *v) {
         for (auto f : {k_add_norm_quant<V, T, RING_ANY>, k_add_norm_quant<V, T, RING_F16>, k_add_norm_quant<V, T, RING_BF16>,
-                       k_add_norm_quant<V, T, RING_F32_F16>, k_add_norm_quant<V, T, RING_F32_BF16>}) {
+                       k_add_norm_quant<V, T, RING_F32_F16>, k_add_norm_quant<V, T, RING_F32_BF16>, k_add_norm_quant<V, T, DIRECT>}) {
             const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM - NORM_FIXED);
             if (r != cudaSuccess) return r;
         }
@@ -421,13 +606,16 @@ cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
     if (per_sm < 1) per_sm = 1;
+    const size_t kept = a.keep ? (size_t)V * T * 16 : 0;
+    if (a.qop)  // one block per row of the operand, padding included
+        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)act_rows(a.M)), dim3(T), kept, pdl, s, a);
     // the ring where blocks take several rows and its rows fit
     const int row_bytes = V * T * 8 * (type_bytes(a.x_type) + (a.res ? type_bytes(a.r_type) : 0));
     const int ring = NSTAGES * row_bytes;
     while (per_sm > 1 && ring > NORM_SMEM / per_sm - NORM_FIXED) --per_sm;
     const long long most = (long long)sms * per_sm;
     if (a.M <= most || ring > NORM_SMEM / per_sm - NORM_FIXED)
-        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)a.M), dim3(T), 0, pdl, s, a);
+        return launch_kernel(k_add_norm_quant<V, T, DIRECT>, dim3((unsigned)a.M), dim3(T), kept, pdl, s, a);
     const bool one = a.res && a.r_type != HQ_F32 && (!a.h || a.h_type == a.r_type), wide = a.x_type == HQ_F32;
     auto f = k_add_norm_quant<V, T, RING_ANY>;
     if (one && a.r_type == HQ_F16 && (wide || a.x_type == HQ_F16))
@@ -439,7 +627,9 @@ cudaError_t launch_norm_t(const NormArgs &a, bool pdl, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs &a, bool pdl, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs &args, bool pdl, cudaStream_t s) {
+    NormArgs a = args;
+    a.keep = !a.res_out || a.r_type == HQ_F32 ? KEEP_NONE : a.res_out == a.x ? KEEP_X : a.res_out == a.res ? KEEP_R : KEEP_NONE;
     const int n8 = a.K / 8;
     // As many threads as the row has octets, up to 1024: a row is one short
     // dependent chain.  Every V * T is a multiple of 16 octets, so the

@@ -284,3 +284,85 @@ def test_norm_weights_that_are_not_finite_reach_every_scale(M, K, G, fmt, xt, rt
     assert not torch.isfinite(h[:, K // 2]).any() and torch.isfinite(h[:, :K // 2]).all()
     if qop:
         assert not torch.isfinite(Y).any()
+
+
+def check_far(x, r, w, signs, eps, res_out, h, qx, sx):
+    """check() for rows of any size: what is below fp32's normal range is off by half of its smallest step more."""
+    K = x.shape[1]
+    s32 = x.float() + r.float() if r is not None else x.float()
+    if res_out is not None:
+        assert torch.equal(res_out, s32.to(res_out.dtype))
+    zero = (s32 == 0).all(1)  # a size below the type's smallest step
+    assert not h[zero].any() and not qx[zero].any() and not sx[zero].any()
+    s32, h, qx, sx = s32[~zero], h[~zero], qx[~zero], sx[~zero]
+    s, w64 = s32.double().cpu().numpy(), w.double().cpu().numpy()
+    rstd = 1.0 / np.sqrt((s * s).mean(1, keepdims=True) + eps)
+    y = s * rstd * w64
+    rel, step = 2.0 ** -17 + torch.finfo(h.dtype).eps / 2, torch.finfo(h.dtype).smallest_normal
+    assert np.all(np.abs(h.double().cpu().numpy() - y) <= rel * np.abs(y) + step)
+    assert np.all(np.abs(h.double().cpu().numpy()).max(1) >= 0.5 * np.where(np.abs(y).max(1) > 4 * step, np.abs(y).max(1), 0))
+    z = rotate64(s * w64, signs)
+    dz = 8 * 2.0 ** -24 * np.abs(s * w64).reshape(s.shape[0], -1, 32).sum(2).max(1, keepdims=True) / np.sqrt(32.0)
+    amax = np.abs(z).max(1, keepdims=True)
+    q = qx.cpu().numpy().astype(np.float64)
+    off = np.abs(q - 127.0 * z / amax) - 0.5
+    assert np.all(off <= 254.0 * dz / amax + 127 * 2.0 ** -22)
+    assert np.all(np.abs(q).max(1) == 127)
+    ref = (rstd * amax / 127.0)[:, 0]
+    assert np.all(np.abs(sx.double().cpu().numpy() - ref) <= ref * (2.0 ** -17 + (dz / amax)[:, 0]) + 4 * 2.0 ** -149)
+
+
+SIZES = [1e-37, 1e-40, 3e-39, 1e-30, 2e-20, 1e-12, 1.0, 1e12, 3e19, 1e25, 3e37, 5e-45]
+
+
+@pytest.mark.parametrize("M,K,G,fmt,xt,rt,qop", [
+    (12, 256, 32, "w4", F32, F32, True), (40, 1024, 64, "w4", BF16, BF16, True), (100, 512, 128, "w8", F32, BF16, True),
+    (16, 16384, 64, "w8", BF16, F32, True), (12, 65536, 64, "w4", BF16, BF16, False), (1500, 2048, 32, "w4", BF16, BF16, False),
+    (700, 4096, 64, "w4", F32, BF16, False), (900, 736, 32, "w4", F32, F32, False), (400, 12288, 32, "w4", BF16, F32, False)])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+@pytest.mark.parametrize("over", [None, "residual", "x"])
+def test_norm_of_rows_of_any_size(M, K, G, fmt, xt, rt, qop, eps, over):
+    """Rows down to a few of fp32's smallest steps and up to a tenth of its largest value."""
+    x, r, w, signs = make(M, K, F32, F32, seed=M + K, spread=3.0)
+    size = torch.ones(M, device=DEV)
+    for i, f in enumerate(SIZES):
+        size[(i * 37 + 3) % M] = f  # among rows of the common kind
+    x, r = (x * size[:, None] / 3).to(xt), (r * size[:, None]).to(rt)
+    if over == "x":
+        r = None
+    x0, r0 = x.clone(), None if r is None else r.clone()
+    d = hq.make_desc(K, 128, G, fmt)
+    out = r if over == "residual" else x if over == "x" else torch.empty_like(r)
+    h, qx, sx = Guarded((M, K), F32, DEV), Guarded((M, K), torch.int8, DEV), Guarded((M,), F32, DEV)
+    gs = Guarded((M, K // G), torch.int32, DEV)
+    op = Guarded((hq.hq_act_operand_bytes(d, M),), torch.uint8, DEV) if qop else None
+    hq.add_norm_quant(d, x, r, w, signs_dev(signs), eps, residual_out=out, h=h.t, qx=qx.t, gsum=gs.t, qop=op.t if qop else None,
+                      sx=sx.t)
+    torch.cuda.synchronize()
+    for g in (h, qx, sx, gs):
+        g.check()
+    check_far(x0, r0, w, signs, eps, out, h.t, qx.t, sx.t)
+    assert torch.equal(gs.t, qx.t.view(M, K // G, G).to(torch.int32).sum(2, dtype=torch.int32))
+    if qop:
+        op.check()
+        layer = hq.pack_layer(0.02 * torch.randn((128, K), device=DEV), G, fmt, signs)
+        ws = torch.zeros(hq.hq_workspace_q8_bytes(layer.desc, M), dtype=torch.uint8, device=DEV)
+        Y, Y8 = (torch.empty((M, 128), device=DEV) for _ in range(2))
+        hq.hq_verify_gemm(layer.desc, layer.blob, op.t, sx.t, M, Y, None, ws, hq.HQ_LAUNCH_EXACT_ORDER)
+        hq.hq_verify_gemm_q8(layer.desc, layer.blob, qx.t, sx.t, None, M, Y8, None, ws, hq.HQ_LAUNCH_EXACT_ORDER)
+        assert torch.equal(Y, Y8) and bool(torch.isfinite(Y).all())
+
+
+def test_norm_of_one_tensor_as_x_residual_and_residual_out():
+    for M, t in ((9, BF16), (1200, BF16), (9, F32)):
+        x, _, w, signs = make(M, 512, F32, F32, seed=M)
+        x = x.to(t)
+        x[1] *= 1e-38
+        x[2] = 0
+        x[3] *= 1e30
+        x0 = x.clone()
+        h, qx, sx = torch.empty((M, 512), device=DEV), torch.empty((M, 512), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+        hq.add_norm_quant(hq.make_desc(512, 128, 32, "w4"), x, x, w, signs_dev(signs), 0.0, residual_out=x, h=h, qx=qx, sx=sx)
+        assert not h[2].any() and not qx[2].any() and float(sx[2]) == 0.0
+        keep = [i for i in range(M) if i != 2]
+        check_far(x0[keep], x0[keep], w, signs, 0.0, x[keep], h[keep], qx[keep], sx[keep])
