@@ -651,8 +651,10 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  * tree and other sequences' pages do not influence a row, whatever they hold
  * (infinities and NaN included).  Scores, softmax statistics and outputs are
  * accumulated in fp32; the probabilities are rounded to `type` for the
- * product with V (at most eps / 2 of `type` relative each).  Sums are taken
- * in a fixed order: results repeat bit for bit. */
+ * product with V, whatever out_type is: at most eps / 2 of `type` relative
+ * each, but with HQ_F16 a probability below 2^-21 of the largest of its part of
+ * the positions by at most 2^-32 of that largest.  Sums are taken in a fixed
+ * order: results repeat bit for bit. */
 size_t hq_prefix_attention_workspace_bytes(int32_t B, int32_t rows, int32_t max_rows, int32_t Hq, int32_t Hkv,
                                            int32_t D);
 int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32_t type, const void *q,

@@ -54,6 +54,11 @@ constexpr int TC_ROWS_OWN = 17;
 // SM takes about this many own positions of a head, in k_prefix_attn and in
 // k_prefix_own.
 constexpr int OWN_POS = 160, OWN_POS_TC = 35;
+// Probabilities are formed relative to the running maximum less this many base-2
+// units.  fp16's smallest normal value is 2^-14, its largest nearly 2^16: 2^15 at
+// the maximum leaves 29 of its powers for the smaller ones (with 0, a flat tail
+// 2^-26 below one key was lost altogether).  bf16 has fp32's range.
+constexpr float P_SHIFT_F16 = 15.0f;
 constexpr int MAX_PARTS = 64;   // shared_parts + own_parts, at most 32 each
 
 template <int D>
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(XTHREADS, 2)
         for (int h = 0; h < 2; ++h) {
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            if constexpr (!BF) mx[h] -= P_SHIFT_F16;  // mrun is the reference, not the maximum
             const float mnew = fmaxf(mrun[h], mx[h]);
             alpha[h] = mnew == -INFINITY ? 1.0f : ex2(mrun[h] - mnew);
             mx[h] = mnew == -INFINITY ? 0.0f : mnew;  // no visible position yet: probabilities 0

@@ -14,7 +14,8 @@
 // of scores and its output accumulator in tensor memory (2 x (128 + 128)
 // columns: all 512):
 //   S = Q K^T        both operands in shared memory
-//   P = exp2(c S - c m), rounded to the cache's type, written over S
+//   P = exp2(c S - c m), in fp16 times 2^7, rounded to the cache's type, written
+//   over S
 //   O += P V         P from tensor memory, V from shared memory
 // While one stream is in its softmax the tensor core works for the other.
 // PAIR: the streams are two 128-row query tiles against the same positions.
@@ -27,8 +28,8 @@
 //                   whose registers go to the softmax
 // The reference maximum m of a row is raised only when a score exceeds it by
 // 8 or more in base-2 units: then O is scaled by the softmax warps themselves,
-// between two products; P stays below 2^8, far from fp16's end, and output and
-// sum are relative to the same m.
+// between two products; P stays below 2^8 (2^15 in fp16), and output and sum are
+// relative to the same m.
 //
 // The wait for S(j + 1) also orders the scaling of O behind P V(j): MMAs of
 // one thread complete in order, and P V(j) is issued before S(j + 1).
@@ -54,6 +55,10 @@ constexpr int CTHREADS = 384;
 // 72 = 3 * 168): a row's 128 scores then stay in registers.
 constexpr int CREG_SOFTMAX = 216, CREG_REST = 72;
 constexpr float LAZY = 8.0f;  // base-2 units a score may exceed the reference maximum by
+// P is 2^7 at the reference maximum in fp16, so that at most 2^15 may occur and the
+// 21 powers below the maximum are normal values (k_prefix.cu: P_SHIFT_F16).
+template <bool BF>
+constexpr float P_SHIFT = BF ? 0.0f : 7.0f;
 
 template <int D>
 struct TcTile {
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                         }
                     }
                 }
-                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const float mc = m == -INFINITY ? 0.0f : m * c - P_SHIFT<BF>;
                 const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
                 f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
 #pragma unroll
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(CTHREADS, 1)
                 }
             tc_fence_after();
             if (l == 0.0f) m = -INFINITY;  // no tile, or no finite score: adds nothing
-            float mb = m == -INFINITY ? -INFINITY : m * c;  // in base-2 units
+            float mb = m == -INFINITY ? -INFINITY : m * c - P_SHIFT<BF>;  // in base-2 units
             float scale = 1.0f, other = 0.0f;
             float *box = reinterpret_cast<float *>(s_ring);  // [D][128 rows], then m, l
             // O of this thread's row, dimensions 32 i .. 32 i + 31
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(OTHREADS, 2)
                 }
                 __syncwarp();
             }
-            const float mc = m == -INFINITY ? 0.0f : m * c;
+            const float mc = m == -INFINITY ? 0.0f : m * c - P_SHIFT<BF>;
             const f2 cc = f2_make(c, c), mm = f2_make(-mc, -mc);
             f2 sum[2] = {f2_make(0.0f, 0.0f), f2_make(0.0f, 0.0f)};
 #pragma unroll
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(OTHREADS, 2)
                 __syncwarp();
             }
             if (row < nrows)
-                *reinterpret_cast<float2 *>(a.ws_ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : m * c, l);
+                *reinterpret_cast<float2 *>(a.ws_ml + at * 2) = make_float2(m == -INFINITY ? -INFINITY : m * c - P_SHIFT<BF>, l);
         }
         tc_fence_before();
     } else if (warp == 4) {

@@ -524,3 +524,38 @@ def test_errors_reach_the_cache_without_a_workspace(B, m):
         t.cache.table[0, at] = was
         t.check(run())
         assert hq.pages_status(t.cache) == hq.HQ_OK
+
+
+@pytest.mark.parametrize("B,m,Hq,Hkv,D,sink", [
+    (3, 1, 8, 2, 128, 0), (3, 1, 8, 2, 64, 3000), (2, 7, 8, 8, 64, 5), (40, 1, 8, 2, 128, 0), (64, 2, 4, 1, 64, 2999), (1, 40, 2, 2, 128, 1),
+    (1, 100, 4, 2, 64, 17)])
+@pytest.mark.parametrize("below", [18.3, 20.6])
+def test_a_flat_tail_far_below_one_key(B, m, Hq, Hkv, D, sink, below):
+    """One key outweighs each of thousands of others by 2^below: in fp16 their
+    probabilities keep its precision (no term for subnormal ones here).
+
+    K holds `k` in dimension 0 of the one key and 0 elsewhere, q 1 there, so the
+    scores are exact: scale * k and 0.  V is 0 at the one key and 1 elsewhere:
+    the output is the tail's share, N w / (1 + N w) with w = 2^-below up to the
+    rounding of scale * log2(e) (2^-23 relative of `below`).  Each probability is
+    off by 2^-11 at most, all alike; the fp32 output by its sums."""
+    shared = 3500
+    t = Batch([shared + 20 + m] * B, [m] * B, shared, Hq, Hkv, D, 16, F16, seed=1, tree=False)
+    t.cache.pool[2] = 0
+    t.cache.pool[1] = 1
+    for b in range(B):
+        page = int(t.cache.table[t.slots[b], sink // 16])
+        t.cache.pool[2, page, :, sink % 16, 0] = 4.0
+        t.cache.pool[1, page, :, sink % 16] = 0
+    t.q.zero_()
+    t.q[:, :, 0] = 1.0
+    t.scale = below * math.log(2.0) / 4.0
+    got = t.run(F32).double()
+    assert t.status == hq.HQ_OK
+    for b in range(B):
+        for i in range(m):
+            n = shared + 20 + i  # the others that the row sees
+            w = 2.0 ** -below
+            ref = n * w / (1.0 + n * w)
+            err = float((got[t.starts[b] + i] - ref).abs().max())
+            assert err <= ref * (2.0 ** -11 + 2.0 ** -16 + 4 * below * 2.0 ** -23), f"{err / ref:.2e}"
