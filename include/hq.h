@@ -633,7 +633,7 @@ int hq_pages_status(const hq_pages *cache, void *stream);
  *             first active sequence
  *   max_len   at least every sequence's length (it sizes the launch), above
  *             `shared`, at most max_pages * page_size and 2^30
- *   scale     softmax scale, finite
+ *   scale     softmax scale, finite also in base-2 units (scale * log2(e))
  *   out       out_type [rows][Hq][D], rows ldo elements apart, 16-byte aligned
  *             rows; out_type is `type` or HQ_F32
  *   workspace hq_prefix_attention_workspace_bytes(B, rows, max_rows, Hq,

@@ -1,5 +1,6 @@
 // hq_batch.cu -- the C ABI of the calls for a batch of requests: argument
 // validation (before anything is launched) and dispatch.
+#include <cfloat>
 #include <climits>
 
 #include "batch.cuh"
@@ -241,7 +242,8 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
     if (B < 0 || B > 65535 || rows < 0 || max_rows < 1 || max_rows > HQ_MAX_M) return HQ_ERR_INVALID_ARG;
     if (!starts && (long long)B * max_rows > rows) return HQ_ERR_INVALID_ARG;
     if (Hq <= 0 || Hq > 65535 || Hq % cache->heads != 0 || (long long)rows * Hq > (1 << 28)) return HQ_ERR_INVALID_ARG;
-    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return HQ_ERR_INVALID_ARG;
+    const float c_log2 = scale * 1.4426950408889634f;
+    if (!(c_log2 <= FLT_MAX && c_log2 >= -FLT_MAX)) return HQ_ERR_INVALID_ARG;
     if (shared < 0 || max_len < 1 || max_len > 1 << 30 || shared >= max_len ||
         max_len > (long long)cache->max_pages * cache->page_size)
         return HQ_ERR_INVALID_ARG;
@@ -281,7 +283,7 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
     a.max_len = max_len;
     a.type = type;
     a.out_type = out_type;
-    a.c_log2 = scale * 1.4426950408889634f;
+    a.c_log2 = c_log2;
     return cuda_status(hq::launch_prefix_attention(*cache, a, D, workspace, pdl_of(flags), stream_of(stream)));
 }
 

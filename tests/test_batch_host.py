@@ -258,3 +258,11 @@ def test_prefix_attention_workspace_serves_smaller_calls():
             sizes = [size(1, rows, m, Hq, Hkv, D) for rows in range(1, 700, 3)]
             assert sizes == sorted(sizes)
             assert size(7, 50, m, Hq, Hkv, D) == size(50, 50, m, Hq, Hkv, D) <= size(1, 50, min(128, m + 1), Hq, Hkv, D)
+
+
+@pytest.mark.parametrize("scale,ok", [(3.0e38, False), (-3.0e38, False), (2.4e38, False), (2.3e38, True), (-2.3e38, True)])
+def test_prefix_attention_refuses_scales_without_a_base_2_form(scale, ok):
+    """scale * log2(e) enters every score: an infinity there would make NaN of a score of 0."""
+    rc = hq.load().hq_prefix_attention(pages(), 0, 1, hq.HQ_F16, FAKE, 512, None, None, 0, 6, 4, None, 4, 20, 150, scale, FAKE,
+                                       hq.HQ_F16, 512, FAKE, 0, None)  # no sequences: nothing is launched
+    assert rc == (hq.HQ_OK if ok else E)
