@@ -89,8 +89,10 @@ typedef struct {
  * previous kernel of the stream is still running and waits for it (and for
  * its memory) before reading anything that kernel could have produced.
  * Some inputs are read before that wait, so with this flag they must not be
- * written by the operation launched immediately before in the same stream:
- * the blob (hq_verify_gemm streams the packed weights early), the committed
+ * written by the operation launched immediately before in the same stream, nor,
+ * where that one has the flag too, by the one before it, and so on back to the
+ * last operation launched without it (an operation may let the next one start
+ * before its own wait is over): the blob (hq_verify_gemm streams the packed weights early), the committed
  * cache positions [0, L) (hq_tree_attention), the committed state
  * (hq_delta_tree), weight and signs (hq_add_norm_quant), and ids, ranks, A and
  * B (hq_lora_apply). */

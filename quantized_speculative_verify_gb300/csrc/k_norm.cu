@@ -160,7 +160,7 @@ template <bool OPERAND>
 struct Codes {
     const NormArgs &a;
     int *s_gs;  // group sums of the row, in shared memory
-    int MT, n8, n8pad, bpt, gpt, ngk, ngp, cb, width;
+    int MT, n8, n8pad, bpt, gpt, ngk, ngp, cb;
     size_t tb;
     bool sums;
     __device__ __forceinline__ Codes(const NormArgs &a, int K, int G, int MT, int *s_gs) : a(a), s_gs(s_gs), MT(MT) {
@@ -169,7 +169,6 @@ struct Codes {
         bpt = act_kt(G) / ACT_BLOCK, gpt = act_kt(G) / G, ngk = K / G, ngp = act_ktiles(K, G) * gpt;
         cb = MT * (a.rs ? ACT_RS_PITCH : 256);
         tb = (size_t)bpt * cb + (a.sums ? (size_t)gpt * MT * 4 : 0);
-        width = G / 8 < 32 ? G / 8 : 32;
         sums = a.gsum != nullptr || (OPERAND && a.qop != nullptr && a.sums != 0);
     }
     // 8 features from 8 idx on
@@ -200,15 +199,15 @@ struct Codes {
         for (int g = threadIdx.x; g < ngk; g += T) s_gs[g] = 0;
     }
     // The codes of an octet of the rotated row; inv: 127 / max|z|.
-    __device__ __forceinline__ void write(int row, int idx, const float (&z)[8], float inv) const {
+    __device__ __forceinline__ void write(int row, int8_t *qr, int idx, const float (&z)[8], float inv) const {
         int q[8], gs = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             // |z| <= amax, 127 / amax is finite: the product rounds to at most 127
             q[i] = idx < n8 ? __float2int_rn(z[i] * inv) : 0;
         }
-        if (a.qx && idx < n8)
-            reinterpret_cast<uint2 *>(a.qx + (size_t)row * a.K)[idx] =
+        if (qr && idx < n8)
+            reinterpret_cast<uint2 *>(qr)[idx] =
                 make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
         if (OPERAND && a.qop && idx < n8pad) {
             uint4 c16 = make_uint4(0, 0, 0, 0);
@@ -231,6 +230,7 @@ struct Codes {
         if (sums) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) gs += q[i];
+            const int width = a.G / 8 < 32 ? a.G / 8 : 32;
             for (int o = width / 2; o > 0; o >>= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
             if (idx < n8 && (threadIdx.x & (width - 1)) == 0) atomicAdd(&s_gs[(idx * 8) / a.G], gs);
         }
@@ -381,7 +381,7 @@ __device__ __forceinline__ void form_again(const NormArgs &a, int row, int MT, c
         if (idx < n8 && a.h) store8(const_cast<void *>(row_of(a.h, a.h_type, a.ldh, row)), a.h_type, idx, u, signs);
         if (!quant) continue;
         rotate8(s, lane);
-        codes.write(row, idx, s, inv);
+        codes.write(row, a.qx ? a.qx + (size_t)row * K : nullptr, idx, s, inv);
     }
     codes.template write_sums<T>(row);
 }
@@ -582,8 +582,9 @@ __global__ void __launch_bounds__(T, 1024 / T) k_add_norm_quant(const NormArgs a
         if (!quant) continue;
         if (tid == 0) a.sx[row] = rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f);
         const float inv = 127.0f / amax;
+        int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
 #pragma unroll
-        for (int j = 0; j < V; ++j) codes.write(row, tid + j * T, z[j], inv);
+        for (int j = 0; j < V; ++j) codes.write(row, qr, tid + j * T, z[j], inv);
         codes.template write_sums<T>(row);
     }
 }
