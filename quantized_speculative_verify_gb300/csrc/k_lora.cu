@@ -17,12 +17,14 @@
 // blocks split the ranks instead, a warp takes one row of A over all of K with
 // multiply-adds, eight 512-byte loads in flight, and nothing is left to add up
 // but its lanes.  (With K split, the items of a row each waited for two cluster
-// barriers: 97 rows of rank 16 to 64, K = 12288: 45 us instead of 33.)
+// barriers: 97 rows of rank 16 to 64, K = 12288, took 45 us instead of 33 then;
+// now 27.)
 // k_lora_expand: each warp forms 16 rows x 32 outputs with the same MMAs over
 // the rank, or with multiply-adds where the item has one or two rows, and adds
-// base.  (A thread per output column with t in shared memory, fp32 products
-// and the next item's loads in flight took 28 us instead of 21 for 97 rows and
-// 34 instead of 21 for 128 rows of 24576 outputs: its reads of t bound it.)
+// base.  97 rows of 4096 outputs take 15 us, 128 rows of 24576 17.5.  (A thread per
+// output column with t in shared memory, fp32 products and the next item's loads
+// in flight took 28 and 34 us where this form took 21 and 21: its reads of t bound
+// it.)
 //
 // Exactness: products of two 16-bit values are exact in fp32.  Where the
 // MMAs' operand is not of the adapter's type (fp32 activations, and t, which
@@ -803,7 +805,7 @@ cudaError_t launch_lora(const LoraArgs &a, int w_type, bool pdl, cudaStream_t s)
     if (sms <= 0) return cudaErrorNoDevice;
     // items in turn by as many blocks as are resident at once: two an SM of the
     // shrink, three of the expand (two, with registers for more loads ahead:
-    // 39 us instead of 31 for 128 rows of 24576 outputs)
+    // the whole call for 128 rows of 24576 outputs 39 us instead of 31 then; now 25)
     const int rg = (a.r_max + LG - 1) / LG, tiles = (int)(((long long)a.N + LCOLS - 1) / LCOLS);
     auto least = [&](long long want) { return (unsigned)(want < 1 ? 1 : want < a.M ? want : a.M); };
     const dim3 grid(LCL, least((2LL * sms / LCL + rg - 1) / rg), (unsigned)rg), block(LWARPS * 32);

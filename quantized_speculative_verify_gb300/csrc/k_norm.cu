@@ -21,15 +21,15 @@
 // resident blocks a block takes several in turn, weight and signs stay in
 // registers and each thread copies its share of the next two rows into a ring
 // in shared memory.  Then the instructions bound it, not the memory: 8190 rows
-// of 8192, all bf16, 111 us = 5.4 TB/s at 400 instructions a warp and row, four
+// of 8192, all bf16, 112 us = 5.4 TB/s at 400 instructions a warp and row, four
 // fifths of the issue slots used.  On the way there: one row per block 232 us
 // (the memory idle during reductions); a loop with the next row in registers
 // 148; the ring 145; types known at compile time 115; the largest value by one
-// instruction 111.  (Two octets a thread and half the threads: 106 in bf16, but
-// 240 instead of 183 with x in fp32.)  The types are known where
+// instruction 111.  (At that step two octets a thread and half the threads took
+// 106 in bf16, but 240 instead of 183 with x in fp32.)  The types are known where
 // residual and h are of one 16-bit type and x of the same or fp32 (8192 rows of
-// 8192, x in fp32, the others in bf16: 161 us, 183 in the general code, which
-// any other types take).
+// 8192, x in fp32, the others in bf16: 149 us); any others take the general code
+// (all in fp32: 251 us).
 // Everything is fp32 until the outputs: residual_out, h and the codes are
 // rounded once each.
 #include "act_common.cuh"
@@ -268,8 +268,8 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int idx, float (&
 // It must not take registers from the rows of the common kind: without a ring it
 // is called (1 row of 4096: 3.5 us as before), in the loop over the ring a call
 // costs every row 60 %, so it is inlined there, with the weights read again after
-// it.  8192 rows of 8192 in bf16 take 116 us as before, of 12288 217 instead of
-// 196 (fp32 x: 292 instead of 266).
+// it.  Without such rows' code and with it, 8192 rows: of 8192 in bf16 113 and 116
+// us, with fp32 x 148 and 151; of 12288 197 and 212, with fp32 x 267 and 289.
 template <int T, bool DIRECT>
 __device__ __forceinline__ void form_again(const NormArgs &a, int row, int MT, const uint8_t *in, int xu, int ru, int *s_gs,
                                            float *s_far) {
@@ -397,8 +397,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Rows in the ring.  Two and three, 8192 rows: of 1024 in bf16 21.6 and 23.6 us,
-// of 8192 in bf16 114 both, of 12288 in fp32 and bf16 321 and (three do not fit) 400.
+// Rows in the ring.  Two and three, 8192 rows, when they were compared: of 1024 in
+// bf16 21.6 and 23.6 us, of 8192 in bf16 114 both, of 12288 in fp32 and bf16 321
+// and (three do not fit) 400.  Now, with two: 16.5, 112 and 282.
 constexpr int NSTAGES = 2;
 constexpr int NORM_SMEM = 220 << 10;  // shared memory of an SM's blocks
 constexpr int NORM_FIXED = 19 << 10;  // of which a block needs beside its ring, with the system's 1 KB

@@ -52,7 +52,8 @@ constexpr int TC_ROWS = 33;
 constexpr int TC_ROWS_OWN = 17;
 // In the time of one tile of the shared parts' tensor-memory kernel (1.6 us) an
 // SM takes about this many own positions of a head, in k_prefix_attn and in
-// k_prefix_own.
+// k_prefix_own.  (From two calls, 128 single tokens and 48 draft trees, with heads
+// of 128 and G = 4; other shapes only take another number of blocks by it.)
 constexpr int OWN_POS = 160, OWN_POS_TC = 35;
 // Probabilities are formed relative to the running maximum less this many base-2
 // units.  fp16's smallest normal value is 2^-14, its largest nearly 2^16: 2^15 at
@@ -752,8 +753,8 @@ cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void
         // are left over work on the own parts meanwhile, so fewer blocks than
         // SMs can end earlier: the count with the least estimated time, in units
         // of a block's tile.  All SMs together, bound by memory, take own parts
-        // at two thirds of a single one's rate; sequences have half the largest
-        // length.  (128 rows, 32768 shared and up to 1024 own positions: 144
+        // at two thirds of a single one's rate; sequences are taken to have half the
+        // largest length (of equal lengths, that is half of what there is).  (128 rows, 32768 shared and up to 1024 own positions: 144
         // blocks 113 us, 112 106, 96 and 80 96, 64 112.)
         const long long tiles = pl.s0 / TC_KEYS, own = sblocks * (a.max_len - pl.s0) / (2 * (pl.tc_own ? OWN_POS_TC : OWN_POS));
         long long best = -1;
