@@ -28,7 +28,7 @@
 // instruction 111.  (At that step two octets a thread and half the threads took
 // 106 in bf16, but 240 instead of 183 with x in fp32.)  The types are known where
 // residual and h are of one 16-bit type and x of the same or fp32 (8192 rows of
-// 8192, x in fp32, the others in bf16: 149 us); any others take the general code
+// 8192, x in fp32, the others in bf16: 152 us); any others take the general code
 // (all in fp32: 251 us).
 // Everything is fp32 until the outputs: residual_out, h and the codes are
 // rounded once each.
@@ -260,16 +260,16 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int idx, float (&
     for (int i = 0; i < 8; ++i) w[i] = flip(w[i], (sg >> i) & 1u);
 }
 
-// A whole row by the block in three passes over its inputs: rows of zeros, rows
-// that are not finite, and those described at SUM_LEAST.  in: the row in the ring,
-// xu and ru pieces an octet; without one (DIRECT), the input that residual_out
-// lies over and has replaced.  s_far: 3 T / 32 floats.
+// A whole row by the block in three passes over its inputs: rows that are not
+// finite, and those described at SUM_LEAST (without codes, rows of zeros too).
+// in: the row in the ring, xu and ru pieces an octet; without one (DIRECT), the
+// input that residual_out lies over and has replaced.  s_far: 3 T / 32 floats.
 //
 // It must not take registers from the rows of the common kind: without a ring it
 // is called (1 row of 4096: 3.5 us as before), in the loop over the ring a call
 // costs every row 60 %, so it is inlined there, with the weights read again after
-// it.  Without such rows' code and with it, 8192 rows: of 8192 in bf16 113 and 116
-// us, with fp32 x 148 and 151; of 12288 197 and 212, with fp32 x 267 and 289.
+// it.  Without such rows' code and with it, 8192 rows: of 8192 in bf16 113 and 117
+// us, with fp32 x 148 and 152; of 12288 197 and 217, with fp32 x 267 and 295.
 template <int T, bool DIRECT>
 __device__ __forceinline__ void form_again(const NormArgs &a, int row, int MT, const uint8_t *in, int xu, int ru, int *s_gs,
                                            float *s_far) {
@@ -399,7 +399,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Rows in the ring.  Two and three, 8192 rows, when they were compared: of 1024 in
 // bf16 21.6 and 23.6 us, of 8192 in bf16 114 both, of 12288 in fp32 and bf16 321
-// and (three do not fit) 400.  Now, with two: 16.5, 112 and 282.
+// and (three do not fit) 400.  Now, with two: 16.7, 117 and 295.
 constexpr int NSTAGES = 2;
 constexpr int NORM_SMEM = 220 << 10;  // shared memory of an SM's blocks
 constexpr int NORM_FIXED = 19 << 10;  // of which a block needs beside its ring, with the system's 1 KB
@@ -552,7 +552,9 @@ __global__ void __launch_bounds__(T, 1024 / T) k_add_norm_quant(const NormArgs a
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         amax = warp_max(amax);
-        if (!(ss >= SUM_LEAST && ss < INFINITY) || (quant && !(amax >= MAX_LEAST && amax < INFINITY))) {
+        // (a row of zeros, padding of a batch, is of the common kind)
+        if ((!(ss >= SUM_LEAST && ss < INFINITY) || (quant && !(amax >= MAX_LEAST && amax < INFINITY))) &&
+            !(quant && ss == 0.0f && amax == 0.0f)) {
             if constexpr (RING == DIRECT) {
                 form_again_call<T>(s_args, row, MT, s_ring, s_gs, &s_far[0][0]);
                 return;
@@ -568,7 +570,7 @@ __global__ void __launch_bounds__(T, 1024 / T) k_add_norm_quant(const NormArgs a
             issue(row + NSTAGES * MT, stage);
             if (++stage == NSTAGES) stage = 0;
         }
-        const float rstd = 1.0f / sqrtf(ss * inv_k + a.eps);
+        const float rstd = 1.0f / sqrtf(fmaxf(ss * inv_k + a.eps, MAX_CODED));  // (finite for zeros)
         if (a.h) {
             void *hr = const_cast<void *>(row_of(a.h, h_type, a.ldh, row));
 #pragma unroll
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(T, 1024 / T) k_add_norm_quant(const NormArgs a
         }
         if (!quant) continue;
         if (tid == 0) a.sx[row] = rstd * (amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f);
-        const float inv = 127.0f / amax;
+        const float inv = 127.0f / fmaxf(amax, MAX_CODED);
         int8_t *qr = a.qx ? a.qx + (size_t)row * K : nullptr;
 #pragma unroll
         for (int j = 0; j < V; ++j) codes.write(row, qr, tid + j * T, z[j], inv);
