@@ -29,8 +29,11 @@
  *
  * For a batch of requests there are the residual addition and norm in front of
  * a layer (hq_add_norm_quant), low-rank adapters beside it (hq_lora_apply), a
- * paged key/value cache (hq_pages_*) and attention over it that reads a shared
- * prefix once (hq_prefix_attention).
+ * paged key/value cache (hq_pages_*), rotary positions on the way into it
+ * (hq_rope_write), attention over it that reads a shared prefix once
+ * (hq_prefix_attention), the gated norm behind a layer's core
+ * (hq_gated_norm_quant), rules on the logits (hq_greedy_tokens) and the
+ * acceptance of all trees at once (hq_tree_accept_batch).
  *
  * Conventions
  *   - Row-major everywhere.  X is [M][K], W is [N][K], Y = X W^T is [M][N].
@@ -664,6 +667,214 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
                         int32_t max_rows, const int32_t *parent, int32_t Hq, int32_t shared, int32_t max_len,
                         float scale, void *out, int32_t out_type, int64_t ldo, void *workspace, uint32_t flags,
                         void *stream);
+
+/* Rotary positions.  Pair i of a head's first `rot` elements turns by freqs[i]
+ * radians a position; the other elements stay as they are.  Host-only.
+ *
+ * hq_rope_freqs: the frequencies of a head with rot rotated elements (even, 2
+ * to 65536), rot / 2 doubles, f_i = base^(-2i / rot) with base > 1, and, for
+ * contexts `factor` >= 1 times as long as the model's own of `original`
+ * positions:
+ *   HQ_ROPE_PLAIN   f_i (factor, original, low and high are not used)
+ *   HQ_ROPE_LINEAR  f_i / factor
+ *   HQ_ROPE_NTK     f_i of the base times factor^(rot / (rot - 2)); rot >= 4
+ *   HQ_ROPE_YARN    f_i where a pair's number is at most lo, f_i / factor from
+ *                   hi on, a ramp t = (i - lo) / (hi - lo) between: f_i (1 - t)
+ *                   + f_i / factor t.  lo and hi are where pairs turn `high` and
+ *                   `low` times over `original` positions (rounded down and up,
+ *                   within 0 and rot - 1): rot ln(original / (2 pi turns)) /
+ *                   (2 ln base).  Usually high = 32, low = 1
+ *   HQ_ROPE_BANDS   the same mix by the turns themselves: 1 - t = (original f_i
+ *                   / (2 pi) - low) / (high - low) within 0 and 1; usually low =
+ *                   1, high = 4
+ * high > low > 0 and original > 0 for the last two.
+ *
+ * hq_rope_turns: n frequencies (0 <= f <= pi) as hq_rope_write reads them:
+ * turns a position, f / (2 pi), in units of 2^-64, rounded to nearest.  The
+ * product with a position is then exact modulo a turn, at any position, in one
+ * integer multiplication. */
+typedef enum { HQ_ROPE_PLAIN = 0, HQ_ROPE_LINEAR = 1, HQ_ROPE_NTK = 2, HQ_ROPE_YARN = 3, HQ_ROPE_BANDS = 4 } hq_rope_kind;
+int hq_rope_freqs(int32_t rot, double base, int32_t kind, double factor, double original, double low, double high,
+                  double *freqs_host);
+int hq_rope_turns(const double *freqs_host, int32_t n, uint64_t *turns_host);
+
+/* Between the projection and hq_prefix_attention: rotates the newest rows' q
+ * and k by their positions and writes k and v into the cache (hq_pages_write
+ * with the rotation), in one launch.  Row i of sequence seqs[b], its rows and
+ * their places in the cache as in hq_pages_write.  A row's rotary position is
+ * positions[row] or, where positions is NULL, len - m_b + d: d is its depth in
+ * the tree of `parent` (numbered within the sequence as in hq_tree_attention;
+ * the walk ends at a parent outside [0, node)), or i where parent is NULL.
+ * Nodes of one depth share a position, so the accepted path's keys hold the
+ * positions that it has after hq_pages_compact.
+ *   q, k, v   in_type (HQ_F32 or `type`) [rows][Hq][D] and [rows][heads][D],
+ *             rows ldq, ldk, ldv elements apart, 16-byte aligned rows; D =
+ *             row_bytes / 2 = 64, 128 or 256; Hq 1..65535
+ *   q_weight, k_weight  fp32 [D] or NULL: the head is normed first, x *
+ *             weight / sqrt(mean(x^2) + eps); eps >= 0, finite
+ *   turns     uint64 [rot / 2] (device), from hq_rope_turns
+ *   rot       a multiple of 16 from 16 to D
+ *   layout    HQ_ROPE_HALF: element i < rot / 2 pairs with i + rot / 2;
+ *             HQ_ROPE_INTERLEAVED: element 2i with 2i + 1
+ *   gain      factor of the rotated elements (1: none), finite
+ *   q_out     type [rows][Hq][D], rows ldo elements apart, 16-byte aligned
+ *             rows; may be q itself where types and strides agree, otherwise no
+ *             overlap with the inputs
+ *   parent    int32 [rows] (device) or NULL; with it max_rows <= HQ_MAX_M
+ *   positions int32 [rows] (device) or NULL; any value
+ * Arithmetic is fp32 with one rounding to `type` per element; the angle is off
+ * by at most 2^-23.  v is rounded or copied.  Rows that no sequence claims
+ * are left as they were, in q_out too.  A row whose sequence, length or place does not
+ * exist is not written, k and v of a row whose page does not exist are not
+ * written (its q is); both set the cache's status word to HQ_ERR_INVALID_ARG.
+ * flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (nothing is read before the wait). */
+typedef enum { HQ_ROPE_HALF = 0, HQ_ROPE_INTERLEAVED = 1 } hq_rope_layout;
+int hq_rope_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32_t type, const void *q, const void *k,
+                  const void *v, int32_t in_type, int64_t ldq, int64_t ldk, int64_t ldv, int32_t Hq,
+                  const float *q_weight, const float *k_weight, float eps, const uint64_t *turns, int32_t rot,
+                  int32_t layout, float gain, const int32_t *seqs, const int32_t *starts, int32_t B, int32_t rows,
+                  int32_t max_rows, const int32_t *parent, const int32_t *positions, void *q_out, int64_t ldo,
+                  uint32_t flags, void *stream);
+
+/* A norm per head with a gate, and its quantization for the output projection
+ * `desc` (behind hq_delta_tree or hq_prefix_attention, in front of
+ * hq_verify_gemm), in one pass over the rows.  For each head of D features:
+ *     y = x * weight / sqrt(mean(x^2) + eps) * act(gate)
+ *     h = round(y);  x', sx, qx, gsum, qop of y as in hq_add_norm_quant
+ *   x      x_type [M][K], rows ldx elements apart
+ *   gate   g_type [M][K], rows ldg elements apart, or NULL: 1
+ *   act    HQ_GATE_NONE: the gate itself; HQ_GATE_SIGMOID: 1 / (1 + e^-gate);
+ *          HQ_GATE_SILU: gate / (1 + e^-gate)
+ *   weight fp32 [D], the same for every head, or NULL: no norm, y = x *
+ *          act(gate)
+ *   D      64, 128 or 256, dividing K = desc->K
+ *   eps    >= 0, finite
+ *   h      h_type [M][K], rows ldh elements apart, or NULL; must not overlap the
+ *          inputs, except that it may be x or gate with the same type and stride
+ *   signs, qx, gsum, qop, sx and their rules as in hq_add_norm_quant; all of
+ *          qx, gsum and qop may be NULL when h is given
+ *   M      0..HQ_MAX_M with qop, else 0..2^20
+ * x, gate, h and weight are 16-byte aligned, rows too.  Heads of any size are
+ * normed as the formula says (their squares are taken in units of a power of
+ * two where fp32's range would end).  A row of y with a NaN or an infinity has
+ * a NaN or infinite sx and codes 0.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL
+ * (nothing is read before the wait). */
+typedef enum { HQ_GATE_NONE = 0, HQ_GATE_SIGMOID = 1, HQ_GATE_SILU = 2 } hq_gate_act;
+int hq_gated_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, int64_t ldx, const void *gate,
+                        int32_t g_type, int64_t ldg, int32_t act, const float *weight, int32_t D, float eps, int32_t M,
+                        const uint32_t *signs, void *h, int32_t h_type, int64_t ldh, int8_t *qx, int32_t *gsum,
+                        void *qop, float *sx, uint32_t flags, void *stream);
+
+/* What requests have said so far.  All arrays are the caller's device memory;
+ * this struct is host memory, read during the call only.
+ *   tokens  int32 [n_slots][cap]: a slot's prompt, then what was generated, the
+ *           root of its next draft tree (its newest token) last
+ *   len     int32 [n_slots]: tokens held; values outside [0, cap] count as the
+ *           nearer end when read
+ *   prompt  int32 [n_slots] or NULL (0): how many of them are the prompt's
+ *   status  int32, zeroed once: the first error of hq_tree_accept_batch since it
+ *           was last read (hq_history_status)
+ * 1 to 65536 slots, cap from 1 to 2^24. */
+typedef struct {
+    int32_t *tokens;
+    int32_t *len;
+    const int32_t *prompt;
+    int32_t *status;
+    int32_t n_slots;
+    int32_t cap;
+} hq_history;
+
+/* Rules on the logits.  Device arrays, each may be NULL (the rule is not
+ * applied); host struct, read during the call only.
+ *   repetition, presence, frequency  fp32 [n_slots]
+ *   bias_starts  int32 [n_slots + 1], ascending, within [0, n_bias]: slot s has the
+ *           biases bias_values[j] of tokens bias_tokens[j] (int32, fp32 [n_bias]),
+ *           bias_starts[s] <= j < bias_starts[s + 1]; of a token listed twice the
+ *           last one counts
+ *   masks   uint32 [n_masks][ldmask], ldmask at least ceil(V / 32): token t is
+ *           allowed where bit t % 32 of word t / 32 is set
+ * n_slots from 0 to 65536 (0: no rule but the masks); 0 <= n_bias, n_masks < 2^31. */
+typedef struct {
+    const float *repetition;
+    const float *presence;
+    const float *frequency;
+    const int32_t *bias_starts;
+    const int32_t *bias_tokens;
+    const float *bias_values;
+    const uint32_t *masks;
+    int64_t ldmask;
+    int32_t n_slots;
+    int32_t n_bias;
+    int32_t n_masks;
+} hq_logit_rules;
+
+/* Penalties, biases and grammar masks on the logits of a batch's trees, and the
+ * greedy token of every row, in one pass.  For row i of the b-th sequence (rows
+ * as in hq_pages_write; slot s = seqs[b], or b) and every token t, in fp32, each
+ * operation rounded once:
+ *     l = logits[row][t]
+ *     t is in the history or drafted on the row's path:
+ *         l = l > 0 ? l / repetition[s] : l * repetition[s]
+ *     it is there n > 0 times behind the prompt:
+ *         l = l - frequency[s] * n;  l = l - presence[s]
+ *     t has a bias:  l = l + bias
+ *     t is masked:   l = -infinity
+ *     greedy[row] = the token of the largest l among those that are not masked,
+ *         the lowest one among equals; a NaN ranks above every number, the first
+ *         NaN wins; -1 if every token is masked
+ *     out[row][t] = l, rounded to out_type
+ * The row's path is that of hq_tree_accept: `tokens` of node i and of its
+ * ancestors but the root (node 0, whose token is the history's last).
+ *   logits  type [rows][V], rows ldl elements apart, any alignment of its
+ *           elements; V from 1 to 2^24
+ *   history, rules  or NULL: none.  A slot outside [0, n_slots) has none
+ *   seqs, starts, B, rows, max_rows  as in hq_pages_write; max_rows <= HQ_MAX_M
+ *   parent  int32 [rows] (device) or NULL: a chain; as in hq_tree_attention
+ *   tokens  int32 [rows] (device) or NULL: nothing drafted
+ *   mask_ids  int32 [rows] (device) or NULL (row r has mask r): the row's mask;
+ *           a row whose id is outside [0, n_masks) has none
+ *   out     out_type (type or HQ_F32) [rows][V], rows ldo elements apart, or
+ *           NULL; may be logits itself with the same type and stride, otherwise
+ *           no overlap
+ *   greedy  int32 [rows]
+ *   workspace hq_greedy_tokens_workspace_bytes(rows) bytes, 16-byte aligned,
+ *           zeroed once; each call leaves it zeroed.  The size grows with rows
+ *           and depends on nothing else
+ * Tokens outside [0, V), in any of the lists, are passed over.  Rows that no
+ * sequence claims are left as they were, in out and greedy.  Results repeat bit
+ * for bit.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (nothing is read before
+ * the wait). */
+size_t hq_greedy_tokens_workspace_bytes(int32_t rows);
+int hq_greedy_tokens(const void *logits, int32_t type, int64_t ldl, int32_t V, const hq_history *history,
+                     const hq_logit_rules *rules, const int32_t *mask_ids, const int32_t *seqs, const int32_t *starts,
+                     int32_t B, int32_t rows, int32_t max_rows, const int32_t *parent, const int32_t *tokens, void *out,
+                     int32_t out_type, int64_t ldo, int32_t *greedy, void *workspace, uint32_t flags, void *stream);
+
+/* Acceptance of a batch of draft trees (hq_tree_accept for each sequence, from
+ * greedy tokens that are there already), which also grows the histories, so
+ * that the next step's penalties follow without the host.
+ *   greedy, parent, tokens  int32 [rows] (device); parent NULL: chains
+ *   seqs, starts, B, rows, max_rows  as in hq_pages_write; max_rows <= HQ_MAX_M
+ *   history   or NULL.  Slot seqs[b] (or b) grows by the accepted drafts and the
+ *             bonus token (if it is not negative).  A slot outside [0, n_slots),
+ *             a length that is outside [0, cap] or would pass cap, and a slot
+ *             listed before leave the history as it was and set its status word to
+ *             HQ_ERR_INVALID_ARG
+ *   path      int32 [B][ldpath], ldpath >= max_rows: the accepted drafted nodes of
+ *             sequence b from the root's child down, then -1 up to max_rows
+ *   n_accept, bonus  int32 [B]; both -1 (and the history as it was) for a
+ *             sequence without rows and for one whose parents are not a tree
+ *             listed parents-first
+ * A negative greedy token accepts nothing.  path and n_accept are what
+ * hq_pages_compact takes as keep and n_keep.  flags: HQ_LAUNCH_DEFAULT or
+ * HQ_LAUNCH_PDL (nothing is read before the wait). */
+int hq_tree_accept_batch(const int32_t *greedy, const int32_t *parent, const int32_t *tokens, const int32_t *seqs,
+                         const int32_t *starts, int32_t B, int32_t rows, int32_t max_rows, const hq_history *history,
+                         int32_t *path, int32_t ldpath, int32_t *n_accept, int32_t *bonus, uint32_t flags,
+                         void *stream);
+
+/* Synchronizes `stream`, then reads and clears the history's status word. */
+int hq_history_status(const hq_history *history, void *stream);
 
 /* Self-test of the bounded-wait path: launches one block that waits on a
  * shared-memory barrier nothing will ever complete, giving up after

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libhq.so")
 SOURCES = ["hq_api.cu", "k_act.cu", "k_pack.cu", "k_gemm_w4.cu", "k_gemm_w8.cu", "k_gemm_rs.cu", "k_gemm_rs_w8.cu", "hq_noalloc.cu", "k_accept.cu",
            "k_attn.cu", "k_delta.cu", "hq_batch.cu", "k_norm.cu", "k_lora.cu", "k_pages.cu",
-           "k_prefix.cu", "k_prefix_tc.cu"]
+           "k_prefix.cu", "k_prefix_tc.cu", "k_rope.cu", "k_gate.cu", "k_greedy.cu", "k_accept_batch.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]

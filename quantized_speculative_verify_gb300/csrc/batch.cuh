@@ -92,7 +92,58 @@ struct PrefixArgs {
 size_t prefix_workspace_bytes(int rows, int max_rows, int Hq, int Hkv, int D);
 cudaError_t launch_prefix_attention(const hq_pages &c, PrefixArgs a, int D, void *workspace, bool pdl, cudaStream_t s);
 
+// Rotary positions on the way into the cache (k_rope.cu).
+struct RopeArgs {
+    const void *q, *k, *v;
+    void *q_out;
+    const float *qw, *kw;
+    const uint64_t *turns;
+    const int32_t *seqs, *starts, *parent, *positions;
+    int64_t ldq, ldk, ldv, ldo;
+    float eps, gain;
+    int in_type, type, layout, rot, Hq, B, rows, max_rows, k_plane, v_plane;
+};
+cudaError_t launch_rope_write(const hq_pages &c, const RopeArgs &a, bool pdl, cudaStream_t s);
+
+// The norm per head with its gate (k_gate.cu).  n: the rows, h and the codes as
+// in the norm of whole rows; its residual is not used and its weight is [D].
+struct GateArgs {
+    NormArgs n;
+    const void *gate;
+    int64_t ldg;
+    int g_type, act, D;
+};
+cudaError_t launch_gated_norm(const GateArgs &a, bool pdl, cudaStream_t s);
+
+// Rules on the logits and greedy tokens (k_greedy.cu), acceptance (k_accept_batch.cu).
+struct GreedyArgs {
+    const void *logits;
+    void *out;
+    const int32_t *mask_ids, *seqs, *starts, *parent, *tokens;
+    int32_t *greedy;
+    unsigned long long *best;  // [rows]: largest key so far
+    unsigned *done;            // [rows]: chunks that are in it
+    hq_history history;        // tokens NULL: none
+    hq_logit_rules rules;
+    int64_t ldl, ldo;
+    int type, out_type, V, B, rows, max_rows;
+};
+cudaError_t launch_greedy_tokens(const GreedyArgs &a, bool pdl, cudaStream_t s);
+
+struct AcceptBatchArgs {
+    const int32_t *greedy, *parent, *tokens, *seqs, *starts;
+    int32_t *path, *n_accept, *bonus;
+    hq_history history;  // tokens NULL: none
+    int ldpath, B, rows, max_rows;
+};
+cudaError_t launch_accept_batch(const AcceptBatchArgs &a, bool pdl, cudaStream_t s);
+
 #ifdef __CUDACC__
+__device__ __forceinline__ void set_status(const hq_pages &c, int err) { atomicCAS(c.status, 0, err); }
+__device__ __forceinline__ bool page_ok(const hq_pages &c, int page) { return page >= 0 && page < c.n_pages; }
+// max_pages * page_size is below 2^31 (checked by the host)
+__device__ __forceinline__ bool len_ok(const hq_pages &c, int len) { return len >= 0 && len <= c.max_pages * c.page_size; }
+
 // Rows of sequence b of a batch: the first row and their number, always
 // within [0, rows) and at most max_rows, whatever `starts` holds.
 __device__ __forceinline__ void batch_rows(const int32_t *starts, int b, int rows, int max_rows, int &first, int &m) {
@@ -112,6 +163,27 @@ __device__ __forceinline__ void batch_rows(const int32_t *starts, int b, int row
     if (hi > rows) hi = rows;
     first = lo;
     m = hi - lo < max_rows ? hi - lo : max_rows;
+}
+
+// The sequence that claims a row, by one warp: how many of starts[1..B] are at
+// most `row` (32 probes a round).  Whatever starts holds, the answer is within
+// [0, B]; batch_rows says whether the row is that sequence's.
+__device__ __forceinline__ int row_sequence(const int32_t *starts, int B, int max_rows, int row) {
+    if (!starts) {
+        const int b = row / max_rows;
+        return b < B ? b : B;
+    }
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = B;
+    while (n > 0) {
+        const int step = (n + 31) / 32;
+        const long long at = (lane + 1ll) * step;
+        const bool below = at <= n && starts[lo + (int)at] <= row;
+        const int k = __popc(__ballot_sync(0xffffffffu, below)) * step;
+        lo += k;
+        n = n - k < step - 1 ? n - k : step - 1;
+    }
+    return lo;
 }
 #endif
 

@@ -1,0 +1,204 @@
+// k_gate.cu -- the norm per head with its gate, and the codes of the result for
+// the output projection, in one pass over the rows.
+//
+//   y = x * w / sqrt(mean_head(x^2) + eps) * act(gate)
+//   z = the rotated y (32-blocks, without the factor 1/sqrt(32))
+//   sx = max|z| / sqrt(32) / 127,  qx = rint(127 z / max|z|)
+//
+// A head is 8, 16 or 32 lanes of 8 features, so the norm is lane exchanges and
+// needs no barrier; only the codes need the row's largest value.
+#include "rows.cuh"
+
+namespace hq {
+namespace {
+
+constexpr float MAX_LEAST = 0x1p-110f;  // below it a row's largest |z| is formed again
+
+__device__ __forceinline__ float gated(float y, float g, int act) {
+    if (act == HQ_GATE_NONE) return y * g;
+    const float e = 1.0f / (1.0f + expf(-g));
+    return act == HQ_GATE_SILU ? y * (g * e) : y * e;
+}
+
+// 8 features of y: head normed, weighted, gated.
+template <int U>
+__device__ __forceinline__ void form(const GateArgs &a, const Raw &rx, const Raw &rg, int idx, float (&y)[8]) {
+    widen(rx, a.n.x_type, y);
+    if (a.n.weight) {
+        head_norm<U>(y, a.n.eps);
+        const float4 *w = reinterpret_cast<const float4 *>(a.n.weight) + 2 * (idx % U);
+        const float4 p = w[0], q = w[1];
+        const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= f[i];
+    }
+    if (a.gate) {
+        float g[8];
+        widen(rg, a.g_type, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = gated(y[i], g[i], a.act);
+    }
+}
+
+// h alone: heads are independent, so the rows' octets are one long list.
+constexpr int FT = 256;    // threads
+constexpr int FLIGHT = 2;  // octets of a thread on their way together
+
+template <int U>
+__global__ void __launch_bounds__(FT) k_gate_heads(const GateArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int n8 = a.n.K / 8, step = gridDim.x * FT;  // (at most 2^20 blocks)
+    const long long total = (long long)a.n.M * n8, start = (long long)blockIdx.x * FT + threadIdx.x;
+    long long row = start / n8;
+    int idx = (int)(start % n8);
+    const int rows_on = step / n8, idx_on = step % n8;
+    // A warp's 32 octets start at a multiple of 32; n8 is a multiple of 8, so the
+    // last warp may have heads that are not there.
+    for (long long base = start - (threadIdx.x & 31); base < total; base += (long long)step * FLIGHT) {
+        Raw x[FLIGHT], g[FLIGHT];
+        int rows[FLIGHT], at[FLIGHT];
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) {
+            x[k] = g[k] = Raw{};
+            rows[k] = row < a.n.M ? (int)row : -1;
+            at[k] = idx;
+            if (rows[k] >= 0) {
+                x[k] = load_raw(row_of(a.n.x, a.n.x_type, a.n.ldx, rows[k]), a.n.x_type, idx);
+                if (a.gate) g[k] = load_raw(row_of(a.gate, a.g_type, a.ldg, rows[k]), a.g_type, idx);
+            }
+            row += rows_on;
+            idx += idx_on;
+            if (idx >= n8) {
+                idx -= n8;
+                ++row;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) {
+            float y[8];
+            form<U>(a, x[k], g[k], at[k], y);
+            if (rows[k] >= 0) store8(const_cast<void *>(row_of(a.n.h, a.n.h_type, a.n.ldh, rows[k])), a.n.h_type, at[k], y);
+        }
+    }
+}
+
+// The largest of the block's values; NaN if one is.  Every thread calls.
+template <int T>
+__device__ __forceinline__ float block_max(float x, float *s_max) {
+    x = warp_max(x);
+    __syncthreads();  // (what was read there before)
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return warp_max((threadIdx.x & 31) < T / 32 ? s_max[threadIdx.x & 31] : 0.0f);
+}
+
+// h and codes: a thread block per row.
+template <int U, int V, int T>
+__global__ void __launch_bounds__(T) k_gate_row(const GateArgs a) {
+    __shared__ float s_max[T / 32];
+    __shared__ int s_gs[MAX_K / 16];  // group sums of this row
+    pdl_launch_dependents();
+    pdl_wait();
+    const int row = blockIdx.x, MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+    const int K = a.n.K, n8 = K / 8;
+    const Codes<true> codes(a.n, K, a.n.G, MT, s_gs);
+    if (row >= a.n.M) {  // padding row of the operand
+        codes.template pad<T>(row);
+        return;
+    }
+    Raw x[V], g[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int idx = tid + j * T;
+        x[j] = g[j] = Raw{};
+        if (idx < n8) {
+            x[j] = load_raw(row_of(a.n.x, a.n.x_type, a.n.ldx, row), a.n.x_type, idx);
+            if (a.gate) g[j] = load_raw(row_of(a.gate, a.g_type, a.ldg, row), a.g_type, idx);
+        }
+    }
+    if (codes.sums) codes.template clear_sums<T>();
+    float y[V][8], z[V][8], amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int idx = tid + j * T;
+        form<U>(a, x[j], g[j], idx, y[j]);
+        if (idx < n8 && a.n.h) store8(const_cast<void *>(row_of(a.n.h, a.n.h_type, a.n.ldh, row)), a.n.h_type, idx, y[j]);
+        const uint32_t sg = idx < n8 ? (__ldg(a.n.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[j][i] = y[j][i] = flip(y[j][i], (sg >> i) & 1u);
+        rotate8(z[j], lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
+    }
+    amax = block_max<T>(amax, s_max);
+    float up = 1.0f, more = 1.0f;
+    if (!(amax >= MAX_LEAST && amax < INFINITY) && amax != 0.0f) {
+        // sums of the rotation, or quotients by the largest, leave fp32's range: in
+        // units of 2^e, the power of two above the row's largest |y|
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(y[j][i]));
+        top = block_max<T>(top, s_max);
+        if (top > 0.0f && top < INFINITY) {
+            const bool small = top < 0x1p-60f;
+            const int e = (__float_as_int(small ? top * 0x1p80f : top) >> 23) - (small ? 206 : 126), half = e / 2;
+            const float down = __int_as_float((127 - half) << 23), rest = __int_as_float((127 - e + half) << 23);
+            up = __int_as_float((127 + half) << 23);
+            more = __int_as_float((127 + e - half) << 23);
+            amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[j][i] = y[j][i] * down * rest;
+                rotate8(z[j], lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
+            }
+            amax = block_max<T>(amax, s_max);
+        }
+    }
+    if (tid == 0) a.n.sx[row] = amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f * up * more;
+    // no codes of zeros, and of rows with an infinity or NaN: 0 * infinity and NaN round to 0
+    const float inv = amax > 0.0f ? 127.0f / amax : 0.0f;
+    int8_t *qr = a.n.qx ? a.n.qx + (size_t)row * K : nullptr;
+#pragma unroll
+    for (int j = 0; j < V; ++j) codes.write(row, qr, tid + j * T, z[j], inv);
+    codes.template write_sums<T>(row);
+}
+
+template <int U>
+cudaError_t launch_u(const GateArgs &a, bool pdl, cudaStream_t s) {
+    const int n8 = a.n.K / 8;
+    if (!a.n.sx) {
+        const int sms = device_sm_count();
+        if (sms <= 0) return cudaErrorNoDevice;
+        const long long blocks = ((long long)a.n.M * n8 + FT * FLIGHT - 1) / (FT * FLIGHT), most = 8ll * sms;
+        return launch_kernel(k_gate_heads<U>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(FT), 0, pdl, s, a);
+    }
+    const dim3 grid((unsigned)(a.n.qop ? act_rows(a.n.M) : a.n.M));
+    // A row's octets over as many threads as it has, two a thread from 4096
+    // features on.  Every V * T is a multiple of 16 octets, so the operand's padding
+    // up to whole 128-feature blocks is covered too.
+    if (n8 <= 128) return launch_kernel(k_gate_row<U, 1, 128>, grid, dim3(128), 0, pdl, s, a);
+    if (n8 <= 256) return launch_kernel(k_gate_row<U, 1, 256>, grid, dim3(256), 0, pdl, s, a);
+    if (n8 <= 512) return launch_kernel(k_gate_row<U, 1, 512>, grid, dim3(512), 0, pdl, s, a);
+    if (n8 <= 1024) return launch_kernel(k_gate_row<U, 2, 512>, grid, dim3(512), 0, pdl, s, a);
+    if (n8 <= 2048) return launch_kernel(k_gate_row<U, 2, 1024>, grid, dim3(1024), 0, pdl, s, a);
+    if (n8 <= 4096) return launch_kernel(k_gate_row<U, 4, 1024>, grid, dim3(1024), 0, pdl, s, a);
+    return launch_kernel(k_gate_row<U, 8, 1024>, grid, dim3(1024), 0, pdl, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_norm(const GateArgs &a, bool pdl, cudaStream_t s) {
+    switch (a.D) {
+        case 64: return launch_u<8>(a, pdl, s);
+        case 128: return launch_u<16>(a, pdl, s);
+        default: return launch_u<32>(a, pdl, s);
+    }
+}
+
+}  // namespace hq

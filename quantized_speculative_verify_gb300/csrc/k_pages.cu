@@ -63,11 +63,7 @@ __device__ __forceinline__ int32_t *old_table(const hq_pages &c, int job) {
            (size_t)job * c.max_pages;
 }
 
-__device__ __forceinline__ void set_status(const hq_pages &c, int err) { atomicCAS(c.status, 0, err); }
 __device__ __forceinline__ int pages_of(int len, int ps) { return len / ps + (len % ps != 0); }
-__device__ __forceinline__ bool page_ok(const hq_pages &c, int page) { return page >= 0 && page < c.n_pages; }
-// max_pages * page_size is below 2^31 (checked by the host)
-__device__ __forceinline__ bool len_ok(const hq_pages &c, int len) { return len >= 0 && len <= c.max_pages * c.page_size; }
 
 // Sum of `v` over the block; `below`: over the threads before this one.
 __device__ int block_scan(int v, int *s_warp, int &below) {

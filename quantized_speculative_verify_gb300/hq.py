@@ -44,10 +44,16 @@ EXPORTS = ("hq_tree_accept_workspace_bytes", "hq_tree_accept", "hq_status_string
            "hq_tree_attention", "hq_tree_commit_kv", "hq_delta_tree", "hq_delta_commit", "hq_add_norm_quant",
            "hq_lora_workspace_bytes", "hq_lora_apply", "hq_pages_scratch_bytes", "hq_pages_fork", "hq_pages_extend",
            "hq_pages_free", "hq_pages_compact", "hq_pages_copy", "hq_pages_write", "hq_pages_status",
-           "hq_prefix_attention_workspace_bytes", "hq_prefix_attention")
+           "hq_prefix_attention_workspace_bytes", "hq_prefix_attention", "hq_rope_freqs", "hq_rope_turns", "hq_rope_write",
+           "hq_gated_norm_quant", "hq_greedy_tokens_workspace_bytes", "hq_greedy_tokens", "hq_tree_accept_batch",
+           "hq_history_status")
 
 HQ_F32, HQ_F16, HQ_BF16 = 0, 1, 2
 TYPES = {torch.float32: HQ_F32, torch.float16: HQ_F16, torch.bfloat16: HQ_BF16}
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+GATE_ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
 HQ_ATTN_HEAD_DIM = 128
 HQ_DELTA_HEAD_DIM = 128
@@ -71,6 +77,18 @@ class hq_pages(ctypes.Structure):
                 ("row_bytes", ctypes.c_int32)]
 
 
+class hq_history(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("len", ctypes.c_void_p), ("prompt", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("n_slots", ctypes.c_int32), ("cap", ctypes.c_int32)]
+
+
+class hq_logit_rules(ctypes.Structure):
+    _fields_ = [("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_starts", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("masks", ctypes.c_void_p), ("ldmask", ctypes.c_int64), ("n_slots", ctypes.c_int32),
+                ("n_bias", ctypes.c_int32), ("n_masks", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -91,6 +109,7 @@ def load() -> ctypes.CDLL:
     P, I32, U32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
     I64, F32 = ctypes.c_int64, ctypes.c_float
     D, C = ctypes.POINTER(hq_layer_desc), ctypes.POINTER(hq_pages)
+    HS, LR, F64 = ctypes.POINTER(hq_history), ctypes.POINTER(hq_logit_rules), ctypes.c_double
     sig = {
         "hq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hq_version": (I32, []),
@@ -130,6 +149,16 @@ def load() -> ctypes.CDLL:
         "hq_prefix_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
         "hq_prefix_attention": (ctypes.c_int, [C, I32, I32, I32, P, I64, P, P, I32, I32, I32, P, I32, I32, I32, F32, P, I32,
                                                I64, P, U32, P]),
+        "hq_rope_freqs": (ctypes.c_int, [I32, F64, I32, F64, F64, F64, F64, P]),
+        "hq_rope_turns": (ctypes.c_int, [P, I32, P]),
+        "hq_rope_write": (ctypes.c_int, [C, I32, I32, I32, P, P, P, I32, I64, I64, I64, I32, P, P, F32, P, I32, I32, F32, P, P,
+                                         I32, I32, I32, P, P, P, I64, U32, P]),
+        "hq_gated_norm_quant": (ctypes.c_int, [D, P, I32, I64, P, I32, I64, I32, P, I32, F32, I32, P, P, I32, I64, P, P, P, P,
+                                               U32, P]),
+        "hq_greedy_tokens_workspace_bytes": (SZ, [I32]),
+        "hq_greedy_tokens": (ctypes.c_int, [P, I32, I64, I32, HS, LR, P, P, P, I32, I32, I32, P, P, P, I32, I64, P, P, U32, P]),
+        "hq_tree_accept_batch": (ctypes.c_int, [P, P, P, P, P, I32, I32, I32, HS, P, I32, P, P, U32, P]),
+        "hq_history_status": (ctypes.c_int, [HS, P]),
         "hq_lora_workspace_bytes": (SZ, [I32, I32]),
         "hq_lora_apply": (ctypes.c_int, [P, I32, I64, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, I64, P, I64, P,
                                          U32, P]),
@@ -672,7 +701,18 @@ def lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Ten
     return Y
 
 
-class PagedCache:
+class _Held:
+    """Attributes whose device addresses the library holds stay the tensors they are."""
+    _held = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self._held and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{type(self).__name__}.{name} is held by its address: change it in place, or make a new "
+                                 f"{type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class PagedCache(_Held):
     """A paged key/value cache (hq_pages) over the caller's tensors: pool
     [planes][pages][heads][page_size][dim] (fp16 or bf16), ref int32 [pages],
     table int32 [sequences][max_pages], lens int32 [sequences].  `empty` makes
@@ -680,11 +720,6 @@ class PagedCache:
     contents may be changed in place, the attributes themselves stay."""
 
     _held = frozenset(("pool", "ref", "table", "lens", "status", "scratch", "c"))
-
-    def __setattr__(self, name, value):
-        if name in self._held and self.__dict__.get(name, value) is not value:
-            raise AttributeError(f"PagedCache.{name} is held by its address: change it in place, or make a new PagedCache")
-        object.__setattr__(self, name, value)
 
     def __init__(self, pool: torch.Tensor, ref: torch.Tensor, table: torch.Tensor, lens: torch.Tensor):
         planes, pages, heads, page_size, dim = pool.shape
@@ -772,8 +807,8 @@ def pages_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, flags: i
     _check(load().hq_pages_copy(cache.c, _ptr(src), _ptr(dst), n, flags, _stream(stream)), "hq_pages_copy")
 
 
-def _batch(cache: PagedCache, rows: int, starts, max_rows: int, seqs, what: str) -> int:
-    """The number of sequences of a batch of rows."""
+def _batch(n_seqs, rows: int, starts, max_rows: int, seqs, what: str) -> int:
+    """The number of sequences of a batch of rows (n_seqs: of the cache, None: no cache)."""
     if max_rows < 1:
         raise ValueError(f"{what}: max_rows must be at least 1, got {max_rows}")
     if starts is not None:
@@ -786,8 +821,8 @@ def _batch(cache: PagedCache, rows: int, starts, max_rows: int, seqs, what: str)
         B = rows // max_rows
     if seqs is not None:
         _list(seqs, B, what)
-    elif B > cache.n_seqs:
-        raise ValueError(f"{what}: {B} sequences, the cache has {cache.n_seqs}")
+    elif n_seqs is not None and B > n_seqs:
+        raise ValueError(f"{what}: {B} sequences, the cache has {n_seqs}")
     return B
 
 
@@ -799,7 +834,7 @@ def pages_write(cache: PagedCache, k_plane: int, v_plane: int, k: torch.Tensor, 
     rows = k.shape[0]
     if v.shape[0] != rows or v.dtype != k.dtype:
         raise ValueError("pages_write: k and v need the same rows and type")
-    B = _batch(cache, rows, starts, max_rows, seqs, "pages_write: starts and seqs")
+    B = _batch(cache.n_seqs, rows, starts, max_rows, seqs, "pages_write: starts and seqs")
     cols = cache.heads * cache.dim
     _check(load().hq_pages_write(cache.c, k_plane, v_plane, _ptr(k), _ptr(v), _type(k), _rows(k, cols, "k"),
                                  _rows(v, cols, "v"), cache.type, _ptr(seqs), _ptr(starts), B, rows, max_rows, flags,
@@ -831,7 +866,7 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
     rows, Hq, D = shape
     if D != cache.dim or q.dtype != cache.pool.dtype:
         raise ValueError(f"prefix_attention: q must be {cache.pool.dtype} [rows][heads][{cache.dim}]")
-    B = _batch(cache, rows, starts, max_rows, seqs, "prefix_attention: starts and seqs")
+    B = _batch(cache.n_seqs, rows, starts, max_rows, seqs, "prefix_attention: starts and seqs")
     if parent is not None:
         _list(parent, rows, "prefix_attention: parent")
     if out is None:
@@ -849,3 +884,249 @@ def prefix_attention(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Ten
                                       _ptr(out), _type(out), Hq * D if out.is_contiguous() else _rows(out, Hq * D, "out"), _ptr(workspace), flags,
                                       _stream(stream)), "hq_prefix_attention")
     return out
+
+
+# ------------------------------------------- between the calls of a step ---
+def rope_freqs(rot: int, base: float = 10000.0, kind: str = "plain", factor: float = 1.0, original: float = 0.0,
+               low: float | None = None, high: float | None = None) -> np.ndarray:
+    """Radians a position of the rot / 2 pairs of a head (hq_rope_freqs).
+    `kind` "linear", "ntk", "yarn" or "bands" scales them for contexts `factor`
+    times as long as the model's own of `original` positions; low and high: the
+    turns over `original` between which "yarn" (1 and 32 if not given) and
+    "bands" (1 and 4) go over from divided frequencies to those as they are."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"rope_freqs: kind must be one of {', '.join(ROPE_KINDS)}, got {kind!r}")
+    out = np.zeros(max(rot // 2, 1), dtype=np.float64)
+    _check(load().hq_rope_freqs(rot, base, ROPE_KINDS[kind], factor, original, 1.0 if low is None else low,
+                                (4.0 if kind == "bands" else 32.0) if high is None else high, out.ctypes.data), "hq_rope_freqs")
+    return out
+
+
+def rope_turns(freqs, device) -> torch.Tensor:
+    """Frequencies (radians a position) as rope_write takes them: int64 [n] on the device (hq_rope_turns)."""
+    f = np.ascontiguousarray(freqs, dtype=np.float64)
+    out = np.zeros(f.shape, dtype=np.int64)
+    if f.ndim != 1:
+        raise ValueError(f"rope_turns: a list of frequencies expected, got shape {f.shape}")
+    _check(load().hq_rope_turns(f.ctypes.data, f.shape[0], out.ctypes.data), "hq_rope_turns")
+    return torch.from_numpy(out).to(device)
+
+
+def rope_write(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+               turns: torch.Tensor, starts, max_rows: int, layout: str = "half", gain: float = 1.0, q_weight=None, k_weight=None,
+               eps: float = 1e-6, parent=None, positions=None, seqs=None, out=None, flags: int = 0, stream=None) -> torch.Tensor:
+    """Rotates the newest rows' q and k by their positions and writes k and v
+    into the paged cache (hq_rope_write): pages_write with the rotation, and q
+    for prefix_attention.  q [rows][Hq][dim], k and v [rows][heads][dim], fp32 or
+    the cache's type, rows any 16-byte-aligned distance apart (the columns of one
+    projection); turns from rope_turns, 8 to dim / 2 pairs.  q_weight, k_weight
+    fp32 [dim]: heads are normed first.  A row's position is positions[row]
+    (int32 [rows]), or its sequence's length before these rows plus its depth in
+    the tree of `parent` (None: a chain).  Returns out [rows][Hq][dim] of the
+    cache's type (may be q itself)."""
+    shape = q.shape
+    rows, Hq, D = shape
+    heads = cache.heads
+    if D != cache.dim or k.shape != (rows, heads, D) or v.shape != k.shape:
+        raise ValueError(f"rope_write: q [rows][heads][{cache.dim}], k and v [rows][{heads}][{cache.dim}] expected, got "
+                         f"{tuple(shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("rope_write: q, k and v need the same type")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError(f"rope_write: turns must be contiguous int64 [pairs], got {turns.dtype} {tuple(turns.shape)}")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"rope_write: layout must be one of {', '.join(ROPE_LAYOUTS)}, got {layout!r}")
+    B = _batch(cache.n_seqs, rows, starts, max_rows, seqs, "rope_write: starts and seqs")
+    if parent is not None:
+        _list(parent, rows, "rope_write: parent")
+    if positions is not None:
+        _list(positions, rows, "rope_write: positions")
+    if q_weight is not None:
+        _dense(q_weight, torch.float32, (D,), "rope_write: q_weight")
+    if k_weight is not None:
+        _dense(k_weight, torch.float32, (D,), "rope_write: k_weight")
+    if out is None:
+        out = _new(shape, cache.pool.dtype, q.device, stream)
+    elif out.shape != shape or out.dtype != cache.pool.dtype:
+        raise ValueError(f"rope_write: out must be {cache.pool.dtype} {list(shape)}")
+    cols, kcols = Hq * D, heads * D
+    rc = load().hq_rope_write(cache.c, k_plane, v_plane, cache.type, _ptr(q), _ptr(k), _ptr(v), _type(q), _rows(q, cols, "q"),
+                              _rows(k, kcols, "k"), _rows(v, kcols, "v"), Hq, _ptr(q_weight), _ptr(k_weight), eps, _ptr(turns),
+                              2 * turns.shape[0], ROPE_LAYOUTS[layout], gain, _ptr(seqs), _ptr(starts), B, rows, max_rows,
+                              _ptr(parent), _ptr(positions), _ptr(out), _rows(out, cols, "out"), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_rope_write")
+    return out
+
+
+def gated_norm_quant(desc: hq_layer_desc, x: torch.Tensor, gate, weight, signs, dim: int, act: str = "silu", eps: float = 1e-6,
+                     h=None, qx=None, gsum=None, qop=None, sx=None, flags: int = 0, stream=None) -> None:
+    """The norm of every head of `dim` features with its gate, and the
+    quantization of the result for the output projection `desc`
+    (hq_gated_norm_quant), in one pass: y = x * weight / rms(head) * act(gate),
+    h = y, qx / gsum / qop / sx = its codes (buffers of act_buffers).  x, gate
+    and h: [M][K], fp32, fp16 or bf16, rows any 16-byte-aligned distance apart;
+    gate may be None (no gate), weight (fp32 [dim]) None (no norm), and any
+    output None; act "silu", "sigmoid" or "none" (the gate itself)."""
+    shape = x.shape
+    M, K = shape
+    if K != desc.K:
+        raise ValueError(f"gated_norm_quant: x has {K} features, the layer {desc.K}")
+    if act not in GATE_ACTS:
+        raise ValueError(f"gated_norm_quant: act must be one of {', '.join(GATE_ACTS)}, got {act!r}")
+    _shaped(gate, shape, "gated_norm_quant: gate")
+    _shaped(h, shape, "gated_norm_quant: h")
+    _dense(weight, torch.float32, (dim,), "gated_norm_quant: weight")
+    _dense(signs, torch.int32, (K // 32,), "gated_norm_quant: signs")
+    _dense(qx, torch.int8, shape, "gated_norm_quant: qx")
+    _dense(sx, torch.float32, (M,), "gated_norm_quant: sx")
+    if gsum is not None:
+        _dense(gsum, torch.int32, (M, K // desc.group), "gated_norm_quant: gsum")
+    if qop is not None:
+        _room(qop, hq_act_operand_bytes(desc, M), "gated_norm_quant: qop")
+    rc = load().hq_gated_norm_quant(desc, _ptr(x), _type(x), _pitch(x, K, "x"), _ptr(gate), _type(gate), _pitch(gate, K, "gate"),
+                                    GATE_ACTS[act], _ptr(weight), dim, eps, M, _ptr(signs), _ptr(h), _type(h), _pitch(h, K, "h"),
+                                    _ptr(qx), _ptr(gsum), _ptr(qop), _ptr(sx), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_gated_norm_quant")
+
+
+class History(_Held):
+    """What requests have said so far (hq_history) over the caller's tensors:
+    tokens int32 [slots][cap], lens int32 [slots], prompt int32 [slots] (how many
+    of them are the prompt's; None: 0).  A slot's newest token, the root of its
+    next draft tree, is its last.  tree_accept_batch lets them grow."""
+
+    _held = frozenset(("tokens", "lens", "prompt", "status", "c"))
+
+    def __init__(self, tokens: torch.Tensor, lens: torch.Tensor, prompt=None):
+        if tokens.dim() != 2:
+            raise ValueError("History: tokens must be [slots][cap]")
+        slots, cap = tokens.shape
+        _dense(tokens, torch.int32, (slots, cap), "History: tokens")
+        _dense(lens, torch.int32, (slots,), "History: lens")
+        _dense(prompt, torch.int32, (slots,), "History: prompt")
+        if not 1 <= slots <= 65536 or not 1 <= cap <= 1 << 24:
+            raise ValueError(f"History: 1 to 65536 slots of 1 to 2^24 tokens, got {slots} of {cap}")
+        self.tokens, self.lens, self.prompt, self.n_slots = tokens, lens, prompt, slots
+        self.status = torch.zeros(4, dtype=torch.int32, device=tokens.device)
+        self.c = hq_history(_ptr(tokens), _ptr(lens), _ptr(prompt), _ptr(self.status), slots, cap)
+
+
+def history_status(history: History, stream=None) -> int:
+    """Synchronizes; the first error of tree_accept_batch on this history since the last call (HQ_OK if none), cleared."""
+    return int(load().hq_history_status(history.c, _stream(stream)))
+
+
+class LogitRules(_Held):
+    """Rules of `slots` requests on their logits (hq_logit_rules) over the
+    caller's tensors, each may be None: repetition, presence and frequency fp32
+    [slots]; bias = (starts int32 [slots + 1], tokens int32 [n], values fp32 [n]),
+    slot s has the entries starts[s] .. starts[s + 1]; masks int32 [masks][at
+    least ceil(vocabulary / 32)], bit t % 32 of word t / 32 set: token t is
+    allowed."""
+
+    _held = frozenset(("repetition", "presence", "frequency", "bias", "masks", "c"))
+
+    def __init__(self, slots: int, repetition=None, presence=None, frequency=None, bias=None, masks=None):
+        for t, what in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
+            _dense(t, torch.float32, (slots,), f"LogitRules: {what}")
+        starts, tokens, values = bias if bias is not None else (None, None, None)
+        n = 0
+        if bias is not None:
+            _dense(starts, torch.int32, (slots + 1,), "LogitRules: bias starts")
+            n = _list(tokens, None, "LogitRules: bias tokens")
+            _dense(values, torch.float32, (n,), "LogitRules: bias values")
+        words = 0
+        if masks is not None:
+            if masks.dtype != torch.int32 or masks.dim() != 2 or (masks.shape[1] > 1 and masks.stride(1) != 1):
+                raise ValueError("LogitRules: masks must be int32 [masks][words], the words of a mask contiguous")
+            words = masks.shape[1]
+        self.repetition, self.presence, self.frequency, self.bias, self.masks = repetition, presence, frequency, bias, masks
+        self.n_slots, self.words = slots, words
+        self.c = hq_logit_rules(_ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(starts), _ptr(tokens), _ptr(values),
+                                _ptr(masks), 0 if masks is None else masks.stride(0) if masks.shape[0] > 1 else words, slots, n,
+                                0 if masks is None else masks.shape[0])
+
+
+@functools.lru_cache(maxsize=1024)
+def hq_greedy_tokens_workspace_bytes(rows: int) -> int:
+    return int(load().hq_greedy_tokens_workspace_bytes(int(rows)))
+
+
+def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, tokens=None, seqs=None, history: History = None,
+                  rules: LogitRules = None, mask_ids=None, out=None, greedy=None, workspace=None, flags: int = 0,
+                  stream=None) -> torch.Tensor:
+    """Penalties, biases and masks on the logits [rows][V] (fp32, fp16 or bf16)
+    of a batch's trees, and the greedy token of every row (hq_greedy_tokens), -1
+    where every token is masked.  Sequence b's rows are starts[b] .. starts[b +
+    1] (None: max_rows rows each); parent and tokens int32 [rows]: its draft tree
+    (parent None: a chain; tokens None: nothing drafted); seqs: its slots in
+    history and rules (None: b).  mask_ids int32 [rows]: the row's mask, -1 none
+    (None: mask r for row r).  out [rows][V] (the logits' type or fp32, or logits
+    itself): the adjusted logits.  workspace: zeroed once.  Returns greedy int32
+    [rows]."""
+    rows, V = logits.shape
+    B = _batch(None, rows, starts, max_rows, seqs, "greedy_tokens: starts and seqs")
+    ty = TYPES.get(logits.dtype)
+    if ty is None:
+        raise TypeError(f"greedy_tokens: fp32, fp16 or bf16 expected, got {logits.dtype}")
+    if parent is not None:
+        _list(parent, rows, "greedy_tokens: parent")
+    if tokens is not None:
+        _list(tokens, rows, "greedy_tokens: tokens")
+    if mask_ids is not None:
+        _list(mask_ids, rows, "greedy_tokens: mask_ids")
+    if rules is not None and rules.masks is not None and rules.words * 32 < V:
+        raise ValueError(f"greedy_tokens: the masks have {rules.words} words, {V} tokens need {-(-V // 32)}")
+    if out is not None and out is not logits and (out.shape != logits.shape or out.dtype not in (logits.dtype, torch.float32)):
+        raise ValueError(f"greedy_tokens: out must be {logits.dtype} or fp32 {[rows, V]}, got {out.dtype} {list(out.shape)}")
+    if greedy is None:
+        greedy = _new(rows, _INT32, logits.device, stream)
+    else:
+        _list(greedy, rows, "greedy_tokens: greedy")
+    need = hq_greedy_tokens_workspace_bytes(rows)
+    if workspace is None:
+        workspace = _new(max(need, 16), torch.uint8, logits.device, stream, torch.zeros)
+    _room(workspace, need, "greedy_tokens: the workspace")
+    rc = load().hq_greedy_tokens(_ptr(logits), ty, _pitch(logits, V, "logits"), V, None if history is None else history.c,
+                                 None if rules is None else rules.c, _ptr(mask_ids), _ptr(seqs), _ptr(starts), B, rows, max_rows,
+                                 _ptr(parent), _ptr(tokens), _ptr(out), ty if out is None else TYPES[out.dtype],
+                                 _pitch(out, V, "out"), _ptr(greedy), _ptr(workspace), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_greedy_tokens")
+    return greedy
+
+
+def tree_accept_batch(greedy: torch.Tensor, parent, tokens: torch.Tensor, starts, max_rows: int, seqs=None,
+                      history: History = None, path=None, n_accept=None, bonus=None, flags: int = 0, stream=None):
+    """Accepted path, number accepted and bonus token of every draft tree of a
+    batch from its greedy tokens (hq_tree_accept_batch); `history` grows by the
+    accepted drafts and the bonus token.  greedy, parent (None: chains) and
+    tokens int32 [rows]; starts, max_rows and seqs as in greedy_tokens.  Returns
+    path int32 [B][max_rows] (-1 past the accepted nodes), n_accept and bonus
+    int32 [B]: pages_compact takes path as keep and n_accept as n_keep."""
+    rows = _list(greedy, None, "tree_accept_batch: greedy")
+    _list(tokens, rows, "tree_accept_batch: tokens")
+    if parent is not None:
+        _list(parent, rows, "tree_accept_batch: parent")
+    B = _batch(None, rows, starts, max_rows, seqs, "tree_accept_batch: starts and seqs")
+    dev = greedy.device
+    if path is None:
+        path = _new((B, max_rows), _INT32, dev, stream)
+    elif path.dtype is not _INT32 or path.dim() != 2 or path.shape[0] != B or path.shape[1] < max_rows or path.stride(1) != 1:
+        raise ValueError(f"tree_accept_batch: path must be int32 [{B}][{max_rows} or more]")
+    if n_accept is None:
+        n_accept = _new(B, _INT32, dev, stream)
+    else:
+        _list(n_accept, B, "tree_accept_batch: n_accept")
+    if bonus is None:
+        bonus = _new(B, _INT32, dev, stream)
+    else:
+        _list(bonus, B, "tree_accept_batch: bonus")
+    rc = load().hq_tree_accept_batch(_ptr(greedy), _ptr(parent), _ptr(tokens), _ptr(seqs), _ptr(starts), B, rows, max_rows,
+                                     None if history is None else history.c, _ptr(path), path.stride(0) if B > 1 else path.shape[1],
+                                     _ptr(n_accept), _ptr(bonus), flags, _stream(stream))
+    if rc != HQ_OK:
+        raise HQError(rc, "hq_tree_accept_batch")
+    return path, n_accept, bonus
