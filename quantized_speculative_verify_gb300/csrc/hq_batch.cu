@@ -319,7 +319,7 @@ int hq_rope_freqs(int32_t rot, double base, int32_t kind, double factor, double 
         if (kind == HQ_ROPE_LINEAR) keep = 0.0;
         if (kind == HQ_ROPE_YARN) keep = 1.0 - std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
         if (kind == HQ_ROPE_BANDS) keep = std::fmin(std::fmax((original * f / pi2 - low) / (high - low), 0.0), 1.0);
-        freqs_host[i] = keep == 1.0 ? f : f * keep + f / factor * (1.0 - keep);
+        freqs_host[i] = keep == 1.0 || kind == HQ_ROPE_PLAIN ? f : f / factor + (f - f / factor) * keep;
     }
     return HQ_OK;
 }

@@ -984,9 +984,11 @@ def gated_norm_quant(desc: hq_layer_desc, x: torch.Tensor, gate, weight, signs, 
         _dense(gsum, torch.int32, (M, K // desc.group), "gated_norm_quant: gsum")
     if qop is not None:
         _room(qop, hq_act_operand_bytes(desc, M), "gated_norm_quant: qop")
-    rc = load().hq_gated_norm_quant(desc, _ptr(x), _type(x), _pitch(x, K, "x"), _ptr(gate), _type(gate), _pitch(gate, K, "gate"),
-                                    GATE_ACTS[act], _ptr(weight), dim, eps, M, _ptr(signs), _ptr(h), _type(h), _pitch(h, K, "h"),
-                                    _ptr(qx), _ptr(gsum), _ptr(qop), _ptr(sx), flags, _stream(stream))
+    x_type, g_type, h_type = _type(x), _type(gate), _type(h)
+    ldx, ldg, ldh = _pitch(x, K, "x"), _pitch(gate, K, "gate"), _pitch(h, K, "h")
+    rc = load().hq_gated_norm_quant(desc, _ptr(x), x_type, ldx, _ptr(gate), g_type, ldg, GATE_ACTS[act], _ptr(weight), dim, eps, M,
+                                    _ptr(signs), _ptr(h), h_type, ldh, _ptr(qx), _ptr(gsum), _ptr(qop), _ptr(sx), flags,
+                                    _stream(stream))
     if rc != HQ_OK:
         raise HQError(rc, "hq_gated_norm_quant")
 
@@ -1089,10 +1091,11 @@ def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, toke
     if workspace is None:
         workspace = _new(max(need, 16), torch.uint8, logits.device, stream, torch.zeros)
     _room(workspace, need, "greedy_tokens: the workspace")
-    rc = load().hq_greedy_tokens(_ptr(logits), ty, _pitch(logits, V, "logits"), V, None if history is None else history.c,
+    ldl, ldo = _pitch(logits, V, "logits"), _pitch(out, V, "out")
+    rc = load().hq_greedy_tokens(_ptr(logits), ty, ldl, V, None if history is None else history.c,
                                  None if rules is None else rules.c, _ptr(mask_ids), _ptr(seqs), _ptr(starts), B, rows, max_rows,
-                                 _ptr(parent), _ptr(tokens), _ptr(out), ty if out is None else TYPES[out.dtype],
-                                 _pitch(out, V, "out"), _ptr(greedy), _ptr(workspace), flags, _stream(stream))
+                                 _ptr(parent), _ptr(tokens), _ptr(out), ty if out is None else TYPES[out.dtype], ldo,
+                                 _ptr(greedy), _ptr(workspace), flags, _stream(stream))
     if rc != HQ_OK:
         raise HQError(rc, "hq_greedy_tokens")
     return greedy
