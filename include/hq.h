@@ -838,8 +838,9 @@ typedef struct {
  *           no overlap
  *   greedy  int32 [rows]
  *   workspace hq_greedy_tokens_workspace_bytes(rows) bytes, 16-byte aligned,
- *           zeroed once; each call leaves it zeroed.  The size grows with rows
- *           and depends on nothing else
+ *           zeroed once: counters, and room for long histories sorted by token
+ *           (64 KB a row, for 256 rows at most).  One workspace of the most rows
+ *           serves every call in turn
  * Tokens outside [0, V), in any of the lists, are passed over.  Rows that no
  * sequence claims are left as they were, in out and greedy.  Results repeat bit
  * for bit.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (nothing is read before

@@ -121,13 +121,13 @@ struct GreedyArgs {
     void *out;
     const int32_t *mask_ids, *seqs, *starts, *parent, *tokens;
     int32_t *greedy;
-    unsigned long long *best;  // [rows]: largest key so far
-    unsigned *done;            // [rows]: chunks that are in it
-    hq_history history;        // tokens NULL: none
+    uint8_t *workspace;
+    hq_history history;  // tokens NULL: none
     hq_logit_rules rules;
     int64_t ldl, ldo;
     int type, out_type, V, B, rows, max_rows;
 };
+size_t greedy_workspace_bytes(int rows);
 cudaError_t launch_greedy_tokens(const GreedyArgs &a, bool pdl, cudaStream_t s);
 
 struct AcceptBatchArgs {

@@ -445,7 +445,7 @@ int hq_gated_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type
 }
 
 size_t hq_greedy_tokens_workspace_bytes(int32_t rows) {
-    return rows > 0 && rows <= 1 << 26 ? ((size_t)rows * 12 + 15) / 16 * 16 : 0;
+    return rows > 0 && rows <= 1 << 26 ? hq::greedy_workspace_bytes(rows) : 0;
 }
 
 int hq_greedy_tokens(const void *logits, int32_t type, int64_t ldl, int32_t V, const hq_history *history,
@@ -482,8 +482,7 @@ int hq_greedy_tokens(const void *logits, int32_t type, int64_t ldl, int32_t V, c
     a.parent = parent;
     a.tokens = tokens;
     a.greedy = greedy;
-    a.best = static_cast<unsigned long long *>(workspace);
-    a.done = reinterpret_cast<unsigned *>(a.best + rows);
+    a.workspace = static_cast<uint8_t *>(workspace);
     if (history) a.history = *history;
     if (rules) a.rules = *rules;
     a.ldl = ldl;

@@ -8,17 +8,32 @@
 //
 // Rows hold 100 thousand logits, a history a few thousand tokens: most logits
 // meet no rule but the mask.  A thread block takes a chunk of the vocabulary for
-// some rows of one sequence.  It counts the history's tokens of its chunk in
-// shared memory (a word a token: seen, biased, drafted, and how often behind the
-// prompt), once for its rows; what a row's own path adds to that is the drafted
-// tokens of its ancestors, at most 127 and found only at the few tokens that are
-// marked as drafted.  Then the rows stream through: four logits a load, four
-// words of shared memory, and code for the rules only where a word is not zero.
+// some rows of one sequence.  In shared memory it makes a table of the tokens of
+// its chunk that a rule reaches, once for its rows: a word a token (seen, biased,
+// drafted, how often behind the prompt), a bit a token, and a list of them in
+// order.  All the code for the rules is in a pass over the list.  The others are in
+// the threads' registers by then, eight logits a load, asked for before anything
+// else (the next row's before this one is looked at); the list's are left out by
+// their bits.  What a row's own path adds to the table is the drafted tokens of its
+// ancestors, at most 127 and looked for only at tokens that are marked as drafted.
 //
-// A block's largest value and its token make one 64-bit key (a larger key is a
-// larger value, or the same value at a lower token); chunks meet by the maximum
-// of their keys, which does not depend on the order, and the last one writes the
-// token and leaves the workspace as it found it.
+// A block is a chain of waits (its sequence, the history's length, the history, the
+// list's logits, the ticket at the end), 6 us of them for 16 KB of logits, so the
+// chunks are small enough for seven blocks an SM.  Frequent tokens have low
+// numbers: the first chunks' lists are far longer than the others', and their
+// blocks come first in the grid.
+//
+// Every chunk's block would read the whole history of its sequence.  Where that
+// adds up, a kernel in front sorts the histories by chunk into the workspace.
+//
+// The order of values is that of a signed integer (a float's bits, the lower 31
+// inverted where it is negative; NaN above all), so the largest of a warp is one
+// instruction.  A thread keeps its largest value and where the eight logits with
+// it lie; which of them it was is looked up once a row and block.  Chunks meet by
+// the maximum of 64-bit keys (value, then the lowest token), which does not depend
+// on the order; the last one writes the token and leaves its words as it found
+// them.
+#include <climits>
 #include <type_traits>
 
 #include "batch.cuh"
@@ -26,28 +41,31 @@
 namespace hq {
 namespace {
 
-constexpr int GT = 256;          // threads
-constexpr int GROUP = 4;         // rows of a sequence that share one count of its history
-constexpr int MOST = 16384, LEAST = 1024;  // tokens of a chunk
+constexpr int GT = 128;          // threads
+constexpr int GROUP = 4;         // rows of a sequence that share one table
+constexpr int MOST = 4096, LEAST_SHIFT = 10;  // tokens of a chunk, a power of two: at most 4096, at least 2^10
+constexpr int EIGHTS = MOST / 8 / GT;     // loads of a thread for a row
+constexpr int FLIGHT = 4;        // loads of the history of a thread on their way together
+constexpr int LISTED = 4;        // the same for tokens of the list
+constexpr int BIASES = 128;      // biases of a chunk that are found in shared memory
 constexpr uint32_t SEEN = 1u << 31, BIASED = 1u << 30, DRAFTED = 1u << 29, TIMES = DRAFTED - 1;
 
-// The larger value, the largest; NaN if one is.
+// The largest value; NaN (one pattern of it) if one is.
 __device__ __forceinline__ float max_nan2(float x, float y) {
     float z;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
     return z;
 }
-
-__device__ __forceinline__ unsigned long long key_of(float v, int token) {
-    if (token < 0) return 0ull;  // below every real key
-    uint32_t u = __float_as_uint(v);
-    if (v != v) u = 0x7FC00000u;  // every NaN ranks above +inf
-    if (v == 0.0f) u = 0u;        // -0 and +0 are equal
-    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((unsigned long long)u << 32) | (0xFFFFFFFFu - (uint32_t)token);
+__device__ __forceinline__ float max_nan3(float x, float y, float w) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(z) : "f"(x), "f"(y), "f"(w));
+    return z;
 }
-__device__ __forceinline__ int token_of(unsigned long long key) {
-    return key == 0ull ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
+// The order of values, NONE below all; NaN as max_nan2 gives it.
+constexpr int NONE = INT_MIN;
+__device__ __forceinline__ int order_of(float x) {
+    const int i = __float_as_int(x + 0.0f);  // (-0 is 0)
+    return i ^ ((i >> 31) & 0x7fffffff);
 }
 
 template <class T>
@@ -63,286 +81,539 @@ __device__ __forceinline__ T from_f32(float x) {
     else return __float2bfloat16_rn(x);
 }
 
+// Eight values, 16 bytes at a time.
 template <class T>
-struct alignas(4 * sizeof(T)) Quad {
-    T x[4];
+struct alignas(16) Oct {
+    T x[8];
 };
+template <class T>
+__device__ __forceinline__ void load(const T *p, Oct<T> &v) {
+#pragma unroll
+    for (int i = 0; i < 8 * (int)sizeof(T) / 16; ++i) reinterpret_cast<uint4 *>(&v)[i] = reinterpret_cast<const uint4 *>(p)[i];
+}
+template <class T>
+__device__ __forceinline__ void store(T *p, const Oct<T> &v) {
+#pragma unroll
+    for (int i = 0; i < 8 * (int)sizeof(T) / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(&v)[i];
+}
+
+// The workspace: a record for each row (its largest key so far, how many chunks are
+// in it) and, in the first SORT_MOST records, a sequence's sorted history.  A
+// record's place depends on its number alone, so calls of different sizes share a
+// workspace without meeting one another's leavings.
+constexpr int SORTED = 16384, CHUNKS = 64;
+constexpr int SORT_MOST = 256;  // sequences
+constexpr size_t RECORD = 16 + (SORTED + CHUNKS) * 4;
+__host__ __device__ inline size_t record_at(int i) {
+    return i < SORT_MOST ? i * RECORD : SORT_MOST * RECORD + (size_t)(i - SORT_MOST) * 16;
+}
 
 struct Shared {
-    unsigned long long key[GROUP][GT / 32];
+    uint32_t word[MOST];            // what reaches each token
+    uint32_t bits[MOST / 32 + 4];   // (one more for reads across the last one's end)
+    uint16_t list[MOST];
+    int32_t bias_at[BIASES];        // biases of this chunk: their number in the slot's list, their token
+    uint16_t bias_of[BIASES];
+    int order[GROUP][GT / 32], at[GROUP][GT / 32];  // of each warp, of the ring
+    int list_order[GROUP][GT / 32], list_at[GROUP][GT / 32];  // and of the list
+    int mask_id[GROUP];
     uint32_t above[GROUP][HQ_MAX_M / 32];  // the nodes on each row's path, without the root
     int32_t node[HQ_MAX_M], token[HQ_MAX_M];  // drafted tokens of this chunk
-    int n;
+    int n_drafted, n_biased, counts[GT / 32];
 };
 
-// RULES: penalties or biases, which need the words in shared memory.
-template <class T, class O, bool RULES>
-__global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chunk, const int group) {
-    extern __shared__ __align__(16) uint32_t s_word[];  // [chunk], then the place of a token's bias, plus one [chunk]
-    __shared__ Shared s;
-    pdl_launch_dependents();
+// Bits d .. d + 7 of a bit field; s = d % 8, the same for all of a row's loads.
+__device__ __forceinline__ uint32_t eight_bits(const uint32_t *words, int d, int s) {
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(words) + (d >> 3);
+    uint32_t w = p[0];
+    if (s != 0) w = ((w | (uint32_t)p[1] << 8) >> s) & 0xffu;
+    return w;
+}
+
+// Histories sorted by chunk.  Of each sequence the first SORTED tokens: which chunk
+// they are of, counted by each warp for itself, then each token's place.  A token
+// of the prompt has its top bit set.  Worth it where all blocks together would
+// otherwise read more than SORT_FROM bytes of histories: 128 rows with 16000 tokens
+// each, 300 MB, 105 us without, 71 with it; eight trees with 2000, 19 MB, 29.5
+// without, 30.6 with it.
+constexpr int ST = 1024;
+constexpr long long SORT_FROM = 64ll << 20;
+__global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const int shift, const int chunks) {
+    __shared__ int s_count[ST / 32][CHUNKS];
+    __shared__ int s_start[CHUNKS + 1];
     pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
+    const int slot = a.seqs ? a.seqs[b] : b;
+    int len = 0, prompt = 0;
+    if (slot >= 0 && slot < a.history.n_slots) {
+        len = a.history.len[slot];
+        if (a.history.prompt) prompt = a.history.prompt[slot];
+    }
+    len = len < 0 ? 0 : len > a.history.cap ? a.history.cap : len;
+    if (len > SORTED) len = SORTED;
+    const int32_t *text = a.history.tokens + (size_t)(len > 0 ? slot : 0) * a.history.cap;
+    int32_t t[SORTED / ST];
+    int place[SORTED / ST];
+#pragma unroll
+    for (int k = 0; k < SORTED / ST; ++k) t[k] = k * ST + tid < len ? text[k * ST + tid] : -1;
+    for (int i = tid; i < ST / 32 * CHUNKS; i += ST) (&s_count[0][0])[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < SORTED / ST; ++k)
+        if (t[k] >= 0 && t[k] < a.V) place[k] = atomicAdd(&s_count[warp][t[k] >> shift], 1);
+    __syncthreads();
+    if (tid < chunks) {  // each warp's first place in a chunk, from the chunk's start
+        int n = 0;
+        for (int w = 0; w < ST / 32; ++w) {
+            const int c = s_count[w][tid];
+            s_count[w][tid] = n;
+            n += c;
+        }
+        s_start[tid + 1] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int carry = 0;
+        if (tid == 0) s_start[0] = 0;
+        for (int i = tid; i - tid < chunks; i += 32) {
+            int x = i < chunks ? s_start[i + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (tid >= o) x += y;
+            }
+            if (i < chunks) s_start[i + 1] = x + carry;
+            carry += __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+    int32_t *sorted = reinterpret_cast<int32_t *>(a.workspace + record_at(b) + 16);
+    if (tid <= chunks && tid < CHUNKS) sorted[SORTED + tid] = s_start[tid];
+#pragma unroll
+    for (int k = 0; k < SORTED / ST; ++k)
+        if (t[k] >= 0 && t[k] < a.V)
+            sorted[s_start[t[k] >> shift] + s_count[warp][t[k] >> shift] + place[k]] =
+                t[k] | (k * ST + tid < prompt ? (int32_t)0x80000000 : 0);
+}
+
+// RULES: penalties or biases, which need the table.  sorted: the histories are.
+template <class T, class O, bool RULES>
+__global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chunk, const int group, const bool sorted) {
+    __shared__ __align__(16) Shared s;
+    pdl_launch_dependents();
+    // The sorting kernel starts this one after its own wait, so that all but its
+    // result is there already.
+    if (!sorted) pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.z;
+    const int groups = (a.max_rows + group - 1) / group, b = blockIdx.x / groups;
     int first, m;
     batch_rows(a.starts, b, a.rows, a.max_rows, first, m);
-    const int r0 = blockIdx.y * group, r1 = r0 + group < m ? r0 + group : m;
-    if (r0 >= m) return;
-    const int lo = blockIdx.x * chunk, n = a.V - lo < chunk ? a.V - lo : chunk;
     const int slot = a.seqs ? a.seqs[b] : b;
-    uint32_t *s_bias = s_word + chunk;
+    const int r0 = blockIdx.x % groups * group, r1 = r0 + group < m ? r0 + group : m;
+    if (r0 >= m) {
+        if (sorted) pdl_wait();
+        return;
+    }
+    const int lo = blockIdx.y * chunk, n = a.V - lo < chunk ? a.V - lo : chunk;
+    auto logits_of = [&](int row) { return static_cast<const T *>(a.logits) + (size_t)row * (size_t)a.ldl + lo; };
+    // A row's logits up to the first aligned eight, the eights, the rest.
+    auto head_of = [&](const T *x) {
+        const int off = (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (16 / (int)sizeof(T) - 1);
+        const int head = off == 0 ? 0 : 16 / (int)sizeof(T) - off;
+        return head < n ? head : n;
+    };
+    Oct<T> v[EIGHTS];
+    auto fetch = [&](int r) {
+        const T *x = logits_of(first + r);
+        const int head = head_of(x), eights = (n - head) / 8;
+#pragma unroll
+        for (int k = 0; k < EIGHTS; ++k)
+            if (tid + k * GT < eights) load(x + head + 8 * (tid + k * GT), v[k]);
+    };
+    fetch(r0);
+    if (a.rules.masks && tid < r1 - r0) s.mask_id[tid] = a.mask_ids ? a.mask_ids[first + r0 + tid] : first + r0 + tid;
+    auto out_of = [&](int row) { return a.out ? static_cast<O *>(a.out) + (size_t)row * (size_t)a.ldo + lo : nullptr; };
+    auto mask_of = [&](int r) -> const uint32_t * {
+        if (!a.rules.masks) return nullptr;
+        const int id = s.mask_id[r - r0];
+        return id >= 0 && id < a.rules.n_masks ? a.rules.masks + (size_t)id * (size_t)a.rules.ldmask + (lo >> 5) : nullptr;
+    };
     float rep = 1.0f, pres = 0.0f, freq = 0.0f;
     bool use_rep = false, use_times = false;
-    const float *bias = nullptr;
+    int listed_tokens = 0;
+    // The tokens of the list, for all rows: the block's warps take the rows in turn.
+    // j0 .. j1: the slot's biases.
+    auto for_list = [&](int held, int j0, int j1) {
+        const int share = GT / 32 / (r1 - r0), r = r0 + warp / share, step = 32 * share;
+        if (r >= r1) return;
+        const T *x = logits_of(first + r);
+        O *out = out_of(first + r);
+        const uint32_t *mask = mask_of(r);
+        int best = NONE, at = INT_MAX;
+        for (int i0 = warp % share * 32 + lane; i0 < held; i0 += LISTED * step) {
+            float v[LISTED];
+            int place[LISTED];
+            bool allowed[LISTED];
+#pragma unroll
+            for (int k = 0; k < LISTED; ++k) {
+                const int i = i0 + k * step;
+                place[k] = i < held ? s.list[i] : -1;
+                allowed[k] = true;
+                if (place[k] >= 0) {
+                    v[k] = to_f32(x[place[k]]);
+                    if (mask) allowed[k] = mask[place[k] >> 5] >> (place[k] & 31) & 1u;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < LISTED; ++k) {
+                const int d = place[k];
+                if (d < 0) break;
+                float l = v[k];
+                const uint32_t word = s.word[d];
+                int times = (int)(word & TIMES);
+                if (word & DRAFTED) {
+#pragma unroll 1
+                    for (int t = 0; t < s.n_drafted; ++t)
+                        if (s.token[t] == lo + d && (s.above[r - r0][s.node[t] >> 5] >> (s.node[t] & 31) & 1u)) ++times;
+                }
+                if (use_rep && (times > 0 || (word & SEEN))) l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
+                if (use_times && times > 0) {
+                    if (a.rules.frequency) l = __fsub_rn(l, __fmul_rn(freq, (float)times));
+                    if (a.rules.presence) l = __fsub_rn(l, pres);
+                }
+                if (word & BIASED) {  // of a token listed twice the last one
+                    int j = j0;
+                    if (s.n_biased <= BIASES) {
+#pragma unroll 1
+                        for (int t = 0; t < s.n_biased; ++t)
+                            if (s.bias_of[t] == d && s.bias_at[t] > j) j = s.bias_at[t];
+                    } else {
+#pragma unroll 1
+                        for (j = j1 - 1; j > j0 && a.rules.bias_tokens[j] != lo + d;) --j;
+                    }
+                    l = __fadd_rn(l, a.rules.bias_values[j]);
+                }
+                if (!allowed[k]) l = -INFINITY;
+                if (out) out[d] = from_f32<O>(l);
+                const int o = order_of(max_nan2(l, l));
+                if (allowed[k] && o > best) {  // (d grows)
+                    best = o;
+                    at = d;
+                }
+            }
+        }
+        const int most = __reduce_max_sync(0xffffffffu, best);
+        at = __reduce_min_sync(0xffffffffu, best == most ? at : INT_MAX);
+        if (lane == 0) {
+            s.list_order[r - r0][warp] = most;
+            s.list_at[r - r0][warp] = at;
+        }
+    };
     if (RULES) {
-        for (int i = tid; i < (n + 3) / 4; i += GT) reinterpret_cast<uint4 *>(s_word)[i] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) s.n = 0;
         const bool ruled = slot >= 0 && slot < a.rules.n_slots;
         use_rep = ruled && a.rules.repetition;
         use_times = ruled && (a.rules.presence || a.rules.frequency);
-        if (use_rep) rep = a.rules.repetition[slot];
-        if (ruled && a.rules.presence) pres = a.rules.presence[slot];
-        if (ruled && a.rules.frequency) freq = a.rules.frequency[slot];
-        int j0 = 0, j1 = 0;  // the slot's biases
+        const bool told = (use_rep || use_times) && a.history.tokens && slot < a.history.n_slots;
+        const bool drafts = (use_rep || use_times) && a.tokens;
+        int len = 0, prompt = 0, j0 = 0, j1 = 0;  // j0 .. j1: the slot's biases
+        if (told) {
+            len = a.history.len[slot];
+            if (a.history.prompt) prompt = a.history.prompt[slot];
+        }
         if (ruled && a.rules.bias_starts) {
             j0 = a.rules.bias_starts[slot];
             j1 = a.rules.bias_starts[slot + 1];
-            if (j0 < 0 || j1 > a.rules.n_bias || j1 < j0) j0 = j1 = 0;
-            bias = a.rules.bias_values + j0;
+        }
+        if (use_rep) rep = a.rules.repetition[slot];
+        if (ruled && a.rules.presence) pres = a.rules.presence[slot];
+        if (ruled && a.rules.frequency) freq = a.rules.frequency[slot];
+        static_assert(GT >= HQ_MAX_M && GT / 32 >= GROUP, "a thread per node, a warp per row");
+        const int32_t draft = drafts && tid > 0 && tid < m ? a.tokens[first + tid] : -1;
+        int up[HQ_MAX_M / 32];  // of the nodes up to this warp's row, four a lane
+        if (drafts && r0 + warp < r1) {
+#pragma unroll
+            for (int k = 0; k < HQ_MAX_M / 32; ++k) {
+                const int i = lane + 32 * k;
+                up[k] = i > r0 + warp ? -1 : a.parent ? a.parent[first + i] : i - 1;
+            }
+        }
+        for (int i = tid; i < (n + 3) / 4; i += GT) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < (n + 31) / 32 + 1; i += GT) s.bits[i] = 0;
+        if (tid == 0) s.n_drafted = s.n_biased = 0;
+        len = len < 0 ? 0 : len > a.history.cap ? a.history.cap : len;
+        if (j0 < 0 || j1 > a.rules.n_bias || j1 < j0) j0 = j1 = 0;
+        const int32_t *text = a.history.tokens + (size_t)(told ? slot : 0) * a.history.cap;
+        const int4 *text4 = reinterpret_cast<const int4 *>(text);
+        const int from = sorted ? SORTED : 0;  // where the tokens that are read from there begin
+        const int fours = told && !sorted && (reinterpret_cast<uintptr_t>(text) & 15) == 0 ? len / 4 : 0;
+        const int4 none = make_int4(-1, -1, -1, -1);
+        int4 t4[FLIGHT];
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) t4[k] = tid + k * GT < fours ? text4[tid + k * GT] : none;
+        const int32_t biased = j0 + tid < j1 ? a.rules.bias_tokens[j0 + tid] : -1;
+        if (drafts && r0 + warp < r1) {
+            uint32_t on[HQ_MAX_M / 32] = {};
+            for (int node = r0 + warp; node > 0;) {
+                int p = up[0];
+#pragma unroll
+                for (int k = 0; k < HQ_MAX_M / 32; ++k) {
+                    if ((node >> 5) == k) {
+                        p = up[k];
+                        on[k] |= 1u << (node & 31);
+                    }
+                }
+                p = __shfl_sync(0xffffffffu, p, node & 31);
+                if (p < 0 || p >= node) break;
+                node = p;
+            }
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < HQ_MAX_M / 32; ++k) s.above[warp][k] = on[k];
+            }
         }
         __syncthreads();
-        if (use_rep || use_times) {
-            if (a.history.tokens && slot < a.history.n_slots) {
-                int len = a.history.len[slot];
-                len = len < 0 ? 0 : len > a.history.cap ? a.history.cap : len;
-                const int prompt = a.history.prompt ? a.history.prompt[slot] : 0;
-                const int32_t *text = a.history.tokens + (size_t)slot * a.history.cap;
-                auto count = [&](int32_t t, int p) {
-                    const uint32_t d = (uint32_t)t - (uint32_t)lo;
-                    if (d < (uint32_t)n) {
-                        if (p >= prompt) atomicAdd(&s_word[d], 1u);
-                        else atomicOr(&s_word[d], SEEN);
-                    }
-                };
-                int p = 0;
-                if ((reinterpret_cast<uintptr_t>(text) & 15) == 0) {
-                    const int4 *q = reinterpret_cast<const int4 *>(text);
-#pragma unroll 4
-                    for (int i = tid; i < len / 4; i += GT) {
-                        const int4 t = q[i];
-                        count(t.x, 4 * i);
-                        count(t.y, 4 * i + 1);
-                        count(t.z, 4 * i + 2);
-                        count(t.w, 4 * i + 3);
-                    }
-                    p = len / 4 * 4;
-                }
-#pragma unroll 4
-                for (int i = p + tid; i < len; i += GT) count(text[i], i);
+        if (sorted) pdl_wait();
+        const int32_t *mine = reinterpret_cast<const int32_t *>(a.workspace + record_at(b) + 16);
+        const int mine0 = sorted && told ? mine[SORTED + blockIdx.y] : 0, mine1 = sorted && told ? mine[SORTED + blockIdx.y + 1] : 0;
+        const uint32_t bits = smem_addr(s.bits), word = smem_addr(s.word);
+        // A rule reaches a token: `how` is set, or one time more is counted.  Without
+        // branches: in most warps some lane's token is in the chunk.
+        auto mark = [bits, word, lo, n](int32_t t, uint32_t how) {
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.or.b32 [%2], %3;\n\t@p red.shared.or.b32 [%4], %5;\n\t}" ::"r"(d),
+                "r"(n), "r"(word + 4 * d), "r"(how), "r"(bits + (d >> 3 & ~3u)), "r"(1u << (d & 31))
+                : "memory");
+        };
+        auto count = [bits, word, lo, n](int32_t t) {
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t@p red.shared.or.b32 [%3], %4;\n\t}" ::"r"(d),
+                "r"(n), "r"(word + 4 * d), "r"(bits + (d >> 3 & ~3u)), "r"(1u << (d & 31))
+                : "memory");
+        };
+        auto told_of = [&](int32_t t, bool prompts) {
+            if (prompts) mark(t, SEEN);
+            else count(t);
+        };
+        for (int i0 = tid; fours > 0;) {
+#pragma unroll
+            for (int k = 0; k < FLIGHT; ++k) {
+                const int at = 4 * (i0 + k * GT);
+                told_of(t4[k].x, at < prompt);
+                told_of(t4[k].y, at + 1 < prompt);
+                told_of(t4[k].z, at + 2 < prompt);
+                told_of(t4[k].w, at + 3 < prompt);
             }
-            if (a.tokens) {
-                for (int i = 1 + tid; i < m; i += GT) {
-                    const int32_t t = a.tokens[first + i];
-                    const uint32_t d = (uint32_t)t - (uint32_t)lo;
-                    if (d < (uint32_t)n) {
-                        const int at = atomicAdd(&s.n, 1);  // (any order: the entries are counted)
-                        s.node[at] = i;
-                        s.token[at] = t;
-                        atomicOr(&s_word[d], DRAFTED);
-                    }
-                }
-                for (int r = r0 + warp; r < r1; r += GT / 32) {
-                    int up[HQ_MAX_M / 32];
-                    uint32_t on[HQ_MAX_M / 32];
+            i0 += FLIGHT * GT;
+            if (i0 >= fours) break;
 #pragma unroll
-                    for (int k = 0; k < HQ_MAX_M / 32; ++k) {
-                        const int i = lane + 32 * k;
-                        up[k] = i > r ? -1 : a.parent ? a.parent[first + i] : i - 1;
-                        on[k] = 0;
-                    }
-                    for (int node = r; node > 0;) {
-                        int p = up[0];
+            for (int k = 0; k < FLIGHT; ++k) t4[k] = i0 + k * GT < fours ? text4[i0 + k * GT] : none;
+        }
+        for (int i = from + 4 * fours + tid; i < len; i += GT) told_of(text[i], i < prompt);
+        for (int i0 = mine0 + tid; i0 < mine1; i0 += 4 * FLIGHT * GT) {
+            int32_t t[4 * FLIGHT];
 #pragma unroll
-                        for (int k = 0; k < HQ_MAX_M / 32; ++k) {
-                            if ((node >> 5) == k) {
-                                p = up[k];
-                                on[k] |= 1u << (node & 31);
-                            }
-                        }
-                        p = __shfl_sync(0xffffffffu, p, node & 31);
-                        if (p < 0 || p >= node) break;
-                        node = p;
-                    }
-                    if (lane == 0) {
+            for (int k = 0; k < 4 * FLIGHT; ++k) t[k] = i0 + k * GT < mine1 ? mine[i0 + k * GT] : 0x7fffffff;
 #pragma unroll
-                        for (int k = 0; k < HQ_MAX_M / 32; ++k) s.above[r - r0][k] = on[k];
-                    }
-                }
-            }
+            for (int k = 0; k < 4 * FLIGHT; ++k) told_of(t[k] & 0x7fffffff, t[k] < 0);
+        }
+        mark(draft, DRAFTED);
+        if (draft >= lo && draft < lo + n) {
+            const int at = atomicAdd(&s.n_drafted, 1);  // (any order: the entries are counted)
+            s.node[at] = tid;
+            s.token[at] = draft;
         }
         for (int j = j0 + tid; j < j1; j += GT) {
-            const uint32_t d = (uint32_t)a.rules.bias_tokens[j] - (uint32_t)lo;
-            if (d < (uint32_t)n) s_bias[d] = 0;
+            const int32_t t = j == j0 + tid ? biased : a.rules.bias_tokens[j];
+            mark(t, BIASED);
+            if (t >= lo && t < lo + n) {
+                const int at = atomicAdd(&s.n_biased, 1);
+                if (at < BIASES) {
+                    s.bias_at[at] = j;
+                    s.bias_of[at] = (uint16_t)(t - lo);
+                }
+            }
         }
         __syncthreads();
-        for (int j = j0 + tid; j < j1; j += GT) {
-            const uint32_t d = (uint32_t)a.rules.bias_tokens[j] - (uint32_t)lo;
-            if (d < (uint32_t)n) {
-                atomicMax(&s_bias[d], (uint32_t)(j - j0 + 1));  // of a token listed twice the last one
-                atomicOr(&s_word[d], BIASED);
-            }
+        // the list: a word of bits a thread
+        static_assert(MOST / 32 <= GT, "a word of bits a thread");
+        uint32_t field = tid < (n + 31) / 32 ? s.bits[tid] : 0u;
+        int before = __popc(field);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
         }
+        if (lane == 31) s.counts[warp] = before;
+        before -= __popc(field);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < GT / 32; ++i) {
+            if (i < warp) before += s.counts[i];
+            listed_tokens += s.counts[i];
+        }
+        for (; field != 0; field &= field - 1) s.list[before++] = (uint16_t)(32 * tid + __ffs(field) - 1);
+        if (listed_tokens > 0) {
+            for (int i = tid; i < (r1 - r0) * (GT / 32); i += GT) s.list_order[i / (GT / 32)][i % (GT / 32)] = NONE;
+            __syncthreads();
+            for_list(listed_tokens, j0, j1);
+        }
+    } else {
         __syncthreads();
     }
-
-    // a logit that a rule reaches
-    auto adjust = [&](float l, uint32_t word, int d, int r) {
-        int times = (int)(word & TIMES);
-        if (word & DRAFTED)
-            for (int i = 0; i < s.n; ++i)
-                if (s.token[i] == lo + d && (s.above[r - r0][s.node[i] >> 5] >> (s.node[i] & 31) & 1u)) ++times;
-        if (use_rep && (times > 0 || (word & SEEN))) l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-        if (use_times && times > 0) {
-            if (a.rules.frequency) l = __fsub_rn(l, __fmul_rn(freq, (float)times));
-            if (a.rules.presence) l = __fsub_rn(l, pres);
-        }
-        if (word & BIASED) l = __fadd_rn(l, bias[s_bias[d] - 1]);
-        return l;
-    };
-
+    // The others.
     for (int r = r0; r < r1; ++r) {
-        const int row = first + r;
-        const T *x = static_cast<const T *>(a.logits) + (size_t)row * (size_t)a.ldl + lo;
-        O *out = a.out ? static_cast<O *>(a.out) + (size_t)row * (size_t)a.ldo + lo : nullptr;
-        const uint32_t *mask = nullptr;
-        if (a.rules.masks) {
-            const int id = a.mask_ids ? a.mask_ids[row] : row;
-            if (id >= 0 && id < a.rules.n_masks) mask = a.rules.masks + (size_t)id * (size_t)a.rules.ldmask + (lo >> 5);
-        }
-        float best = -INFINITY;
-        int token = -1;
-        auto take = [&](float l, int d) {  // d grows
-            if (token < 0 || l > best || (l != l && best == best)) {
-                best = l;
-                token = lo + d;
-            }
-        };
-        auto one = [&](int d) {
-            float l = to_f32(x[d]);
-            if (RULES && s_word[d]) l = adjust(l, s_word[d], d, r);
+        const T *x = logits_of(first + r);
+        O *out = out_of(first + r);
+        const uint32_t *mask = mask_of(r);
+        int best = NONE, at = INT_MAX;  // at: the first of the eight
+        auto one = [&](int d) {         // a logit outside the aligned eights
+            if (RULES && (s.bits[d >> 5] >> (d & 31) & 1u)) return;
+            const float l = to_f32(x[d]);
             const bool allowed = !mask || (mask[d >> 5] >> (d & 31) & 1u);
-            if (!allowed) l = -INFINITY;
-            if (out) out[d] = from_f32<O>(l);
-            if (allowed) take(l, d);
+            if (out) out[d] = from_f32<O>(allowed ? l : -INFINITY);
+            const int o = order_of(max_nan2(l, l));
+            if (allowed && o > best) {
+                best = o;
+                at = d;
+            }
         };
-        if ((reinterpret_cast<uintptr_t>(x) & (4 * sizeof(T) - 1)) == 0) {
-            const bool whole = out && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(O) - 1)) == 0;
-            for (int q0 = tid; q0 < n / 4; q0 += 4 * GT) {
-                Quad<T> v[4];
-                uint32_t bits[4];
+        const int head = head_of(x), eights = (n - head) / 8;
+        const bool whole = out && (reinterpret_cast<uintptr_t>(out + head) & 15) == 0;
+        uint32_t bits[EIGHTS];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int q = q0 + k * GT;
-                    bits[k] = 0xffffffffu;
-                    if (q < n / 4) {
-                        v[k] = reinterpret_cast<const Quad<T> *>(x)[q];
-                        if (mask) bits[k] = mask[q >> 3] >> (4 * (q & 7));
-                    }
-                }
+        for (int k = 0; k < EIGHTS; ++k) {
+            bits[k] = 0xffu;
+            if (mask && tid + k * GT < eights) bits[k] = eight_bits(mask, head + 8 * (tid + k * GT), head & 7);
+        }
+        if (tid < head) one(tid);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int q = q0 + k * GT, d = 4 * q;
-                    if (q >= n / 4) break;
-                    float l[4];
+        for (int k = 0; k < EIGHTS; ++k) {
+            const int d = head + 8 * (tid + k * GT);
+            if (tid + k * GT >= eights) break;
+            const uint32_t listed = RULES ? eight_bits(s.bits, d, head & 7) : 0u;
+            float l[8];
+            if (out) {
+                Oct<O> o;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) l[e] = to_f32(v[k].x[e]);
-                    if (RULES) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(s_word + d);
-                        if (w.x | w.y | w.z | w.w) {
-                            const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+                for (int e = 0; e < 8; ++e) o.x[e] = from_f32<O>((bits[k] >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY);
+                if (whole && listed == 0) {
+                    store(out + d, o);
+                } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (word[e]) l[e] = adjust(l[e], word[e], d + e, r);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!(bits[k] >> e & 1u)) l[e] = -INFINITY;
-                    if (out) {
-                        Quad<O> o;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o.x[e] = from_f32<O>(l[e]);
-                        if (whole) {
-                            reinterpret_cast<Quad<O> *>(out)[q] = o;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) out[d + e] = o.x[e];
-                        }
-                    }
-                    const float top = max_nan2(max_nan2(l[0], l[1]), max_nan2(l[2], l[3]));
-                    if (token < 0 || !(top <= best)) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (bits[k] >> e & 1u) take(l[e], d + e);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (!(listed >> e & 1u)) out[d + e] = o.x[e];
                 }
             }
-            for (int d = n / 4 * 4 + tid; d < n; d += GT) one(d);
-        } else {
-#pragma unroll 4
-            for (int d = tid; d < n; d += GT) one(d);
-        }
-        unsigned long long key = key_of(best, token);
+            const uint32_t use = bits[k] & ~listed;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
-            key = other > key ? other : key;
+            for (int e = 0; e < 8; ++e) l[e] = (use >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY;
+            const int o = order_of(max_nan3(max_nan3(l[0], l[1], l[2]), max_nan3(l[3], l[4], l[5]), max_nan2(l[6], l[7])));
+            if (use != 0 && o > best) {
+                best = o;
+                at = d;
+            }
         }
-        if (lane == 0) s.key[r - r0][warp] = key;
+        if (r + 1 < r1) fetch(r + 1);
+        const int d = head + 8 * eights + tid;
+        if (d < n) one(d);
+        const int most = __reduce_max_sync(0xffffffffu, best);
+        at = __reduce_min_sync(0xffffffffu, best == most ? at : INT_MAX);
+        if (lane == 0) {
+            s.order[r - r0][warp] = most;
+            s.at[r - r0][warp] = at;
+        }
     }
     __syncthreads();
-    if (tid < r1 - r0) {
-        const int row = first + r0 + tid;
-        unsigned long long key = s.key[tid][0];
+    if (tid >= r1 - r0) return;
+    const int row = first + r0 + tid;
+    int best = NONE, at = INT_MAX;
 #pragma unroll
-        for (int i = 1; i < GT / 32; ++i) key = s.key[tid][i] > key ? s.key[tid][i] : key;
-        if (gridDim.x > 1) {
-            atomicMax(&a.best[row], key);
-            __threadfence();
-            if (atomicInc(&a.done[row], gridDim.x - 1) != gridDim.x - 1) return;  // (the last one sets it to 0)
-            __threadfence();
-            key = atomicExch(&a.best[row], 0ull);
+    for (int i = 0; i < GT / 32; ++i) {
+        const int o = s.order[tid][i], d = s.at[tid][i];
+        if (o > best || (o == best && d < at)) {
+            best = o;
+            at = d;
         }
-        a.greedy[row] = token_of(key);
     }
+    if (best != NONE) {  // which of the eight (a logit that was taken by itself is the first)
+        const T *x = logits_of(row);
+        const uint32_t *mask = mask_of(r0 + tid);
+        float l[8];
+        uint32_t use[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int d = at + e < n ? at + e : at;
+            l[e] = to_f32(x[d]);
+            use[e] = mask ? mask[d >> 5] >> (d & 31) & 1u : 1u;
+            if (RULES) use[e] &= ~(s.bits[d >> 5] >> (d & 31));
+        }
+        int e = 0;
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+            if ((use[k] & 1u) && order_of(max_nan2(l[k], l[k])) == best) e = k;
+        at += e;
+    }
+    if (RULES && listed_tokens > 0) {
+#pragma unroll
+        for (int i = 0; i < GT / 32; ++i) {
+            const int o = s.list_order[tid][i], d = s.list_at[tid][i];
+            if (o > best || (o == best && d < at)) {
+                best = o;
+                at = d;
+            }
+        }
+    }
+    unsigned long long key = 0;  // below those of tokens
+    if (best != NONE)
+        key = ((unsigned long long)((uint32_t)best ^ 0x80000000u) << 32) | (0xFFFFFFFFu - (uint32_t)(lo + at));
+    if (gridDim.y > 1) {
+        // released by the ticket, which the last chunk acquires and sets to 0
+        unsigned long long *most = reinterpret_cast<unsigned long long *>(a.workspace + record_at(row));
+        unsigned before;
+        asm volatile("red.relaxed.gpu.global.max.u64 [%0], %1;" ::"l"(most), "l"(key) : "memory");
+        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(before) : "l"(most + 1), "r"(gridDim.y - 1) : "memory");
+        if (before != gridDim.y - 1) return;
+        key = atomicExch(most, 0ull);
+    }
+    a.greedy[row] = key == 0ull ? -1 : (int)(0xFFFFFFFFu - (uint32_t)key);
 }
 
 template <class T, class O>
 cudaError_t launch_t(const GreedyArgs &a, bool pdl, cudaStream_t s) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    int dev = 0, ready = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::atomic<int> set[CACHE_DEVICES];
-    e = cached_per_device(set, dev, &ready, [&](int *v) {
-        *v = 0;
-        return cudaFuncSetAttribute(k_greedy<T, O, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST * 4);
-    });
-    if (e != cudaSuccess) return e;
     const bool biased = a.rules.n_slots > 0 && a.rules.bias_starts && a.rules.n_bias > 0;
     const bool penalties = a.rules.n_slots > 0 && (a.rules.repetition || a.rules.presence || a.rules.frequency) &&
                            (a.history.tokens || a.tokens);
-    const int group = a.max_rows < GROUP ? a.max_rows : GROUP, groups = (a.max_rows + group - 1) / group;
-    int chunk = biased ? MOST / 2 : MOST;
-    while (chunk > LEAST && (long long)a.B * groups * ((a.V + chunk - 1) / chunk) < 4ll * sms) chunk /= 2;
-    const dim3 grid((unsigned)((a.V + chunk - 1) / chunk), (unsigned)groups, (unsigned)a.B);
-    if (biased || penalties)
-        return launch_kernel(k_greedy<T, O, true>, grid, dim3(GT), (size_t)chunk * (biased ? 8 : 4), pdl, s, a, chunk, group);
-    return launch_kernel(k_greedy<T, O, false>, grid, dim3(GT), 0, pdl, s, a, chunk, group);
+    // Chunks as large as leaves four blocks an SM, each row by itself (a token's row
+    // of 151552 in chunks of 1024 7.2 us); then two or four rows of a sequence to a
+    // block where there are more than 16 blocks an SM (eight trees of 16 nodes, V =
+    // 151552, chunks of 4096: one row a block 42 us, two 29.5, four 31.6; five
+    // sequences of 7 rows, V = 32003, chunks of 1024: 10.4, 12.0 and 14.7).
+    int shift = LEAST_SHIFT;
+    while ((1 << shift) < MOST && (long long)a.B * a.max_rows * ((a.V + (2 << shift) - 1) >> (shift + 1)) >= 4ll * sms) ++shift;
+    const int chunk = 1 << shift, chunks = (a.V + chunk - 1) >> shift;
+    int group = 1;
+    while (group < GROUP && group < a.max_rows && (long long)a.B * ((a.max_rows + group - 1) / group) * chunks > 16ll * sms) group *= 2;
+    const int groups = (a.max_rows + group - 1) / group;
+    const dim3 grid((unsigned)(a.B * groups), (unsigned)chunks);
+    if (!biased && !penalties)
+        return launch_kernel(k_greedy<T, O, false>, grid, dim3(GT), 0, pdl, s, a, chunk, group, false);
+    const bool sorted = penalties && a.history.tokens && a.B <= SORT_MOST && a.B <= a.rows && chunks < CHUNKS &&
+                        4ll * a.history.cap * a.B * groups * chunks > SORT_FROM;
+    if (sorted) {
+        const cudaError_t e = launch_kernel(k_sort_history, dim3((unsigned)a.B), dim3(ST), 0, pdl, s, a, shift, chunks);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(k_greedy<T, O, true>, grid, dim3(GT), 0, pdl || sorted, s, a, chunk, group, sorted);
 }
 
 }  // namespace
+
+size_t greedy_workspace_bytes(int rows) { return record_at(rows); }
 
 cudaError_t launch_greedy_tokens(const GreedyArgs &a, bool pdl, cudaStream_t s) {
     if (a.type == HQ_F32) return launch_t<float, float>(a, pdl, s);

@@ -1066,8 +1066,8 @@ def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, toke
     (parent None: a chain; tokens None: nothing drafted); seqs: its slots in
     history and rules (None: b).  mask_ids int32 [rows]: the row's mask, -1 none
     (None: mask r for row r).  out [rows][V] (the logits' type or fp32, or logits
-    itself): the adjusted logits.  workspace: zeroed once.  Returns greedy int32
-    [rows]."""
+    itself): the adjusted logits.  workspace: zeroed once, of at least these
+    rows' size.  Returns greedy int32 [rows]."""
     rows, V = logits.shape
     B = _batch(None, rows, starts, max_rows, seqs, "greedy_tokens: starts and seqs")
     ty = TYPES.get(logits.dtype)
