@@ -6,7 +6,13 @@
 //   sx = max|z| / sqrt(32) / 127,  qx = rint(127 z / max|z|)
 //
 // A head is 8, 16 or 32 lanes of 8 features, so the norm is lane exchanges and
-// needs no barrier; only the codes need the row's largest value.
+// needs no barrier; only the codes need the row's largest value.  So h alone is one
+// long list of octets over resident blocks, bound by memory and, nearly, by
+// instructions: 8190 rows of 8192, all bf16, with a silu gate 74 us = 5.4 TB/s.  On
+// the way there: an exact division and expf per gate 112 us; the quotient by the
+// approximate reciprocal and the types known at compile time 83.  One, two and four
+// octets a thread on their way 76, 74 and 94 us (registers end the fourth block an
+// SM); five blocks an SM 88.  With codes a row is one block and one chain of waits.
 #include "rows.cuh"
 
 namespace hq {
@@ -14,27 +20,44 @@ namespace {
 
 constexpr float MAX_LEAST = 0x1p-110f;  // below it a row's largest |z| is formed again
 
+// 1 / (1 + e^-g) in eight instructions, two of them of the special unit: expf and a
+// division with their care for subnormal results take 25 and bound the kernel.  e^-g
+// = 2^t (1 + r ln 2), t = -g log2(e) as it is rounded and r what that left out (NaN
+// for infinite g: the maximum takes the bound instead).  The power is off by 2^-22,
+// the reciprocal by one unit in the last place; a quotient below 2^-126 is 0.
+__device__ __forceinline__ float sigmoid(float g) {
+    constexpr float L = -1.4426950408889634f, LN2 = 0.6931471805599453f;
+    const float t = g * L, r = fmaf(g, L, -t);
+    float p, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + p * fmaxf(fmaf(r, LN2, 1.0f), 0.99f)));
+    return q;
+}
 __device__ __forceinline__ float gated(float y, float g, int act) {
-    if (act == HQ_GATE_NONE) return y * g;
-    const float e = 1.0f / (1.0f + expf(-g));
-    return act == HQ_GATE_SILU ? y * (g * e) : y * e;
+    return act == HQ_GATE_NONE ? y * g : act == HQ_GATE_SILU ? y * (g * sigmoid(g)) : y * sigmoid(g);
+}
+
+// 8 weights of a head, 1 each where there are none.
+template <int U>
+__device__ __forceinline__ void load_weight(const GateArgs &a, int idx, float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (a.n.weight) widen(load_raw(a.n.weight, HQ_F32, idx % U), HQ_F32, w);
 }
 
 // 8 features of y: head normed, weighted, gated.
 template <int U>
-__device__ __forceinline__ void form(const GateArgs &a, const Raw &rx, const Raw &rg, int idx, float (&y)[8]) {
-    widen(rx, a.n.x_type, y);
+__device__ __forceinline__ void form(const GateArgs &a, const Raw &rx, int x_type, const Raw &rg, int g_type, const float (&w)[8],
+                                     float (&y)[8]) {
+    widen(rx, x_type, y);
     if (a.n.weight) {
         head_norm<U>(y, a.n.eps);
-        const float4 *w = reinterpret_cast<const float4 *>(a.n.weight) + 2 * (idx % U);
-        const float4 p = w[0], q = w[1];
-        const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= f[i];
+        for (int i = 0; i < 8; ++i) y[i] *= w[i];
     }
     if (a.gate) {
         float g[8];
-        widen(rg, a.g_type, g);
+        widen(rg, g_type, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = gated(y[i], g[i], a.act);
     }
@@ -44,14 +67,19 @@ __device__ __forceinline__ void form(const GateArgs &a, const Raw &rx, const Raw
 constexpr int FT = 256;    // threads
 constexpr int FLIGHT = 2;  // octets of a thread on their way together
 
-template <int U>
-__global__ void __launch_bounds__(FT) k_gate_heads(const GateArgs a) {
+// XT, GT: the types of x, and of gate and h, where they are known at compile time
+// (else -1).
+template <int U, int XT, int GT>
+__global__ void __launch_bounds__(FT, 4) k_gate_heads(const GateArgs a) {
     pdl_launch_dependents();
     pdl_wait();
+    const int x_type = XT >= 0 ? XT : a.n.x_type, g_type = GT >= 0 ? GT : a.g_type, h_type = GT >= 0 ? GT : a.n.h_type;
     const int n8 = a.n.K / 8, step = gridDim.x * FT;  // (at most 2^20 blocks)
     const long long total = (long long)a.n.M * n8, start = (long long)blockIdx.x * FT + threadIdx.x;
     long long row = start / n8;
     int idx = (int)(start % n8);
+    float w[8];  // (steps are whole heads: the thread's features keep their place)
+    load_weight<U>(a, idx, w);
     const int rows_on = step / n8, idx_on = step % n8;
     // A warp's 32 octets start at a multiple of 32; n8 is a multiple of 8, so the
     // last warp may have heads that are not there.
@@ -64,8 +92,8 @@ __global__ void __launch_bounds__(FT) k_gate_heads(const GateArgs a) {
             rows[k] = row < a.n.M ? (int)row : -1;
             at[k] = idx;
             if (rows[k] >= 0) {
-                x[k] = load_raw(row_of(a.n.x, a.n.x_type, a.n.ldx, rows[k]), a.n.x_type, idx);
-                if (a.gate) g[k] = load_raw(row_of(a.gate, a.g_type, a.ldg, rows[k]), a.g_type, idx);
+                x[k] = load_raw(row_of(a.n.x, x_type, a.n.ldx, rows[k]), x_type, idx);
+                if (a.gate) g[k] = load_raw(row_of(a.gate, g_type, a.ldg, rows[k]), g_type, idx);
             }
             row += rows_on;
             idx += idx_on;
@@ -77,8 +105,8 @@ __global__ void __launch_bounds__(FT) k_gate_heads(const GateArgs a) {
 #pragma unroll
         for (int k = 0; k < FLIGHT; ++k) {
             float y[8];
-            form<U>(a, x[k], g[k], at[k], y);
-            if (rows[k] >= 0) store8(const_cast<void *>(row_of(a.n.h, a.n.h_type, a.n.ldh, rows[k])), a.n.h_type, at[k], y);
+            form<U>(a, x[k], x_type, g[k], g_type, w, y);
+            if (rows[k] >= 0) store8(const_cast<void *>(row_of(a.n.h, h_type, a.n.ldh, rows[k])), h_type, at[k], y);
         }
     }
 }
@@ -122,7 +150,9 @@ __global__ void __launch_bounds__(T) k_gate_row(const GateArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int idx = tid + j * T;
-        form<U>(a, x[j], g[j], idx, y[j]);
+        float w[8];
+        load_weight<U>(a, idx, w);
+        form<U>(a, x[j], a.n.x_type, g[j], a.g_type, w, y[j]);
         if (idx < n8 && a.n.h) store8(const_cast<void *>(row_of(a.n.h, a.n.h_type, a.n.ldh, row)), a.n.h_type, idx, y[j]);
         const uint32_t sg = idx < n8 ? (__ldg(a.n.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu : 0u;
 #pragma unroll
@@ -176,7 +206,13 @@ cudaError_t launch_u(const GateArgs &a, bool pdl, cudaStream_t s) {
         const int sms = device_sm_count();
         if (sms <= 0) return cudaErrorNoDevice;
         const long long blocks = ((long long)a.n.M * n8 + FT * FLIGHT - 1) / (FT * FLIGHT), most = 8ll * sms;
-        return launch_kernel(k_gate_heads<U>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(FT), 0, pdl, s, a);
+        const bool one = a.gate && a.g_type == a.n.h_type && a.g_type != HQ_F32, wide = a.n.x_type == HQ_F32;
+        auto f = k_gate_heads<U, -1, -1>;
+        if (one && a.g_type == HQ_F16 && (wide || a.n.x_type == HQ_F16))
+            f = wide ? k_gate_heads<U, HQ_F32, HQ_F16> : k_gate_heads<U, HQ_F16, HQ_F16>;
+        else if (one && a.g_type == HQ_BF16 && (wide || a.n.x_type == HQ_BF16))
+            f = wide ? k_gate_heads<U, HQ_F32, HQ_BF16> : k_gate_heads<U, HQ_BF16, HQ_BF16>;
+        return launch_kernel(f, dim3((unsigned)(blocks < most ? blocks : most)), dim3(FT), 0, pdl, s, a);
     }
     const dim3 grid((unsigned)(a.n.qop ? act_rows(a.n.M) : a.n.M));
     // A row's octets over as many threads as it has, two a thread from 4096
