@@ -590,6 +590,15 @@ def _pitch(t, cols: int, what: str) -> int:
     return cols if t is None or t.is_contiguous() else _rows(t, cols, what)
 
 
+def _heads(t, dim: int, what: str) -> int:
+    """The distance in elements between the rows of a tensor [rows][heads][dim] whose rows are contiguous."""
+    rows, heads, _ = t.shape
+    ld, of_head, one = t.stride()
+    if one != 1 or (of_head != dim and heads != 1):
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return ld if rows > 1 else heads * dim
+
+
 def _dense(t, dtype, shape, what: str) -> None:
     """A contiguous tensor of the given type and shape, or None."""
     if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
@@ -924,17 +933,17 @@ def rope_write(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, k
     (int32 [rows]), or its sequence's length before these rows plus its depth in
     the tree of `parent` (None: a chain).  Returns out [rows][Hq][dim] of the
     cache's type (may be q itself)."""
-    shape = q.shape
+    shape, heads, dtype = q.shape, cache.heads, q.dtype
     rows, Hq, D = shape
-    heads = cache.heads
     if D != cache.dim or k.shape != (rows, heads, D) or v.shape != k.shape:
         raise ValueError(f"rope_write: q [rows][heads][{cache.dim}], k and v [rows][{heads}][{cache.dim}] expected, got "
                          f"{tuple(shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("rope_write: q, k and v need the same type")
-    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+    if turns.dtype is not torch.int64 or len(turns.shape) != 1 or not turns.is_contiguous():
         raise ValueError(f"rope_write: turns must be contiguous int64 [pairs], got {turns.dtype} {tuple(turns.shape)}")
-    if layout not in ROPE_LAYOUTS:
+    side = ROPE_LAYOUTS.get(layout)
+    if side is None:
         raise ValueError(f"rope_write: layout must be one of {', '.join(ROPE_LAYOUTS)}, got {layout!r}")
     B = _batch(cache.n_seqs, rows, starts, max_rows, seqs, "rope_write: starts and seqs")
     if parent is not None:
@@ -947,13 +956,12 @@ def rope_write(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, k
         _dense(k_weight, torch.float32, (D,), "rope_write: k_weight")
     if out is None:
         out = _new(shape, cache.pool.dtype, q.device, stream)
-    elif out.shape != shape or out.dtype != cache.pool.dtype:
+    elif out.shape != shape or out.dtype is not cache.pool.dtype:
         raise ValueError(f"rope_write: out must be {cache.pool.dtype} {list(shape)}")
-    cols, kcols = Hq * D, heads * D
-    rc = load().hq_rope_write(cache.c, k_plane, v_plane, cache.type, _ptr(q), _ptr(k), _ptr(v), _type(q), _rows(q, cols, "q"),
-                              _rows(k, kcols, "k"), _rows(v, kcols, "v"), Hq, _ptr(q_weight), _ptr(k_weight), eps, _ptr(turns),
-                              2 * turns.shape[0], ROPE_LAYOUTS[layout], gain, _ptr(seqs), _ptr(starts), B, rows, max_rows,
-                              _ptr(parent), _ptr(positions), _ptr(out), _rows(out, cols, "out"), flags, _stream(stream))
+    rc = load().hq_rope_write(cache.c, k_plane, v_plane, cache.type, _ptr(q), _ptr(k), _ptr(v), _type(q), _heads(q, D, "q"),
+                              _heads(k, D, "k"), _heads(v, D, "v"), Hq, _ptr(q_weight), _ptr(k_weight), eps, _ptr(turns),
+                              2 * turns.shape[0], side, gain, _ptr(seqs), _ptr(starts), B, rows, max_rows, _ptr(parent),
+                              _ptr(positions), _ptr(out), _heads(out, D, "out"), flags, _stream(stream))
     if rc != HQ_OK:
         raise HQError(rc, "hq_rope_write")
     return out

@@ -201,6 +201,21 @@ def test_many_sequences_some_without_rows(B):
     check(r, out, turns)
 
 
+@pytest.mark.parametrize("it,dt,layout,norm", [(BF16, BF16, "half", False), (F32, F16, "interleaved", True), (F16, F16, "half", True),
+                                                (F32, BF16, "half", False)])
+def test_prompts_of_many_rows(it, dt, layout, norm):
+    """Enough rows for the kernel that takes few threads a row."""
+    rows, before = [1500, 3, 0, 1400], [0, 40, 0, 17]
+    r = Rows(before, rows, 3, 1, 64, 64, it, dt, seed=17, pad=8, gap=1)
+    turns, w = hq.rope_turns(hq.rope_freqs(48), DEV), torch.rand(64, device=DEV) + 0.5 if norm else None
+    out = Guarded(tuple(r.q.shape), dt, DEV, fill=7.0)
+    hq.rope_write(r.cache, 0, 1, r.q, r.k, r.v, turns, ints(r.starts), 1500, layout, q_weight=w, k_weight=w, out=out.t)
+    torch.cuda.synchronize()
+    out.check()
+    assert bool((out.t[-1] == 7.0).all())
+    check(r, out.t, turns, layout, qw=w, kw=w)
+
+
 def test_equal_rows_without_starts_and_rows_past_max_rows():
     r = Rows([5, 6, 7], [4, 4, 4], 2, 1, 64, 16, F32, F16, seed=8)
     turns = hq.rope_turns(hq.rope_freqs(64), DEV)
