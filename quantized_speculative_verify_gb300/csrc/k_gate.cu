@@ -12,7 +12,11 @@
 // the way there: an exact division and expf per gate 112 us; the quotient by the
 // approximate reciprocal and the types known at compile time 83.  One, two and four
 // octets a thread on their way 76, 74 and 94 us (registers end the fourth block an
-// SM); five blocks an SM 88.  With codes a row is one block and one chain of waits.
+// SM); five blocks an SM 88.  With codes few rows are one chain of waits (128 rows of
+// 8192 4.3 us, 3.1 of which one row of 4096 takes), many are bound by instructions:
+// 8190 rows of 8192 in bf16 111 us = 4.2 TB/s.  On the way there: a block per row 213;
+// resident blocks with the next row's loads ahead 138; weights and signs in registers
+// 130; types known at compile time 111 (a thread holds one octet, else registers spill).
 #include "rows.cuh"
 
 namespace hq {
@@ -45,13 +49,14 @@ __device__ __forceinline__ void load_weight(const GateArgs &a, int idx, float (&
     if (a.n.weight) widen(load_raw(a.n.weight, HQ_F32, idx % U), HQ_F32, w);
 }
 
-// 8 features of y: head normed, weighted, gated.
-template <int U>
+// 8 features of y: head normed, weighted (ALWAYS: where there is no norm too),
+// gated.
+template <int U, bool ALWAYS = false>
 __device__ __forceinline__ void form(const GateArgs &a, const Raw &rx, int x_type, const Raw &rg, int g_type, const float (&w)[8],
                                      float (&y)[8]) {
     widen(rx, x_type, y);
-    if (a.n.weight) {
-        head_norm<U>(y, a.n.eps);
+    if (a.n.weight) head_norm<U>(y, a.n.eps);
+    if (ALWAYS || a.n.weight) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] *= w[i];
     }
@@ -111,92 +116,138 @@ __global__ void __launch_bounds__(FT, 4) k_gate_heads(const GateArgs a) {
     }
 }
 
-// The largest of the block's values; NaN if one is.  Every thread calls.
+// The largest of the block's values; NaN if one is.  Every thread calls; s_max is
+// not in use by another call before the next barrier.
 template <int T>
 __device__ __forceinline__ float block_max(float x, float *s_max) {
     x = warp_max(x);
-    __syncthreads();  // (what was read there before)
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = x;
     __syncthreads();
     return warp_max((threadIdx.x & 31) < T / 32 ? s_max[threadIdx.x & 31] : 0.0f);
 }
 
-// h and codes: a thread block per row.
-template <int U, int V, int T>
-__global__ void __launch_bounds__(T) k_gate_row(const GateArgs a) {
-    __shared__ float s_max[T / 32];
+// h and codes.  ROWS: resident blocks take rows in turn, the next one's loads on
+// their way while this one is rotated, reduced and written (no operand); else a
+// block per row of the operand or the codes.  XT, GT as above.
+template <int U, int V, int T, bool ROWS, int XT = -1, int GT = -1>
+__global__ void __launch_bounds__(T, 1024 / T) k_gate_row(const GateArgs a) {
+    const int x_type = XT >= 0 ? XT : a.n.x_type, g_type = GT >= 0 ? GT : a.g_type, h_type = GT >= 0 ? GT : a.n.h_type;
+    __shared__ float s_max[2][T / 32], s_far[2][T / 32];  // by the row's turn; for rows of unusual size
     __shared__ int s_gs[MAX_K / 16];  // group sums of this row
     pdl_launch_dependents();
     pdl_wait();
-    const int row = blockIdx.x, MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+    const int MT = gridDim.x, tid = threadIdx.x, lane = tid & 31;
+    int row = blockIdx.x, turn = 0;
     const int K = a.n.K, n8 = K / 8;
-    const Codes<true> codes(a.n, K, a.n.G, MT, s_gs);
-    if (row >= a.n.M) {  // padding row of the operand
+    const Codes<!ROWS> codes(a.n, K, a.n.G, MT, s_gs);
+    if (!ROWS && row >= a.n.M) {  // padding row of the operand
         codes.template pad<T>(row);
         return;
     }
     Raw x[V], g[V];
+    auto fetch = [&](int row) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-        x[j] = g[j] = Raw{};
-        if (idx < n8) {
-            x[j] = load_raw(row_of(a.n.x, a.n.x_type, a.n.ldx, row), a.n.x_type, idx);
-            if (a.gate) g[j] = load_raw(row_of(a.gate, a.g_type, a.ldg, row), a.g_type, idx);
-        }
-    }
-    if (codes.sums) codes.template clear_sums<T>();
-    float y[V][8], z[V][8], amax = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int idx = tid + j * T;
-        float w[8];
-        load_weight<U>(a, idx, w);
-        form<U>(a, x[j], a.n.x_type, g[j], a.g_type, w, y[j]);
-        if (idx < n8 && a.n.h) store8(const_cast<void *>(row_of(a.n.h, a.n.h_type, a.n.ldh, row)), a.n.h_type, idx, y[j]);
-        const uint32_t sg = idx < n8 ? (__ldg(a.n.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu : 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[j][i] = y[j][i] = flip(y[j][i], (sg >> i) & 1u);
-        rotate8(z[j], lane);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
-    }
-    amax = block_max<T>(amax, s_max);
-    float up = 1.0f, more = 1.0f;
-    if (!(amax >= MAX_LEAST && amax < INFINITY) && amax != 0.0f) {
-        // sums of the rotation, or quotients by the largest, leave fp32's range: in
-        // units of 2^e, the power of two above the row's largest |y|
-        float top = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(y[j][i]));
-        top = block_max<T>(top, s_max);
-        if (top > 0.0f && top < INFINITY) {
-            const bool small = top < 0x1p-60f;
-            const int e = (__float_as_int(small ? top * 0x1p80f : top) >> 23) - (small ? 206 : 126), half = e / 2;
-            const float down = __int_as_float((127 - half) << 23), rest = __int_as_float((127 - e + half) << 23);
-            up = __int_as_float((127 + half) << 23);
-            more = __int_as_float((127 + e - half) << 23);
-            amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[j][i] = y[j][i] * down * rest;
-                rotate8(z[j], lane);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
+        for (int j = 0; j < V; ++j) {
+            const int idx = tid + j * T;
+            x[j] = g[j] = Raw{};
+            if (idx < n8) {
+                x[j] = load_raw(row_of(a.n.x, x_type, a.n.ldx, row), x_type, idx);
+                if (a.gate) g[j] = load_raw(row_of(a.gate, g_type, a.ldg, row), g_type, idx);
             }
-            amax = block_max<T>(amax, s_max);
         }
-    }
-    if (tid == 0) a.n.sx[row] = amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f * up * more;
-    // no codes of zeros, and of rows with an infinity or NaN: 0 * infinity and NaN round to 0
-    const float inv = amax > 0.0f ? 127.0f / amax : 0.0f;
-    int8_t *qr = a.n.qx ? a.n.qx + (size_t)row * K : nullptr;
+    };
+    fetch(row);
+    // the weights with the features' signs: what leaves the gate is what is rotated,
+    // and h takes the sign back
+    float w[V][8];
+    uint32_t sg[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) codes.write(row, qr, tid + j * T, z[j], inv);
-    codes.template write_sums<T>(row);
+    for (int j = 0; j < V; ++j) {
+        const int idx = tid + j * T;
+        sg[j] = idx < n8 ? (__ldg(a.n.signs + (idx >> 2)) >> ((idx & 3) * 8)) & 0xffu : 0u;
+        load_weight<U>(a, idx, w[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[j][i] = flip(w[j][i], (sg[j] >> i) & 1u);
+    }
+    for (; row < a.n.M; row += MT, turn ^= 1) {
+        if (codes.sums) {
+            if (ROWS) __syncthreads();  // the last row's sums have been read
+            codes.template clear_sums<T>();
+        }
+        float y[V][8], z[V][8], amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            form<U, true>(a, x[j], x_type, g[j], g_type, w[j], y[j]);
+        }
+        if (ROWS && row + MT < a.n.M) fetch(row + MT);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int idx = tid + j * T;
+            if (idx < n8 && a.n.h) store8(const_cast<void *>(row_of(a.n.h, h_type, a.n.ldh, row)), h_type, idx, y[j], sg[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[j][i] = y[j][i];
+            rotate8(z[j], lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
+        }
+        amax = block_max<T>(amax, s_max[turn]);
+        float up = 1.0f, more = 1.0f;
+        if (!(amax >= MAX_LEAST && amax < INFINITY) && amax != 0.0f) {
+            // sums of the rotation, or quotients by the largest, leave fp32's range: in
+            // units of 2^e, the power of two above the row's largest |y|
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(y[j][i]));
+            top = block_max<T>(top, s_far[0]);
+            if (top > 0.0f && top < INFINITY) {
+                const bool small = top < 0x1p-60f;
+                const int e = (__float_as_int(small ? top * 0x1p80f : top) >> 23) - (small ? 206 : 126), half = e / 2;
+                const float down = __int_as_float((127 - half) << 23), rest = __int_as_float((127 - e + half) << 23);
+                up = __int_as_float((127 + half) << 23);
+                more = __int_as_float((127 + e - half) << 23);
+                amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[j][i] = y[j][i] * down * rest;
+                    rotate8(z[j], lane);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(z[j][i]));
+                }
+                amax = block_max<T>(amax, s_far[1]);
+            }
+        }
+        if (tid == 0) a.n.sx[row] = amax * __int_as_float((int)HADAMARD_SCALE_BITS) / 127.0f * up * more;
+        // no codes of zeros, and of rows with an infinity or NaN: 0 * infinity and NaN round to 0
+        const float inv = amax > 0.0f ? 127.0f / amax : 0.0f;
+        int8_t *qr = a.n.qx ? a.n.qx + (size_t)row * K : nullptr;
+#pragma unroll
+        for (int j = 0; j < V; ++j) codes.write(row, qr, tid + j * T, z[j], inv);
+        codes.template write_sums<T>(row);
+        if (!ROWS) break;
+    }
+}
+
+template <int U, int V, int T>
+cudaError_t launch_rows(const GateArgs &a, bool pdl, cudaStream_t s) {
+    if (a.n.qop) return launch_kernel(k_gate_row<U, V, T, false>, dim3((unsigned)act_rows(a.n.M)), dim3(T), 0, pdl, s, a);
+    if constexpr (V * T > 2048) {
+        return launch_kernel(k_gate_row<U, V, T, false>, dim3((unsigned)a.n.M), dim3(T), 0, pdl, s, a);
+    } else {
+        const int sms = device_sm_count(), most = sms * (1024 / T);
+        if (sms <= 0) return cudaErrorNoDevice;
+        auto f = k_gate_row<U, V, T, true>;
+        if constexpr (V * T == 512 || V * T == 1024) {
+            const bool one = a.gate && a.g_type != HQ_F32 && (!a.n.h || a.g_type == a.n.h_type), wide = a.n.x_type == HQ_F32;
+            if (one && a.g_type == HQ_F16 && (wide || a.n.x_type == HQ_F16))
+                f = wide ? k_gate_row<U, V, T, true, HQ_F32, HQ_F16> : k_gate_row<U, V, T, true, HQ_F16, HQ_F16>;
+            else if (one && a.g_type == HQ_BF16 && (wide || a.n.x_type == HQ_BF16))
+                f = wide ? k_gate_row<U, V, T, true, HQ_F32, HQ_BF16> : k_gate_row<U, V, T, true, HQ_BF16, HQ_BF16>;
+        }
+        return launch_kernel(f, dim3((unsigned)(a.n.M < most ? a.n.M : most)), dim3(T), 0, pdl, s, a);
+    }
 }
 
 template <int U>
@@ -214,17 +265,16 @@ cudaError_t launch_u(const GateArgs &a, bool pdl, cudaStream_t s) {
             f = wide ? k_gate_heads<U, HQ_F32, HQ_BF16> : k_gate_heads<U, HQ_BF16, HQ_BF16>;
         return launch_kernel(f, dim3((unsigned)(blocks < most ? blocks : most)), dim3(FT), 0, pdl, s, a);
     }
-    const dim3 grid((unsigned)(a.n.qop ? act_rows(a.n.M) : a.n.M));
-    // A row's octets over as many threads as it has, two a thread from 4096
-    // features on.  Every V * T is a multiple of 16 octets, so the operand's padding
-    // up to whole 128-feature blocks is covered too.
-    if (n8 <= 128) return launch_kernel(k_gate_row<U, 1, 128>, grid, dim3(128), 0, pdl, s, a);
-    if (n8 <= 256) return launch_kernel(k_gate_row<U, 1, 256>, grid, dim3(256), 0, pdl, s, a);
-    if (n8 <= 512) return launch_kernel(k_gate_row<U, 1, 512>, grid, dim3(512), 0, pdl, s, a);
-    if (n8 <= 1024) return launch_kernel(k_gate_row<U, 2, 512>, grid, dim3(512), 0, pdl, s, a);
-    if (n8 <= 2048) return launch_kernel(k_gate_row<U, 2, 1024>, grid, dim3(1024), 0, pdl, s, a);
-    if (n8 <= 4096) return launch_kernel(k_gate_row<U, 4, 1024>, grid, dim3(1024), 0, pdl, s, a);
-    return launch_kernel(k_gate_row<U, 8, 1024>, grid, dim3(1024), 0, pdl, s, a);
+    // As many threads as a row has octets, up to 1024.  Every V * T is a multiple of
+    // 16 octets, so the operand's padding up to whole 128-feature blocks is covered
+    // too.
+    if (n8 <= 128) return launch_rows<U, 1, 128>(a, pdl, s);
+    if (n8 <= 256) return launch_rows<U, 1, 256>(a, pdl, s);
+    if (n8 <= 512) return launch_rows<U, 1, 512>(a, pdl, s);
+    if (n8 <= 1024) return launch_rows<U, 1, 1024>(a, pdl, s);
+    if (n8 <= 2048) return launch_rows<U, 2, 1024>(a, pdl, s);
+    if (n8 <= 4096) return launch_rows<U, 4, 1024>(a, pdl, s);
+    return launch_rows<U, 8, 1024>(a, pdl, s);
 }
 
 }  // namespace

@@ -108,15 +108,21 @@ def test_gated_norm_matches_64_bits(M, K, D, G, fmt, xt, gt, ht, act, norm):
 
 
 @pytest.mark.parametrize("M,K,D,xt,gt,ht", [(1, 64, 64, F32, F32, BF16), (7, 192, 64, F16, F16, F16), (1000, 4096, 128, BF16, BF16, BF16),
-                                            (3001, 1024, 256, F32, BF16, BF16), (257, 8192, 128, F32, F32, F32), (4000, 704, 64, BF16, F32, F16)])
+                                            (3001, 1024, 256, F32, BF16, BF16), (257, 8192, 128, F32, F32, F32), (4000, 704, 64, BF16, F32, F16),
+                                            (400, 8192, 128, F16, F16, F16), (500, 8192, 256, F32, BF16, BF16), (700, 2560, 64, F32, F16, F16),
+                                            (1300, 4096, 64, F16, F16, F32), (333, 16384, 128, BF16, BF16, BF16), (400, 8192, 64, BF16, BF16, BF16)])
 @pytest.mark.parametrize("codes", [False, True])
 def test_many_rows(M, K, D, xt, gt, ht, codes):
     x, gate, w, signs = make(M, K, D, xt, gt, seed=M, pad=16)
     d = hq.make_desc(K, 128, 32, "w4")
     h = torch.full((M, K + 8), 7.0, dtype=ht, device=DEV)
     qx, sx = (Guarded((M, K), torch.int8, DEV), Guarded((M,), F32, DEV)) if codes else (None, None)
-    hq.gated_norm_quant(d, x, gate, w, signs_dev(signs), D, "silu", 1e-6, h=h[:, :K], qx=qx and qx.t, sx=sx and sx.t)
+    gs = Guarded((M, K // 32), torch.int32, DEV) if codes else None
+    hq.gated_norm_quant(d, x, gate, w, signs_dev(signs), D, "silu", 1e-6, h=h[:, :K], qx=qx and qx.t, gsum=gs and gs.t, sx=sx and sx.t)
     torch.cuda.synchronize()
+    if codes:
+        gs.check()
+        assert torch.equal(gs.t, qx.t.view(M, K // 32, 32).to(torch.int32).sum(2, dtype=torch.int32))
     assert bool((h[:, K:] == 7.0).all())
     check(value(x, gate, w, D, "silu", 1e-6), signs, h[:, :K], qx and qx.t, sx and sx.t)
     for t in (qx, sx):
@@ -149,6 +155,22 @@ def test_heads_of_any_size(D, eps):
     h, qx, sx = torch.empty((3, K), device=DEV), torch.empty((3, K), dtype=torch.int8, device=DEV), torch.empty(3, device=DEV)
     hq.gated_norm_quant(hq.make_desc(K, 128, 32, "w4"), x, gate, w, signs_dev(signs), D, "silu", eps, h=h, qx=qx, sx=sx)
     check(value(x, gate, w, D, "silu", eps), signs, h, qx, sx)
+
+
+def test_rows_of_any_size_among_many():
+    """Rows whose codes are formed in other units, and rows that are not finite, between common ones of the same block."""
+    M, K, D = 500, 8192, 128
+    x, gate, w, signs = make(M, K, D, F32, BF16, seed=9)
+    scale = torch.ones(M, device=DEV)
+    scale[::7], scale[3::11], scale[5::13] = 1e-36, 1e30, 0.0
+    x = (x.double().clamp(-4, 4) * scale.unsqueeze(1)).float()
+    bad = list(range(6, M, 29))
+    x[bad, 17] = float("inf")
+    qx, sx = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    hq.gated_norm_quant(hq.make_desc(K, 128, 32, "w4"), x, gate, None, signs_dev(signs), D, "none", 0.0, qx=qx, sx=sx)
+    rows = [r for r in range(M) if r not in bad]
+    check(value(x[rows], gate[rows], None, D, "none", 0.0), signs, None, qx[rows], sx[rows])
+    assert not bool(torch.isfinite(sx[bad]).any()) and not bool(qx[bad].any())
 
 
 @pytest.mark.parametrize("size", [0.0, 1e-44, 1e-40, 1e-37, 1e-33, 1e-20, 1.0, 1e30, 4e37])

@@ -325,6 +325,33 @@ def test_starts_that_are_not_ascending_leave_the_workspace_usable(starts):
     r.check(greedy.t, None)
 
 
+def test_a_captured_call_with_long_histories():
+    """Two kernels: the histories sorted by token, then the logits."""
+    rows, V, ws = [1] * 64, 60000, torch.zeros(hq.hq_greedy_tokens_workspace_bytes(64), dtype=torch.uint8, device=DEV)
+    r = Request(rows, V, seed=21, history=15000, near=V)
+    kw = r.device()
+    starts, _ = kw.pop("starts"), kw.pop("max_rows")
+    x, greedy = r.x.to(DEV), torch.empty(64, dtype=torch.int32, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    hq.greedy_tokens(x, starts, 1, greedy=greedy, workspace=ws, stream=s, **kw)
+    s.synchronize()
+    r.check(greedy, None)
+    for flags in (hq.HQ_LAUNCH_DEFAULT, hq.HQ_LAUNCH_PDL):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(2):  # the second sorts into what the first has read
+                hq.greedy_tokens(x, starts, 1, greedy=greedy, workspace=ws, flags=flags, **kw)
+        n = Request(rows, V, seed=22 + flags, history=15000, near=V)
+        r.len, r.text = n.len, n.text
+        r.history.lens.copy_(torch.from_numpy(n.len))
+        r.history.tokens.copy_(torch.from_numpy(n.text))
+        graph.replay()
+        torch.cuda.synchronize()
+        r.check(greedy, None)
+        assert counters(ws, 64) == 0
+
+
 def test_a_captured_call_follows_its_inputs_and_streams():
     r = Request([3, 4], 30000, seed=17)
     kw = r.device()
