@@ -19,9 +19,19 @@
 //
 // A block is a chain of waits (its sequence, the history's length, the history, the
 // list's logits, the ticket at the end), 6 us of them for 16 KB of logits, so the
-// chunks are small enough for seven blocks an SM.  Frequent tokens have low
+// chunks are small enough for six blocks an SM.  Frequent tokens have low
 // numbers: the first chunks' lists are far longer than the others', and their
 // blocks come first in the grid.
+//
+// V = 151552, fp32: one row 7.1 us (a chain), eight trees of up to 16 nodes with
+// masks and biases 30 us (57 MB), 128 rows with histories of 16000 tokens, adjusted
+// logits kept, 67 us (162 MB, 2.4 TB/s).  What bounds the last two is instructions
+// and waits about alike (46 % of the issue slots; 1800 instructions a warp, 200 of
+// them for its logits).  On the way there (trees, 128 rows): the rules at each logit
+// 80 and 115 us; the table and its list 30 and 73, with chunks of 8192 and each
+// block reading the whole history; logits in a ring in shared memory 38 and 124 (it
+// leaves room for two blocks an SM); a table by rank for 1024 tokens at a time 33 and
+// 118 (the first chunk's block takes 70); this, with the histories sorted, 30 and 67.
 //
 // Every chunk's block would read the whole history of its sequence.  Where that
 // adds up, a kernel in front sorts the histories by chunk into the workspace.
@@ -46,7 +56,6 @@ constexpr int GROUP = 4;         // rows of a sequence that share one table
 constexpr int MOST = 4096, LEAST_SHIFT = 10;  // tokens of a chunk, a power of two: at most 4096, at least 2^10
 constexpr int EIGHTS = MOST / 8 / GT;     // loads of a thread for a row
 constexpr int FLIGHT = 4;        // loads of the history of a thread on their way together
-constexpr int LISTED = 4;        // the same for tokens of the list
 constexpr int BIASES = 128;      // biases of a chunk that are found in shared memory
 constexpr uint32_t SEEN = 1u << 31, BIASED = 1u << 30, DRAFTED = 1u << 29, TIMES = DRAFTED - 1;
 
@@ -134,7 +143,7 @@ __device__ __forceinline__ uint32_t eight_bits(const uint32_t *words, int d, int
 // they are of, counted by each warp for itself, then each token's place.  A token
 // of the prompt has its top bit set.  Worth it where all blocks together would
 // otherwise read more than SORT_FROM bytes of histories: 128 rows with 16000 tokens
-// each, 300 MB, 105 us without, 71 with it; eight trees with 2000, 19 MB, 29.5
+// each, 300 MB, 105 us without, 67 with it; eight trees with 2000, 19 MB, 29.5
 // without, 30.6 with it.
 constexpr int ST = 1024;
 constexpr long long SORT_FROM = 64ll << 20;
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const i
 
 // RULES: penalties or biases, which need the table.  sorted: the histories are.
 template <class T, class O, bool RULES>
-__global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chunk, const int group, const bool sorted) {
+__global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int chunk, const int group, const bool sorted) {
     __shared__ __align__(16) Shared s;
     pdl_launch_dependents();
     // The sorting kernel starts this one after its own wait, so that all but its
@@ -245,62 +254,43 @@ __global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chu
     // The tokens of the list, for all rows: the block's warps take the rows in turn.
     // j0 .. j1: the slot's biases.
     auto for_list = [&](int held, int j0, int j1) {
-        const int share = GT / 32 / (r1 - r0), r = r0 + warp / share, step = 32 * share;
+        const int share = GT / 32 / (r1 - r0), r = r0 + warp / share;
         if (r >= r1) return;
         const T *x = logits_of(first + r);
         O *out = out_of(first + r);
         const uint32_t *mask = mask_of(r);
         int best = NONE, at = INT_MAX;
-        for (int i0 = warp % share * 32 + lane; i0 < held; i0 += LISTED * step) {
-            float v[LISTED];
-            int place[LISTED];
-            bool allowed[LISTED];
-#pragma unroll
-            for (int k = 0; k < LISTED; ++k) {
-                const int i = i0 + k * step;
-                place[k] = i < held ? s.list[i] : -1;
-                allowed[k] = true;
-                if (place[k] >= 0) {
-                    v[k] = to_f32(x[place[k]]);
-                    if (mask) allowed[k] = mask[place[k] >> 5] >> (place[k] & 31) & 1u;
-                }
+        for (int i = warp % share * 32 + lane; i < held; i += 32 * share) {
+            const int d = s.list[i];
+            const uint32_t word = s.word[d];
+            const bool allowed = !mask || (mask[d >> 5] >> (d & 31) & 1u);
+            float l = to_f32(x[d]);
+            int times = (int)(word & TIMES);
+            if (word & DRAFTED) {
+                for (int t = 0; t < s.n_drafted; ++t)
+                    if (s.token[t] == lo + d && (s.above[r - r0][s.node[t] >> 5] >> (s.node[t] & 31) & 1u)) ++times;
             }
-#pragma unroll
-            for (int k = 0; k < LISTED; ++k) {
-                const int d = place[k];
-                if (d < 0) break;
-                float l = v[k];
-                const uint32_t word = s.word[d];
-                int times = (int)(word & TIMES);
-                if (word & DRAFTED) {
-#pragma unroll 1
-                    for (int t = 0; t < s.n_drafted; ++t)
-                        if (s.token[t] == lo + d && (s.above[r - r0][s.node[t] >> 5] >> (s.node[t] & 31) & 1u)) ++times;
+            if (use_rep && (times > 0 || (word & SEEN))) l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
+            if (use_times && times > 0) {
+                if (a.rules.frequency) l = __fsub_rn(l, __fmul_rn(freq, (float)times));
+                if (a.rules.presence) l = __fsub_rn(l, pres);
+            }
+            if (word & BIASED) {  // of a token listed twice the last one
+                int j = j0;
+                if (s.n_biased <= BIASES) {
+                    for (int t = 0; t < s.n_biased; ++t)
+                        if (s.bias_of[t] == d && s.bias_at[t] > j) j = s.bias_at[t];
+                } else {
+                    for (j = j1 - 1; j > j0 && a.rules.bias_tokens[j] != lo + d;) --j;
                 }
-                if (use_rep && (times > 0 || (word & SEEN))) l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-                if (use_times && times > 0) {
-                    if (a.rules.frequency) l = __fsub_rn(l, __fmul_rn(freq, (float)times));
-                    if (a.rules.presence) l = __fsub_rn(l, pres);
-                }
-                if (word & BIASED) {  // of a token listed twice the last one
-                    int j = j0;
-                    if (s.n_biased <= BIASES) {
-#pragma unroll 1
-                        for (int t = 0; t < s.n_biased; ++t)
-                            if (s.bias_of[t] == d && s.bias_at[t] > j) j = s.bias_at[t];
-                    } else {
-#pragma unroll 1
-                        for (j = j1 - 1; j > j0 && a.rules.bias_tokens[j] != lo + d;) --j;
-                    }
-                    l = __fadd_rn(l, a.rules.bias_values[j]);
-                }
-                if (!allowed[k]) l = -INFINITY;
-                if (out) out[d] = from_f32<O>(l);
-                const int o = order_of(max_nan2(l, l));
-                if (allowed[k] && o > best) {  // (d grows)
-                    best = o;
-                    at = d;
-                }
+                l = __fadd_rn(l, a.rules.bias_values[j]);
+            }
+            if (!allowed) l = -INFINITY;
+            if (out) out[d] = from_f32<O>(l);
+            const int o = order_of(max_nan2(l, l));
+            if (allowed && o > best) {  // (d grows)
+                best = o;
+                at = d;
             }
         }
         const int most = __reduce_max_sync(0xffffffffu, best);
@@ -377,8 +367,9 @@ __global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chu
         const int32_t *mine = reinterpret_cast<const int32_t *>(a.workspace + record_at(b) + 16);
         const int mine0 = sorted && told ? mine[SORTED + blockIdx.y] : 0, mine1 = sorted && told ? mine[SORTED + blockIdx.y + 1] : 0;
         const uint32_t bits = smem_addr(s.bits), word = smem_addr(s.word);
-        // A rule reaches a token: `how` is set, or one time more is counted.  Without
-        // branches: in most warps some lane's token is in the chunk.
+        // A rule reaches a token: `how` is set; or it is in the history, and SEEN is set or
+        // one time more is counted.  Without branches: in most warps some lane's token is
+        // in the chunk.
         auto mark = [bits, word, lo, n](int32_t t, uint32_t how) {
             const uint32_t d = (uint32_t)t - (uint32_t)lo;
             asm volatile(
@@ -386,16 +377,13 @@ __global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chu
                 "r"(n), "r"(word + 4 * d), "r"(how), "r"(bits + (d >> 3 & ~3u)), "r"(1u << (d & 31))
                 : "memory");
         };
-        auto count = [bits, word, lo, n](int32_t t) {
+        auto told_of = [bits, word, lo, n](int32_t t, bool prompts) {
             const uint32_t d = (uint32_t)t - (uint32_t)lo;
             asm volatile(
-                "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t@p red.shared.or.b32 [%3], %4;\n\t}" ::"r"(d),
-                "r"(n), "r"(word + 4 * d), "r"(bits + (d >> 3 & ~3u)), "r"(1u << (d & 31))
+                "{\n\t.reg .pred p, q;\n\tsetp.lt.u32 p, %0, %1;\n\tsetp.ne.and.u32 q, %6, 0, p;\n\t@q red.shared.or.b32 [%2], %3;\n\t"
+                "setp.eq.and.u32 q, %6, 0, p;\n\t@q red.shared.add.u32 [%2], 1;\n\t@p red.shared.or.b32 [%4], %5;\n\t}" ::"r"(d),
+                "r"(n), "r"(word + 4 * d), "r"(SEEN), "r"(bits + (d >> 3 & ~3u)), "r"(1u << (d & 31)), "r"((uint32_t)prompts)
                 : "memory");
-        };
-        auto told_of = [&](int32_t t, bool prompts) {
-            if (prompts) mark(t, SEEN);
-            else count(t);
         };
         for (int i0 = tid; fours > 0;) {
 #pragma unroll
@@ -412,12 +400,12 @@ __global__ void __launch_bounds__(GT) k_greedy(const GreedyArgs a, const int chu
             for (int k = 0; k < FLIGHT; ++k) t4[k] = i0 + k * GT < fours ? text4[i0 + k * GT] : none;
         }
         for (int i = from + 4 * fours + tid; i < len; i += GT) told_of(text[i], i < prompt);
-        for (int i0 = mine0 + tid; i0 < mine1; i0 += 4 * FLIGHT * GT) {
-            int32_t t[4 * FLIGHT];
+        for (int i0 = mine0 + tid; i0 < mine1; i0 += FLIGHT * GT) {
+            int32_t t[FLIGHT];
 #pragma unroll
-            for (int k = 0; k < 4 * FLIGHT; ++k) t[k] = i0 + k * GT < mine1 ? mine[i0 + k * GT] : 0x7fffffff;
+            for (int k = 0; k < FLIGHT; ++k) t[k] = i0 + k * GT < mine1 ? mine[i0 + k * GT] : 0x7fffffff;
 #pragma unroll
-            for (int k = 0; k < 4 * FLIGHT; ++k) told_of(t[k] & 0x7fffffff, t[k] < 0);
+            for (int k = 0; k < FLIGHT; ++k) told_of(t[k] & 0x7fffffff, t[k] < 0);
         }
         mark(draft, DRAFTED);
         if (draft >= lo && draft < lo + n) {
