@@ -701,7 +701,8 @@ int hq_rope_turns(const double *freqs_host, int32_t n, uint64_t *turns_host);
 /* Between the projection and hq_prefix_attention: rotates the newest rows' q
  * and k by their positions and writes k and v into the cache (hq_pages_write
  * with the rotation), in one launch.  Row i of sequence seqs[b], its rows and
- * their places in the cache as in hq_pages_write.  A row's rotary position is
+ * their places in the cache as in hq_pages_write (k_plane and v_plane differ, and
+ * a sequence stands in seqs once).  A row's rotary position is
  * positions[row] or, where positions is NULL, len - m_b + d: d is its depth in
  * the tree of `parent` (numbered within the sequence as in hq_tree_attention;
  * the walk ends at a parent outside [0, node)), or i where parent is NULL.

@@ -349,6 +349,7 @@ int hq_rope_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32
                   uint32_t flags, void *stream) {
     if (!cache_ok(cache) || (flags & ~HQ_LAUNCH_PDL) != 0) return HQ_ERR_INVALID_ARG;
     if (k_plane < 0 || k_plane >= cache->n_planes || v_plane < 0 || v_plane >= cache->n_planes) return HQ_ERR_INVALID_ARG;
+    if (k_plane == v_plane) return HQ_ERR_INVALID_ARG;  // they are written side by side
     if (!type16(type) || (in_type != HQ_F32 && in_type != type)) return HQ_ERR_INVALID_ARG;
     if (Hq <= 0 || Hq > 65535 || (layout != HQ_ROPE_HALF && layout != HQ_ROPE_INTERLEAVED)) return HQ_ERR_INVALID_ARG;
     if (!(eps >= 0.0f && eps <= FLT_MAX) || !(gain <= FLT_MAX && gain >= -FLT_MAX)) return HQ_ERR_INVALID_ARG;

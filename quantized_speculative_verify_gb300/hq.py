@@ -932,7 +932,8 @@ def rope_write(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, k
     fp32 [dim]: heads are normed first.  A row's position is positions[row]
     (int32 [rows]), or its sequence's length before these rows plus its depth in
     the tree of `parent` (None: a chain).  Returns out [rows][Hq][dim] of the
-    cache's type (may be q itself)."""
+    cache's type (may be q itself); one that the call makes is zero in rows that no
+    sequence claims."""
     shape, heads, dtype = q.shape, cache.heads, q.dtype
     rows, Hq, D = shape
     if D != cache.dim or k.shape != (rows, heads, D) or v.shape != k.shape:
@@ -955,7 +956,7 @@ def rope_write(cache: PagedCache, k_plane: int, v_plane: int, q: torch.Tensor, k
     if k_weight is not None:
         _dense(k_weight, torch.float32, (D,), "rope_write: k_weight")
     if out is None:
-        out = _new(shape, cache.pool.dtype, q.device, stream)
+        out = _new(shape, cache.pool.dtype, q.device, stream, torch.zeros)  # (rows that no sequence claims)
     elif out.shape != shape or out.dtype is not cache.pool.dtype:
         raise ValueError(f"rope_write: out must be {cache.pool.dtype} {list(shape)}")
     rc = load().hq_rope_write(cache.c, k_plane, v_plane, cache.type, _ptr(q), _ptr(k), _ptr(v), _type(q), _heads(q, D, "q"),
@@ -1059,6 +1060,9 @@ class LogitRules(_Held):
                                 0 if masks is None else masks.shape[0])
 
 
+_minus_one = functools.partial(torch.full, fill_value=-1)
+
+
 @functools.lru_cache(maxsize=1024)
 def hq_greedy_tokens_workspace_bytes(rows: int) -> int:
     return int(load().hq_greedy_tokens_workspace_bytes(int(rows)))
@@ -1075,7 +1079,8 @@ def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, toke
     history and rules (None: b).  mask_ids int32 [rows]: the row's mask, -1 none
     (None: mask r for row r).  out [rows][V] (the logits' type or fp32, or logits
     itself): the adjusted logits.  workspace: zeroed once, of at least these
-    rows' size.  Returns greedy int32 [rows]."""
+    rows' size.  Returns greedy int32 [rows] (one that the call makes is -1 in rows
+    that no sequence claims)."""
     rows, V = logits.shape
     B = _batch(None, rows, starts, max_rows, seqs, "greedy_tokens: starts and seqs")
     ty = TYPES.get(logits.dtype)
@@ -1092,7 +1097,7 @@ def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, toke
     if out is not None and out is not logits and (out.shape != logits.shape or out.dtype not in (logits.dtype, torch.float32)):
         raise ValueError(f"greedy_tokens: out must be {logits.dtype} or fp32 {[rows, V]}, got {out.dtype} {list(out.shape)}")
     if greedy is None:
-        greedy = _new(rows, _INT32, logits.device, stream)
+        greedy = _new((rows,), _INT32, logits.device, stream, _minus_one)  # (rows that no sequence claims)
     else:
         _list(greedy, rows, "greedy_tokens: greedy")
     need = hq_greedy_tokens_workspace_bytes(rows)

@@ -108,7 +108,7 @@ def test_rope_write_refuses_bad_arguments():
                                  a["ldo"], a["flags"], None)
     assert call(B=0) == hq.HQ_OK and call(rows=0) == hq.HQ_OK
     nan, inf = float("nan"), float("inf")
-    bad = [dict(kp=-1), dict(kp=2), dict(vp=2), dict(t=hq.HQ_F32), dict(it=hq.HQ_BF16), dict(it=9), dict(q=None), dict(k=None),
+    bad = [dict(kp=-1), dict(kp=2), dict(vp=2), dict(kp=1), dict(t=hq.HQ_F32), dict(it=hq.HQ_BF16), dict(it=9), dict(q=None), dict(k=None),
            dict(v=None), dict(out=None), dict(turns=None), dict(q=FAKE + 8), dict(k=FAKE + 4), dict(v=FAKE + 8),
            dict(out=FAKE + 8), dict(ldq=508), dict(ldq=514), dict(ldk=252), dict(ldv=255), dict(ldo=511), dict(ldo=516),
            dict(Hq=0), dict(Hq=65536), dict(qw=FAKE + 8), dict(kw=FAKE + 4), dict(eps=-1.0), dict(eps=nan), dict(eps=inf),

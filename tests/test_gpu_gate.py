@@ -211,6 +211,24 @@ def test_rows_that_are_not_finite(bad, where):
         assert bool(torch.isnan(h[1, 300]))
 
 
+@pytest.mark.parametrize("M,K,D", [(3, 1024, 128), (700, 4096, 64), (5, 20480, 256)])
+def test_group_sums_or_the_operand_alone(M, K, D):
+    x, gate, w, signs = make(M, K, D, F32, F16, seed=10)
+    d, sg = hq.make_desc(K, 128, 64, "w4"), signs_dev(signs)
+    qx, gs, sx = torch.empty((M, K), dtype=torch.int8, device=DEV), Guarded((M, K // 64), torch.int32, DEV), torch.empty(M, device=DEV)
+    hq.gated_norm_quant(d, x, gate, w, sg, D, "silu", gsum=gs.t, sx=sx)
+    hq.gated_norm_quant(d, x, gate, w, sg, D, "silu", qx=qx, sx=sx)
+    gs.check()
+    assert torch.equal(gs.t, qx.view(M, -1, 64).to(torch.int32).sum(2, dtype=torch.int32))
+    if M <= hq.HQ_MAX_M:
+        n = hq.hq_act_operand_bytes(d, M)
+        a, b = Guarded((n,), torch.uint8, DEV), Guarded((n,), torch.uint8, DEV)
+        hq.gated_norm_quant(d, x, gate, w, sg, D, "silu", qop=a.t, sx=sx)
+        hq.gated_norm_quant(d, x, gate, w, sg, D, "silu", qx=qx, qop=b.t, gsum=gs.t, sx=sx)
+        a.check()
+        assert torch.equal(a.t, b.t)
+
+
 def test_a_captured_call_and_another_stream():
     M, K, D = 9, 4096, 128
     x, gate, w, signs = make(M, K, D, F32, BF16, seed=7)

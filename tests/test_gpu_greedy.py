@@ -247,6 +247,33 @@ def test_ties_go_to_the_lowest_token():
     r.run(out_type=F32)
 
 
+def test_a_chain_without_parents_and_tokens_without_a_history():
+    r = Request([5, 1, 7], 900, seed=23)
+    r.parent = np.array([max(0, i - 1) for m in r.rows for i in range(m)], dtype=np.int32)
+    kw = r.device()
+    kw["parent"] = None
+    x = r.x.to(DEV)
+    greedy = hq.greedy_tokens(x, kw.pop("starts"), kw.pop("max_rows"), **kw)
+    r.check(greedy, None)
+    r.use["history"] = r.use["mask"] = False  # drafted tokens alone
+    kw = r.device()
+    kw["parent"] = None
+    r.check(hq.greedy_tokens(x, kw.pop("starts"), kw.pop("max_rows"), **kw), None)
+
+
+def test_buffers_that_a_call_makes_say_nothing_of_rows_without_a_sequence():
+    x = torch.randn((5, 300), device=DEV)
+    assert hq.greedy_tokens(x, ints([0, 2]), 2)[2:].tolist() == [-1, -1, -1]
+    assert hq.greedy_tokens(x, ints([0]), 1).tolist() == [-1] * 5
+
+
+def test_more_biases_in_a_chunk_than_are_held_there():
+    r = Request([2, 1], 3000, seed=24)
+    rng = np.random.default_rng(3)
+    r.bias[0] = [(int(t), np.float32(v)) for t, v in zip(rng.integers(0, 3000, 2500), rng.standard_normal(2500) * 4)]
+    r.run(out_type=F32)
+
+
 def test_tokens_outside_the_vocabulary_and_bad_lengths_and_slots():
     r = Request([4, 3, 2, 2, 2], 700, seed=12, slots=[0, 1, 2, 9, -1], n_slots=4, history=60)
     r.text[0, ::3], r.text[1, ::2] = -1, 700

@@ -229,6 +229,15 @@ def test_equal_rows_without_starts_and_rows_past_max_rows():
     assert bool((out[3] == 7.0).all()) and not bool((out[2] == 7.0).any()) and not bool((out[4:] == 7.0).all())
 
 
+def test_a_buffer_that_the_call_makes_is_zero_without_sequences():
+    r = Rows([5], [4], 2, 1, 64, 16, F32, F16, seed=18, gap=2)
+    turns = hq.rope_turns(hq.rope_freqs(64), DEV)
+    assert not bool(hq.rope_write(r.cache, 0, 1, r.q, r.k, r.v, turns, ints([0]), 4).any())
+    out = hq.rope_write(r.cache, 0, 1, r.q, r.k, r.v, turns, ints(r.starts), 4)
+    assert not bool(out[4:].any())
+    check(r, out, turns)
+
+
 def test_parents_that_are_none_end_the_walk():
     r = Rows([10], [6], 2, 1, 64, 16, F32, F16, seed=10)
     r.parent = [5, 0, 7, 2, -3, 4]  # the walks end at 0, 2 and 4
