@@ -123,7 +123,7 @@ struct Shared {
     uint16_t list[MOST];
     int32_t bias_at[BIASES];        // biases of this chunk: their number in the slot's list, their token
     uint16_t bias_of[BIASES];
-    int order[GROUP][GT / 32], at[GROUP][GT / 32];  // of each warp, of the ring
+    int order[GROUP][GT / 32], at[GROUP][GT / 32];  // of each warp, of the logits that stream
     int list_order[GROUP][GT / 32], list_at[GROUP][GT / 32];  // and of the list
     int mask_id[GROUP];
     uint32_t above[GROUP][HQ_MAX_M / 32];  // the nodes on each row's path, without the root
@@ -399,7 +399,13 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
 #pragma unroll
             for (int k = 0; k < FLIGHT; ++k) t4[k] = i0 + k * GT < fours ? text4[i0 + k * GT] : none;
         }
-        for (int i = from + 4 * fours + tid; i < len; i += GT) told_of(text[i], i < prompt);
+        for (int i0 = from + 4 * fours + tid; i0 < len; i0 += 2 * FLIGHT * GT) {
+            int32_t t[2 * FLIGHT];
+#pragma unroll
+            for (int k = 0; k < 2 * FLIGHT; ++k) t[k] = i0 + k * GT < len ? text[i0 + k * GT] : -1;
+#pragma unroll
+            for (int k = 0; k < 2 * FLIGHT; ++k) told_of(t[k], i0 + k * GT < prompt);
+        }
         for (int i0 = mine0 + tid; i0 < mine1; i0 += FLIGHT * GT) {
             int32_t t[FLIGHT];
 #pragma unroll
