@@ -11,10 +11,10 @@
 // some rows of one sequence.  In shared memory it makes a table of the tokens of
 // its chunk that a rule reaches, once for its rows: a word a token (seen, biased,
 // drafted, how often behind the prompt), a bit a token, and a list of them in
-// order.  All the code for the rules is in a pass over the list.  The others are in
-// the threads' registers by then, eight logits a load, asked for before anything
-// else (the next row's before this one is looked at); the list's are left out by
-// their bits.  What a row's own path adds to the table is the drafted tokens of its
+// order.  Meanwhile the logits are on their way into the threads' registers, eight
+// a load, asked for before anything else (the next row's before this one is looked
+// at); the list's take no part in their maximum, by their bits.  All the code for
+// the rules is in a pass over the list after that.  What a row's own path adds to the table is the drafted tokens of its
 // ancestors, at most 127 and looked for only at tokens that are marked as drafted.
 //
 // A block is a chain of waits (its sequence, the history's length, the history, the
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
     };
     float rep = 1.0f, pres = 0.0f, freq = 0.0f;
     bool use_rep = false, use_times = false;
-    int listed_tokens = 0;
+    int listed_tokens = 0, first_bias = 0, last_bias = 0;
     // The tokens of the list, for all rows: the block's warps take the rows in turn.
     // j0 .. j1: the slot's biases.
     auto for_list = [&](int held, int j0, int j1) {
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
         for (int i = tid; i < (n + 3) / 4; i += GT) reinterpret_cast<uint4 *>(s.word)[i] = make_uint4(0, 0, 0, 0);
         for (int i = tid; i < (n + 31) / 32 + 1; i += GT) s.bits[i] = 0;
         if (tid == 0) s.n_drafted = s.n_biased = 0;
+        if (tid < GROUP * (GT / 32)) (&s.list_order[0][0])[tid] = NONE;
         len = len < 0 ? 0 : len > a.history.cap ? a.history.cap : len;
         if (j0 < 0 || j1 > a.rules.n_bias || j1 < j0) j0 = j1 = 0;
         const int32_t *text = a.history.tokens + (size_t)(told ? slot : 0) * a.history.cap;
@@ -449,78 +450,86 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
             listed_tokens += s.counts[i];
         }
         for (; field != 0; field &= field - 1) s.list[before++] = (uint16_t)(32 * tid + __ffs(field) - 1);
-        if (listed_tokens > 0) {
-            for (int i = tid; i < (r1 - r0) * (GT / 32); i += GT) s.list_order[i / (GT / 32)][i % (GT / 32)] = NONE;
-            __syncthreads();
-            for_list(listed_tokens, j0, j1);
-        }
+        first_bias = j0;
+        last_bias = j1;
+        __syncthreads();  // the list is whole
     } else {
         __syncthreads();
     }
-    // The others.
-    for (int r = r0; r < r1; ++r) {
-        const T *x = logits_of(first + r);
-        O *out = out_of(first + r);
-        const uint32_t *mask = mask_of(r);
-        int best = NONE, at = INT_MAX;  // at: the first of the eight
-        auto one = [&](int d) {         // a logit outside the aligned eights
-            if (RULES && (s.bits[d >> 5] >> (d & 31) & 1u)) return;
-            const float l = to_f32(x[d]);
-            const bool allowed = !mask || (mask[d >> 5] >> (d & 31) & 1u);
-            if (out) out[d] = from_f32<O>(allowed ? l : -INFINITY);
-            const int o = order_of(max_nan2(l, l));
-            if (allowed && o > best) {
-                best = o;
-                at = d;
+    // The logits that stream.
+    auto stream = [&]() {
+        for (int r = r0; r < r1; ++r) {
+            const T *x = logits_of(first + r);
+            O *out = out_of(first + r);
+            const uint32_t *mask = mask_of(r);
+            int best = NONE, at = INT_MAX;  // at: the first of the eight
+            auto one = [&](int d) {         // a logit outside the aligned eights
+                const bool listed = RULES && (s.bits[d >> 5] >> (d & 31) & 1u);
+                const float l = to_f32(x[d]);
+                const bool allowed = !mask || (mask[d >> 5] >> (d & 31) & 1u);
+                if (out) out[d] = from_f32<O>(allowed ? l : -INFINITY);
+                const int o = order_of(max_nan2(l, l));
+                if (allowed && !listed && o > best) {
+                    best = o;
+                    at = d;
+                }
+            };
+            const int head = head_of(x), eights = (n - head) / 8;
+            const bool whole = out && (reinterpret_cast<uintptr_t>(out + head) & 15) == 0;
+            uint32_t bits[EIGHTS];
+#pragma unroll
+            for (int k = 0; k < EIGHTS; ++k) {
+                bits[k] = 0xffu;
+                if (mask && tid + k * GT < eights) bits[k] = eight_bits(mask, head + 8 * (tid + k * GT), head & 7);
             }
-        };
-        const int head = head_of(x), eights = (n - head) / 8;
-        const bool whole = out && (reinterpret_cast<uintptr_t>(out + head) & 15) == 0;
-        uint32_t bits[EIGHTS];
+            if (tid < head) one(tid);
 #pragma unroll
-        for (int k = 0; k < EIGHTS; ++k) {
-            bits[k] = 0xffu;
-            if (mask && tid + k * GT < eights) bits[k] = eight_bits(mask, head + 8 * (tid + k * GT), head & 7);
-        }
-        if (tid < head) one(tid);
+            for (int k = 0; k < EIGHTS; ++k) {
+                const int d = head + 8 * (tid + k * GT);
+                if (tid + k * GT >= eights) break;
+                const uint32_t listed = RULES ? eight_bits(s.bits, d, head & 7) : 0u;
+                float l[8];
+                if (out) {
+                    Oct<O> o;
 #pragma unroll
-        for (int k = 0; k < EIGHTS; ++k) {
-            const int d = head + 8 * (tid + k * GT);
-            if (tid + k * GT >= eights) break;
-            const uint32_t listed = RULES ? eight_bits(s.bits, d, head & 7) : 0u;
-            float l[8];
-            if (out) {
-                Oct<O> o;
+                    for (int e = 0; e < 8; ++e) o.x[e] = from_f32<O>((bits[k] >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY);
+                    if (whole) {
+                        store(out + d, o);
+                    } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o.x[e] = from_f32<O>((bits[k] >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY);
-                if (whole && listed == 0) {
-                    store(out + d, o);
-                } else {
+                        for (int e = 0; e < 8; ++e) out[d + e] = o.x[e];
+                    }
+                }
+                const uint32_t use = bits[k] & ~listed;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (!(listed >> e & 1u)) out[d + e] = o.x[e];
+                for (int e = 0; e < 8; ++e) l[e] = (use >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY;
+                const int o = order_of(max_nan3(max_nan3(l[0], l[1], l[2]), max_nan3(l[3], l[4], l[5]), max_nan2(l[6], l[7])));
+                if (use != 0 && o > best) {
+                    best = o;
+                    at = d;
                 }
             }
-            const uint32_t use = bits[k] & ~listed;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) l[e] = (use >> e & 1u) ? to_f32(v[k].x[e]) : -INFINITY;
-            const int o = order_of(max_nan3(max_nan3(l[0], l[1], l[2]), max_nan3(l[3], l[4], l[5]), max_nan2(l[6], l[7])));
-            if (use != 0 && o > best) {
-                best = o;
-                at = d;
+            if (r + 1 < r1) fetch(r + 1);
+            const int d = head + 8 * eights + tid;
+            if (d < n) one(d);
+            const int most = __reduce_max_sync(0xffffffffu, best);
+            at = __reduce_min_sync(0xffffffffu, best == most ? at : INT_MAX);
+            if (lane == 0) {
+                s.order[r - r0][warp] = most;
+                s.at[r - r0][warp] = at;
             }
         }
-        if (r + 1 < r1) fetch(r + 1);
-        const int d = head + 8 * eights + tid;
-        if (d < n) one(d);
-        const int most = __reduce_max_sync(0xffffffffu, best);
-        at = __reduce_min_sync(0xffffffffu, best == most ? at : INT_MAX);
-        if (lane == 0) {
-            s.order[r - r0][warp] = most;
-            s.at[r - r0][warp] = at;
-        }
+    };
+    // Where the logits are kept the stream comes first, with what the list is of, and
+    // the list is written over it: one store of eight instead of one for each logit in
+    // between (128 rows 62 us, else 67).  Where they are not, the list's loads come
+    // first (eight trees 30 us, else 32).
+#pragma unroll 1
+    for (int phase = 0; phase < 2; ++phase) {
+        if ((phase == 0) == (a.out != nullptr)) stream();
+        else if (RULES && listed_tokens > 0) for_list(listed_tokens, first_bias, last_bias);
+        __syncthreads();
     }
-    __syncthreads();
     if (tid >= r1 - r0) return;
     const int row = first + r0 + tid;
     int best = NONE, at = INT_MAX;
