@@ -25,13 +25,14 @@
 //
 // V = 151552, fp32: one row 7.1 us (a chain), eight trees of up to 16 nodes with
 // masks and biases 30 us (57 MB), 128 rows with histories of 16000 tokens, adjusted
-// logits kept, 67 us (162 MB, 2.4 TB/s).  What bounds the last two is instructions
+// logits kept, 61 us (162 MB, 2.7 TB/s).  What bounds the last two is instructions
 // and waits about alike (46 % of the issue slots; 1800 instructions a warp, 200 of
 // them for its logits).  On the way there (trees, 128 rows): the rules at each logit
 // 80 and 115 us; the table and its list 30 and 73, with chunks of 8192 and each
 // block reading the whole history; logits in a ring in shared memory 38 and 124 (it
 // leaves room for two blocks an SM); a table by rank for 1024 tokens at a time 33 and
-// 118 (the first chunk's block takes 70); this, with the histories sorted, 30 and 67.
+// 118 (the first chunk's block takes 70); this, with the histories sorted, 30 and 67;
+// the stream before the list and a sort that stores in rows, 30 and 61.
 //
 // Every chunk's block would read the whole history of its sequence.  Where that
 // adds up, a kernel in front sorts the histories by chunk into the workspace.
@@ -140,19 +141,22 @@ __device__ __forceinline__ uint32_t eight_bits(const uint32_t *words, int d, int
 }
 
 // Histories sorted by chunk.  Of each sequence the first SORTED tokens: which chunk
-// they are of, counted by each warp for itself, then each token's place.  A token
+// they are of, counted by each lane for itself (64 counters a chunk next to one
+// another: a third of a text lies in one chunk, and no two lanes of a warp meet at a
+// counter or a bank), then each token's place.  A token
 // of the prompt has its top bit set.  Worth it where all blocks together would
 // otherwise read more than SORT_FROM bytes of histories: 128 rows with 16000 tokens
-// each, 300 MB, 105 us without, 67 with it; eight trees with 2000, 19 MB, 29.5
-// without, 30.6 with it.
+// each, 300 MB, 105 us without, 61 with it (9 of them the sort); eight trees with
+// 2000, 19 MB, 29.5 without, 30.6 with it.
 constexpr int ST = 1024;
 constexpr long long SORT_FROM = 64ll << 20;
 __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const int shift, const int chunks) {
-    __shared__ int s_count[ST / 32][CHUNKS];
+    extern __shared__ __align__(16) int32_t s_sorted[];  // [SORTED]
+    __shared__ int s_count[CHUNKS][64];
     __shared__ int s_start[CHUNKS + 1];
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
+    const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mine = tid & 63;
     const int slot = a.seqs ? a.seqs[b] : b;
     int len = 0, prompt = 0;
     if (slot >= 0 && slot < a.history.n_slots) {
@@ -166,20 +170,23 @@ __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const i
     int place[SORTED / ST];
 #pragma unroll
     for (int k = 0; k < SORTED / ST; ++k) t[k] = k * ST + tid < len ? text[k * ST + tid] : -1;
-    for (int i = tid; i < ST / 32 * CHUNKS; i += ST) (&s_count[0][0])[i] = 0;
+    for (int i = tid; i < CHUNKS * 64; i += ST) (&s_count[0][0])[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < SORTED / ST; ++k)
-        if (t[k] >= 0 && t[k] < a.V) place[k] = atomicAdd(&s_count[warp][t[k] >> shift], 1);
+        if (t[k] >= 0 && t[k] < a.V) place[k] = atomicAdd(&s_count[t[k] >> shift][mine], 1);
     __syncthreads();
-    if (tid < chunks) {  // each warp's first place in a chunk, from the chunk's start
-        int n = 0;
-        for (int w = 0; w < ST / 32; ++w) {
-            const int c = s_count[w][tid];
-            s_count[w][tid] = n;
-            n += c;
+    for (int c = warp; c < chunks; c += ST / 32) {  // each counter's first place in its chunk, from the chunk's start
+        const int x = s_count[c][2 * lane], y = s_count[c][2 * lane + 1];
+        int n = x + y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += z;
         }
-        s_start[tid + 1] = n;
+        s_count[c][2 * lane] = n - x - y;
+        s_count[c][2 * lane + 1] = n - y;
+        if (lane == 31) s_start[c + 1] = n;
     }
     __syncthreads();
     if (warp == 0) {
@@ -202,8 +209,11 @@ __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const i
 #pragma unroll
     for (int k = 0; k < SORTED / ST; ++k)
         if (t[k] >= 0 && t[k] < a.V)
-            sorted[s_start[t[k] >> shift] + s_count[warp][t[k] >> shift] + place[k]] =
+            s_sorted[s_start[t[k] >> shift] + s_count[t[k] >> shift][mine] + place[k]] =
                 t[k] | (k * ST + tid < prompt ? (int32_t)0x80000000 : 0);
+    // (stored from there in rows: 16000 stores to places of their own take 8 us)
+    __syncthreads();
+    for (int i = tid; i < s_start[chunks]; i += ST) sorted[i] = s_sorted[i];
 }
 
 // RULES: penalties or biases, which need the table.  sorted: the histories are.
@@ -522,7 +532,7 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
     };
     // Where the logits are kept the stream comes first, with what the list is of, and
     // the list is written over it: one store of eight instead of one for each logit in
-    // between (128 rows 62 us, else 67).  Where they are not, the list's loads come
+    // between (128 rows 64 us, else 67).  Where they are not, the list's loads come
     // first (eight trees 30 us, else 32).
 #pragma unroll 1
     for (int phase = 0; phase < 2; ++phase) {
@@ -608,7 +618,16 @@ cudaError_t launch_t(const GreedyArgs &a, bool pdl, cudaStream_t s) {
     const bool sorted = penalties && a.history.tokens && a.B <= SORT_MOST && a.B <= a.rows && chunks < CHUNKS &&
                         4ll * a.history.cap * a.B * groups * chunks > SORT_FROM;
     if (sorted) {
-        const cudaError_t e = launch_kernel(k_sort_history, dim3((unsigned)a.B), dim3(ST), 0, pdl, s, a, shift, chunks);
+        int dev = 0, ready = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        static std::atomic<int> set[CACHE_DEVICES];
+        e = cached_per_device(set, dev, &ready, [](int *v) {
+            *v = 0;
+            return cudaFuncSetAttribute(k_sort_history, cudaFuncAttributeMaxDynamicSharedMemorySize, SORTED * 4);
+        });
+        if (e != cudaSuccess) return e;
+        e = launch_kernel(k_sort_history, dim3((unsigned)a.B), dim3(ST), SORTED * 4, pdl, s, a, shift, chunks);
         if (e != cudaSuccess) return e;
     }
     return launch_kernel(k_greedy<T, O, true>, grid, dim3(GT), 0, pdl || sorted, s, a, chunk, group, sorted);
