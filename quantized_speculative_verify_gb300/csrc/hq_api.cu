@@ -197,7 +197,7 @@ const char *hq_status_string(int status) {
 
 // 2.0: tensor-memory GEMM, one launch up to 128 rows; opaque activation operand with group sums
 // 2.1: the calls for a batch of requests
-int32_t hq_version(void) { return (2 << 16) | 1; }
+int32_t hq_version(void) { return (2 << 16) | 2; }
 
 size_t hq_packed_bytes(const hq_layer_desc *desc) {
     if (!desc_ok(desc)) return 0;
