@@ -745,7 +745,8 @@ int hq_rope_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32
  *   x      x_type [M][K], rows ldx elements apart
  *   gate   g_type [M][K], rows ldg elements apart, or NULL: 1
  *   act    HQ_GATE_NONE: the gate itself; HQ_GATE_SIGMOID: 1 / (1 + e^-gate);
- *          HQ_GATE_SILU: gate / (1 + e^-gate)
+ *          HQ_GATE_SILU: gate / (1 + e^-gate); a quotient 1 / (1 + e^-gate) below
+ *          2^-126 is 0
  *   weight fp32 [D], the same for every head, or NULL: no norm, y = x *
  *          act(gate)
  *   D      64, 128 or 256, dividing K = desc->K

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(FT, 4) k_gate_heads(const GateArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     const int x_type = XT >= 0 ? XT : a.n.x_type, g_type = GT >= 0 ? GT : a.g_type, h_type = GT >= 0 ? GT : a.n.h_type;
-    const int n8 = a.n.K / 8, step = gridDim.x * FT;  // (at most 2^20 blocks)
+    const int n8 = a.n.K / 8, step = gridDim.x * FT;
     const long long total = (long long)a.n.M * n8, start = (long long)blockIdx.x * FT + threadIdx.x;
     long long row = start / n8;
     int idx = (int)(start % n8);
