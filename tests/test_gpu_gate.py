@@ -211,6 +211,18 @@ def test_rows_that_are_not_finite(bad, where):
         assert bool(torch.isnan(h[1, 300]))
 
 
+@pytest.mark.parametrize("codes", [False, True])
+def test_rows_past_32_bits(codes):
+    M, K, D, ld = 3, 1024, 128, 2 ** 30
+    x, gate, w, signs = make(M, K, D, BF16, BF16, seed=11)
+    far = [torch.empty(2 * ld + K, dtype=BF16, device=DEV).as_strided((M, K), (ld, 1)) for _ in range(2)]
+    for t, v in zip(far, (x, gate)):
+        t.copy_(v)
+    qx, sx = (torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)) if codes else (None, None)
+    hq.gated_norm_quant(hq.make_desc(K, 128, 64, "w4"), far[0], far[1], w, signs_dev(signs), D, "silu", 1e-6, h=far[0], qx=qx, sx=sx)
+    check(value(x, gate, w, D, "silu", 1e-6), signs, far[0], qx, sx)
+
+
 @pytest.mark.parametrize("M,K,D", [(3, 1024, 128), (700, 4096, 64), (5, 20480, 256)])
 def test_group_sums_or_the_operand_alone(M, K, D):
     x, gate, w, signs = make(M, K, D, F32, F16, seed=10)

@@ -202,6 +202,18 @@ def test_strides_and_any_alignment(dtype, out, pad, lead, opad):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_past_32_bits(dtype):
+    r = Request([1, 2], 5000, seed=25, dtype=dtype)
+    ld = 2 ** 30 + 3
+    wide = torch.empty(2 * ld + 5000, dtype=dtype, device=DEV)
+    x = wide.as_strided((3, 5000), (ld, 1))
+    x.copy_(r.x)
+    kw = r.device()
+    greedy = hq.greedy_tokens(x, kw.pop("starts"), kw.pop("max_rows"), out=x, **kw)
+    r.check(greedy, x)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_in_place(dtype):
     Request([2, 5], 5003, seed=8, dtype=dtype).run(in_place=True)
     Request([2, 5], 5004, seed=8, dtype=dtype).run(in_place=True, pad=4)

@@ -345,3 +345,26 @@ def test_a_captured_write_follows_its_inputs_and_streams():
     graph.replay()
     torch.cuda.synchronize()
     check(r, out, turns)
+
+
+def test_pages_and_rows_past_32_bits():
+    """A pool of over 4 GB a plane, and input rows over 2^31 elements apart."""
+    D, Hkv, ps, pages = 128, 8, 256, 9000  # 4.7 GB a plane
+    pool = torch.empty((2, pages, Hkv, ps, D), dtype=BF16, device=DEV)
+    table = torch.tensor([[pages - 1, pages - 2], [0, 1]], dtype=torch.int32, device=DEV)
+    cache = hq.PagedCache(pool, torch.ones(pages, dtype=torch.int32, device=DEV), table, ints([300, 2]))
+    wide = torch.empty(2 ** 31 + 64 * D, dtype=BF16, device=DEV)
+    ld, R = 2 ** 30, 3
+    parts = [wide.as_strided((R, h, D), (ld, D, 1), o * D) for o, h in ((0, 4), (4, Hkv), (4 + Hkv, Hkv))]
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for t in parts:
+        t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+    turns = hq.rope_turns(hq.rope_freqs(D), DEV)
+    out = hq.rope_write(cache, 0, 1, *parts, turns, ints([0, 1, 3]), 2)
+    t = turns.cpu().numpy().view(np.uint64).tolist()
+    pos = [299, 0, 1]
+    close(out, *expected(parts[0], pos, t, "half", 1.0, None, 0.0))
+    for i, (page, slot) in enumerate([(pages - 2, 299 - ps), (0, 0), (0, 1)]):
+        close(pool[0, page, :, slot].unsqueeze(0), *expected(parts[1][i:i + 1], pos[i:i + 1], t, "half", 1.0, None, 0.0))
+        assert torch.equal(pool[1, page, :, slot], parts[2][i])
+    assert hq.pages_status(cache) == hq.HQ_OK
