@@ -145,11 +145,13 @@ __device__ __forceinline__ uint32_t eight_bits(const uint32_t *words, int d, int
 // another: a third of a text lies in one chunk, and no two lanes of a warp meet at a
 // counter or a bank), then each token's place.  A token
 // of the prompt has its top bit set.  Worth it where all blocks together would
-// otherwise read more than SORT_FROM bytes of histories: 128 rows with 16000 tokens
-// each, 300 MB, 105 us without, 61 with it (9 of them the sort); eight trees with
-// 2000, 19 MB, 29.5 without, 30.6 with it.
+// otherwise read more than SORT_FROM bytes of histories, V = 151552: 128 rows with
+// 16000 tokens each, 300 MB, 105 us without, 61 with it (9 of them the sort); 64 with
+// 4000, 37 MB, 31 and 26; 32 with 4000, 19 MB, 19.7 and 16.8; 128 of V = 32000 with
+// 4000, 16 MB, 19.9 and 18.2; 16 trees of 8 nodes, V = 100000, with 1000, 6 MB, 21 and
+// 20, where it is one more launch for the host.
 constexpr int ST = 1024;
-constexpr long long SORT_FROM = 64ll << 20;
+constexpr long long SORT_FROM = 12ll << 20;
 __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const int shift, const int chunks) {
     extern __shared__ __align__(16) int32_t s_sorted[];  // [SORTED]
     __shared__ int s_count[CHUNKS][64];
