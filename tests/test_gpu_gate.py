@@ -259,3 +259,32 @@ def test_a_captured_call_and_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     check(value(x, gate, w, D, "silu", 1e-6), signs, h, qx, sx)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("K", [1024, 8192, 16384])
+@pytest.mark.parametrize("gt", [F32, BF16, F16])
+def test_finite_gates_of_any_size(gt, K, act):
+    """A row for each gate, up to the type's largest; a quotient 1 / (1 + e^-gate) below 2^-126 is 0.  |x| <= 1/2, so silu's
+    products stay finite."""
+    sizes = [0.0, 1e-30, 50.0, 88.0, 100.0] + ([1e4] if gt == F16 else [1e30, 2.4e38]) + [torch.finfo(gt).max]
+    gates = torch.tensor(sizes + [-s for s in sizes], device=DEV).to(gt)
+    M, D = len(gates), 128
+    x, _, _, signs = make(M, K, D, F32, None, seed=13)
+    x, gate = (x / 8).clamp(-0.5, 0.5), gates.unsqueeze(1).expand(M, K).contiguous()
+    z = gate.double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        s = 1.0 / (1.0 + np.exp(-z))
+    s = np.where(s < 2.0 ** -126, 0.0, s)
+    y = x.double().cpu().numpy() * (z * s if act == "silu" else s)
+    d, sg = hq.make_desc(K, 128, 32, "w4"), signs_dev(signs)
+    h, both = torch.empty((M, K), dtype=gt, device=DEV), torch.empty((M, K), dtype=gt, device=DEV)
+    qx, sx = torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    hq.gated_norm_quant(d, x, gate, None, None, D, act, h=h)
+    hq.gated_norm_quant(d, x, gate, None, sg, D, act, h=both, qx=qx, sx=sx)
+    check(y, signs, h, qx, sx)
+    assert torch.equal(h, both)
+    qx2, sx2 = torch.empty_like(qx), torch.empty_like(sx)  # beside the operand: another kernel
+    qop = torch.empty(hq.hq_act_operand_bytes(d, M), dtype=torch.uint8, device=DEV)
+    hq.gated_norm_quant(d, x, gate, None, sg, D, act, qx=qx2, qop=qop, sx=sx2)
+    assert torch.equal(qx, qx2) and torch.equal(sx, sx2)
