@@ -758,8 +758,11 @@ int hq_rope_write(const hq_pages *cache, int32_t k_plane, int32_t v_plane, int32
  *   M      0..HQ_MAX_M with qop, else 0..2^20
  * x, gate, h and weight are 16-byte aligned, rows too.  Heads of any size are
  * normed as the formula says (their squares are taken in units of a power of
- * two where fp32's range would end).  A row of y with a NaN or an infinity has
- * a NaN or infinite sx and codes 0.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL
+ * two where fp32's range would end).  Arithmetic is fp32: the quotient 1 / (1 +
+ * e^-gate) is within 2^-20 of its value, y within 2^-19 (relative to it; a
+ * normed head's sum, root and products 14 * 2^-24 of that), and h has its own
+ * rounding.  A row of y with a NaN or an infinity has a NaN or infinite sx and
+ * codes 0.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL
  * (nothing is read before the wait). */
 typedef enum { HQ_GATE_NONE = 0, HQ_GATE_SIGMOID = 1, HQ_GATE_SILU = 2 } hq_gate_act;
 int hq_gated_norm_quant(const hq_layer_desc *desc, const void *x, int32_t x_type, int64_t ldx, const void *gate,

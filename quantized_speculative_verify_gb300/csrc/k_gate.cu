@@ -8,13 +8,13 @@
 // A head is 8, 16 or 32 lanes of 8 features, so the norm is lane exchanges and
 // needs no barrier; only the codes need the row's largest value.  So h alone is one
 // long list of octets over resident blocks, bound by memory and, nearly, by
-// instructions: 8190 rows of 8192, all bf16, with a silu gate 74 us = 5.4 TB/s.  On
+// instructions: 8190 rows of 8192, all bf16, with a silu gate 75 us = 5.4 TB/s.  On
 // the way there: an exact division and expf per gate 112 us; the quotient by the
 // approximate reciprocal and the types known at compile time 83.  One, two and four
 // octets a thread on their way 76, 74 and 94 us (registers end the fourth block an
 // SM); five blocks an SM 88.  With codes few rows are one chain of waits (128 rows of
 // 8192 4.3 us, 3.1 of which one row of 4096 takes), many are bound by instructions:
-// 8190 rows of 8192 in bf16 112 us = 4.2 TB/s.  On the way there: a block per row 213;
+// 8190 rows of 8192 in bf16 111 us = 4.2 TB/s.  On the way there: a block per row 213;
 // resident blocks with the next row's loads ahead 138; weights and signs in registers
 // 130; types known at compile time 111 (a thread holds one octet, else registers spill).
 #include "rows.cuh"
@@ -26,18 +26,18 @@ constexpr float MAX_LEAST = 0x1p-110f;  // below it a row's largest |z| is forme
 
 // 1 / (1 + e^-g) in nine instructions, two of them of the special unit: expf and a
 // division with their care for subnormal results take 25 and bound the kernel.  e^-g
-// = 2^t (1 + r ln 2), t = -g log2(e) as it is rounded and r what that left out.  r is
-// NaN for infinite g, infinite where g log2(e) passes fp32's range, and large long
-// before; where 2^t is neither 0 nor infinite |r| is below 2^-16, so the factor's
-// bounds change no result that it decides, and 0 and infinity stay what they are.  The
-// power is off by 2^-22, the reciprocal by one unit in the last place; a quotient
-// below 2^-126 is 0.
+// = 2^t (1 + d), t = -g log2(e) as it is rounded and d = -g - t ln 2 what that left
+// out, of the constant's own rounding too: below 2^-17 where 2^t is neither 0 nor
+// infinite.  Past that d is large, infinite or (infinite g) NaN; the factor's bounds
+// leave the 0 or infinity in front of it what it is.  The power is off by 2^-22, d by t
+// times 2^-29 (ln 2 rounded; 2^-22 at the most), the reciprocal by one unit in the last
+// place, with three roundings 13 * 2^-24 together; a quotient below 2^-126 is 0.
 __device__ __forceinline__ float sigmoid(float g) {
     constexpr float L = -1.4426950408889634f, LN2 = 0.6931471805599453f;
-    const float t = g * L, r = fmaf(g, L, -t);
+    const float t = g * L, d = fmaf(t, -LN2, -g);
     float p, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + p * fminf(fmaxf(fmaf(r, LN2, 1.0f), 0.99f), 1.01f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + p * fminf(fmaxf(1.0f + d, 0.99f), 1.01f)));
     return q;
 }
 __device__ __forceinline__ float gated(float y, float g, int act) {

@@ -288,3 +288,19 @@ def test_finite_gates_of_any_size(gt, K, act):
     qop = torch.empty(hq.hq_act_operand_bytes(d, M), dtype=torch.uint8, device=DEV)
     hq.gated_norm_quant(d, x, gate, None, sg, D, act, qx=qx2, qop=qop, sx=sx2)
     assert torch.equal(qx, qx2) and torch.equal(sx, sx2)
+
+
+@pytest.mark.parametrize("M,K", [(16, 8192), (3, 16384)])
+def test_the_sigmoid_keeps_its_accuracy_far_below_zero(M, K):
+    """x is a power of two and h fp32, so h is the sigmoid as it was computed: power 2^-22, ln 2 as it is rounded 2^-22 at
+    the far end, reciprocal 2^-23, three roundings: 13 * 2^-24."""
+    gate = torch.linspace(-87.2, 20.0, M * K, dtype=torch.float64, device=DEV).float().view(M, K)
+    x = 2.0 ** torch.randint(0, 10, (M, K), device=DEV).float()
+    h, both = torch.empty((M, K), device=DEV), torch.empty((M, K), device=DEV)
+    d, sg = hq.make_desc(K, 128, 32, "w4"), signs_dev(hq.hq_make_signs(1, K))
+    hq.gated_norm_quant(d, x, gate, None, None, 128, "sigmoid", h=h)
+    hq.gated_norm_quant(d, x, gate, None, sg, 128, "sigmoid", h=both, qx=torch.empty((M, K), dtype=torch.int8, device=DEV),
+                        sx=torch.empty(M, device=DEV))
+    want = x.double() / (1.0 + torch.exp(-gate.double()))
+    for t in (h, both):
+        assert float(((t.double() - want) / want).abs().max()) <= 13 * 2.0 ** -24
