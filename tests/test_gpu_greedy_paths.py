@@ -1,0 +1,78 @@
+"""Greedy tokens on each way through the kernel that a launch takes: one, two or
+four rows of a sequence to a block, histories sorted by a kernel in front or not,
+adjusted logits kept or not; and biases in any number.
+
+Which way a call takes follows from its sizes; `way` states the rule again, so
+that every case says what it is for.  Results are compared bit for bit with the
+same rules in numpy's fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_greedy import BF16, DEV, F16, F32, Request
+
+pytestmark = pytest.mark.gpu
+
+
+def way(rows, V, room):
+    """Tokens of a chunk, rows of a block, and whether histories in rooms of `room` tokens are sorted."""
+    B, m, sms = len(rows), max(rows), torch.cuda.get_device_properties(0).multi_processor_count
+    chunk, group = 1024, 1
+    while chunk < 4096 and B * m * -(-V // (2 * chunk)) >= 4 * sms:
+        chunk *= 2
+    chunks = -(-V // chunk)
+    while group < 4 and group < m and B * -(-m // group) * chunks > 16 * sms:
+        group *= 2
+    return chunk, group, chunks < 64 and B <= 256 and 4 * min(room, 16384) * B * -(-m // group) * chunks > 12 << 20
+
+
+WAYS = [  # rows, V, history, chunk, rows a block, sorted
+    ([16, 9, 15, 2, 13, 16, 1, 7], 151551, 50, 4096, 2, False),   # groups of two and one, chunks that end early
+    ([16, 9, 15, 2, 13, 16, 1, 7], 151551, 9000, 4096, 2, True),
+    ([7, 6, 5, 4, 3, 2, 1, 0] * 8, 40963, 300, 4096, 4, False),   # groups of four, three, two and one; a last chunk of three
+    ([7, 6, 5, 4, 3, 2, 1, 0] * 8, 40963, 3000, 4096, 4, True),
+    ([1] * 128, 50257, 4000, 4096, 1, True),
+    ([3, 1, 2] * 20, 30011, 17000, 4096, 1, True),                # more than what is sorted
+]
+
+
+@pytest.mark.parametrize("rows,V,history,chunk,group,sort", WAYS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_way_with_and_without_the_logits_kept(rows, V, history, chunk, group, sort, dtype):
+    assert way(rows, V, history + 7) == (chunk, group, sort)
+    r = Request(rows, V, seed=V + history, history=history, dtype=dtype, near=V // 3)
+    r.len[::3] = history
+    r.run()
+    r.run(out_type=dtype, pad=V % 2, opad=1)  # rows of a block that start at other alignments
+    r.run(in_place=True, lead=1, pad=5)
+
+
+@pytest.mark.parametrize("rows,V,history,chunk,group,sort", WAYS[:4])
+def test_groups_with_16_bit_logits_kept_in_fp32(rows, V, history, chunk, group, sort):
+    assert way(rows, V, history + 7) == (chunk, group, sort)
+    Request(rows, V, seed=V - history, history=history, dtype=F16, near=500).run(out_type=F32, lead=3, opad=2)
+
+
+def test_groups_without_rules_or_with_masks_alone():
+    rows, V = [16, 9, 15, 2, 13, 16, 1, 7], 151551
+    for mask in (False, True):
+        r = Request(rows, V, seed=31)
+        r.use = dict.fromkeys(r.use, False)
+        r.use["mask"] = mask
+        r.run(out_type=F32, pad=1)
+
+
+def test_groups_whose_rows_are_masked_out_or_not_finite():
+    rows, V = [7, 6, 5, 4, 3, 2, 1, 0] * 8, 40963
+    assert way(rows, V, 3007) == (4096, 4, True)
+    r = Request(rows, V, seed=32, history=3000)
+    R = r.starts[-1]
+    r.mask_ids = np.arange(R, dtype=np.int32)
+    r.masks[::5] = 0
+    r.masks[1::5] = 0xFFFFFFFF
+    r.x[2::7, ::9] = float("nan")
+    r.x[3::7, 5::11] = float("inf")
+    r.x[4::7] = -float("inf")
+    r.x[6::7] = torch.finfo(F32).min
+    r.run(out_type=F32)
