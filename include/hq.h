@@ -795,7 +795,9 @@ typedef struct {
  *   bias_starts  int32 [n_slots + 1], ascending, within [0, n_bias]: slot s has the
  *           biases bias_values[j] of tokens bias_tokens[j] (int32, fp32 [n_bias]),
  *           bias_starts[s] <= j < bias_starts[s + 1]; of a token listed twice the
- *           last one counts
+ *           last one counts.  Each part of the vocabulary (1024 to 4096 tokens)
+ *           reads its slot's list once or twice: thousands of entries cost
+ *           microseconds, one for each of 151552 tokens a third of a millisecond
  *   masks   uint32 [n_masks][ldmask], ldmask at least ceil(V / 32): token t is
  *           allowed where bit t % 32 of word t / 32 is set
  * n_slots from 0 to 65536 (0: no rule but the masks); 0 <= n_bias, n_masks < 2^31. */

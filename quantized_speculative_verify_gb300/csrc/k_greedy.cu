@@ -37,6 +37,12 @@
 // Every chunk's block would read the whole history of its sequence.  Where that
 // adds up, a kernel in front sorts the histories by chunk into the workspace.
 //
+// Of a slot's biases a block keeps those of its chunk, up to 128; where there are
+// more, another pass over the slot's list finds each token's last one.  So a block's
+// work grows with the list and not with its square: one row of 151552 with 300 biases
+// next to one another 8.3 us (a walk through the list for each: 33), with 5000
+// anywhere 16.5, with one for every token 0.34 ms (70).
+//
 // The order of values is that of a signed integer (a float's bits, the lower 31
 // inverted where it is negative; NaN above all), so the largest of a warp is one
 // instruction.  A thread keeps its largest value and where the eight logits with
@@ -57,7 +63,8 @@ constexpr int GROUP = 4;         // rows of a sequence that share one table
 constexpr int MOST = 4096, LEAST_SHIFT = 10;  // tokens of a chunk, a power of two: at most 4096, at least 2^10
 constexpr int EIGHTS = MOST / 8 / GT;     // loads of a thread for a row
 constexpr int FLIGHT = 4;        // loads of the history of a thread on their way together
-constexpr int BIASES = 128;      // biases of a chunk that are found in shared memory
+constexpr int BIASES = 128;      // biases of a chunk that are kept; with more, a place for each of
+constexpr int LASTS = MOST / 2;  // so many tokens at a time
 constexpr uint32_t SEEN = 1u << 31, BIASED = 1u << 30, DRAFTED = 1u << 29, TIMES = DRAFTED - 1;
 
 // The largest value; NaN (one pattern of it) if one is.
@@ -121,7 +128,10 @@ __host__ __device__ inline size_t record_at(int i) {
 struct Shared {
     uint32_t word[MOST];            // what reaches each token
     uint32_t bits[MOST / 32 + 4];   // (one more for reads across the last one's end)
-    uint16_t list[MOST];
+    union {
+        uint16_t list[MOST];
+        int32_t last[LASTS];        // with more than BIASES biases: each token's last one
+    };
     int32_t bias_at[BIASES];        // biases of this chunk: their number in the slot's list, their token
     uint16_t bias_of[BIASES];
     int order[GROUP][GT / 32], at[GROUP][GT / 32];  // of each warp, of the logits that stream
@@ -218,8 +228,10 @@ __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const i
     for (int i = tid; i < s_start[chunks]; i += ST) sorted[i] = s_sorted[i];
 }
 
-// RULES: penalties or biases, which need the table.  sorted: the histories are.
-template <class T, class O, bool RULES>
+// RULES: penalties or biases, which need the table.  MANY: a slot may have more than
+// BIASES of them (else their code is left out: the chain of one row waits for its
+// instructions too, 7.1 us without it and 7.35 with it).  sorted: the histories are.
+template <class T, class O, bool RULES, bool MANY = false>
 __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int chunk, const int group, const bool sorted) {
     __shared__ __align__(16) Shared s;
     pdl_launch_dependents();
@@ -263,17 +275,20 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
     float rep = 1.0f, pres = 0.0f, freq = 0.0f;
     bool use_rep = false, use_times = false;
     int listed_tokens = 0, first_bias = 0, last_bias = 0;
-    // The tokens of the list, for all rows: the block's warps take the rows in turn.
-    // j0 .. j1: the slot's biases.
-    auto for_list = [&](int held, int j0, int j1) {
+    bool many_biases = false;
+    // The tokens of the list from i0 to i1, for all rows: the block's warps take the
+    // rows in turn.  by_token: the tokens themselves, those of the bit field, with
+    // their last biases in s.last.
+    auto for_list = [&](auto by_token, int i0, int i1) {
         const int share = GT / 32 / (r1 - r0), r = r0 + warp / share;
         if (r >= r1) return;
         const T *x = logits_of(first + r);
         O *out = out_of(first + r);
         const uint32_t *mask = mask_of(r);
         int best = NONE, at = INT_MAX;
-        for (int i = warp % share * 32 + lane; i < held; i += 32 * share) {
-            const int d = s.list[i];
+        for (int i = i0 + warp % share * 32 + lane; i < i1; i += 32 * share) {
+            const int d = by_token ? i : s.list[i];
+            if (by_token && !(s.bits[d >> 5] >> (d & 31) & 1u)) continue;
             const uint32_t word = s.word[d];
             const bool allowed = !mask || (mask[d >> 5] >> (d & 31) & 1u);
             float l = to_f32(x[d]);
@@ -288,12 +303,10 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
                 if (a.rules.presence) l = __fsub_rn(l, pres);
             }
             if (word & BIASED) {  // of a token listed twice the last one
-                int j = j0;
-                if (s.n_biased <= BIASES) {
+                int j = by_token ? s.last[i - i0] : 0;
+                if (!by_token) {
                     for (int t = 0; t < s.n_biased; ++t)
                         if (s.bias_of[t] == d && s.bias_at[t] > j) j = s.bias_at[t];
-                } else {
-                    for (j = j1 - 1; j > j0 && a.rules.bias_tokens[j] != lo + d;) --j;
                 }
                 l = __fadd_rn(l, a.rules.bias_values[j]);
             }
@@ -307,9 +320,25 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
         }
         const int most = __reduce_max_sync(0xffffffffu, best);
         at = __reduce_min_sync(0xffffffffu, best == most ? at : INT_MAX);
-        if (lane == 0) {
+        if (lane == 0 && (!by_token || most > s.list_order[r - r0][warp])) {
             s.list_order[r - r0][warp] = most;
             s.list_at[r - r0][warp] = at;
+        }
+    };
+    // The same where a chunk has many biases, LASTS tokens at a time: the last bias of
+    // each by another pass over the slot's (j0 .. j1).  Every thread calls.
+    auto for_tokens = [&](int j0, int j1) {
+        for (int from = 0; from < n; from += LASTS) {
+            const int to = from + LASTS < n ? from + LASTS : n;
+            for (int i = tid; i < to - from; i += GT) s.last[i] = 0;
+            __syncthreads();
+            for (int j = j0 + tid; j < j1; j += GT) {
+                const int32_t t = a.rules.bias_tokens[j];
+                if (t >= lo + from && t < lo + to) atomicMax(&s.last[t - lo - from], j);
+            }
+            __syncthreads();
+            for_list(std::true_type{}, from, to);
+            __syncthreads();
         }
     };
     if (RULES) {
@@ -462,6 +491,7 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
             listed_tokens += s.counts[i];
         }
         for (; field != 0; field &= field - 1) s.list[before++] = (uint16_t)(32 * tid + __ffs(field) - 1);
+        many_biases = MANY && s.n_biased > BIASES;
         first_bias = j0;
         last_bias = j1;
         __syncthreads();  // the list is whole
@@ -539,7 +569,8 @@ __global__ void __launch_bounds__(GT, 6) k_greedy(const GreedyArgs a, const int 
 #pragma unroll 1
     for (int phase = 0; phase < 2; ++phase) {
         if ((phase == 0) == (a.out != nullptr)) stream();
-        else if (RULES && listed_tokens > 0) for_list(listed_tokens, first_bias, last_bias);
+        else if (MANY && many_biases) for_tokens(first_bias, last_bias);
+        else if (RULES && listed_tokens > 0) for_list(std::false_type{}, 0, listed_tokens);
         __syncthreads();
     }
     if (tid >= r1 - r0) return;
@@ -632,7 +663,9 @@ cudaError_t launch_t(const GreedyArgs &a, bool pdl, cudaStream_t s) {
         e = launch_kernel(k_sort_history, dim3((unsigned)a.B), dim3(ST), SORTED * 4, pdl, s, a, shift, chunks);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel(k_greedy<T, O, true>, grid, dim3(GT), 0, pdl || sorted, s, a, chunk, group, sorted);
+    const bool many = biased && a.rules.n_bias > BIASES;
+    return launch_kernel(many ? k_greedy<T, O, true, true> : k_greedy<T, O, true>, grid, dim3(GT), 0, pdl || sorted, s, a, chunk, group,
+                         sorted);
 }
 
 }  // namespace

@@ -10,7 +10,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_greedy import BF16, DEV, F16, F32, Request
+from quantized_speculative_verify_gb300 import hq
+from test_gpu_greedy import BF16, DEV, F16, F32, Request, counters
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,52 @@ def test_groups_whose_rows_are_masked_out_or_not_finite():
     r.x[4::7] = -float("inf")
     r.x[6::7] = torch.finfo(F32).min
     r.run(out_type=F32)
+
+
+@pytest.mark.parametrize("V,n", [(3000, 128), (3000, 129), (3000, 300), (151552, 300), (151552, 5000), (20011, 40000), (151553, 151553)])
+def test_many_biases(V, n):
+    """Next to one another, spread, several to a token, one for every token; of a token listed again the last one counts."""
+    r = Request([3, 1, 2], V, seed=n, n_slots=3)
+    rng = np.random.default_rng(n)
+    first = int(rng.integers(0, V - min(n, V) + 1))
+    near = first + rng.permutation(min(n, V))
+    r.bias[0] = [(int(t), np.float32(v)) for t, v in zip(near, rng.standard_normal(len(near)) * 4)]
+    far = rng.integers(-2, V + 2, n)
+    r.bias[1], r.bias[2] = [], [(int(t), np.float32(v)) for t, v in zip(far, rng.standard_normal(n) * 4)] if n > 129 else []
+    r.run(out_type=F32)
+    r.run()
+
+
+def test_many_biases_in_groups():
+    rows, V = [7, 6, 5, 4, 3, 2, 1, 0] * 8, 40963
+    r = Request(rows, V, seed=35, history=3000)
+    rng = np.random.default_rng(36)
+    for s in range(0, 64, 9):
+        r.bias[s] = [(int(t), np.float32(v)) for t, v in zip(rng.integers(0, V, 2000), rng.standard_normal(2000) * 4)]
+        r.bias[s] += [(int(t), np.float32(v)) for t, v in zip(4096 + rng.integers(0, 300, 600), rng.standard_normal(600) * 4)]
+    r.run(out_type=F32)
+    assert way(rows, V, 3007) == (4096, 4, True)
+
+
+def test_the_work_for_a_bias_does_not_grow_with_the_list():
+    """A bias for every token of a large vocabulary: each block reads the list twice, a third of a millisecond.  A walk through
+    the list for each token took 70."""
+    V = 151552
+    x = torch.randn((1, V), device=DEV)
+    ints = dict(dtype=torch.int32, device=DEV)
+    tokens, values = torch.randperm(V, device=DEV).to(torch.int32), torch.randn(V, device=DEV)
+    rules = hq.LogitRules(1, bias=(torch.tensor([0, V], **ints), tokens, values))
+    ws = torch.zeros(hq.hq_greedy_tokens_workspace_bytes(1), dtype=torch.uint8, device=DEV)
+    greedy = torch.empty(1, **ints)
+    want = x[0].clone()
+    want[tokens.long()] += values
+    times = []
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        hq.greedy_tokens(x, None, 1, rules=rules, greedy=greedy, workspace=ws)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    assert int(greedy[0]) == int(want.argmax()) and counters(ws, 1) == 0
+    assert min(times) < 1.0, times  # ms
