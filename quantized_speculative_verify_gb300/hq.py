@@ -902,7 +902,8 @@ def rope_freqs(rot: int, base: float = 10000.0, kind: str = "plain", factor: flo
     `kind` "linear", "ntk", "yarn" or "bands" scales them for contexts `factor`
     times as long as the model's own of `original` positions; low and high: the
     turns over `original` between which "yarn" (1 and 32 if not given) and
-    "bands" (1 and 4) go over from divided frequencies to those as they are."""
+    "bands" (1 and 4) go over from divided frequencies to those as they are.
+    Models with "yarn" also have a gain of rope_write, usually 0.1 ln(factor) + 1."""
     if kind not in ROPE_KINDS:
         raise ValueError(f"rope_freqs: kind must be one of {', '.join(ROPE_KINDS)}, got {kind!r}")
     out = np.zeros(max(rot // 2, 1), dtype=np.float64)

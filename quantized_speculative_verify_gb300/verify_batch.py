@@ -37,11 +37,16 @@ from . import hq, synth
 class BatchLayer:
     """A layer's packed projections, norm weight and adapters, with the buffers
     for up to `rows` tree nodes (at most HQ_MAX_M) of a batch.  freqs: radians a
-    position of the heads' pairs (rope_freqs), None: no rotary positions; gate:
+    position of the heads' pairs (rope_freqs), None: no rotary positions; layout,
+    gain, q_norm and k_norm (fp32 [dim], with eps), as rope_write takes them, go
+    with them (frequencies of kind "yarn" with a gain of 0.1 ln(factor) + 1); gate:
     the attention's output is gated by the sigmoid of a projection of its own."""
 
     def __init__(self, hidden: int, heads: int, kv_heads: int, dim: int, rows: int, adapters: int, rank: int, seed: int = 0,
-                 group: int = 64, fmt: str = "w4", device="cuda", freqs=None, gate: bool = False):
+                 group: int = 64, fmt: str = "w4", device="cuda", freqs=None, gate: bool = False, layout: str = "half",
+                 gain: float = 1.0, q_norm=None, k_norm=None, eps: float = 1e-6):
+        if freqs is None and (gain != 1.0 or q_norm is not None or k_norm is not None):
+            raise ValueError("BatchLayer: gain, q_norm and k_norm go with the rotary positions (freqs)")
         self.hidden, self.heads, self.kv_heads, self.dim, self.rows = hidden, heads, kv_heads, dim, rows
         q, kv = heads * dim, kv_heads * dim
         signs = hq.hq_make_signs(seed, hidden), hq.hq_make_signs(seed + 1, q)
@@ -61,6 +66,7 @@ class BatchLayer:
         self.adapters = {"q": adapter(hidden, q), "k": adapter(hidden, kv), "v": adapter(hidden, kv), "o": adapter(q, hidden)}
         self.scale = torch.ones(adapters, device=device)
         self.turns = None if freqs is None else hq.rope_turns(freqs, device)
+        self.rope = dict(layout=layout, gain=gain, q_weight=q_norm, k_weight=k_norm, eps=eps)
         self.gated = torch.empty((rows, q), dtype=torch.float16, device=device) if gate else None
         self.Y = torch.empty((rows, self.qkv.layer.N), device=device)
         self.out = torch.empty((rows, hidden), device=device)
@@ -95,7 +101,8 @@ class BatchLayer:
             hq.pages_write(cache, planes[0], planes[1], k, v, starts, max_rows, seqs=seqs)
             q16.copy_(q)
         else:
-            hq.rope_write(cache, planes[0], planes[1], q, k, v, self.turns, starts, max_rows, parent=parent, seqs=seqs, out=q16)
+            hq.rope_write(cache, planes[0], planes[1], q, k, v, self.turns, starts, max_rows, parent=parent, seqs=seqs, out=q16,
+                          **self.rope)
         hq.prefix_attention(cache, planes[0], planes[1], q16, starts, max_rows, shared, max_len, 1.0 / math.sqrt(self.dim),
                             parent=parent, seqs=seqs, out=att, workspace=self.ws_attn)
         flat = att.view(M, self.heads * self.dim)
@@ -165,8 +172,9 @@ def main() -> None:
         p.error(f"requests x nodes must be at most {hq.HQ_MAX_M}")
     dev, D, M = "cuda", hq.HQ_ATTN_HEAD_DIM, B * m
     heads, kv_heads, ps = cfg["hidden"] // D, cfg["kv"] // D, 64
-    freqs = hq.rope_freqs(D, kind="yarn", factor=4.0, original=8192)
-    layer = BatchLayer(cfg["hidden"], heads, kv_heads, D, M, adapters=B, rank=16, freqs=freqs, gate=True)
+    factor = 4.0
+    freqs, gain = hq.rope_freqs(D, kind="yarn", factor=factor, original=8192), 0.1 * math.log(factor) + 1.0
+    layer = BatchLayer(cfg["hidden"], heads, kv_heads, D, M, adapters=B, rank=16, freqs=freqs, gain=gain, gate=True)
     head = Head(cfg["hidden"], a.vocab, M, B, (a.steps + 1) * m)
     max_pages = -(-(a.shared + (a.steps + 1) * m) // ps)
     cache = hq.PagedCache.empty(2, max_pages + B * (a.steps * m // ps + 3), kv_heads, ps, D, B + 1, max_pages)

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from quantized_speculative_verify_gb300 import hq
+from quantized_speculative_verify_gb300 import hq, verify_batch
 from test_batch_host import BAD_CACHES, FAKE, pages
 
 E, U = hq.HQ_ERR_INVALID_ARG, hq.HQ_ERR_UNSUPPORTED
@@ -333,3 +333,28 @@ def test_greedy_and_accept_binding_checks(host_pointers):
         hq.tree_accept_batch(g, None, g, None, 2, path=z((2, 1), **I32))
     with pytest.raises(ValueError, match="bonus"):
         hq.tree_accept_batch(g, None, g, None, 2, bonus=z(3, **I32))
+
+
+class Stop(Exception):
+    pass
+
+
+def test_the_step_of_the_command_has_its_frequencies_gain(monkeypatch):
+    """Frequencies for contexts four times as long, of the kind whose rotated elements have a gain."""
+    seen = {}
+
+    def layer(*a, **kw):
+        seen.update(kw)
+        raise Stop
+    monkeypatch.setattr("sys.argv", ["verify_batch"])
+    monkeypatch.setattr(verify_batch, "BatchLayer", layer)
+    with pytest.raises(Stop):
+        verify_batch.main()
+    assert np.array_equal(seen["freqs"], hq.rope_freqs(128, kind="yarn", factor=4.0, original=8192))
+    assert seen["gain"] == pytest.approx(0.1 * math.log(4.0) + 1.0)
+
+
+def test_a_layer_without_rotary_positions_refuses_what_goes_with_them():
+    for bad in (dict(gain=1.1), dict(q_norm=torch.ones(64)), dict(k_norm=torch.ones(64))):
+        with pytest.raises(ValueError, match="rotary"):
+            verify_batch.BatchLayer(512, 8, 2, 64, 4, 1, 8, **bad)

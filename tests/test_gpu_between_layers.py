@@ -154,6 +154,34 @@ def test_a_step_replayed_from_a_graph_goes_on_like_eager_steps():
     assert all(torch.equal(a, b) for a, b in zip(seen[0][3], seen[1][3])) and torch.equal(seen[0][4], seen[1][4])
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_a_layer_rotates_as_its_model_does(layout):
+    """Gain, layout and the weights of q's and k's norms reach the rotation: queries and keys are the formula's."""
+    rows, shared, gain, eps = [5, 3], 90, 0.1 * np.log(4.0) + 1.0, 1e-5
+    M, starts, parent = sum(rows), [0, 5, 8], [0, 0, 0, 1, 2, 0, 0, 1]
+    g = torch.Generator(device=DEV).manual_seed(21)
+    qw, kw = (1.0 + 0.2 * torch.randn(D, generator=g, device=DEV) for _ in range(2))
+    freqs = hq.rope_freqs(48, kind="yarn", factor=4.0, original=100.0)
+    layer = BatchLayer(HIDDEN, HEADS, KV, D, M, adapters=3, rank=8, seed=2, freqs=freqs, gain=gain, layout=layout, q_norm=qw, k_norm=kw,
+                       eps=eps, gate=True)
+    cache = fresh(3, shared)
+    x, r = torch.randn((M, HIDDEN), generator=g, device=DEV), torch.randn((M, HIDDEN), generator=g, device=DEV).bfloat16()
+    layer.step(cache, (0, 1), x, r, ints([1, 2]), ints(starts), ints(rows), ints(parent), ints([0] * M), 5, shared, 200)
+    q, k, _ = (t.unflatten(1, (-1, D)) for t in layer.qkv.split(layer.Y[:M])[:3])
+    turns = layer.turns.cpu().numpy().view(np.uint64).tolist()
+    gain, eps = float(np.float32(gain)), float(np.float32(eps))
+    for b, m in enumerate(rows):
+        lo, depth = starts[b], [0] * m
+        for i in range(1, m):
+            depth[i] = depth[parent[lo + i]] + 1
+        pos = [shared + d for d in depth]
+        close(layer.q16[lo:lo + m], *expected(q[lo:lo + m], pos, turns, layout, gain, qw, eps))
+        at = [shared + i for i in range(m)]
+        page = [int(cache.table[b + 1, p // PS]) for p in at]
+        close(cache.pool[0, page, :, [p % PS for p in at]], *expected(k[lo:lo + m], pos, turns, layout, gain, kw, eps))
+    assert hq.pages_status(cache) == hq.HQ_OK
+
+
 def test_the_delta_rule_layer_behind_its_gate():
     """delta_tree, the gated norm per head, the output projection: the operand holds the codes of the formula."""
     M, H, DD = 16, 4, hq.HQ_DELTA_HEAD_DIM
