@@ -188,6 +188,9 @@ def main() -> None:
     g = torch.Generator().manual_seed(3)
     parent = ints([0 if i == 0 else max(0, i - 1 - int(torch.randint(0, 3, (1,), generator=g))) for _ in range(B) for i in range(m)])
     tokens = torch.randint(0, a.vocab, (M,), generator=g).to(dev, torch.int32)
+    # each tree's root is its request's newest token, the last of its history
+    head.history.tokens[:, 0] = tokens[::m]
+    head.history.lens.fill_(1)
     x, residual = torch.randn((M, cfg["hidden"]), device=dev), torch.randn((M, cfg["hidden"]), device=dev).bfloat16()
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for step in range(a.steps):
@@ -199,6 +202,7 @@ def main() -> None:
         end.record()
         # the next trees, drafted from what the model said of these
         tokens = torch.where(torch.rand(M, device=dev) < 0.5, bonus.repeat_interleave(m), tokens)
+        tokens[::m] = bonus
         torch.cuda.synchronize()
         print(f"step {step}: {M} rows, lengths {cache.lens[1:].tolist()}, {int((cache.ref > 0).sum())} pages held, "
               f"{begin.elapsed_time(end) * 1e3:.0f} us")

@@ -11,7 +11,7 @@ import numpy as np
 import pytest
 import torch
 
-from quantized_speculative_verify_gb300 import hq
+from quantized_speculative_verify_gb300 import hq, verify_batch
 from quantized_speculative_verify_gb300.verify_batch import BatchLayer, Head, prefill
 from test_gpu_gate import check as check_codes
 from test_gpu_gate import value
@@ -180,6 +180,23 @@ def test_a_layer_rotates_as_its_model_does(layout):
         page = [int(cache.table[b + 1, p // PS]) for p in at]
         close(cache.pool[0, page, :, [p % PS for p in at]], *expected(k[lo:lo + m], pos, turns, layout, gain, kw, eps))
     assert hq.pages_status(cache) == hq.HQ_OK
+
+
+def test_the_command_drafts_from_the_newest_tokens(monkeypatch):
+    """Every tree's root is the last token of its request's history."""
+    seen, greedy = [], hq.greedy_tokens
+
+    def spy(logits, starts, max_rows, parent, tokens, **kw):
+        h, roots = kw["history"], tokens[starts[:-1].long()]
+        assert h.lens.tolist() == [max(1, n) for n in h.lens.tolist()]
+        assert torch.equal(h.tokens.gather(1, h.lens.long().unsqueeze(1) - 1)[:, 0], roots)
+        seen.append(roots.tolist())
+        return greedy(logits, starts, max_rows, parent, tokens, **kw)
+    monkeypatch.setattr(verify_batch.hq, "greedy_tokens", spy)
+    monkeypatch.setattr(verify_batch.synth, "DECODER_9B", dict(verify_batch.synth.DECODER_9B, hidden=512, kv=256))
+    monkeypatch.setattr("sys.argv", ["verify_batch", "--requests", "3", "--nodes", "5", "--shared", "100", "--steps", "3", "--vocab", "700"])
+    verify_batch.main()
+    assert len(seen) == 3 and seen[0] != seen[1]
 
 
 def test_the_delta_rule_layer_behind_its_gate():
