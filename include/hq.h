@@ -848,6 +848,12 @@ typedef struct {
  *           zeroed once: counters, and room for long histories sorted by token
  *           (64 KB a row, for 256 rows at most).  One workspace of the most rows
  *           serves every call in turn
+ * Long histories of many rows are sorted by token in front, by another kernel:
+ * where cap (at most 16384 of it) and the rows are so large that it pays for
+ * histories that fill it.  Up to 256 sequences and vocabularies below 258049 do
+ * that, with more rows than 16 at 151552 tokens; other calls read a history once
+ * for each 1024 to 4096 tokens of the vocabulary, and so do all what lies past a
+ * history's first 16384.
  * Tokens outside [0, V), in any of the lists, are passed over.  Rows that no
  * sequence claims are left as they were, in out and greedy.  Results repeat bit
  * for bit.  flags: HQ_LAUNCH_DEFAULT or HQ_LAUNCH_PDL (nothing is read before

@@ -154,12 +154,23 @@ __device__ __forceinline__ uint32_t eight_bits(const uint32_t *words, int d, int
 // they are of, counted by each lane for itself (64 counters a chunk next to one
 // another: a third of a text lies in one chunk, and no two lanes of a warp meet at a
 // counter or a bank), then each token's place.  A token
-// of the prompt has its top bit set.  Worth it where all blocks together would
-// otherwise read more than SORT_FROM bytes of histories, V = 151552: 128 rows with
-// 16000 tokens each, 300 MB, 105 us without, 61 with it (9 of them the sort); 64 with
-// 4000, 37 MB, 31 and 26; 32 with 4000, 19 MB, 19.7 and 16.8; 128 of V = 32000 with
-// 4000, 16 MB, 19.9 and 18.2; 16 trees of 8 nodes, V = 100000, with 1000, 6 MB, 21 and
-// 20, where it is one more launch for the host.
+// of the prompt has its top bit set.
+//
+// Worth it where all blocks together would otherwise read more than SORT_FROM bytes
+// of what it sorts; the host knows the histories' room, not their lengths, and goes by
+// that.  Without and with it, full rooms, V = 151552: 128 rows with 16000 tokens each,
+// kept (289 MB), 102 and 56 us, with 500 (9 MB) 52 and 48; 64 with 4000 (36 MB) 31.6 and
+// 26.0; eight trees with all rules and 2000 (18 MB) 30.6 and 30.5.  V = 32000: 128 with 4000
+// (16 MB) 20.0 and 18.0, with 2000 (8 MB) 16.6 and 17.3; 32 with 4000 (16 MB) 17.5 and
+// 15.1; 8 with 16000 (16 MB) 18.5 and 19.0; one with 16000 (2 MB) 18.5 and 19.8.  In rooms
+// of 131072, V = 32000, a tree of 16 nodes with 500 tokens 9.25 and 9.8, with 16000 20.7
+// and 19.6 (by the room 32 MB: sorted); one row with 500 7.3 and 9.3 (2 MB: not).
+//
+// It has its limits: 256 sequences; 63 chunks, so no vocabulary from 258049 tokens on
+// (128 rows of 262144 76 us with 500 tokens each, 153 with 16000) and, as few rows have
+// smaller chunks, with V = 151552 no call of 16 rows or fewer (a tree of 16 nodes with
+// 16000 tokens 35 us); and of a longer text every block reads the tokens past the
+// first SORTED (16 rows of 32000 with 60000 tokens 49 us).
 constexpr int ST = 1024;
 constexpr long long SORT_FROM = 12ll << 20;
 __global__ void __launch_bounds__(ST) k_sort_history(const GreedyArgs a, const int shift, const int chunks) {
@@ -649,7 +660,7 @@ cudaError_t launch_t(const GreedyArgs &a, bool pdl, cudaStream_t s) {
     if (!biased && !penalties)
         return launch_kernel(k_greedy<T, O, false>, grid, dim3(GT), 0, pdl, s, a, chunk, group, false);
     const bool sorted = penalties && a.history.tokens && a.B <= SORT_MOST && a.B <= a.rows && chunks < CHUNKS &&
-                        4ll * a.history.cap * a.B * groups * chunks > SORT_FROM;
+                        4ll * (a.history.cap < SORTED ? a.history.cap : SORTED) * a.B * groups * chunks > SORT_FROM;
     if (sorted) {
         int dev = 0, ready = 0;
         cudaError_t e = cudaGetDevice(&dev);

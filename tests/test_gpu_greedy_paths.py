@@ -79,6 +79,31 @@ def test_groups_whose_rows_are_masked_out_or_not_finite():
     r.run(out_type=F32)
 
 
+@pytest.mark.parametrize("B,V,history,room,sort", [
+    (1, 32000, 500, 131072, False),   # one request in a large room: 2 MB of what would be sorted
+    (4, 32000, 16384, 131072, False),
+    (64, 32000, 500, 131072, True),   # by the room
+    (64, 32000, 500, 507, False),
+    (64, 32000, 4000, 4000, True),
+    (128, 258048, 300, 20000, True),  # 63 chunks
+    (128, 258049, 300, 20000, False),
+    (257, 20000, 300, 20000, False),
+])
+def test_which_calls_sort(B, V, history, room, sort):
+    """The sorted histories stay in the workspace, so a call that does not sort leaves it as it was, all zeros."""
+    assert way([1] * B, V, room)[2] == sort
+    g = torch.Generator(device=DEV).manual_seed(B)
+    tokens = torch.randint(0, V, (B, room), generator=g, device=DEV).to(torch.int32)
+    lens = torch.full((B,), history, dtype=torch.int32, device=DEV)
+    rules = hq.LogitRules(B, presence=torch.full((B,), 100.0, device=DEV))
+    x = torch.randn((B, V), generator=g, device=DEV)
+    ws = torch.zeros(hq.hq_greedy_tokens_workspace_bytes(B), dtype=torch.uint8, device=DEV)
+    greedy = hq.greedy_tokens(x, None, 1, history=hq.History(tokens, lens), rules=rules, workspace=ws)
+    said = torch.zeros((B, V), dtype=torch.bool, device=DEV).scatter_(1, tokens[:, :history].long(), True)
+    assert torch.equal(greedy.long(), torch.where(said, x - 100.0, x).argmax(1))
+    assert counters(ws, B) == 0 and bool(ws.any()) == sort
+
+
 @pytest.mark.parametrize("V,n", [(3000, 128), (3000, 129), (3000, 300), (151552, 300), (151552, 5000), (20011, 40000), (151553, 151553)])
 def test_many_biases(V, n):
     """Next to one another, spread, several to a token, one for every token; of a token listed again the last one counts."""
