@@ -304,3 +304,18 @@ def test_the_sigmoid_keeps_its_accuracy_far_below_zero(M, K):
     want = x.double() / (1.0 + torch.exp(-gate.double()))
     for t in (h, both):
         assert float(((t.double() - want) / want).abs().max()) <= 13 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("K", [448, 1024, 1984, 2048, 4096, 8192])
+@pytest.mark.parametrize("xt,gt", [(F32, BF16), (BF16, BF16), (F32, F16), (F16, F16)])
+def test_codes_with_types_known_at_compile_time(xt, gt, K):
+    """The same values in types that the kernel looks up at run time give the same bits."""
+    M, D = 1500, 64
+    x, gate, w, signs = make(M, K, D, xt, gt, seed=K, pad=8)
+    d, sg = hq.make_desc(K, 128, 32, "w4"), signs_dev(signs)
+    h, qx, sx = torch.empty((M, K), dtype=gt, device=DEV), torch.empty((M, K), dtype=torch.int8, device=DEV), torch.empty(M, device=DEV)
+    hq.gated_norm_quant(d, x, gate, w, sg, D, "silu", 1e-6, h=h, qx=qx, sx=sx)
+    check(value(x, gate, w, D, "silu", 1e-6), signs, h, qx, sx)
+    h2, qx2, sx2 = torch.empty_like(h), torch.empty_like(qx), torch.empty_like(sx)
+    hq.gated_norm_quant(d, x, gate.float(), w, sg, D, "silu", 1e-6, h=h2, qx=qx2, sx=sx2)
+    assert torch.equal(h, h2) and torch.equal(qx, qx2) and torch.equal(sx, sx2)
