@@ -14,8 +14,9 @@
 // order.  Meanwhile the logits are on their way into the threads' registers, eight
 // a load, asked for before anything else (the next row's before this one is looked
 // at); the list's take no part in their maximum, by their bits.  All the code for
-// the rules is in a pass over the list after that.  What a row's own path adds to the table is the drafted tokens of its
-// ancestors, at most 127 and looked for only at tokens that are marked as drafted.
+// the rules is in a pass over the list after that.  What a row's own path adds to
+// the table is the drafted tokens of its ancestors, at most 127 and looked for only
+// at tokens that are marked as drafted.
 //
 // A block is a chain of waits (its sequence, the history's length, the history, the
 // list's logits, the ticket at the end), 6 us of them for 16 KB of logits, so the
@@ -23,12 +24,13 @@
 // numbers: the first chunks' lists are far longer than the others', and their
 // blocks come first in the grid.
 //
-// V = 151552, fp32: one row 7.1 us (a chain), eight trees of up to 16 nodes with
-// masks and biases 30 us (57 MB), 128 rows with histories of 16000 tokens, adjusted
-// logits kept, 61 us (162 MB, 2.7 TB/s).  What bounds the last two is instructions
-// and waits about alike (46 % of the issue slots; 1800 instructions a warp, 200 of
-// them for its logits).  On the way there (trees, 128 rows): the rules at each logit
-// 80 and 115 us; the table and its list 30 and 73, with chunks of 8192 and each
+// V = 151552, fp32: one row 7.1 us (a chain; the rules at each logit, without a table,
+// took 6.0 for it), eight trees of up to 16 nodes with masks and biases 30 us (57 MB),
+// 128 rows with histories of 16000 tokens, adjusted logits kept, 61 us (162 MB, 2.7
+// TB/s).  Histories are sorted first in the last two.  What bounds them is instructions
+// and waits about alike (41 and 46 % of the issue slots; 1300 and 1600 instructions a
+// warp, 200 of them for its logits).  Without rules the trees take 14 us, with masks
+// alone 21.  On the way there (trees, 128 rows): the rules at each logit 80 and 115 us; the table and its list 30 and 73, with chunks of 8192 and each
 // block reading the whole history; logits in a ring in shared memory 38 and 124 (it
 // leaves room for two blocks an SM); a table by rank for 1024 tokens at a time 33 and
 // 118 (the first chunk's block takes 70); this, with the histories sorted, 30 and 67;

@@ -1080,7 +1080,8 @@ def greedy_tokens(logits: torch.Tensor, starts, max_rows: int, parent=None, toke
     history and rules (None: b).  mask_ids int32 [rows]: the row's mask, -1 none
     (None: mask r for row r).  out [rows][V] (the logits' type or fp32, or logits
     itself): the adjusted logits.  workspace: zeroed once, of at least these
-    rows' size.  Returns greedy int32 [rows] (one that the call makes is -1 in rows
+    rows' size (None: the call makes and zeroes one, up to 64 KB a row: 3 us of 20
+    for 128 rows without rules).  Returns greedy int32 [rows] (one that the call makes is -1 in rows
     that no sequence claims)."""
     rows, V = logits.shape
     B = _batch(None, rows, starts, max_rows, seqs, "greedy_tokens: starts and seqs")
