@@ -683,7 +683,8 @@ int hq_prefix_attention(const hq_pages *cache, int32_t k_plane, int32_t v_plane,
  *                   + f_i / factor t.  lo and hi are where pairs turn `high` and
  *                   `low` times over `original` positions (rounded down and up,
  *                   within 0 and rot - 1): rot ln(original / (2 pi turns)) /
- *                   (2 ln base).  Usually high = 32, low = 1
+ *                   (2 ln base).  Usually high = 32, low = 1, and the gain of
+ *                   hq_rope_write 0.1 ln(factor) + 1
  *   HQ_ROPE_BANDS   the same mix by the turns themselves: 1 - t = (original f_i
  *                   / (2 pi) - low) / (high - low) within 0 and 1; usually low =
  *                   1, high = 4
@@ -724,7 +725,7 @@ int hq_rope_turns(const double *freqs_host, int32_t n, uint64_t *turns_host);
  *   parent    int32 [rows] (device) or NULL; with it max_rows <= HQ_MAX_M
  *   positions int32 [rows] (device) or NULL; any value
  * Arithmetic is fp32 with one rounding to `type` per element; the angle is off
- * by at most 2^-23.  v is rounded or copied.  Rows that no sequence claims
+ * by at most 2^-23, a normed head by 2^-20 of each element.  v is rounded or copied.  Rows that no sequence claims
  * are left as they were, in q_out too.  A row whose sequence, length or place does not
  * exist is not written, k and v of a row whose page does not exist are not
  * written (its q is); both set the cache's status word to HQ_ERR_INVALID_ARG.
